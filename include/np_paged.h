@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define NP_ABI_VERSION 2
+#define NP_ABI_VERSION 3
 
 /* Same type as cudaStream_t / CUstream, without pulling in CUDA headers. */
 typedef struct CUstream_st* np_stream_t;
@@ -101,6 +101,10 @@ typedef enum np_dtype { NP_F32 = 0, NP_BF16 = 1 } np_dtype;
                                 expected; the output of that block is wrong) */
 #define NP_FLAG_CONFIG 0x10  /* a thread block found its launch configuration
                                 inconsistent and did nothing (never expected) */
+#define NP_FLAG_POSITION 0x20 /* np_rope_append: a position outside [0,
+                                max_positions); the nearest one was used */
+#define NP_FLAG_QUERY 0x40   /* np_paged_prefill: query_starts not ascending
+                                within [0, num_tokens]; clamped into it */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* np_status_string(np_status status);
@@ -126,6 +130,101 @@ np_status np_kv_append(void* k_pool, void* v_pool, np_dtype dtype,
                        const void* v_new, const int64_t* slot_mapping,
                        int32_t num_tokens, int32_t* err_word,
                        np_stream_t stream);
+
+/*
+ * np_rope_append -- np_kv_append with what a model does to q and k first:
+ * the new tokens' q and k heads are (optionally) RMS-normalised, rotated by
+ * their positions, and q goes to q_out while k and v go to the tokens' pool
+ * slots, in one pass.  For prompts, chunks and decode batches alike.
+ *   q_out          [num_tokens, q_heads, head_dim] dtype (written, dense)
+ *   q              [num_tokens, q_heads, head_dim] dtype; heads dense, tokens
+ *                  q_stride elements apart (a view of a fused projection's
+ *                  rows, or q_heads * head_dim when dense)
+ *   k_new, v_new   [num_tokens, kv_heads, head_dim] dtype, k_stride and
+ *                  v_stride elements between tokens
+ *   slot_mapping   [num_tokens] int64, as in np_kv_append: a negative slot
+ *                  writes no k and v (q_out is written for every token); a
+ *                  slot past the pool is skipped and flagged (NP_FLAG_SLOT).
+ *                  Two tokens with the same slot leave a mixture of theirs.
+ *   cos_sin        [max_positions, rot_dim] fp32: row p holds the cosines of
+ *                  the rot_dim/2 pairs' angles at position p, then their
+ *                  sines.  Any base or frequency scaling is in this table.
+ *   rot_dim        leading dims that rotate: a multiple of 16, <= head_dim;
+ *                  the rest pass through
+ *   positions      [num_axes, num_tokens] int32; a position outside the table
+ *                  is clamped into it and flagged (NP_FLAG_POSITION)
+ *   num_axes       1 to 4 position axes (1: text; 3: time, height, width)
+ *   sections       HOST array [num_axes]: how many of the rot_dim/2 pairs turn
+ *                  by each axis, in order; sums to rot_dim/2.  NULL with one
+ *                  axis.
+ *   interleaved    0: pair j is dims (j, j + rot_dim/2); 1: (2j, 2j + 1)
+ *   q_weight, k_weight  [head_dim] dtype or NULL: x is replaced by
+ *                  x * weight / sqrt(mean(x^2) + eps) over the whole head
+ *                  before it rotates; NULL leaves that side as it is
+ *   eps            >= 0, finite (unused without a weight)
+ * Arithmetic is fp32; each result is rounded to dtype once.  v is copied bit
+ * for bit.  q_heads == 0 with q, q_out and q_weight NULL: k and v only.
+ * q_out may be q itself where q is dense; else what is written (q_out, the
+ * pools) must not overlap what is read: NP_ERR_INVALID_ARG.  Pointers 16-byte
+ * aligned; strides a multiple of 16 bytes, at least a token's heads.  Any
+ * kv_heads and q_heads up to 4096 (q_heads need not be a multiple here);
+ * head_dim as in the list above.  num_tokens == 0 is a no-op.
+ */
+np_status np_rope_append(void* q_out, const void* q, const void* k_new,
+                         const void* v_new, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, const int64_t* slot_mapping,
+                         void* k_pool, void* v_pool, np_dtype dtype,
+                         int64_t num_blocks, int32_t block_size,
+                         int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                         const float* cos_sin, int32_t max_positions,
+                         int32_t rot_dim, const int32_t* positions,
+                         int32_t num_axes, const int32_t* sections,
+                         int32_t interleaved, const void* q_weight,
+                         const void* k_weight, float eps, int32_t num_tokens,
+                         int32_t* err_word, np_stream_t stream);
+
+/*
+ * np_paged_prefill -- attention of chunks of new tokens over the paged cache
+ * (prompts, chunks of prompts, and rows with a single token among them).
+ * Row r's chunk is tokens query_starts[r] .. query_starts[r + 1] - 1 of q; they are
+ * the row's newest n positions c - n .. c - 1 (c = context_lens[r], counting
+ * them), their K and V already in the pools (np_rope_append, np_kv_append).
+ * Chunk token i attends causally to positions 0 .. c - n + i.
+ *   out, q         [num_tokens, q_heads, head_dim] dtype.  Tokens that no
+ *                  row's chunk holds are left as they were in out.
+ *   query_starts   [rows + 1] int32, ascending within [0, num_tokens] (clamped
+ *                  and flagged NP_FLAG_QUERY otherwise; tokens then claimed by
+ *                  two rows get either row's result)
+ *   block_tables, context_lens, pools, err_word: as np_paged_decode.  A chunk
+ *                  token whose row has fewer positions than its chunk has
+ *                  tokens, so that it sees nothing, gets zeros.
+ *   scale          finite, any sign
+ *   workspace      >= np_paged_prefill_workspace_bytes(head_dim) bytes,
+ *                  256-byte aligned, not shared by calls that may overlap;
+ *                  contents need no initialisation and mean nothing after
+ * K and V of the row's c positions must be finite.  Slots past a row's
+ * context, in its last block too, are never part of a result, whatever they
+ * hold.  Supported: the dtypes, head_dims and groups of the list above; up
+ * to 4096 rows; any block_size; tables of up to 2^31 - 257 tokens.
+ * out must not overlap q or the pools.  rows or num_tokens 0: a no-op.
+ * Three launches (plan, attention, join) on `stream`; results are
+ * deterministic.
+ */
+size_t np_paged_prefill_workspace_bytes(int32_t head_dim);
+/* enough for every head_dim */
+#define NP_PREFILL_WORKSPACE_BYTES (64u << 20)
+
+np_status np_paged_prefill(void* out, const void* q, const void* k_pool,
+                           const void* v_pool, np_dtype dtype,
+                           int64_t num_blocks, int32_t block_size,
+                           int32_t kv_heads, int32_t head_dim,
+                           const int32_t* block_tables,
+                           int32_t max_blocks_per_row,
+                           const int32_t* context_lens,
+                           const int32_t* query_starts, int32_t rows,
+                           int32_t num_tokens, int32_t q_heads, float scale,
+                           void* workspace, size_t workspace_bytes,
+                           int32_t* err_word, np_stream_t stream);
 
 /*
  * np_paged_decode_plan -- the schedule the library recommends, as a

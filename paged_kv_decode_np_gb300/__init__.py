@@ -40,11 +40,13 @@ __all__ = [
     "np_paged_decode_plan", "np_paged_decode_split_len",
     "np_paged_decode_workspace_bytes", "np_paged_decode", "np_paged_decode_reduce",
     "np_paged_decode_noalloc", "NP_NOALLOC_SCRATCH_BYTES", "np_paged_append_decode",
-    "np_selftest_bounded_wait",
-    "workspace", "decode_step", "PreparedStep", "NP_OK", "NP_ERR_INVALID_ARG",
+    "np_selftest_bounded_wait", "np_rope_append", "np_paged_prefill",
+    "np_paged_prefill_workspace_bytes", "rope_table", "prefill_workspace", "prefill_step",
+    "NP_PREFILL_WORKSPACE_BYTES", "workspace", "decode_step", "PreparedStep", "NP_OK", "NP_ERR_INVALID_ARG",
     "NP_ERR_UNSUPPORTED",
     "NP_ERR_WORKSPACE", "NP_ERR_OUT_OF_RANGE", "NP_ERR_CUDA", "NP_F32", "NP_BF16",
     "NP_FLAG_BLOCK_ID", "NP_FLAG_CONTEXT", "NP_FLAG_SLOT", "NP_FLAG_TIMEOUT", "NP_FLAG_CONFIG",
+    "NP_FLAG_POSITION", "NP_FLAG_QUERY",
 ]
 
 NP_OK = 0
@@ -62,8 +64,11 @@ NP_FLAG_CONTEXT = 0x2
 NP_FLAG_SLOT = 0x4
 NP_FLAG_TIMEOUT = 0x8
 NP_FLAG_CONFIG = 0x10
+NP_FLAG_POSITION = 0x20
+NP_FLAG_QUERY = 0x40
 
 NP_NOALLOC_SCRATCH_BYTES = 32 << 20
+NP_PREFILL_WORKSPACE_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libnp_paged.so")
@@ -122,9 +127,25 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                            _I32, _I32, _P]
     lib.np_selftest_bounded_wait.restype = ctypes.c_int
     lib.np_selftest_bounded_wait.argtypes = [_P, _I64, _P]
+    if hasattr(lib, "np_rope_append"):  # a library of ABI version 2 has no prompt side
+        _declare_prompt(lib)
     if path is None:
         _LIB = lib
     return lib
+
+
+def _declare_prompt(lib: ctypes.CDLL) -> None:
+    lib.np_rope_append.restype = ctypes.c_int
+    lib.np_rope_append.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_int, _I64,
+                                   _I32, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32,
+                                   ctypes.POINTER(_I32), _I32, _P, _P, ctypes.c_float, _I32, _P,
+                                   _P]
+    lib.np_paged_prefill_workspace_bytes.restype = ctypes.c_size_t
+    lib.np_paged_prefill_workspace_bytes.argtypes = [_I32]
+    lib.np_paged_prefill.restype = ctypes.c_int
+    lib.np_paged_prefill.argtypes = [_P, _P, _P, _P, ctypes.c_int, _I64, _I32, _I32, _I32, _P, _I32,
+                                     _P, _P, _I32, _I32, _I32, ctypes.c_float, _P, ctypes.c_size_t,
+                                     _P, _P]
 
 
 def _check(status: int, call: str) -> None:
@@ -223,6 +244,166 @@ def np_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, err_word=None, stre
         _dev(slot_mapping, "slot_mapping", cur), k_new.shape[0], _opt(err_word, "err_word", cur),
         _stream(stream))
     _check(st, "np_kv_append")
+
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, inv_freq=None,
+               device="cuda") -> torch.Tensor:
+    """np_rope_append's table: fp32 [max_positions, rot_dim], row p the cosines
+    of the rot_dim/2 pairs' angles p * inv_freq[j] and then their sines, formed
+    in 64 bits (a far position's angle has lost its fraction in 32).
+    ``inv_freq`` (rot_dim/2 values) replaces base ** (-2 j / rot_dim)."""
+    half = rot_dim // 2
+    if inv_freq is None:
+        f = float(base) ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    else:
+        f = torch.as_tensor(inv_freq, device=device).to(torch.float64)
+        if f.shape != (half,):
+            raise ValueError("rope_table: inv_freq must have rot_dim/2 values")
+    ang = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+def _token_rows(t: torch.Tensor, name: str, cur: int, heads: int, d: int):
+    """(address, elements between tokens) of a [T, heads, d] tensor whose heads
+    are dense; its tokens may lie further apart (a view of wider rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (no CPU path exists)")
+    if t.device.index != cur:
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}; "
+                         "call inside torch.cuda.device(...) of the tensors' GPU")
+    if t.numel() > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: heads and dims must be dense (only tokens may be strided)")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * d)
+
+
+def np_rope_append(q_out, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin, positions,
+                   sections=None, interleaved: bool = False, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, err_word=None, stream=None):
+    """Normalise (where a weight is given) and rotate the new tokens' q and k;
+    q goes to ``q_out`` (which may be ``q``), k and v to their pool slots (see
+    np_paged.h).
+
+    q [T, q_heads, head_dim], k_new/v_new [T, kv_heads, head_dim]: views whose
+    tokens are strided (slices of a fused projection's rows) are taken as they
+    are.  slot_mapping int64 [T]; cos_sin fp32 [max_positions, rot_dim] (see
+    rope_table); positions int32 [T], or [axes, T] with ``sections`` pairs per
+    axis.  q and q_out None: k and v only.
+    """
+    name = "np_rope_append"
+    nb, bs, hk, d = k_pool.shape
+    if k_new.dim() != 3 or v_pool.shape != k_pool.shape or k_new.shape != v_new.shape or \
+            tuple(k_new.shape[1:]) != (hk, d):
+        raise ValueError(f"{name}: k_new/v_new must be [tokens, kv_heads, head_dim] of the pools")
+    n = k_new.shape[0]
+    if any(t.dtype != k_pool.dtype for t in (v_pool, k_new, v_new)):
+        raise ValueError(f"{name}: k_new, v_new and the pools must share a dtype")
+    hq = 0
+    if (q is None) != (q_out is None) or (q is None and q_weight is not None):
+        raise ValueError(f"{name}: q and q_out go together")
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.dtype != k_pool.dtype:
+            raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim] of the pools' dtype")
+        if q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError(f"{name}: q_out must match q")
+        hq = q.shape[1]
+        if hq == 0:
+            raise ValueError(f"{name}: q has no heads; pass q and q_out as None")
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != k_pool.dtype or tuple(w.shape) != (d,)):
+            raise ValueError(f"{name}: {what} must be [head_dim] of the pools' dtype")
+    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (n,):
+        raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError(f"{name}: cos_sin must be float32 [max_positions, rot_dim]")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or \
+            positions.shape[-1] != n:
+        raise ValueError(f"{name}: positions must be int32 [tokens] or [axes, tokens]")
+    if sections is not None and len(sections) != axes:
+        raise ValueError(f"{name}: one section per position axis")
+    sec = None if sections is None else (_I32 * axes)(*[int(x) for x in sections])
+    cur = _current_device()
+    qp, qs = (None, 0) if q is None else _token_rows(q, "q", cur, hq, d)
+    kp, ks = _token_rows(k_new, "k_new", cur, hk, d)
+    vp, vs = _token_rows(v_new, "v_new", cur, hk, d)
+    st = load().np_rope_append(
+        _opt(q_out, "q_out", cur), qp, kp, vp, qs, ks, vs, _dev(slot_mapping, "slot_mapping", cur),
+        _dev(k_pool, "k_pool", cur), _dev(v_pool, "v_pool", cur), _dtype_code(k_pool.dtype), nb, bs,
+        hq, hk, d, _dev(cos_sin, "cos_sin", cur), cos_sin.shape[0], cos_sin.shape[1],
+        _dev(positions, "positions", cur), axes, sec, int(bool(interleaved)),
+        _opt(q_weight, "q_weight", cur), _opt(k_weight, "k_weight", cur), float(eps), n,
+        _opt(err_word, "err_word", cur), _stream(stream))
+    _check(st, name)
+
+
+def np_paged_prefill_workspace_bytes(head_dim) -> int:
+    return load().np_paged_prefill_workspace_bytes(head_dim)
+
+
+def prefill_workspace(head_dim, device="cuda") -> torch.Tensor:
+    """A workspace for np_paged_prefill (its contents need no initialisation)."""
+    n = np_paged_prefill_workspace_bytes(head_dim)
+    if n == 0:
+        raise ValueError(f"unsupported head_dim {head_dim}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def np_paged_prefill(out, q, k_pool, v_pool, block_tables, context_lens, query_starts, scale,
+                     workspace, err_word=None, stream=None):
+    """Attention of ragged chunks of new tokens over the paged cache (see
+    np_paged.h).  q/out [tokens, q_heads, head_dim]; query_starts int32
+    [rows + 1]; row r's chunk q[query_starts[r]:query_starts[r + 1]] holds its
+    newest positions, already appended to the pools."""
+    name = "np_paged_prefill"
+    if q.dim() != 3 or k_pool.dim() != 4:
+        raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim]")
+    nb, bs, hk, d = k_pool.shape
+    if q.shape[2] != d or v_pool.shape != k_pool.shape or q.dtype != k_pool.dtype or \
+            v_pool.dtype != k_pool.dtype:
+        raise ValueError(f"{name}: q/pool shape or dtype mismatch")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"{name}: out must match q")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
+    rows = block_tables.shape[0]
+    if context_lens.dtype != torch.int32 or tuple(context_lens.shape) != (rows,):
+        raise ValueError(f"{name}: context_lens must be int32 [rows]")
+    if query_starts.dtype != torch.int32 or tuple(query_starts.shape) != (rows + 1,):
+        raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
+    cur = _current_device()
+    st = load().np_paged_prefill(
+        _dev(out, "out", cur), _dev(q, "q", cur), _dev(k_pool, "k_pool", cur),
+        _dev(v_pool, "v_pool", cur), _dtype_code(q.dtype), nb, bs, hk, d,
+        _dev(block_tables, "block_tables", cur), block_tables.shape[1],
+        _dev(context_lens, "context_lens", cur), _dev(query_starts, "query_starts", cur), rows,
+        q.shape[0], q.shape[1], float(scale), _opt(workspace, "workspace", cur),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _opt(err_word, "err_word", cur), _stream(stream))
+    _check(st, name)
+
+
+def prefill_step(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, block_tables, context_lens,
+                 query_starts, scale, workspace, *, cos_sin=None, positions=None, sections=None,
+                 interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 q_rotated=None, err_word=None, stream=None):
+    """One layer's prompt step: the new tokens' k and v into the pools, then
+    their attention.  With ``cos_sin`` and ``positions`` np_rope_append rotates
+    (and, with weights, normalises) q and k on the way: the rotated q goes to
+    ``q_rotated`` (default: back into q, which must then be dense).  Without
+    them np_kv_append copies k_new and v_new as they are."""
+    if cos_sin is not None:
+        qr = q if q_rotated is None else q_rotated
+        np_rope_append(qr, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin, positions,
+                       sections, interleaved, q_weight, k_weight, eps, err_word, stream)
+    else:
+        if any(x is not None for x in (positions, sections, q_weight, k_weight, q_rotated)):
+            raise ValueError("prefill_step: positions, sections, weights and q_rotated need cos_sin")
+        qr = q
+        np_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, err_word, stream)
+    np_paged_prefill(out, qr, k_pool, v_pool, block_tables, context_lens, query_starts, scale,
+                     workspace, err_word, stream)
 
 
 def np_paged_decode_plan(rows, q_heads, kv_heads, head_dim, block_size, max_blocks_per_row,

@@ -37,6 +37,10 @@ def _units(extra: list[str], build_dir: str, csrc: str) -> list[tuple[str, str, 
         (os.path.join(csrc, "api.cu"), os.path.join(objdir, "api.o"), []),
         (os.path.join(csrc, "append_reduce.cu"), os.path.join(objdir, "append_reduce.o"), []),
         (os.path.join(csrc, "noalloc.cu"), os.path.join(objdir, "noalloc.o"), []),
+        (os.path.join(csrc, "rope_append.cu"), os.path.join(objdir, "rope_append.o"), []),
+        (os.path.join(csrc, "prefill_api.cu"), os.path.join(objdir, "prefill_api.o"), []),
+        (os.path.join(csrc, "prefill_plan.cu"), os.path.join(objdir, "prefill_plan.o"), []),
+        (os.path.join(csrc, "prefill_simt.cu"), os.path.join(objdir, "prefill_simt.o"), []),
     ]
     for bf16 in (0, 1):
         for d in HEAD_DIMS:

@@ -1,0 +1,129 @@
+// prefill_api.cu -- np_paged_prefill: argument validation, the workspace's
+// layout and the launches.
+#include <limits.h>
+
+#include <atomic>
+
+#include "prefill.cuh"
+
+namespace {
+
+using npk::PrefillParams;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && n > 0 && m > 0 && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
+}
+
+// Plan and cut list, then the partials of kPrefillMaxCtas blocks.
+constexpr size_t kPlanBytes = 3 * npk::kPrefillMaxCtas * sizeof(int4);
+
+// rows of the largest unit any kernel of this head_dim takes
+int unit_rows(int32_t head_dim) { return head_dim == 256 ? 128 : 256; }
+
+std::atomic<int> g_sms[64];
+
+int sm_count() {
+  int dev = 0, s = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64) s = g_sms[dev].load();
+  if (s == 0) {
+    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) g_sms[dev].store(s);
+  }
+  return s;
+}
+
+}  // namespace
+
+extern "C" size_t np_paged_prefill_workspace_bytes(int32_t head_dim) {
+  if (head_dim != 16 && head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return 0;
+  return round_up(kPlanBytes, 256) +
+         2 * npk::kPrefillMaxCtas * npk::prefill_part_floats(unit_rows(head_dim), head_dim) * 4;
+}
+
+extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_pool,
+                                      const void* v_pool, np_dtype dtype, int64_t num_blocks,
+                                      int32_t block_size, int32_t kv_heads, int32_t head_dim,
+                                      const int32_t* block_tables, int32_t max_blocks_per_row,
+                                      const int32_t* context_lens, const int32_t* query_starts,
+                                      int32_t rows, int32_t num_tokens, int32_t q_heads,
+                                      float scale, void* workspace, size_t workspace_bytes,
+                                      int32_t* err_word, np_stream_t stream) {
+  const int es = dtype == NP_F32 ? 4 : (dtype == NP_BF16 ? 2 : 0);
+  if (es == 0) return NP_ERR_UNSUPPORTED;
+  if (rows < 0 || num_tokens < 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 ||
+      num_blocks <= 0 || block_size <= 0 || max_blocks_per_row <= 0 || head_dim <= 0 ||
+      !isfinite(scale))
+    return NP_ERR_INVALID_ARG;
+  if (head_dim != 16 && head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return NP_ERR_UNSUPPORTED;
+  const int group = q_heads / kv_heads;
+  if (group > (dtype == NP_BF16 ? 16 : 8)) return NP_ERR_UNSUPPORTED;
+  int64_t slots = 0, pool = 0, cap = 0, qn = 0, tab = 0;
+  if (!mul_ok(num_blocks, block_size, &slots) ||
+      !mul_ok(slots, (int64_t)kv_heads * head_dim * es, &pool) ||
+      !mul_ok(num_tokens, (int64_t)q_heads * head_dim * es, &qn) ||
+      !mul_ok(max_blocks_per_row, block_size, &cap) || !mul_ok(rows, max_blocks_per_row, &tab))
+    return NP_ERR_OUT_OF_RANGE;
+  // positions are int32 with a kv tile to spare
+  if (cap > INT32_MAX - 256 || num_tokens > INT32_MAX - 512) return NP_ERR_UNSUPPORTED;
+  if (rows > npk::kPrefillMaxRows) return NP_ERR_UNSUPPORTED;
+  if (rows == 0 || num_tokens == 0) return NP_OK;
+  if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens || !query_starts)
+    return NP_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_starts, 4) ||
+      (err_word && !aligned(err_word, 4)))
+    return NP_ERR_INVALID_ARG;
+  if (overlap(out, qn, q, qn) || overlap(out, qn, k_pool, pool) || overlap(out, qn, v_pool, pool))
+    return NP_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < np_paged_prefill_workspace_bytes(head_dim) ||
+      !aligned(workspace, 256))
+    return NP_ERR_WORKSPACE;
+  const int sms = sm_count();
+  if (sms <= 0) return NP_ERR_CUDA;
+
+  PrefillParams p{};
+  p.out = out;
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_starts = query_starts;
+  p.err = err_word;
+  p.plan = static_cast<int4*>(workspace);
+  p.cuts = p.plan + 2 * npk::kPrefillMaxCtas;
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(kPlanBytes, 256));
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.kv_heads = kv_heads;
+  p.q_heads = q_heads;
+  p.group = group;
+  p.max_blocks_per_row = max_blocks_per_row;
+  p.rows = rows;
+  p.tokens = num_tokens;
+  p.ctas = sms < npk::kPrefillMaxCtas ? sms : npk::kPrefillMaxCtas;
+  p.head_dim = head_dim;
+  p.qscale = fabsf(scale) * 1.4426950408889634f;  // log2(e)
+  p.negate = scale < 0.f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+
+  p.tiles = 1;
+  p.tile_rows = 64;
+  p.bn = 64;
+  p.tile_tokens = p.tile_rows / group;
+  p.min_tiles = 2;
+  np_status rc = npk::launch_prefill_plan(p, st);
+  if (rc == NP_OK) rc = npk::launch_prefill_simt(p, dtype, st);
+  if (rc == NP_OK) rc = npk::launch_prefill_join(p, dtype, st);
+  return rc;
+}

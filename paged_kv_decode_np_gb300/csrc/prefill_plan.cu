@@ -1,0 +1,251 @@
+// prefill_plan.cu -- the shares of np_paged_prefill's thread blocks, and the
+// join of the units that a share's end cuts.
+#include "prefill.cuh"
+
+namespace npk {
+
+// sum over i < n of floor((a i + b) / m), for a, b >= 0, m > 0: the lattice
+// points under a line, counted by Euclid's reduction of (a, m).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// kv tiles of a row's first k units (of one kv head), k <= units
+__device__ int64_t prefill_row_prefix(const PrefillParams& p, const PrefillRow& g, int units, int k) {
+  if (k <= 0) return 0;
+  const int64_t U = (int64_t)p.tile_tokens * p.tiles;
+  int64_t last = 0;
+  if (k == units) {  // the last unit ends with the chunk, not U tokens on
+    last = prefill_kv_tiles(p, g, g.n);
+    --k;
+  }
+  const int64_t base = (int64_t)g.c - g.n;
+  const int64_t z0 = base < 0 ? -base / U : 0;  // units that see nothing: one tile each
+  const int z = z0 < k ? (int)z0 : k;
+  return z + floor_sum(k - z, p.bn, U, base + (z + 1) * U + p.bn - 1) + last;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// One block.  Scans the rows' kv tile counts, cuts the stream of W tiles into
+// equal shares and writes each block's first (row, kv head, unit, kv tile)
+// and length, and which units the shares' ends cut.
+__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid_constant__
+                                                                    PrefillParams p) {
+  __shared__ int64_t pre[kPrefillMaxRows + 1];  // tiles before each row
+  __shared__ int64_t warp_sum[32];
+  __shared__ int64_t at[kPrefillMaxCtas + 1];   // the shares' ends
+  __shared__ int64_t unit_end[kPrefillMaxCtas + 1];  // of the unit that `at` lies in
+  __shared__ int4 pos[kPrefillMaxCtas + 1];
+  constexpr unsigned FULL = 0xffffffffu;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PER = kPrefillMaxRows / kPlanThreads;
+  const int per = (p.rows + kPlanThreads - 1) / kPlanThreads;  // <= PER rows a thread
+  int64_t w[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int r = tid * per + i;
+    w[i] = 0;
+    if (i < per && r < p.rows) {
+      const PrefillRow g = prefill_row(p, r, true);
+      const int units = prefill_units(p, g.n);
+      w[i] = prefill_row_prefix(p, g, units, units) * p.kv_heads;
+    }
+    sum += w[i];
+  }
+  int64_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(FULL, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t y = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(FULL, y, o);
+      if (lane >= o) y += u;
+    }
+    warp_sum[lane] = y;
+  }
+  __syncthreads();
+  int64_t run = x - sum + (warp > 0 ? warp_sum[warp - 1] : 0);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int r = tid * per + i;
+    if (i < per && r < p.rows) pre[r] = run;
+    run += w[i];
+  }
+  if (tid == 0) pre[p.rows] = warp_sum[31];
+  __syncthreads();
+  const int64_t W = pre[p.rows];
+  // blocks that share the work: a share holds min_tiles at least
+  const int64_t want = (W + p.min_tiles - 1) / p.min_tiles;
+  const int Pe = (int)(want < 1 ? 1 : (want < p.ctas ? want : p.ctas));
+  if (tid <= p.ctas) {
+    const int64_t share = W / Pe;
+    int64_t t = tid >= Pe ? W : share * tid + (W % Pe) * tid / Pe;
+    int4 q = make_int4(p.rows, 0, 0, 0);
+    int64_t end = W;
+    if (t < W) {
+      int lo = 0, hi = p.rows;  // the last row with pre[row] <= t: it has tiles there
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      const PrefillRow g = prefill_row(p, lo);
+      const int units = prefill_units(p, g.n);
+      const int64_t wh = (pre[lo + 1] - pre[lo]) / p.kv_heads;
+      const int64_t rem = t - pre[lo];
+      const int kvh = (int)(rem / wh);
+      const int64_t in = rem - kvh * wh;
+      int a = 0, b = units;  // the last unit with prefix <= in
+      while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (prefill_row_prefix(p, g, units, mid) <= in) a = mid;
+        else b = mid;
+      }
+      const int64_t s0 = prefill_row_prefix(p, g, units, a);
+      const int64_t s1 = prefill_row_prefix(p, g, units, a + 1);
+      const int64_t ustart = t - (in - s0);
+      end = ustart + (s1 - s0);
+      int off = (int)(in - s0);
+      // an end that lies near a unit's own start is moved there: the partials
+      // it saves cost more than the imbalance
+      if (off > 0 && off * 16 <= share) {
+        t = ustart;
+        off = 0;
+      } else if (off > 0 && (end - t) * 16 <= share) {
+        t = end;
+        off = 0;
+        // the unit after: (a + 1) of this head, the next head, or the next row with units
+        int r2 = lo, k2 = kvh, a2 = a + 1;
+        if (a2 >= units) {
+          a2 = 0;
+          if (++k2 >= p.kv_heads) {
+            k2 = 0;
+            ++r2;
+          }
+        }
+        q = make_int4(r2, k2, a2, 0);
+        end = t;  // not cut
+      }
+      if (q.x == p.rows && t < W) q = make_int4(lo, kvh, a, off);
+    }
+    at[tid] = t;
+    unit_end[tid] = end;
+    pos[tid] = q;
+  }
+  __syncthreads();
+  if (tid < p.ctas) {
+    const int64_t len = at[tid + 1] - at[tid];
+    p.plan[tid] = pos[tid];
+    p.plan[p.ctas + tid] = make_int4((int)(len & 0xffffffff), (int)(len >> 32), 0, 0);
+    // the unit that this share's end cuts, if the share began it
+    int4 cut = make_int4(-1, 0, 0, 0);
+    const int4 e = pos[tid + 1];
+    if (len > 0 && at[tid + 1] < W && e.w > 0 && at[tid + 1] - e.w >= at[tid]) {
+      int last = tid + 1;
+      while (last + 1 < p.ctas && at[last + 1] < unit_end[tid + 1]) ++last;
+      cut = make_int4(e.x, e.y, e.z, last);
+    }
+    p.cuts[tid] = cut;
+  }
+}
+
+np_status launch_prefill_plan(const PrefillParams& p, cudaStream_t s) {
+  prefill_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? NP_OK : NP_ERR_CUDA;
+}
+
+// The join: block (b, y) merges rows [32 y, 32 y + 32) of the unit that block
+// b's share began and its end cuts.  Piece b lies in b's slot 1, the pieces
+// of blocks b + 1 .. last in their slot 0.  A thread holds one row's 4 dims at
+// a time; consecutive lanes hold consecutive rows, so partial loads are
+// coalesced; the result goes through shared memory so that the stores are
+// too.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__
+                                                                    PrefillParams p) {
+  __shared__ float tile[32][D + 4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention is complete
+  const int b = blockIdx.x;
+  const int4 cut = p.cuts[b];
+  if (cut.x < 0) return;
+  const int bm = p.tile_rows * p.tiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.y * 32 + lane;  // < bm
+  const size_t pf = prefill_part_floats(bm, D);
+  const float* first = p.parts + (size_t)(2 * b + 1) * pf;
+  auto part = [&](int i) { return i == b ? first : p.parts + (size_t)(2 * i) * pf; };
+  float M = -INFINITY;
+  for (int i = b; i <= cut.w; ++i) M = fmaxf(M, part(i)[row]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int i = b; i <= cut.w; ++i) L = fmaf(ex2(part(i)[row] - ref), part(i)[bm + row], L);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  for (int g = warp; g < D / 4; g += kJoinThreads / 32) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = b; i <= cut.w; ++i) {
+      const float* q = part(i);
+      const float w = ex2(q[row] - ref);
+      const float4 o = *reinterpret_cast<const float4*>(q + 2 * bm + ((size_t)g * bm + row) * 4);
+      acc.x = fmaf(w, o.x, acc.x);
+      acc.y = fmaf(w, o.y, acc.y);
+      acc.z = fmaf(w, o.z, acc.z);
+      acc.w = fmaf(w, o.w, acc.w);
+    }
+    *reinterpret_cast<float4*>(&tile[lane][4 * g]) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
+  __syncthreads();
+  const PrefillRow gr = prefill_row(p, cut.x);
+  for (int e = threadIdx.x; e < 32 * (D / 4); e += kJoinThreads) {
+    const int rr = e / (D / 4), d = (e % (D / 4)) * 4;
+    const int urow = blockIdx.y * 32 + rr;           // row of the unit
+    const int mt = urow / p.tile_rows, in = urow % p.tile_rows;
+    const int tt = in / p.group, h = in % p.group;
+    const int64_t tok = ((int64_t)cut.z * p.tiles + mt) * p.tile_tokens + tt;
+    if (tt >= p.tile_tokens || tok >= gr.n) continue;
+    T* o = static_cast<T*>(p.out) + ((gr.q0 + tok) * p.q_heads + (int64_t)cut.y * p.group + h) * D;
+    Storage<T>::template store<4>(o + d, &tile[rr][d]);
+  }
+}
+
+template <typename T>
+static np_status launch_join_t(const PrefillParams& p, cudaStream_t s) {
+  const unsigned gy = (unsigned)(p.tile_rows * p.tiles / 32);
+  switch (p.head_dim) {
+    case 16: return launch_dependent(prefill_join_kernel<T, 16>, p.ctas, gy, kJoinThreads, 0, s, p);
+    case 32: return launch_dependent(prefill_join_kernel<T, 32>, p.ctas, gy, kJoinThreads, 0, s, p);
+    case 64: return launch_dependent(prefill_join_kernel<T, 64>, p.ctas, gy, kJoinThreads, 0, s, p);
+    case 128: return launch_dependent(prefill_join_kernel<T, 128>, p.ctas, gy, kJoinThreads, 0, s, p);
+    case 256: return launch_dependent(prefill_join_kernel<T, 256>, p.ctas, gy, kJoinThreads, 0, s, p);
+  }
+  return NP_ERR_UNSUPPORTED;
+}
+
+np_status launch_prefill_join(const PrefillParams& p, np_dtype dtype, cudaStream_t s) {
+  return dtype == NP_BF16 ? launch_join_t<__nv_bfloat16>(p, s) : launch_join_t<float>(p, s);
+}
+
+}  // namespace npk
