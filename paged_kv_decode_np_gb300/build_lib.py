@@ -47,6 +47,9 @@ def _units(extra: list[str], build_dir: str, csrc: str) -> list[tuple[str, str, 
             name = f"decode_{'bf16' if bf16 else 'f32'}_d{d}.o"
             units.append((os.path.join(csrc, "decode_inst.cu"), os.path.join(objdir, name),
                           [f"-DNPK_BF16={bf16}", f"-DNPK_D={d}"]))
+    for d in HEAD_DIMS:
+        units.append((os.path.join(csrc, "prefill_tc.cu"),
+                      os.path.join(objdir, f"prefill_tc_d{d}.o"), [f"-DNPK_D={d}"]))
     return [(s, o, ["-I", csrc] + f + extra) for s, o, f in units]
 
 

@@ -163,6 +163,13 @@ np_status launch_prefill_join(const PrefillParams& p, np_dtype dtype, cudaStream
 // prefill_simt.cu
 np_status launch_prefill_simt(const PrefillParams& p, np_dtype dtype, cudaStream_t s);
 
+// prefill_tc.cu, per head_dim
+np_status prefill_tc_d16(const PrefillParams& p, bool tiled, cudaStream_t s);
+np_status prefill_tc_d32(const PrefillParams& p, bool tiled, cudaStream_t s);
+np_status prefill_tc_d64(const PrefillParams& p, bool tiled, cudaStream_t s);
+np_status prefill_tc_d128(const PrefillParams& p, bool tiled, cudaStream_t s);
+np_status prefill_tc_d256(const PrefillParams& p, bool tiled, cudaStream_t s);
+
 // Launches `kern` so that it may become resident while the launch before it
 // still runs; its griddepcontrol.wait holds it until that one is complete.
 template <typename K, typename... A>

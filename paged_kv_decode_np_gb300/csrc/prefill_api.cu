@@ -3,6 +3,9 @@
 #include <limits.h>
 
 #include <atomic>
+#include <mutex>
+
+#include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled_v12000
 
 #include "prefill.cuh"
 
@@ -38,6 +41,74 @@ int sm_count() {
     if (dev < 64) g_sms[dev].store(s);
   }
   return s;
+}
+
+// The driver's tensor map encoder, through the runtime (no libcuda link).
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A bf16 tensor (dims innermost first, byte strides of dims 1 and 2), copied in
+// boxes of 64 x box1 x box2 in the 128-byte swizzle.
+bool encode_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3],
+                const cuuint64_t (&strides)[2], cuuint32_t box1, cuuint32_t box2) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint32_t box[3] = {64u, box1, box2};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16: the tensor-core kernel of this head_dim
+np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
+  const int d = p.head_dim;
+  // a masked score is -inf before it is scaled: no 0 x inf
+  p.qscale = fmaxf(p.qscale, 1e-30f);
+  p.tiles = d == 256 ? 1 : 2;
+  p.tile_rows = 128;
+  p.bn = d == 256 ? 64 : 128;
+  p.tile_tokens = p.tile_rows / p.group;
+  p.min_tiles = 2;
+  // Tiled copies: boxes of whole 8-row swizzle atoms inside one block, slot
+  // coordinates in int32.  box_tokens: the largest power of two that divides
+  // the block size, at most a kv tile.
+  int bt = 1;
+  while (bt < p.bn && p.block_size % (2 * bt) == 0) bt *= 2;
+  p.box_tokens = bt;
+  bool tiled = d >= 64 && bt >= 8 && slots <= INT32_MAX;
+  if (tiled) {
+    const cuuint64_t row = (cuuint64_t)p.kv_heads * d * 2, qrow = (cuuint64_t)p.q_heads * d * 2;
+    const cuuint64_t kv_dims[3] = {(cuuint64_t)d, (cuuint64_t)slots, (cuuint64_t)p.kv_heads};
+    const cuuint64_t kv_strides[2] = {row, (cuuint64_t)d * 2};
+    const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)p.q_heads, (cuuint64_t)p.tokens};
+    const cuuint64_t q_strides[2] = {(cuuint64_t)d * 2, qrow};
+    tiled = encode_map(&p.tm_k, p.k_pool, kv_dims, kv_strides, (cuuint32_t)bt, 1u) &&
+            encode_map(&p.tm_v, p.v_pool, kv_dims, kv_strides, (cuuint32_t)bt, 1u) &&
+            encode_map(&p.tm_q, p.q, q_dims, q_strides, (cuuint32_t)p.group,
+                       (cuuint32_t)p.tile_tokens);
+  }
+  np_status rc = npk::launch_prefill_plan(p, s);
+  if (rc != NP_OK) return rc;
+  switch (d) {
+    case 16: return npk::prefill_tc_d16(p, tiled, s);
+    case 32: return npk::prefill_tc_d32(p, tiled, s);
+    case 64: return npk::prefill_tc_d64(p, tiled, s);
+    case 128: return npk::prefill_tc_d128(p, tiled, s);
+    case 256: return npk::prefill_tc_d256(p, tiled, s);
+  }
+  return NP_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -117,13 +188,18 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
   p.negate = scale < 0.f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
-  p.tiles = 1;
-  p.tile_rows = 64;
-  p.bn = 64;
-  p.tile_tokens = p.tile_rows / group;
-  p.min_tiles = 2;
-  np_status rc = npk::launch_prefill_plan(p, st);
-  if (rc == NP_OK) rc = npk::launch_prefill_simt(p, dtype, st);
+  np_status rc;
+  if (dtype == NP_BF16) {
+    rc = launch_tc(p, slots, st);
+  } else {
+    p.tiles = 1;
+    p.tile_rows = 64;
+    p.bn = 64;
+    p.tile_tokens = p.tile_rows / group;
+    p.min_tiles = 2;
+    rc = npk::launch_prefill_plan(p, st);
+    if (rc == NP_OK) rc = npk::launch_prefill_simt(p, dtype, st);
+  }
   if (rc == NP_OK) rc = npk::launch_prefill_join(p, dtype, st);
   return rc;
 }
