@@ -9,7 +9,7 @@
 //     P_w = 2^(c S_w - m)      fp32 -> bf16, into the tensor memory of S_w
 //     O_w += P_w V             tcgen05.mma, A = P_w from tensor memory
 // Roles: MT warpgroups of softmax (one thread a row: no shuffles), one warp
-// that issues the mma, one that loads.  With two q tiles (head_dim <= 128)
+// that issues the mma, one that loads q and K, one that loads V.  With two q tiles (head_dim <= 128)
 // the tensor cores work on one while the other's softmax runs:
 //     ... PV_0(j), S_0(j+1) | PV_1(j), S_1(j+1) ...
 // and the two share every K and V tile, 128 operations a byte of it in
@@ -51,7 +51,7 @@ struct TcCfg {
   static constexpr int RING = MT * QT;              // offset of the ring
   static constexpr int BARS = RING + NS * SLOT;     // offset of the barriers
   static constexpr int SMEM = 1024 + BARS + 512;    // + up to 1024 of alignment
-  static constexpr int THREADS = 128 * (MT + 1);    // whole warpgroups: setmaxnreg is theirs
+  static constexpr int THREADS = 32 * (4 * MT + 3);
   static constexpr int BM = 128 * MT;
   static constexpr uint32_t O0 = 256;               // tensor memory column of O_0
   static_assert(NS >= 4, "ring");
@@ -64,7 +64,7 @@ struct TcBars {
   static constexpr int q_full = 0, q_empty = 1, kv_full = 2, kv_empty = 2 + NS;
   static constexpr int s_full = 2 + 2 * NS, p_full = s_full + 2, o_full = p_full + 2;
   static constexpr int pv_done = o_full + 1;  // MT == 1: one phase a kv tile
-  static constexpr int drain = o_full + 2, count = drain + 1;
+  static constexpr int drain = o_full + 2, tail_full = drain + 1, count = tail_full + 1;
 };
 
 // kv tiles of the current segment that q tile t sees, from kv0 on
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tail + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int LOADER = 4 * MT, ISSUER = 4 * MT + 1;
+  constexpr int LOAD_K = 4 * MT, LOAD_V = 4 * MT + 1, ISSUER = 4 * MT + 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i)
@@ -124,11 +124,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   bool ok = true;
   PrefillWalk w;
 
-  // Registers: a softmax thread holds a row of S (BN values).  With 384 threads
-  // each has 168 at launch; 2 x 208 + 88 = 3 x 168.
+  w.start(p, blockIdx.x);
+
   if (warp < 4 * MT) {
-    if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    w.start(p, blockIdx.x);
     // ============================================================= softmax
     const int t = warp >> 2;                         // q tile
     const int row = (warp & 3) * 32 + lane;          // its row: tensor memory lane
@@ -156,25 +154,35 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         if (!ok) break;
         tmem_fence_after();
         const uint32_t s_at = lanes + buf * BN;
-        uint32_t r[BN];
-#pragma unroll
-        for (int c = 0; c < BN; c += 32) tmem_ld32(s_at + c, r + c);
-        tmem_wait_ld();
-        tmem_pin<BN>(r);
-        float* s = reinterpret_cast<float*>(r);
         const int rel = lim - (w.kv0 + j) * BN;  // last visible column
-        if (__any_sync(FULL, rel < BN - 1)) {
+        const bool masked = __any_sync(FULL, rel < BN - 1);
+        // The row's maximum, 32 columns at a time: S is read from tensor memory
+        // again for the exponentials, so a thread holds 2 x 32 values and not
+        // BN (three warps of a scheduler have 168 registers a thread).
+        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+        uint32_t r[2][32];
+        tmem_ld32(s_at, r[0]);
 #pragma unroll
-          for (int c = 0; c < BN; ++c) s[c] = c <= rel ? s[c] : -INFINITY;
-        }
-        float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+        for (int c = 0; c < BN; c += 32) {
+          tmem_wait_ld();
+          tmem_pin<32>(r[(c >> 5) & 1]);
+          if (c + 32 < BN) tmem_ld32(s_at + c + 32, r[((c >> 5) + 1) & 1]);
+          const uint32_t* s = r[(c >> 5) & 1];
+          if (masked) {
 #pragma unroll
-        for (int c = 4; c < BN; c += 4) {
-          x0 = fmaxf(x0, s[c]);
-          x1 = fmaxf(x1, s[c + 1]);
-          x2 = fmaxf(x2, s[c + 2]);
-          x3 = fmaxf(x3, s[c + 3]);
+            for (int e = 0; e < 32; ++e)
+              if (c + e <= rel) x0 = fmaxf(x0, __uint_as_float(s[e]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              x0 = fmaxf(x0, __uint_as_float(s[e]));
+              x1 = fmaxf(x1, __uint_as_float(s[e + 1]));
+              x2 = fmaxf(x2, __uint_as_float(s[e + 2]));
+              x3 = fmaxf(x3, __uint_as_float(s[e + 3]));
+            }
+          }
         }
+        tmem_ld32(s_at, r[0]);  // the second pass' first columns
         const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.qscale;
         const bool grow = mt > m + 8.f;  // also the first visible tile: m = -inf
         if (__any_sync(FULL, grow)) {
@@ -208,10 +216,19 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
         for (int c = 0; c < BN; c += 32) {
+          tmem_wait_ld();
+          tmem_pin<32>(r[(c >> 5) & 1]);
+          if (c + 32 < BN) tmem_ld32(s_at + c + 32, r[((c >> 5) + 1) & 1]);
+          uint32_t* s = r[(c >> 5) & 1];
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c + e > rel) s[e] = 0xff800000u;  // -inf
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float a = s[c + e], b = s[c + e + 1];
+            float a = __uint_as_float(s[e]), b = __uint_as_float(s[e + 1]);
             fma2(a, b, p.qscale, ref);
             a = ex2(a);
             b = ex2(b);
@@ -219,6 +236,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
             pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
           }
+          // columns c / 2 .. of S: read already
           tmem_st16(s_at + (c >> 1), pk);
         }
         l += l0 + l1;
@@ -278,314 +296,304 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       tmem_fence_before();  // O is read before the next unit's first P is reported
       w.advance();
     }
-  } else {
-   if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-   w.start(p, blockIdx.x);
-   if (warp == LOADER) {
+  } else if (warp == LOAD_K || warp == LOAD_V) {
     // =============================================================== loads
-    RingPos pos{0, 0};
-    int issued = 0;       // tiles issued so far (saturates: only 0..NS and "more" matter)
-    RingPos told{0, 0};   // token-by-token copies: the next tile to report
-    int untold = 0;
+    // One warp copies q and the K tiles, another the V tiles: a copy costs its
+    // issuing thread tens of cycles, and a tile is up to 32 of them.
+    const bool isv = warp == LOAD_V;
     const int G = p.group;
-    uint32_t seg = 0;
+    uint32_t seg = 0, seq0 = 0;  // segments; ring tiles before this segment
+    int64_t last = -1;  // the last tile's ring position (for the drain)
+    uint32_t tails = 0; // TILED: phases of tail_full
+    int pending = -1;   // token by token: the slot whose copies are in flight
 
-    // reports the oldest unreported tile: its copies are complete
-    auto tell = [&]() {
+    // the pool slot of the row's position t, its block id checked
+    auto pool_slot = [&](unsigned t) {
+      const unsigned j = t / (unsigned)p.block_size;
+      int64_t b = p.block_tables[(int64_t)w.r * p.max_blocks_per_row + j];
+      if (b < 0 || b >= p.num_blocks) {
+        set_flag(p.err, NP_FLAG_BLOCK_ID);
+        b = 0;
+      }
+      return b * p.block_size + (t - j * p.block_size);
+    };
+    // TILED: the pool slot of lane i's box of kv tile kt, read a tile ahead
+    auto look_up = [&](int kt) {
+      const int tok = kt * BN + lane * p.box_tokens;
+      return lane * p.box_tokens < BN && tok < w.g.c ? (int32_t)pool_slot((unsigned)tok) : 0;
+    };
+    // token by token: the pending tile's copies are complete, for the mma too
+    auto report = [&]() {
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B::kv_full + told.slot));
-      told.template step<NS>();
-      --untold;
+      if (lane == 0) mbar_arrive(bar(B::kv_full + pending));
     };
-    // copies K or V of kv tile kt into the ring's next slot
-    auto load_tile = [&](bool isv, int kt) {
-      if (issued >= NS) {
-        ok = __all_sync(FULL, mbar_wait(bar(B::kv_empty + pos.slot), pos.phase ^ 1u, abort));
+    // V rows past the context are zeroed, whatever their slots hold: 0 x NaN is
+    // NaN.  (K's only make scores that are masked.)
+    auto clear_tail = [&](uint32_t slot, int valid) {
+      const int from = max(valid, 0), rows = BN - from;
+      unsigned char* to = smem + C::RING + slot * C::SLOT;
+      for (int slab = 0; slab < SL; ++slab)
+        for (int e = lane; e < rows * 8; e += 32)
+          *reinterpret_cast<uint4*>(to + (slab * BN + from) * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    // copies kv tile kt of K or V to position `seq` of the ring; at: look_up(kt)
+    auto load_tile = [&](int kt, uint32_t seq, int32_t at) {
+      const uint32_t slot = seq % NS;
+      if (seq >= NS) {
+        ok = __all_sync(FULL, mbar_wait(bar(B::kv_empty + slot), (seq / NS - 1u) & 1u, abort));
         if (!ok) return;
-      } else {
-        ++issued;
       }
-      const int t0 = kt * BN;
-      const int valid = min(BN, w.g.c - t0);  // <= 0: a row without history
-      const uint32_t dst = ring + (uint32_t)pos.slot * C::SLOT;
-      const int32_t* table = p.block_tables + (int64_t)w.r * p.max_blocks_per_row;
+      const int valid = min(BN, w.g.c - kt * BN);  // <= 0: a row without history
+      const uint32_t dst = ring + slot * C::SLOT;
       if constexpr (TILED) {
-        const uint32_t fb = bar(B::kv_full + pos.slot);
+        // a context's last V tile lands on a barrier of this warp's, which
+        // clears its tail and then reports it
+        const bool tail = isv && valid < BN;
+        const uint32_t fb = bar(tail ? B::tail_full : B::kv_full + slot);
         const int bt = p.box_tokens;
         const int nbox = valid > 0 ? (valid + bt - 1) / bt : 0;
         if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(nbox * SL * bt) * 128u);
-        __syncwarp();
-        for (int i = lane; i < nbox * SL; i += 32) {
-          const int box = i / SL, slab = i % SL;
-          const unsigned t = (unsigned)(t0 + box * bt);
-          const unsigned j = t / (unsigned)p.block_size;
-          int64_t b = table[j];
-          if (b < 0 || b >= p.num_blocks) {
-            set_flag(p.err, NP_FLAG_BLOCK_ID);
-            b = 0;
-          }
-          const int32_t slot = (int32_t)(b * p.block_size + (t - j * p.block_size));
-          tma_load_3d_plain(dst + (uint32_t)(slab * BN + box * bt) * 128u, isv ? &p.tm_v : &p.tm_k,
-                      slab * 64, slot, w.kvh, fb);
+        const CUtensorMap* map = isv ? &p.tm_v : &p.tm_k;
+        for (int i0 = 0; i0 < nbox * SL; i0 += 32) {  // item i: box i / SL, slab i % SL
+          const int i = i0 + lane;
+          const int32_t sl = __shfl_sync(FULL, at, (i / SL) & 31);
+          if (i < nbox * SL)
+            tma_load_3d_plain(dst + (uint32_t)((i % SL) * BN + (i / SL) * bt) * 128u, map,
+                              (i % SL) * 64, sl, w.kvh, fb);
         }
+        if (tail) {
+          ok = __all_sync(FULL, mbar_wait(fb, tails & 1u, abort));
+          ++tails;
+          if (!ok) {
+            mbar_wait_drain(fb, (tails - 1u) & 1u);
+            return;
+          }
+          clear_tail(slot, valid);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B::kv_full + slot));
+        }
+        last = seq;
       } else {
-        constexpr int CH = D / 8;           // 16-byte pieces of a token
-        constexpr int PER = 32 / CH > 0 ? 32 / CH : 1;  // tokens a warp copies at a time
-        const char* src = static_cast<const char*>(isv ? p.v_pool : p.k_pool);
+        constexpr int CH = D / 8;      // 16-byte pieces of a token
+        constexpr int PER = 32 / CH;   // tokens a warp copies at a time
+        static_assert(CH <= 32, "a token's pieces fit a warp");
+        const char* src = static_cast<const char*>(isv ? p.v_pool : p.k_pool) + (int64_t)w.kvh * D * 2;
+        const int64_t token = (int64_t)p.kv_heads * D * 2;
+        const int ch = lane % CH, sub = lane / CH;
         for (int r0 = 0; r0 < valid; r0 += 32) {
-          int64_t at = -1;  // element offset of token r0 + lane
-          if (r0 + lane < valid) {
-            const unsigned t = (unsigned)(t0 + r0 + lane);
-            const unsigned j = t / (unsigned)p.block_size;
-            int64_t b = table[j];
-            if (b < 0 || b >= p.num_blocks) {
-              set_flag(p.err, NP_FLAG_BLOCK_ID);
-              b = 0;
-            }
-            at = ((b * p.block_size + (t - j * p.block_size)) * p.kv_heads + w.kvh) * D;
-          }
-          if constexpr (CH <= 32) {
-            const int ch = lane % CH, sub = lane / CH;
+          const int64_t mine = r0 + lane < valid ? pool_slot((unsigned)(kt * BN + r0 + lane)) : -1;
 #pragma unroll 4
-            for (int i = 0; i < 32; i += PER) {
-              const int row = r0 + i + sub;
-              const int64_t a = __shfl_sync(FULL, at, i + sub);
-              if (a >= 0)
-                cp_async16(dst + (uint32_t)((ch >> 3) * BN + row) * 128u +
-                               (uint32_t)(((ch & 7) ^ (row & 7)) << 4),
-                           src + (a + ch * 8) * 2);
-            }
+          for (int i = 0; i < 32; i += PER) {
+            const int row = r0 + i + sub;
+            const int64_t sl = __shfl_sync(FULL, mine, i + sub);
+            if (sl >= 0)
+              cp_async16(dst + (uint32_t)((ch >> 3) * BN + row) * 128u +
+                             (uint32_t)(((ch & 7) ^ (row & 7)) << 4),
+                         src + sl * token + ch * 16);
           }
         }
+        if (isv && valid < BN) clear_tail(slot, valid);
         cp_async_commit();
-        if (++untold > 2) {
-          cp_async_wait<2>();
-          tell();
+        if (pending >= 0) {  // one tile's copies stay in flight
+          cp_async_wait<1>();
+          report();
         }
+        pending = (int)slot;
       }
-      pos.template step<NS>();
     };
 
     while (ok && w.next(p)) {
-      // ---- q
-      if (seg > 0) {
-        ok = __all_sync(FULL, mbar_wait(bar(B::q_empty), (seg - 1) & 1u, abort));
-        if (!ok) break;
-      }
-      int qt = 0;
-      for (int t = 0; t < MT; ++t)
-        if (((int64_t)w.m * MT + t) * p.tile_tokens < w.g.n) ++qt;
-      if constexpr (TILED) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(B::q_full), (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
-          for (int t = 0; t < qt; ++t)
-            for (int s = 0; s < SL; ++s)
-              tma_load_3d_plain(base + (uint32_t)(t * SL + s) * 16384u, &p.tm_q, s * 64, w.kvh * G,
-                          w.g.q0 + (w.m * MT + t) * p.tile_tokens, bar(B::q_full));
+      int32_t ahead = TILED ? look_up(w.kv0) : 0;
+      if (!isv) {
+        // ---- q
+        if (seg > 0) {
+          ok = __all_sync(FULL, mbar_wait(bar(B::q_empty), (seg - 1) & 1u, abort));
+          if (!ok) break;
         }
-        __syncwarp();
-      } else {
-        constexpr int CH = D / 8;
-        for (int e = lane; e < qt * 128 * CH; e += 32) {
-          const int row = e / CH, ch = e % CH;  // row of the unit
-          const int t = row >> 7, in = row & 127;
-          const int tt = in / G, h = in - tt * G;
-          const int tok = (w.m * MT + t) * p.tile_tokens + tt;
-          if (tt < p.tile_tokens && tok < w.g.n)
-            cp_async16(base + (uint32_t)t * C::QT + (uint32_t)((ch >> 3) * 128 + in) * 128u +
-                           (uint32_t)(((ch & 7) ^ (in & 7)) << 4),
-                       static_cast<const char*>(p.q) +
-                           (((int64_t)(w.g.q0 + tok) * p.q_heads + w.kvh * G + h) * D + ch * 8) * 2);
+        int qt = 0;
+        for (int t = 0; t < MT; ++t)
+          if (((int64_t)w.m * MT + t) * p.tile_tokens < w.g.n) ++qt;
+        if constexpr (TILED) {
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(B::q_full), (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
+          __syncwarp();
+          if (lane < qt * SL)
+            tma_load_3d_plain(base + (uint32_t)lane * 16384u, &p.tm_q, (lane % SL) * 64, w.kvh * G,
+                              w.g.q0 + (w.m * MT + lane / SL) * p.tile_tokens, bar(B::q_full));
+        } else {
+          constexpr int CH = D / 8;
+          for (int e = lane; e < qt * 128 * CH; e += 32) {
+            const int row = e / CH, ch = e % CH;  // row of the unit
+            const int t = row >> 7, in = row & 127;
+            const int tt = in / G, h = in - tt * G;
+            const int tok = (w.m * MT + t) * p.tile_tokens + tt;
+            if (tt < p.tile_tokens && tok < w.g.n)
+              cp_async16(base + (uint32_t)t * C::QT + (uint32_t)((ch >> 3) * 128 + in) * 128u +
+                             (uint32_t)(((ch & 7) ^ (in & 7)) << 4),
+                         static_cast<const char*>(p.q) +
+                             (((int64_t)(w.g.q0 + tok) * p.q_heads + w.kvh * G + h) * D + ch * 8) * 2);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();  // nothing else is in flight at a segment's start
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B::q_full));
         }
-        cp_async_commit();
-        cp_async_wait<0>();  // nothing else is in flight at a segment's start
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B::q_full));
       }
       ++seg;
-      // ---- K and V tiles in the order the mma takes them
+      // ---- this warp's tiles, at their positions in the order the mma takes
+      // them: K0 V0 K1 V1 ... with two q tiles, K0 K1 V0 K2 V1 ... V with one
       const int n = w.kv1 - w.kv0;
-      if constexpr (MT == 2) {
-        for (int j = 0; j < n && ok; ++j) {
-          load_tile(false, w.kv0 + j);
-          if (ok) load_tile(true, w.kv0 + j);
-        }
-      } else {
-        load_tile(false, w.kv0);
-        for (int j = 0; j < n && ok; ++j) {
-          if (j + 1 < n) load_tile(false, w.kv0 + j + 1);
-          if (ok) load_tile(true, w.kv0 + j);
-        }
+      for (int j = 0; j < n && ok; ++j) {
+        const int32_t at = ahead;
+        if (TILED && j + 1 < n) ahead = look_up(w.kv0 + j + 1);
+        uint32_t seq;
+        if (MT == 2) seq = 2u * j + (isv ? 1u : 0u);
+        else if (isv) seq = j + 1 < n ? 2u * j + 2u : 2u * n - 1u;
+        else seq = j == 0 ? 0u : 2u * j - 1u;
+        load_tile(w.kv0 + j, seq0 + seq, at);
       }
+      seq0 += 2u * n;
       if constexpr (!TILED) {  // all of it is reported before the next q waits for it
         cp_async_wait<0>();
-        while (untold > 0) tell();
+        if (pending >= 0) report();
+        pending = -1;
       }
       w.advance();
     }
     if (*abort) {  // never leave copies in flight (bounded)
       if constexpr (TILED) {
-        if (seg > 0) mbar_wait_drain(bar(B::q_full), (seg - 1) & 1u);
-        RingPos d = pos;  // the tile before pos, and back
-        for (int i = 0; i < NS && i < issued; ++i) {
-          if (--d.slot < 0) {
-            d.slot = NS - 1;
-            d.phase ^= 1u;
-          }
-          mbar_wait_drain(bar(B::kv_full + d.slot), d.phase);
-        }
+        if (!isv && seg > 0) mbar_wait_drain(bar(B::q_full), (seg - 1) & 1u);
+        // this warp's tiles among the last NS positions; the others' phases are
+        // as good: an earlier phase of a slot is complete
+        for (int64_t q = last > NS ? last - NS : 0; q <= last; ++q)
+          if (MT == 1 || (q & 1) == (isv ? 1 : 0))
+            mbar_wait_drain(bar(B::kv_full + (int)(q % NS)), (uint32_t)(q / NS) & 1u);
       } else {
         cp_async_wait<0>();
       }
     }
-   } else if (warp == ISSUER) {
+  } else if (warp == ISSUER) {
     // ================================================================= mma
-    constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
-    const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
-    RingPos pos{0, 0};
-    uint32_t seg = 0;
-    uint32_t done[2] = {0u, 0u};  // tiles of each S buffer so far: phase of p_full
-    uint32_t it = 0;              // MT == 1: tiles so far
+    // One thread runs the whole role.
+    if (lane == 0) {
+      constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
+      constexpr uint32_t HI = umma_desc_hi(1024);
+      const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
+      RingPos pos{0, 0};
+      uint32_t seg = 0;
+      uint32_t done0 = 0, done1 = 0;  // MT == 2: P tiles taken of each q tile so far
+      uint32_t it = 0;                // MT == 1: tiles so far
 
-    auto wait = [&](int b, uint32_t phase) {
-      ok = ok && __all_sync(FULL, mbar_wait(bar(b), phase, abort));
-      return ok;
-    };
-    auto issue_s = [&](int t, int buf, uint32_t k) {  // S_buf = Q_t K^T
-      if (lane == 0) {
+      auto wait = [&](int b, uint32_t phase) {
+        ok = ok && mbar_wait(bar(b), phase, abort);
+        return ok;
+      };
+      auto issue_s = [&](int t, uint32_t buf, int slot) {  // S_buf = Q_t K^T
+        const uint32_t q = umma_desc_lo(base + (uint32_t)t * C::QT, 16);
+        const uint32_t k = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 16);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t q = base + (uint32_t)t * C::QT + (ks >> 2) * 16384u + (ks & 3) * 32u;
-          const uint32_t kk = k + (uint32_t)(ks >> 2) * (BN * 128u) + (ks & 3) * 32u;
-          umma_ss(tmem + buf * BN, umma_desc(q, 16, 1024), umma_desc(kk, 16, 1024), QK, ks > 0);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_ss(tmem + buf * BN, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u,
+                  k + ((ks >> 2) * (BN * 128u) + (ks & 3) * 32u) / 16u, HI, QK, ks > 0);
         umma_commit(bar(B::s_full + buf));
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int t, int buf, uint32_t v, bool acc) {  // O_t += P_buf V
-      tmem_fence_after();
-      if (lane == 0) {
+      };
+      auto issue_pv = [&](int t, uint32_t buf, int slot, bool acc) {  // O_t += P_buf V
+        tmem_fence_after();
+        const uint32_t v = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, BN * 128);
 #pragma unroll
         for (int ks = 0; ks < BN / 16; ++ks)
-          umma_ts(tmem + C::O0 + t * D, tmem + buf * BN + ks * 8,
-                  umma_desc(v + ks * 2048u, BN * 128, 1024), PV, acc || ks > 0);
-      }
-      __syncwarp();
-    };
-    // V rows past the context are whatever their slots held: zeroed, for 0 x
-    // NaN is NaN
-    auto clear_tail = [&](uint32_t v, int kt) {
-      const int valid = max(0, min(BN, w.g.c - kt * BN));
-      if (valid == BN) return;
-      unsigned char* at = smem + (v - base);
-      for (int e = lane; e < SL * (BN - valid) * 8; e += 32) {
-        const int slab = e / ((BN - valid) * 8), x = e % ((BN - valid) * 8);
-        *reinterpret_cast<uint4*>(at + (slab * BN + valid) * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async_smem();
-      __syncwarp();
-    };
+          umma_ts(tmem + C::O0 + t * D, tmem + buf * BN + ks * 8, v + ks * 128u, HI, PV,
+                  ks > 0 ? 1u : (acc ? 1u : 0u));
+      };
 
-    while (ok && w.next(p)) {
-      const int n = w.kv1 - w.kv0;
-      if (!wait(B::q_full, seg & 1u)) break;
-      ++seg;
-      if constexpr (MT == 2) {
-        const int n0 = tc_tiles<D>(p, w, 0), n1 = tc_tiles<D>(p, w, 1);
-        // n == max(n0, n1): the unit's last tokens see the most
-        uint32_t kaddr = ring + (uint32_t)pos.slot * C::SLOT;
-        int kslot = pos.slot;
-        if (!wait(B::kv_full + kslot, pos.phase)) break;
-        pos.template step<NS>();
-        if (n0 > 0) issue_s(0, 0, kaddr);
-        if (n1 > 0) issue_s(1, 1, kaddr);
-        if (lane == 0) {
+      while (ok && w.next(p)) {
+        const int n = w.kv1 - w.kv0;
+        if (!wait(B::q_full, seg & 1u)) break;
+        ++seg;
+        if constexpr (MT == 2) {
+          // n == max(n0, n1): the unit's last tokens see the most
+          const int n0 = tc_tiles<D>(p, w, 0), n1 = tc_tiles<D>(p, w, 1);
+          int kslot = pos.slot;
+          if (!wait(B::kv_full + kslot, pos.phase)) break;
+          pos.template step<NS>();
+          if (n0 > 0) issue_s(0, 0, kslot);
+          if (n1 > 0) issue_s(1, 1, kslot);
           umma_commit(bar(B::kv_empty + kslot));
           if (n == 1) umma_commit(bar(B::q_empty));
-        }
-        for (int j = 0; j < n && ok; ++j) {
-          const int vslot = pos.slot;
-          const uint32_t vphase = pos.phase;
-          const uint32_t vaddr = ring + (uint32_t)vslot * C::SLOT;
-          pos.template step<NS>();
-          bool have_v = false, have_k = false;
-          kslot = pos.slot;
-          kaddr = ring + (uint32_t)kslot * C::SLOT;
-          const uint32_t kphase = pos.phase;
-          if (j + 1 < n) pos.template step<NS>();
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nt = t == 0 ? n0 : n1;
-            if (j >= nt) continue;
-            if (!wait(B::p_full + t, done[t] & 1u)) break;
-            ++done[t];
-            if (!have_v) {
-              if (!wait(B::kv_full + vslot, vphase)) break;
-              clear_tail(vaddr, w.kv0 + j);
-              have_v = true;
-            }
-            issue_pv(t, t, vaddr, j > 0);
-            // the last tile that reads this V frees it
-            if (lane == 0 && (t == 1 || j >= n1)) umma_commit(bar(B::kv_empty + vslot));
-            if (j + 1 < nt) {
-              if (!have_k) {
+          for (int j = 0; j < n; ++j) {
+            const int vslot = pos.slot;
+            const uint32_t vphase = pos.phase;
+            pos.template step<NS>();
+            kslot = pos.slot;
+            const uint32_t kphase = pos.phase;
+            if (j + 1 < n) pos.template step<NS>();
+            bool have_k = false;
+            if (j < n0) {
+              if (!wait(B::p_full, done0 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
+              ++done0;
+              issue_pv(0, 0, vslot, j > 0);
+              if (j >= n1) umma_commit(bar(B::kv_empty + vslot));  // no other reader of V
+              if (j + 1 < n0) {
                 if (!wait(B::kv_full + kslot, kphase)) break;
                 have_k = true;
+                issue_s(0, 0, kslot);
+                if (j + 1 >= n1) {
+                  umma_commit(bar(B::kv_empty + kslot));
+                  if (j + 2 == n) umma_commit(bar(B::q_empty));
+                }
+              } else {
+                umma_commit(bar(B::o_full));
               }
-              issue_s(t, t, kaddr);
-              if (lane == 0 && (t == 1 || j + 1 >= n1)) {
+            }
+            if (j < n1) {
+              if (!wait(B::p_full + 1, done1 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
+              ++done1;
+              issue_pv(1, 1, vslot, j > 0);
+              umma_commit(bar(B::kv_empty + vslot));
+              if (j + 1 < n1) {
+                if (!have_k && !wait(B::kv_full + kslot, kphase)) break;
+                issue_s(1, 1, kslot);
                 umma_commit(bar(B::kv_empty + kslot));
                 if (j + 2 == n) umma_commit(bar(B::q_empty));
+              } else {
+                umma_commit(bar(B::o_full + 1));
               }
-            } else if (lane == 0) {
-              umma_commit(bar(B::o_full + t));
             }
-            __syncwarp();
           }
-        }
-      } else {
-        const uint32_t first = it;
-        for (int j = -1; j < n && ok; ++j) {
-          if (j + 1 < n) {  // S(j + 1)
-            const int slot = pos.slot;
-            if (!wait(B::kv_full + slot, pos.phase)) break;
-            pos.template step<NS>();
-            issue_s(0, (first + j + 1) & 1u, ring + (uint32_t)slot * C::SLOT);
-            if (lane == 0) {
+        } else {
+          for (int j = -1; j < n; ++j) {
+            if (j + 1 < n) {  // S(j + 1), into the buffer that P(j - 1) has left
+              const int slot = pos.slot;
+              if (!wait(B::kv_full + slot, pos.phase)) break;
+              pos.template step<NS>();
+              issue_s(0, (it + (j >= 0 ? 1u : 0u)) & 1u, slot);
               umma_commit(bar(B::kv_empty + slot));
               if (j + 2 == n) umma_commit(bar(B::q_empty));
             }
-          }
-          if (j >= 0) {  // O += P(j) V(j)
-            const uint32_t buf = it & 1u;
-            const int slot = pos.slot;
-            const uint32_t phase = pos.phase;
-            pos.template step<NS>();
-            if (!wait(B::p_full + buf, (it >> 1) & 1u)) break;
-            if (!wait(B::kv_full + slot, phase)) break;
-            ++it;
-            clear_tail(ring + (uint32_t)slot * C::SLOT, w.kv0 + j);
-            issue_pv(0, buf, ring + (uint32_t)slot * C::SLOT, j > 0);
-            if (lane == 0) {
+            if (j >= 0) {  // O += P(j) V(j)
+              const uint32_t buf = it & 1u;
+              const int slot = pos.slot;
+              const uint32_t phase = pos.phase;
+              pos.template step<NS>();
+              if (!wait(B::p_full + buf, (it >> 1) & 1u) || !wait(B::kv_full + slot, phase)) break;
+              ++it;
+              issue_pv(0, buf, slot, j > 0);
               umma_commit(bar(B::pv_done));
               umma_commit(bar(B::kv_empty + slot));
               if (j + 1 == n) umma_commit(bar(B::o_full));
             }
           }
         }
+        w.advance();
       }
-      w.advance();
-    }
-    // nothing of this block is left running in the tensor cores (bounded)
-    if (lane == 0) {
+      // nothing of this block is left running in the tensor cores (bounded)
       umma_commit(bar(B::drain));
       mbar_wait_drain(bar(B::drain), 0u);
     }
     __syncwarp();
-   }
   }
   if (!ok && lane == 0) set_flag(p.err, NP_FLAG_TIMEOUT);
   __syncwarp();

@@ -97,10 +97,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 // Shared-memory operand in the 128-byte swizzle: 64 16-bit elements a row of
 // 128 bytes, 8 rows an atom of 1024 bytes.  lead: bytes between 64-element
 // slabs of the M/N extent (an operand whose M/N is contiguous; unused where K
-// is).  stride: bytes between 8-row groups.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((lead >> 4) & 0x3fffu) << 16) |
-         ((uint64_t)((stride >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
+// is).  stride: bytes between 8-row groups.  The two 32-bit halves: moving an
+// operand by b bytes adds b / 16 to the low one.
+__device__ __forceinline__ constexpr uint32_t umma_desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3fffu) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ constexpr uint32_t umma_desc_hi(uint32_t stride) {
+  return (stride >> 4) | (1u << 14) | (2u << 29);
 }
 
 // bf16 x bf16 -> fp32, M x N; b_mn: B's N extent is contiguous; neg_a: -A
@@ -110,21 +113,26 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn, 
 }
 
 // ----------------------------------------------------------------- mma ----
-// D (tensor memory) = A B (+ D where acc); one thread issues.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// D (tensor memory) = A B (+ D where acc); one thread issues.  hi: both
+// operands' (they have the same stride).
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
 // A from tensor memory (16-bit elements, two a column)
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
