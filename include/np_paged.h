@@ -183,6 +183,32 @@ np_status np_rope_append(void* q_out, const void* q, const void* k_new,
                          const void* k_weight, float eps, int32_t num_tokens,
                          int32_t* err_word, np_stream_t stream);
 
+/* np_rope_append with its arguments in a struct, for callers whose foreign
+ * function calls cost by the argument.  sections is an array here, read when
+ * has_sections is 1 (num_axes of its entries). */
+typedef struct np_rope_append_args {
+  void* q_out;
+  const void* q;
+  const void* k_new;
+  const void* v_new;
+  const int64_t* slot_mapping;
+  void* k_pool;
+  void* v_pool;
+  const float* cos_sin;
+  const int32_t* positions;
+  const void* q_weight;
+  const void* k_weight;
+  int32_t* err_word;
+  np_stream_t stream;
+  int64_t q_stride, k_stride, v_stride, num_blocks;
+  int32_t dtype, block_size, q_heads, kv_heads, head_dim, max_positions;
+  int32_t rot_dim, num_axes, interleaved, num_tokens, has_sections;
+  int32_t sections[4];
+  float eps;
+} np_rope_append_args;
+
+np_status np_rope_append_packed(const np_rope_append_args* args);
+
 /*
  * np_paged_prefill -- attention of chunks of new tokens over the paged cache
  * (prompts, chunks of prompts, and rows with a single token among them).
@@ -225,6 +251,26 @@ np_status np_paged_prefill(void* out, const void* q, const void* k_pool,
                            int32_t num_tokens, int32_t q_heads, float scale,
                            void* workspace, size_t workspace_bytes,
                            int32_t* err_word, np_stream_t stream);
+
+/* np_paged_prefill with its arguments in a struct (see np_rope_append_args). */
+typedef struct np_paged_prefill_args {
+  void* out;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_starts;
+  void* workspace;
+  int32_t* err_word;
+  np_stream_t stream;
+  int64_t num_blocks, workspace_bytes;
+  int32_t dtype, block_size, kv_heads, head_dim, max_blocks_per_row, rows;
+  int32_t num_tokens, q_heads;
+  float scale;
+} np_paged_prefill_args;
+
+np_status np_paged_prefill_packed(const np_paged_prefill_args* args);
 
 /*
  * np_paged_decode_plan -- the schedule the library recommends, as a

@@ -32,6 +32,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -140,6 +141,10 @@ def _declare_prompt(lib: ctypes.CDLL) -> None:
                                    _I32, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32,
                                    ctypes.POINTER(_I32), _I32, _P, _P, ctypes.c_float, _I32, _P,
                                    _P]
+    for name in ("np_rope_append_packed", "np_paged_prefill_packed"):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.c_char_p]
     lib.np_paged_prefill_workspace_bytes.restype = ctypes.c_size_t
     lib.np_paged_prefill_workspace_bytes.argtypes = [_I32]
     lib.np_paged_prefill.restype = ctypes.c_int
@@ -263,19 +268,52 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, inv_freq
     return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
 
 
-def _token_rows(t: torch.Tensor, name: str, cur: int, heads: int, d: int):
-    """(address, elements between tokens) of a [T, heads, d] tensor whose heads
+# np_rope_append_args and np_paged_prefill_args (np_paged.h): a foreign call
+# converts one argument instead of thirty, which is most of a small call's time.
+_ROPE_ARGS = struct.Struct("@13P4q15if")
+_PREFILL_ARGS = struct.Struct("@10P2q8if")
+
+
+def _device_now() -> int:
+    """torch's current CUDA device (as _current_device, without its lazy
+    initialisation: a CUDA tensor exists wherever the answer matters); -2, no
+    tensor's device, where there is none."""
+    try:
+        cur = torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):
+        cur = _current_device()
+    return cur if cur >= 0 else -2
+
+
+def _at(t: torch.Tensor, name: str, cur: int) -> int:
+    """_dev's address and refusals, the usual case first."""
+    if t.get_device() == cur and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, cur)
+
+
+def _stream_now(stream, cur: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(cur)
+    return _stream(stream) or 0
+
+
+def _pack(form: struct.Struct, call: str, *values) -> bytes:
+    try:
+        return form.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"{call}: a size does not fit its type ({e})") from None
+
+
+def _token_rows(t: torch.Tensor, name: str, cur: int, n: int, heads: int, d: int):
+    """(address, elements between tokens) of a [n, heads, d] tensor whose heads
     are dense; its tokens may lie further apart (a view of wider rows)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (no CPU path exists)")
-    if t.device.index != cur:
-        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}; "
-                         "call inside torch.cuda.device(...) of the tensors' GPU")
-    if t.numel() > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    if t.get_device() != cur:
+        _dev(t, name, cur)  # raises
+    s0, s1, s2 = t.stride()
+    if n > 0 and (s2 != 1 or (heads > 1 and s1 != d)):
         raise ValueError(f"{name}: heads and dims must be dense (only tokens may be strided)")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * d)
+    return t.data_ptr(), (s0 if n > 1 else heads * d)
 
 
 def np_rope_append(q_out, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin, positions,
@@ -293,49 +331,59 @@ def np_rope_append(q_out, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin
     """
     name = "np_rope_append"
     nb, bs, hk, d = k_pool.shape
-    if k_new.dim() != 3 or v_pool.shape != k_pool.shape or k_new.shape != v_new.shape or \
-            tuple(k_new.shape[1:]) != (hk, d):
+    dt = k_pool.dtype
+    if k_new.dim() != 3 or v_pool.shape != k_pool.shape or k_new.shape != v_new.shape:
         raise ValueError(f"{name}: k_new/v_new must be [tokens, kv_heads, head_dim] of the pools")
-    n = k_new.shape[0]
-    if any(t.dtype != k_pool.dtype for t in (v_pool, k_new, v_new)):
+    n, h1, d1 = k_new.shape
+    if h1 != hk or d1 != d:
+        raise ValueError(f"{name}: k_new/v_new must be [tokens, kv_heads, head_dim] of the pools")
+    if v_pool.dtype is not dt or k_new.dtype is not dt or v_new.dtype is not dt:
         raise ValueError(f"{name}: k_new, v_new and the pools must share a dtype")
     hq = 0
     if (q is None) != (q_out is None) or (q is None and q_weight is not None):
         raise ValueError(f"{name}: q and q_out go together")
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.dtype != k_pool.dtype:
+        if q.dim() != 3 or q.dtype is not dt:
             raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim] of the pools' dtype")
-        if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        n1, hq, d1 = q.shape
+        if n1 != n or d1 != d:
+            raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim] of the pools' dtype")
+        if q_out.shape != q.shape or q_out.dtype is not dt:
             raise ValueError(f"{name}: q_out must match q")
-        hq = q.shape[1]
         if hq == 0:
             raise ValueError(f"{name}: q has no heads; pass q and q_out as None")
     for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != k_pool.dtype or tuple(w.shape) != (d,)):
+        if w is not None and (w.dtype is not dt or w.shape != (d,)):
             raise ValueError(f"{name}: {what} must be [head_dim] of the pools' dtype")
-    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (n,):
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,):
         raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2:
         raise ValueError(f"{name}: cos_sin must be float32 [max_positions, rot_dim]")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or \
-            positions.shape[-1] != n:
+    dims = positions.dim()
+    if positions.dtype is not torch.int32 or dims not in (1, 2) or positions.shape[-1] != n:
         raise ValueError(f"{name}: positions must be int32 [tokens] or [axes, tokens]")
-    if sections is not None and len(sections) != axes:
-        raise ValueError(f"{name}: one section per position axis")
-    sec = None if sections is None else (_I32 * axes)(*[int(x) for x in sections])
-    cur = _current_device()
-    qp, qs = (None, 0) if q is None else _token_rows(q, "q", cur, hq, d)
-    kp, ks = _token_rows(k_new, "k_new", cur, hk, d)
-    vp, vs = _token_rows(v_new, "v_new", cur, hk, d)
-    st = load().np_rope_append(
-        _opt(q_out, "q_out", cur), qp, kp, vp, qs, ks, vs, _dev(slot_mapping, "slot_mapping", cur),
-        _dev(k_pool, "k_pool", cur), _dev(v_pool, "v_pool", cur), _dtype_code(k_pool.dtype), nb, bs,
-        hq, hk, d, _dev(cos_sin, "cos_sin", cur), cos_sin.shape[0], cos_sin.shape[1],
-        _dev(positions, "positions", cur), axes, sec, int(bool(interleaved)),
-        _opt(q_weight, "q_weight", cur), _opt(k_weight, "k_weight", cur), float(eps), n,
-        _opt(err_word, "err_word", cur), _stream(stream))
-    _check(st, name)
+    axes = 1 if dims == 1 else positions.shape[0]
+    sec = (0, 0, 0, 0)
+    if sections is not None:
+        if len(sections) != axes:
+            raise ValueError(f"{name}: one section per position axis")
+        sec = (tuple(sections) + sec)[:4]  # more than four axes: refused by the library
+    cur = _device_now()
+    qp, qs = (0, 0) if q is None else _token_rows(q, "q", cur, n, hq, d)
+    kp, ks = _token_rows(k_new, "k_new", cur, n, hk, d)
+    vp, vs = _token_rows(v_new, "v_new", cur, n, hk, d)
+    max_pos, rot = cos_sin.shape
+    st = load().np_rope_append_packed(_pack(
+        _ROPE_ARGS, name, 0 if q_out is None else _at(q_out, "q_out", cur), qp, kp, vp,
+        _at(slot_mapping, "slot_mapping", cur), _at(k_pool, "k_pool", cur),
+        _at(v_pool, "v_pool", cur), _at(cos_sin, "cos_sin", cur), _at(positions, "positions", cur),
+        0 if q_weight is None else _at(q_weight, "q_weight", cur),
+        0 if k_weight is None else _at(k_weight, "k_weight", cur),
+        0 if err_word is None else _at(err_word, "err_word", cur), _stream_now(stream, cur),
+        qs, ks, vs, nb, _dtype_code(dt), bs, hq, hk, d, max_pos, rot, axes, 1 if interleaved else 0,
+        n, 0 if sections is None else 1, *sec, eps))
+    if st != NP_OK:
+        raise NPError(st, name)
 
 
 def np_paged_prefill_workspace_bytes(head_dim) -> int:
@@ -360,28 +408,30 @@ def np_paged_prefill(out, q, k_pool, v_pool, block_tables, context_lens, query_s
     if q.dim() != 3 or k_pool.dim() != 4:
         raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim]")
     nb, bs, hk, d = k_pool.shape
-    if q.shape[2] != d or v_pool.shape != k_pool.shape or q.dtype != k_pool.dtype or \
-            v_pool.dtype != k_pool.dtype:
+    tokens, hq, d1 = q.shape
+    dt = q.dtype
+    if d1 != d or v_pool.shape != k_pool.shape or k_pool.dtype is not dt or v_pool.dtype is not dt:
         raise ValueError(f"{name}: q/pool shape or dtype mismatch")
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != q.shape or out.dtype is not dt:
         raise ValueError(f"{name}: out must match q")
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2:
+    if block_tables.dtype is not torch.int32 or block_tables.dim() != 2:
         raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
-    rows = block_tables.shape[0]
-    if context_lens.dtype != torch.int32 or tuple(context_lens.shape) != (rows,):
+    rows, mb = block_tables.shape
+    if context_lens.dtype is not torch.int32 or context_lens.shape != (rows,):
         raise ValueError(f"{name}: context_lens must be int32 [rows]")
-    if query_starts.dtype != torch.int32 or tuple(query_starts.shape) != (rows + 1,):
+    if query_starts.dtype is not torch.int32 or query_starts.shape != (rows + 1,):
         raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
-    cur = _current_device()
-    st = load().np_paged_prefill(
-        _dev(out, "out", cur), _dev(q, "q", cur), _dev(k_pool, "k_pool", cur),
-        _dev(v_pool, "v_pool", cur), _dtype_code(q.dtype), nb, bs, hk, d,
-        _dev(block_tables, "block_tables", cur), block_tables.shape[1],
-        _dev(context_lens, "context_lens", cur), _dev(query_starts, "query_starts", cur), rows,
-        q.shape[0], q.shape[1], float(scale), _opt(workspace, "workspace", cur),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _opt(err_word, "err_word", cur), _stream(stream))
-    _check(st, name)
+    cur = _device_now()
+    st = load().np_paged_prefill_packed(_pack(
+        _PREFILL_ARGS, name, _at(out, "out", cur), _at(q, "q", cur), _at(k_pool, "k_pool", cur),
+        _at(v_pool, "v_pool", cur), _at(block_tables, "block_tables", cur),
+        _at(context_lens, "context_lens", cur), _at(query_starts, "query_starts", cur),
+        0 if workspace is None else _at(workspace, "workspace", cur),
+        0 if err_word is None else _at(err_word, "err_word", cur), _stream_now(stream, cur), nb,
+        0 if workspace is None else workspace.nbytes, _dtype_code(dt), bs, hk, d, mb, rows, tokens,
+        hq, scale))
+    if st != NP_OK:
+        raise NPError(st, name)
 
 
 def prefill_step(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, block_tables, context_lens,

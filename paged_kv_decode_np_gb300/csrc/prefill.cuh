@@ -9,9 +9,9 @@
 // tokens: nk(m) = max(1, ceil((c - n + min(n, (m + 1) U)) / BN)) tiles.
 //
 // All units, in the order (row, kv head, m), are laid end to end as one
-// stream of kv tiles, and the stream is cut into one equal share per thread
-// block: every SM has the same amount of work whatever the mix of long and
-// short chunks, causal triangles and histories.  A block walks its share; a
+// stream, nk(m) kv tiles and a fixed cost each, and the stream is cut into one
+// equal share per thread block: every SM has the same amount of work whatever
+// the mix of long and short chunks, causal triangles and histories.  A block walks its share; a
 // unit that lies inside one block is normalised and stored directly, a unit
 // cut by a share's end leaves a partial (m, l, unnormalised O in fp32) per
 // block that touched it, and a second launch joins them in block order
@@ -44,7 +44,7 @@ struct PrefillParams {
   const int32_t* context_lens;
   const int32_t* query_starts;
   int32_t* err;
-  int4* plan;    // [ctas] {row, kv head, m, first kv tile}, then [ctas] {kv tiles (64 bits), 0, 0}
+  int4* plan;    // [ctas + 1] {row, kv head, m, kv tile}: where each block's share begins
   int4* cuts;    // [ctas] {row (-1: none), kv head, m, last block}: units cut by a share's end
   float* parts;  // [ctas][2] partials
   int64_t num_blocks;
@@ -54,7 +54,8 @@ struct PrefillParams {
   int32_t tile_rows;    // BMT
   int32_t tiles;        // MT
   int32_t bn;           // kv tile
-  int32_t min_tiles;    // least kv tiles a share is cut down to
+  int32_t unit_cost;    // what beginning a unit costs a block, in kv tiles
+  int32_t min_share;    // least share a block is given, in kv tiles
   int32_t box_tokens;   // tokens per tiled copy
   float qscale;         // |scale| * log2(e)
   int32_t negate;       // scale < 0
@@ -112,8 +113,8 @@ __device__ __forceinline__ int prefill_kv_tiles(const PrefillParams& p, const Pr
 // of one unit.  Every role of the block walks it by itself.
 struct PrefillWalk {
   int r, kvh, m;
-  int off;        // first kv tile of the next segment
-  int64_t left;   // kv tiles left in the share
+  int off;      // first kv tile of the next segment
+  int4 end;     // where the next block's share begins
   PrefillRow g;
   int units;
   // the current segment
@@ -121,36 +122,39 @@ struct PrefillWalk {
 
   __device__ __forceinline__ void start(const PrefillParams& p, int cta) {
     const int4 a = p.plan[cta];
-    const int4 l = p.plan[p.ctas + cta];
-    left = (int64_t)(((uint64_t)(uint32_t)l.y << 32) | (uint32_t)l.x);
+    end = p.plan[cta + 1];
     r = a.x;
     kvh = a.y;
     m = a.z;
     off = a.w;
-    if (left > 0) {
+    units = 0;
+    if (r < p.rows) {
       g = prefill_row(p, r);
       units = prefill_units(p, g.n);
     }
   }
   // the next segment; false at the share's end
   __device__ __forceinline__ bool next(const PrefillParams& p) {
-    if (left <= 0) return false;
+    if (r >= p.rows) return false;
     while (m >= units) {  // past the kv head's last unit
       m = 0;
       if (++kvh < p.kv_heads && units > 0) break;
       kvh = 0;
-      if (++r >= p.rows) return false;  // never: the plan's shares end with the rows
+      if (++r >= p.rows) return false;
       g = prefill_row(p, r);
       units = prefill_units(p, g.n);
     }
+    const bool last = r == end.x && kvh == end.y && m == end.z;  // the unit that the share ends in
+    if (last ? off >= end.w
+             : r > end.x || (r == end.x && (kvh > end.y || (kvh == end.y && m > end.z))))
+      return false;
     nk = prefill_kv_tiles(p, g, (int64_t)(m + 1) * p.tile_tokens * p.tiles);
     kv0 = off;
-    kv1 = left < nk - off ? off + (int)left : nk;
+    kv1 = last ? end.w : nk;
     return true;
   }
   // past the current segment (its fields stay valid until next())
   __device__ __forceinline__ void advance() {
-    left -= kv1 - kv0;
     off = 0;
     ++m;
   }
@@ -161,7 +165,7 @@ struct PrefillWalk {
 np_status launch_prefill_plan(const PrefillParams& p, cudaStream_t s);
 np_status launch_prefill_join(const PrefillParams& p, np_dtype dtype, cudaStream_t s);
 // prefill_simt.cu
-np_status launch_prefill_simt(const PrefillParams& p, np_dtype dtype, cudaStream_t s);
+np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s);
 
 // prefill_tc.cu, per head_dim
 np_status prefill_tc_d16(const PrefillParams& p, bool tiled, cudaStream_t s);
@@ -169,6 +173,20 @@ np_status prefill_tc_d32(const PrefillParams& p, bool tiled, cudaStream_t s);
 np_status prefill_tc_d64(const PrefillParams& p, bool tiled, cudaStream_t s);
 np_status prefill_tc_d128(const PrefillParams& p, bool tiled, cudaStream_t s);
 np_status prefill_tc_d256(const PrefillParams& p, bool tiled, cudaStream_t s);
+
+// The opt-in shared-memory limit of a kernel, a per-device attribute: set at
+// its first launch on a device.  `done`: one word per kernel, bit d for device d.
+template <typename K>
+np_status allow_smem(K kern, size_t bytes, unsigned long long* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return NP_ERR_CUDA;
+  if (dev < 64 && ((__atomic_load_n(done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) return NP_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+      cudaSuccess)
+    return NP_ERR_CUDA;
+  if (dev < 64) __atomic_fetch_or(done, 1ull << dev, __ATOMIC_ACQ_REL);
+  return NP_OK;
+}
 
 // Launches `kern` so that it may become resident while the launch before it
 // still runs; its griddepcontrol.wait holds it until that one is complete.

@@ -25,7 +25,7 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
 }
 
 // Plan and cut list, then the partials of kPrefillMaxCtas blocks.
-constexpr size_t kPlanBytes = 3 * npk::kPrefillMaxCtas * sizeof(int4);
+constexpr size_t kPlanBytes = (2 * npk::kPrefillMaxCtas + 1) * sizeof(int4);
 
 // rows of the largest unit any kernel of this head_dim takes
 int unit_rows(int32_t head_dim) { return head_dim == 256 ? 128 : 256; }
@@ -80,7 +80,8 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   p.tile_rows = 128;
   p.bn = d == 256 ? 64 : 128;
   p.tile_tokens = p.tile_rows / p.group;
-  p.min_tiles = 2;
+  p.unit_cost = 2;
+  p.min_share = 4;
   // Tiled copies: boxes of whole 8-row swizzle atoms inside one block, slot
   // coordinates in int32.  box_tokens: the largest power of two that divides
   // the block size, at most a kv tile.
@@ -172,7 +173,7 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
   p.query_starts = query_starts;
   p.err = err_word;
   p.plan = static_cast<int4*>(workspace);
-  p.cuts = p.plan + 2 * npk::kPrefillMaxCtas;
+  p.cuts = p.plan + npk::kPrefillMaxCtas + 1;
   p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(kPlanBytes, 256));
   p.num_blocks = num_blocks;
   p.block_size = block_size;
@@ -196,10 +197,21 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
     p.tile_rows = 64;
     p.bn = 64;
     p.tile_tokens = p.tile_rows / group;
-    p.min_tiles = 2;
+    p.unit_cost = 1;
+    p.min_share = 3;
     rc = npk::launch_prefill_plan(p, st);
-    if (rc == NP_OK) rc = npk::launch_prefill_simt(p, dtype, st);
+    if (rc == NP_OK) rc = npk::launch_prefill_simt(p, st);
   }
   if (rc == NP_OK) rc = npk::launch_prefill_join(p, dtype, st);
   return rc;
+}
+
+extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
+  if (!a) return NP_ERR_INVALID_ARG;
+  return np_paged_prefill(a->out, a->q, a->k_pool, a->v_pool, static_cast<np_dtype>(a->dtype),
+                          a->num_blocks, a->block_size, a->kv_heads, a->head_dim, a->block_tables,
+                          a->max_blocks_per_row, a->context_lens, a->query_starts, a->rows,
+                          a->num_tokens, a->q_heads, a->scale, a->workspace,
+                          a->workspace_bytes < 0 ? 0 : (size_t)a->workspace_bytes, a->err_word,
+                          a->stream);
 }

@@ -40,15 +40,13 @@ __device__ int64_t prefill_row_prefix(const PrefillParams& p, const PrefillRow& 
 
 constexpr int kPlanThreads = 1024;
 
-// One block.  Scans the rows' kv tile counts, cuts the stream of W tiles into
-// equal shares and writes each block's first (row, kv head, unit, kv tile)
-// and length, and which units the shares' ends cut.
+// One block.  Scans the rows' work -- a unit counts its kv tiles and unit_cost
+// -- cuts the stream into equal shares and writes where each block's begins
+// (row, kv head, unit, kv tile), and which units the shares' ends cut.
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid_constant__
                                                                     PrefillParams p) {
-  __shared__ int64_t pre[kPrefillMaxRows + 1];  // tiles before each row
+  __shared__ int64_t pre[kPrefillMaxRows + 1];  // work before each row
   __shared__ int64_t warp_sum[32];
-  __shared__ int64_t at[kPrefillMaxCtas + 1];   // the shares' ends
-  __shared__ int64_t unit_end[kPrefillMaxCtas + 1];  // of the unit that `at` lies in
   __shared__ int4 pos[kPrefillMaxCtas + 1];
   constexpr unsigned FULL = 0xffffffffu;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -62,7 +60,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
     if (i < per && r < p.rows) {
       const PrefillRow g = prefill_row(p, r, true);
       const int units = prefill_units(p, g.n);
-      w[i] = prefill_row_prefix(p, g, units, units) * p.kv_heads;
+      w[i] = (prefill_row_prefix(p, g, units, units) + (int64_t)units * p.unit_cost) * p.kv_heads;
     }
     sum += w[i];
   }
@@ -94,75 +92,63 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
   if (tid == 0) pre[p.rows] = warp_sum[31];
   __syncthreads();
   const int64_t W = pre[p.rows];
-  // blocks that share the work: a share holds min_tiles at least
-  const int64_t want = (W + p.min_tiles - 1) / p.min_tiles;
+  // blocks that share the work: a share holds min_share at least
+  const int64_t want = (W + p.min_share - 1) / p.min_share;
   const int Pe = (int)(want < 1 ? 1 : (want < p.ctas ? want : p.ctas));
   if (tid <= p.ctas) {
     const int64_t share = W / Pe;
-    int64_t t = tid >= Pe ? W : share * tid + (W % Pe) * tid / Pe;
+    const int64_t x = tid >= Pe ? W : share * tid + (W % Pe) * tid / Pe;
     int4 q = make_int4(p.rows, 0, 0, 0);
-    int64_t end = W;
-    if (t < W) {
-      int lo = 0, hi = p.rows;  // the last row with pre[row] <= t: it has tiles there
+    if (x < W) {
+      int lo = 0, hi = p.rows;  // the last row with pre[row] <= x: it has work there
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= t) lo = mid;
+        if (pre[mid] <= x) lo = mid;
         else hi = mid;
       }
       const PrefillRow g = prefill_row(p, lo);
       const int units = prefill_units(p, g.n);
       const int64_t wh = (pre[lo + 1] - pre[lo]) / p.kv_heads;
-      const int64_t rem = t - pre[lo];
-      const int kvh = (int)(rem / wh);
-      const int64_t in = rem - kvh * wh;
-      int a = 0, b = units;  // the last unit with prefix <= in
+      int kvh = (int)((x - pre[lo]) / wh);
+      const int64_t in = (x - pre[lo]) - kvh * wh;
+      int a = 0, b = units;  // the last unit that begins at or before `in`
       while (b - a > 1) {
         const int mid = (a + b) >> 1;
-        if (prefill_row_prefix(p, g, units, mid) <= in) a = mid;
+        if (prefill_row_prefix(p, g, units, mid) + (int64_t)mid * p.unit_cost <= in) a = mid;
         else b = mid;
       }
-      const int64_t s0 = prefill_row_prefix(p, g, units, a);
-      const int64_t s1 = prefill_row_prefix(p, g, units, a + 1);
-      const int64_t ustart = t - (in - s0);
-      end = ustart + (s1 - s0);
-      int off = (int)(in - s0);
-      // an end that lies near a unit's own start is moved there: the partials
-      // it saves cost more than the imbalance
-      if (off > 0 && off * 16 <= share) {
-        t = ustart;
+      const int64_t s0 = prefill_row_prefix(p, g, units, a) + (int64_t)a * p.unit_cost;
+      const int nk = prefill_kv_tiles(p, g, (int64_t)(a + 1) * p.tile_tokens * p.tiles);
+      int off = (int)(in - s0) - p.unit_cost;  // < 0: within the fixed cost
+      // an end that lies near a unit's own start or end is moved there: the
+      // partials it saves cost more than the imbalance
+      if (off <= 0 || (int64_t)off * 16 <= share) {
         off = 0;
-      } else if (off > 0 && (end - t) * 16 <= share) {
-        t = end;
+      } else if ((int64_t)(nk - off) * 16 <= share) {
         off = 0;
-        // the unit after: (a + 1) of this head, the next head, or the next row with units
-        int r2 = lo, k2 = kvh, a2 = a + 1;
-        if (a2 >= units) {
-          a2 = 0;
-          if (++k2 >= p.kv_heads) {
-            k2 = 0;
-            ++r2;
+        // the unit after: of this head, the next head, or the next row
+        if (++a >= units) {
+          a = 0;
+          if (++kvh >= p.kv_heads) {
+            kvh = 0;
+            ++lo;
           }
         }
-        q = make_int4(r2, k2, a2, 0);
-        end = t;  // not cut
       }
-      if (q.x == p.rows && t < W) q = make_int4(lo, kvh, a, off);
+      q = make_int4(lo, kvh, a, off);
     }
-    at[tid] = t;
-    unit_end[tid] = end;
     pos[tid] = q;
+    p.plan[tid] = q;
   }
   __syncthreads();
   if (tid < p.ctas) {
-    const int64_t len = at[tid + 1] - at[tid];
-    p.plan[tid] = pos[tid];
-    p.plan[p.ctas + tid] = make_int4((int)(len & 0xffffffff), (int)(len >> 32), 0, 0);
-    // the unit that this share's end cuts, if the share began it
+    // the unit that this share's end cuts, if the share holds its first tile
     int4 cut = make_int4(-1, 0, 0, 0);
-    const int4 e = pos[tid + 1];
-    if (len > 0 && at[tid + 1] < W && e.w > 0 && at[tid + 1] - e.w >= at[tid]) {
-      int last = tid + 1;
-      while (last + 1 < p.ctas && at[last + 1] < unit_end[tid + 1]) ++last;
+    const int4 s = pos[tid], e = pos[tid + 1];
+    auto same = [](int4 u, int4 v) { return u.x == v.x && u.y == v.y && u.z == v.z; };
+    if (e.w > 0 && (!same(s, e) || s.w == 0)) {
+      int last = tid + 1;  // the last block whose share begins in the unit
+      while (last + 1 <= p.ctas && same(pos[last + 1], e)) ++last;
       cut = make_int4(e.x, e.y, e.z, last);
     }
     p.cuts[tid] = cut;

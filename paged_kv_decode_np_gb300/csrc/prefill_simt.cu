@@ -1,11 +1,11 @@
-// prefill_simt.cu -- np_paged_prefill on the FMA pipes: every type and
-// head_dim, any block size.
+// prefill_simt.cu -- np_paged_prefill on the FMA pipes: fp32 pools, every
+// head_dim and block size.
 //
 // A unit is one tile of 64 (token, head) rows; a kv tile is 64 tokens.  256
 // threads form S = Q K^T as 4 x 4 microtiles from shared memory (rows 4 ty +
 // i, tokens tx + 16 j), run the online softmax with each row spread over the
 // 16 lanes of its ty, and add P V as 4 rows x (D / 16) dims.  Everything is
-// fp32; bf16 operands are widened exactly as they are staged.
+// fp32.
 #include "prefill.cuh"
 
 namespace npk {
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
   PrefillWalk w;
   w.start(p, blockIdx.x);
   while (w.next(p)) {
-    // ---- q of the unit: row = token * G + head, widened; rows past the chunk are zero
+    // ---- q of the unit: row = token * G + head; rows past the chunk are zero
     const int tok0 = w.m * p.tile_tokens;
     __syncthreads();
     for (int e = threadIdx.x; e < kSimtRows * (D / V); e += kSimtThreads) {
@@ -234,9 +234,9 @@ template <typename T, int D>
 static np_status launch_simt(const PrefillParams& p, cudaStream_t s) {
   constexpr size_t bytes = SimtSmem<T, D>::bytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)bytes) != cudaSuccess)
-    return NP_ERR_CUDA;
+  static unsigned long long allowed = 0;
+  const np_status rc = allow_smem(prefill_simt_kernel<T, D>, bytes, &allowed);
+  if (rc != NP_OK) return rc;
   return launch_dependent(prefill_simt_kernel<T, D>, p.ctas, 1, kSimtThreads, bytes, s, p);
 }
 
@@ -252,8 +252,8 @@ static np_status launch_simt_dim(const PrefillParams& p, cudaStream_t s) {
   return NP_ERR_UNSUPPORTED;
 }
 
-np_status launch_prefill_simt(const PrefillParams& p, np_dtype dtype, cudaStream_t s) {
-  return dtype == NP_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);
+np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s) {
+  return launch_simt_dim<float>(p, s);
 }
 
 }  // namespace npk

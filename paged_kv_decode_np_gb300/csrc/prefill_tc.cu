@@ -13,8 +13,9 @@
 // the tensor cores work on one while the other's softmax runs:
 //     ... PV_0(j), S_0(j+1) | PV_1(j), S_1(j+1) ...
 // and the two share every K and V tile, 128 operations a byte of it in
-// shared memory.  head_dim 256 has tensor memory for one O only (256
-// columns): S is double-buffered instead, S(j+1) running under softmax j.
+// shared memory.  A unit of one tile (a row with few tokens; always at
+// head_dim 256, whose O takes 256 of the 512 columns) uses both S buffers for
+// it: S(j+1) runs under softmax j.
 //
 // The running maximum is replaced only where it would grow by more than 2^8
 // (m need not be the maximum, only near it: p <= 256 keeps its relative
@@ -62,9 +63,12 @@ template <int D>
 struct TcBars {
   static constexpr int NS = TcCfg<D>::NS;
   static constexpr int q_full = 0, q_empty = 1, kv_full = 2, kv_empty = 2 + NS;
-  static constexpr int s_full = 2 + 2 * NS, p_full = s_full + 2, o_full = p_full + 2;
-  static constexpr int pv_done = o_full + 1;  // MT == 1: one phase a kv tile
-  static constexpr int drain = o_full + 2, tail_full = drain + 1, count = tail_full + 1;
+  // of an S buffer: 0 and 1 by their q tiles, 2 buffer 1 lent to q tile 0.  A
+  // warp waits on all phases of a barrier or on none: one that skips some
+  // could take an earlier phase of the same parity for its own.
+  static constexpr int s_full = 2 + 2 * NS, p_full = s_full + 3, o_full = p_full + 3;
+  static constexpr int pv_done = o_full + 2;  // one-tile units: one phase a kv tile
+  static constexpr int drain = pv_done + 1, tail_full = drain + 1, count = tail_full + 1;
 };
 
 // kv tiles of the current segment that q tile t sees, from kv0 on
@@ -75,6 +79,12 @@ __device__ __forceinline__ int tc_tiles(const PrefillParams& p, const PrefillWal
   const int nk = prefill_kv_tiles(p, w.g, first + p.tile_tokens);
   const int end = nk < w.kv1 ? nk : w.kv1;
   return end > w.kv0 ? end - w.kv0 : 0;
+}
+
+// The current segment's unit has one q tile with tokens.
+template <int D>
+__device__ __forceinline__ bool tc_single(const PrefillParams& p, const PrefillWalk& w) {
+  return TcCfg<D>::MT == 1 || ((int64_t)w.m * TcCfg<D>::MT + 1) * p.tile_tokens >= w.g.n;
 }
 
 struct RingPos {
@@ -110,7 +120,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i)
-      mbar_init(bar(i), i >= B::p_full && i < B::p_full + 2 ? 4 : 1);
+      mbar_init(bar(i), i >= B::p_full && i < B::p_full + 3 ? 4 : 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -134,26 +144,35 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const uint32_t o_at = lanes + C::O0 + t * D;
     const int tt = row / p.group, h = row - tt * p.group;
     constexpr int OC = D < 32 ? 16 : 32;             // columns of O at a time
-    uint32_t it = 0, oc = 0;
+    uint32_t used = 0, lent = 0;  // S tiles so far in the tile's own buffer; in the lent one
+    uint32_t pv = 0, oc = 0;      // phases of pv_done; of this tile's o_full
     while (ok && w.next(p)) {
       const int64_t first = ((int64_t)w.m * MT + t) * p.tile_tokens;
       if (first >= w.g.n) {  // no tokens in this tile
         w.advance();
         continue;
       }
+      const bool single = tc_single<D>(p, w);
       const int n = tc_tiles<D>(p, w, t);
       const int64_t tok = first + tt;
       const bool live = tt < p.tile_tokens && tok < w.g.n;
+      const bool idle = !__any_sync(FULL, live);  // none of the warp's rows is stored
       // the last position the row sees; rows that are not stored need no mask
       const int lim = live ? (int)((int64_t)w.g.c - w.g.n + tok) : INT_MAX;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t buf = MT == 2 ? (uint32_t)t : (it & 1u);
-        const uint32_t phase = MT == 2 ? (it & 1u) : ((it >> 1) & 1u);
-        ok = __all_sync(FULL, mbar_wait(bar(B::s_full + buf), phase, abort));
+      for (int j = 0; j < n; ++j) {
+        const bool alt = single && (j & 1);  // in the lent buffer
+        const int sb = alt ? 2 : t;          // barrier index
+        ok = __all_sync(FULL, mbar_wait(bar(B::s_full + sb), (alt ? lent : used) & 1u, abort));
         if (!ok) break;
+        if (alt) ++lent;
+        else ++used;
+        if (idle) {  // P of these rows is whatever S left: it moves their own O only
+          if (lane == 0) mbar_arrive(bar(B::p_full + sb));
+          continue;
+        }
         tmem_fence_after();
-        const uint32_t s_at = lanes + buf * BN;
+        const uint32_t s_at = lanes + (alt ? 1 : t) * BN;
         const int rel = lim - (w.kv0 + j) * BN;  // last visible column
         const bool masked = __any_sync(FULL, rel < BN - 1);
         // The row's maximum, 32 columns at a time: S is read from tensor memory
@@ -192,8 +211,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           if (j > 0) {
             // PV(j - 1) must be complete.  With two q tiles it is: S(j) was
             // issued after it.  With one, S(j) was issued before it.
-            if constexpr (MT == 1) {
-              ok = __all_sync(FULL, mbar_wait(bar(B::pv_done), (it - 1) & 1u, abort));
+            if (single) {
+              ok = __all_sync(FULL, mbar_wait(bar(B::pv_done), (pv + (uint32_t)j - 1u) & 1u, abort));
               if (!ok) break;
               tmem_fence_after();
             }
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B::p_full + buf));
+        if (lane == 0) mbar_arrive(bar(B::p_full + sb));
       }
       if (!ok) break;
       if (n > 0) {
@@ -251,6 +270,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         if (!ok) break;
         ++oc;
         tmem_fence_after();
+      }
+      if (single) pv += (uint32_t)n;
+      if (idle) {
+        tmem_fence_before();
+        w.advance();
+        continue;
       }
       // ---- the row's result: out, or this block's partial of a cut unit
       const bool whole = w.whole();
@@ -406,15 +431,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
     while (ok && w.next(p)) {
       int32_t ahead = TILED ? look_up(w.kv0) : 0;
+      const bool single = tc_single<D>(p, w);
       if (!isv) {
         // ---- q
         if (seg > 0) {
           ok = __all_sync(FULL, mbar_wait(bar(B::q_empty), (seg - 1) & 1u, abort));
           if (!ok) break;
         }
-        int qt = 0;
-        for (int t = 0; t < MT; ++t)
-          if (((int64_t)w.m * MT + t) * p.tile_tokens < w.g.n) ++qt;
+        const int qt = single ? 1 : 2;
         if constexpr (TILED) {
           if (lane == 0)
             mbar_arrive_expect_tx(bar(B::q_full), (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
@@ -450,7 +474,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const int32_t at = ahead;
         if (TILED && j + 1 < n) ahead = look_up(w.kv0 + j + 1);
         uint32_t seq;
-        if (MT == 2) seq = 2u * j + (isv ? 1u : 0u);
+        if (!single) seq = 2u * j + (isv ? 1u : 0u);
         else if (isv) seq = j + 1 < n ? 2u * j + 2u : 2u * n - 1u;
         else seq = j == 0 ? 0u : 2u * j - 1u;
         load_tile(w.kv0 + j, seq0 + seq, at);
@@ -466,133 +490,126 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     if (*abort) {  // never leave copies in flight (bounded)
       if constexpr (TILED) {
         if (!isv && seg > 0) mbar_wait_drain(bar(B::q_full), (seg - 1) & 1u);
-        // this warp's tiles among the last NS positions; the others' phases are
-        // as good: an earlier phase of a slot is complete
+        // the last NS positions up to this warp's last tile: those of the other
+        // warp's that never came run into the wait's limit
         for (int64_t q = last > NS ? last - NS : 0; q <= last; ++q)
-          if (MT == 1 || (q & 1) == (isv ? 1 : 0))
-            mbar_wait_drain(bar(B::kv_full + (int)(q % NS)), (uint32_t)(q / NS) & 1u);
+          mbar_wait_drain(bar(B::kv_full + (int)(q % NS)), (uint32_t)(q / NS) & 1u);
       } else {
         cp_async_wait<0>();
       }
     }
   } else if (warp == ISSUER) {
     // ================================================================= mma
-    // One thread runs the whole role.
-    if (lane == 0) {
-      constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
-      constexpr uint32_t HI = umma_desc_hi(1024);
-      const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
-      RingPos pos{0, 0};
-      uint32_t seg = 0;
-      uint32_t done0 = 0, done1 = 0;  // MT == 2: P tiles taken of each q tile so far
-      uint32_t it = 0;                // MT == 1: tiles so far
+    // The whole warp runs the role, its lanes alike; one of them issues.
+    constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
+    constexpr uint32_t HI = umma_desc_hi(1024);
+    const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
+    RingPos pos{0, 0};
+    uint32_t seg = 0;
+    uint32_t done0 = 0, done1 = 0, done2 = 0;  // phases of each p_full so far
 
-      auto wait = [&](int b, uint32_t phase) {
-        ok = ok && mbar_wait(bar(b), phase, abort);
-        return ok;
-      };
-      auto issue_s = [&](int t, uint32_t buf, int slot) {  // S_buf = Q_t K^T
-        const uint32_t q = umma_desc_lo(base + (uint32_t)t * C::QT, 16);
-        const uint32_t k = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 16);
+    auto wait = [&](int b, uint32_t phase) {
+      ok = ok && __all_sync(FULL, mbar_wait(bar(b), phase, abort));
+      return ok;
+    };
+    // S = Q_t K^T into buffer sb (2: buffer 1, lent)
+    auto issue_s = [&](int t, int sb, int slot) {
+      const uint32_t d = tmem + (sb ? BN : 0);
+      const uint32_t q = umma_desc_lo(base + (uint32_t)t * C::QT, 16);
+      const uint32_t k = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 16);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_ss(tmem + buf * BN, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u,
-                  k + ((ks >> 2) * (BN * 128u) + (ks & 3) * 32u) / 16u, HI, QK, ks > 0);
-        umma_commit(bar(B::s_full + buf));
-      };
-      auto issue_pv = [&](int t, uint32_t buf, int slot, bool acc) {  // O_t += P_buf V
-        tmem_fence_after();
-        const uint32_t v = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, BN * 128);
+      for (int ks = 0; ks < D / 16; ++ks)
+        umma_ss(d, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u,
+                k + ((ks >> 2) * (BN * 128u) + (ks & 3) * 32u) / 16u, HI, QK, ks > 0);
+      umma_commit(bar(B::s_full + sb));
+    };
+    auto issue_pv = [&](int t, int sb, int slot, bool acc) {  // O_t += P V
+      tmem_fence_after();
+      const uint32_t pa = tmem + (sb ? BN : 0);
+      const uint32_t v = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, BN * 128);
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          umma_ts(tmem + C::O0 + t * D, tmem + buf * BN + ks * 8, v + ks * 128u, HI, PV,
-                  ks > 0 ? 1u : (acc ? 1u : 0u));
-      };
+      for (int ks = 0; ks < BN / 16; ++ks)
+        umma_ts(tmem + C::O0 + t * D, pa + ks * 8, v + ks * 128u, HI, PV,
+                ks > 0 ? 1u : (acc ? 1u : 0u));
+    };
 
-      while (ok && w.next(p)) {
-        const int n = w.kv1 - w.kv0;
-        if (!wait(B::q_full, seg & 1u)) break;
-        ++seg;
-        if constexpr (MT == 2) {
-          // n == max(n0, n1): the unit's last tokens see the most
-          const int n0 = tc_tiles<D>(p, w, 0), n1 = tc_tiles<D>(p, w, 1);
-          int kslot = pos.slot;
-          if (!wait(B::kv_full + kslot, pos.phase)) break;
+    while (ok && w.next(p)) {
+      const int n = w.kv1 - w.kv0;
+      if (!wait(B::q_full, seg & 1u)) break;
+      ++seg;
+      if (!tc_single<D>(p, w)) {
+        const int n0 = tc_tiles<D>(p, w, 0);  // <= n: the unit's last tokens see the most
+        int kslot = pos.slot;
+        if (!wait(B::kv_full + kslot, pos.phase)) break;
+        pos.template step<NS>();
+        if (n0 > 0) issue_s(0, 0, kslot);
+        issue_s(1, 1, kslot);
+        umma_commit(bar(B::kv_empty + kslot));
+        if (n == 1) umma_commit(bar(B::q_empty));
+        for (int j = 0; j < n; ++j) {
+          const int vslot = pos.slot;
+          const uint32_t vphase = pos.phase;
           pos.template step<NS>();
-          if (n0 > 0) issue_s(0, 0, kslot);
-          if (n1 > 0) issue_s(1, 1, kslot);
-          umma_commit(bar(B::kv_empty + kslot));
-          if (n == 1) umma_commit(bar(B::q_empty));
-          for (int j = 0; j < n; ++j) {
-            const int vslot = pos.slot;
-            const uint32_t vphase = pos.phase;
-            pos.template step<NS>();
-            kslot = pos.slot;
-            const uint32_t kphase = pos.phase;
-            if (j + 1 < n) pos.template step<NS>();
-            bool have_k = false;
-            if (j < n0) {
-              if (!wait(B::p_full, done0 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
-              ++done0;
-              issue_pv(0, 0, vslot, j > 0);
-              if (j >= n1) umma_commit(bar(B::kv_empty + vslot));  // no other reader of V
-              if (j + 1 < n0) {
-                if (!wait(B::kv_full + kslot, kphase)) break;
-                have_k = true;
-                issue_s(0, 0, kslot);
-                if (j + 1 >= n1) {
-                  umma_commit(bar(B::kv_empty + kslot));
-                  if (j + 2 == n) umma_commit(bar(B::q_empty));
-                }
-              } else {
-                umma_commit(bar(B::o_full));
-              }
-            }
-            if (j < n1) {
-              if (!wait(B::p_full + 1, done1 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
-              ++done1;
-              issue_pv(1, 1, vslot, j > 0);
-              umma_commit(bar(B::kv_empty + vslot));
-              if (j + 1 < n1) {
-                if (!have_k && !wait(B::kv_full + kslot, kphase)) break;
-                issue_s(1, 1, kslot);
-                umma_commit(bar(B::kv_empty + kslot));
-                if (j + 2 == n) umma_commit(bar(B::q_empty));
-              } else {
-                umma_commit(bar(B::o_full + 1));
-              }
+          kslot = pos.slot;
+          const uint32_t kphase = pos.phase;
+          if (j + 1 < n) pos.template step<NS>();
+          bool have_k = false;
+          if (j < n0) {
+            if (!wait(B::p_full, done0 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
+            ++done0;
+            issue_pv(0, 0, vslot, j > 0);
+            if (j + 1 < n0) {
+              if (!wait(B::kv_full + kslot, kphase)) break;
+              have_k = true;
+              issue_s(0, 0, kslot);
+            } else {
+              umma_commit(bar(B::o_full));
             }
           }
-        } else {
-          for (int j = -1; j < n; ++j) {
-            if (j + 1 < n) {  // S(j + 1), into the buffer that P(j - 1) has left
-              const int slot = pos.slot;
-              if (!wait(B::kv_full + slot, pos.phase)) break;
-              pos.template step<NS>();
-              issue_s(0, (it + (j >= 0 ? 1u : 0u)) & 1u, slot);
-              umma_commit(bar(B::kv_empty + slot));
-              if (j + 2 == n) umma_commit(bar(B::q_empty));
-            }
-            if (j >= 0) {  // O += P(j) V(j)
-              const uint32_t buf = it & 1u;
-              const int slot = pos.slot;
-              const uint32_t phase = pos.phase;
-              pos.template step<NS>();
-              if (!wait(B::p_full + buf, (it >> 1) & 1u) || !wait(B::kv_full + slot, phase)) break;
-              ++it;
-              issue_pv(0, buf, slot, j > 0);
-              umma_commit(bar(B::pv_done));
-              umma_commit(bar(B::kv_empty + slot));
-              if (j + 1 == n) umma_commit(bar(B::o_full));
-            }
+          if (!wait(B::p_full + 1, done1 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
+          ++done1;
+          issue_pv(1, 1, vslot, j > 0);
+          umma_commit(bar(B::kv_empty + vslot));
+          if (j + 1 < n) {
+            if (!have_k && !wait(B::kv_full + kslot, kphase)) break;
+            issue_s(1, 1, kslot);
+            umma_commit(bar(B::kv_empty + kslot));
+            if (j + 2 == n) umma_commit(bar(B::q_empty));
+          } else {
+            umma_commit(bar(B::o_full + 1));
           }
         }
-        w.advance();
+      } else {
+        for (int j = -1; j < n; ++j) {
+          if (j + 1 < n) {  // S(j + 1), into the buffer that P(j - 1) has left
+            const int slot = pos.slot;
+            if (!wait(B::kv_full + slot, pos.phase)) break;
+            pos.template step<NS>();
+            issue_s(0, (j + 1) & 1 ? 2 : 0, slot);
+            umma_commit(bar(B::kv_empty + slot));
+            if (j + 2 == n) umma_commit(bar(B::q_empty));
+          }
+          if (j >= 0) {  // O += P(j) V(j)
+            const int slot = pos.slot;
+            const uint32_t phase = pos.phase;
+            pos.template step<NS>();
+            if (!wait(B::p_full + (j & 1 ? 2 : 0), (j & 1 ? done2 : done0) & 1u) ||
+                !wait(B::kv_full + slot, phase))
+              break;
+            if (j & 1) ++done2;
+            else ++done0;
+            issue_pv(0, j & 1 ? 2 : 0, slot, j > 0);
+            umma_commit(bar(B::pv_done));
+            umma_commit(bar(B::kv_empty + slot));
+            if (j + 1 == n) umma_commit(bar(B::o_full));
+          }
+        }
       }
-      // nothing of this block is left running in the tensor cores (bounded)
-      umma_commit(bar(B::drain));
-      mbar_wait_drain(bar(B::drain), 0u);
+      w.advance();
     }
+    // nothing of this block is left running in the tensor cores (bounded)
+    umma_commit(bar(B::drain));
+    mbar_wait_drain(bar(B::drain), 0u);
     __syncwarp();
   }
   if (!ok && lane == 0) set_flag(p.err, NP_FLAG_TIMEOUT);
@@ -607,9 +624,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
 template <int D, bool TILED>
 static np_status launch(const PrefillParams& p, cudaStream_t s) {
-  if (cudaFuncSetAttribute(prefill_tc_kernel<D, TILED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           TcCfg<D>::SMEM) != cudaSuccess)
-    return NP_ERR_CUDA;
+  static unsigned long long allowed = 0;
+  const np_status rc = allow_smem(prefill_tc_kernel<D, TILED>, TcCfg<D>::SMEM, &allowed);
+  if (rc != NP_OK) return rc;
   return launch_dependent(prefill_tc_kernel<D, TILED>, p.ctas, 1, TcCfg<D>::THREADS, TcCfg<D>::SMEM, s,
                           p);
 }

@@ -364,3 +364,13 @@ extern "C" np_status np_rope_append(
   return dtype == NP_BF16 ? npk::launch_rope_dim<__nv_bfloat16>(p, head_dim, st)
                           : npk::launch_rope_dim<float>(p, head_dim, st);
 }
+
+extern "C" np_status np_rope_append_packed(const np_rope_append_args* a) {
+  if (!a) return NP_ERR_INVALID_ARG;
+  return np_rope_append(a->q_out, a->q, a->k_new, a->v_new, a->q_stride, a->k_stride, a->v_stride,
+                        a->slot_mapping, a->k_pool, a->v_pool, static_cast<np_dtype>(a->dtype),
+                        a->num_blocks, a->block_size, a->q_heads, a->kv_heads, a->head_dim, a->cos_sin,
+                        a->max_positions, a->rot_dim, a->positions, a->num_axes,
+                        a->has_sections ? a->sections : nullptr, a->interleaved, a->q_weight,
+                        a->k_weight, a->eps, a->num_tokens, a->err_word, a->stream);
+}

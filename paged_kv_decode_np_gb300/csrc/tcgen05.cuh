@@ -113,14 +113,21 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn, 
 }
 
 // ----------------------------------------------------------------- mma ----
-// D (tensor memory) = A B (+ D where acc); one thread issues.  hi: both
-// operands' (they have the same stride).
+// The calls below are made by a whole converged warp whose lanes hold the same
+// operands; one elected lane issues.  (The election is part of each: where a
+// branch on a lane's predicate guards them instead, their operands go from
+// vector to uniform registers one by one, about 100 cycles an mma; and where
+// that predicate was an earlier election's, kept in a register, small guarded
+// blocks faulted.)
+
+// D (tensor memory) = A B (+ D where acc).  hi: both operands' (they have the
+// same stride).
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                         uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -129,17 +136,19 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
                                         uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
-// One arrival on `bar` once every mma this thread has issued is complete.
+// One arrival on `bar` once every mma issued by the warp so far is complete.
+// (The elected lane of a converged warp is the same each time.)
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 

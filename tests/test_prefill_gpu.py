@@ -145,6 +145,16 @@ def test_one_token_rows_match_the_decode_read(nplib, dtype, d):
     assert ((out.double() - dec.double()).abs() <= 2 * tol).all()
 
 
+@pytest.mark.parametrize("dtype,d,g", [(BF, 128, 4), (BF, 64, 1), (BF, 16, 8), (BF, 256, 4), (F32, 64, 2)])
+def test_mixed_batches(nplib, dtype, d, g):
+    """Many one-token rows among chunks: a block passes again and again from units of one tile to
+    units of two, a dozen kv tiles each."""
+    rnd = random.Random(d)
+    rows = [(1, rnd.randint(200, 2500)) for _ in range(40)] + [(300, 1500), (513, 800), (300, 300)]
+    rnd.shuffle(rows)
+    _check(nplib, dtype, d, 8, g, 16, rows, seed=d + g)
+
+
 def test_no_rows_and_no_tokens(nplib):
     inp = chunk_inputs(BF, 64, 1, 2, 16, [(4, 4)])
     out = torch.full_like(inp["q"], 5.0)

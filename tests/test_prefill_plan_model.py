@@ -1,6 +1,6 @@
 """The prompt attention's division of work, on the CPU: a line-by-line Python
-model of the plan kernel's arithmetic (prefix sums of kv tiles in closed form,
-equal shares, ends moved to unit starts, the list of cut units) and of the
+model of the plan kernel's arithmetic (prefix sums of kv tiles in closed form and
+a fixed cost per unit, equal shares, ends moved to unit starts, the list of cut units) and of the
 blocks' walk, against brute force over random chunks and contexts: every kv
 tile of every unit is read exactly once, every cut unit is named once with all
 the blocks that hold its pieces, and every other unit lies whole in one block.
@@ -45,76 +45,68 @@ def row_prefix(n, c, U, bn, units, k):
     return z + floor_sum(k - z, bn, U, base + (z + 1) * U + bn - 1) + last
 
 
-def plan(rows, heads, U, bn, ctas, min_tiles):
-    """rows: [(n, c)]; returns (pos, length, cuts) per block."""
+def plan(rows, heads, U, bn, ctas, unit_cost, min_share):
+    """rows: [(n, c)]; returns where each block's share begins (and the end), and the cut units."""
     pre = [0]
     for n, c in rows:
         u = units_of(n, U)
-        pre.append(pre[-1] + row_prefix(n, c, U, bn, u, u) * heads)
+        pre.append(pre[-1] + (row_prefix(n, c, U, bn, u, u) + u * unit_cost) * heads)
     W = pre[-1]
-    pe = min(ctas, max(1, -(-W // min_tiles)))
-    at, unit_end, pos = [], [], []
+    pe = min(ctas, max(1, -(-W // min_share)))
+    pos = []
     for b in range(ctas + 1):
         share = W // pe
-        t = W if b >= pe else share * b + (W % pe) * b // pe
-        q, end = (len(rows), 0, 0, 0), W
-        if t < W:
+        x = W if b >= pe else share * b + (W % pe) * b // pe
+        q = (len(rows), 0, 0, 0)
+        if x < W:
             lo, hi = 0, len(rows)
             while hi - lo > 1:
                 mid = (lo + hi) // 2
-                if pre[mid] <= t:
+                if pre[mid] <= x:
                     lo = mid
                 else:
                     hi = mid
             n, c = rows[lo]
             u = units_of(n, U)
             wh = (pre[lo + 1] - pre[lo]) // heads
-            rem = t - pre[lo]
-            kvh, inn = rem // wh, rem % wh
+            kvh = (x - pre[lo]) // wh
+            inn = (x - pre[lo]) - kvh * wh
             a, e = 0, u
             while e - a > 1:
                 mid = (a + e) // 2
-                if row_prefix(n, c, U, bn, u, mid) <= inn:
+                if row_prefix(n, c, U, bn, u, mid) + mid * unit_cost <= inn:
                     a = mid
                 else:
                     e = mid
-            s0 = row_prefix(n, c, U, bn, u, a)
-            s1 = row_prefix(n, c, U, bn, u, a + 1)
-            ustart = t - (inn - s0)
-            end = ustart + s1 - s0
-            off = inn - s0
-            if off > 0 and off * 16 <= share:
-                t, off = ustart, 0
-            elif off > 0 and (end - t) * 16 <= share:
-                t, off = end, 0
-                r2, k2, a2 = lo, kvh, a + 1
-                if a2 >= u:
-                    a2, k2 = 0, k2 + 1
-                    if k2 >= heads:
-                        k2, r2 = 0, r2 + 1
-                q, end = (r2, k2, a2, 0), t
-            if q[0] == len(rows) and t < W:
-                q = (lo, kvh, a, off)
-        at.append(t)
-        unit_end.append(end)
+            s0 = row_prefix(n, c, U, bn, u, a) + a * unit_cost
+            nk = kv_tiles(n, c, bn, (a + 1) * U)
+            off = inn - s0 - unit_cost
+            if off <= 0 or off * 16 <= share:
+                off = 0
+            elif (nk - off) * 16 <= share:
+                off, a = 0, a + 1
+                if a >= u:
+                    a, kvh = 0, kvh + 1
+                    if kvh >= heads:
+                        kvh, lo = 0, lo + 1
+            q = (lo, kvh, a, off)
         pos.append(q)
     cuts = []
     for b in range(ctas):
-        cut = None
-        e = pos[b + 1]
-        if at[b + 1] > at[b] and at[b + 1] < W and e[3] > 0 and at[b + 1] - e[3] >= at[b]:
+        cut, s, e = None, pos[b], pos[b + 1]
+        if e[3] > 0 and (s[:3] != e[:3] or s[3] == 0):
             last = b + 1
-            while last + 1 < ctas and at[last + 1] < unit_end[b + 1]:
+            while last + 1 <= ctas and pos[last + 1][:3] == e[:3]:
                 last += 1
             cut = (e[0], e[1], e[2], last)
         cuts.append(cut)
-    return pos[:ctas], [at[b + 1] - at[b] for b in range(ctas)], cuts
+    return pos, cuts
 
 
-def walk(rows, heads, U, bn, pos, left):
+def walk(rows, heads, U, bn, pos, end):
     """The segments (row, head, unit, kv0, kv1, nk) of one block."""
     r, kvh, m, off = pos
-    while left > 0:
+    while r < len(rows):
         u = units_of(rows[r][0], U)
         while m >= u:
             m = 0
@@ -123,22 +115,24 @@ def walk(rows, heads, U, bn, pos, left):
                 break
             kvh = 0
             r += 1
-            assert r < len(rows)
+            if r >= len(rows):
+                return
             u = units_of(rows[r][0], U)
+        last = (r, kvh, m) == end[:3]
+        if off >= end[3] if last else (r, kvh, m) > end[:3]:
+            return
         nk = kv_tiles(*rows[r], bn, (m + 1) * U)
-        kv1 = off + left if left < nk - off else nk
-        yield r, kvh, m, off, kv1, nk
-        left -= kv1 - off
+        yield r, kvh, m, off, end[3] if last else nk, nk
         off = 0
         m += 1
 
 
-def check(rows, heads, U, bn, ctas, min_tiles):
-    pos, length, cuts = plan(rows, heads, U, bn, ctas, min_tiles)
-    assert all(x >= 0 for x in length)
+def check(rows, heads, U, bn, ctas, unit_cost, min_share):
+    pos, cuts = plan(rows, heads, U, bn, ctas, unit_cost, min_share)
+    assert all(x <= y for x, y in zip(pos, pos[1:]))
     pieces = {}
     for b in range(ctas):
-        segs = list(walk(rows, heads, U, bn, pos[b], length[b]))
+        segs = list(walk(rows, heads, U, bn, pos[b], pos[b + 1]))
         # a block cuts at most its first and its last unit: one slot each
         slots = [0 if kv0 > 0 else 1 for _, _, _, kv0, kv1, nk in segs if kv0 > 0 or kv1 < nk]
         assert len(slots) == len(set(slots))
@@ -174,7 +168,7 @@ def test_shares_cover_every_tile_once(seed):
             c = rnd.choice([n, n, rnd.randint(0, 3 * n + 1), n + rnd.randint(0, 9000)])
             rows.append((n, c))
         check(rows, rnd.choice([1, 2, 3, 8]), tile // G * mt, bn, rnd.choice([1, 4, 148, 152, 160]),
-              rnd.choice([1, 2, 4, 7]))
+              rnd.choice([0, 1, 2, 5]), rnd.choice([1, 2, 4, 7]))
 
 
 def test_prefix_in_closed_form():
