@@ -233,8 +233,9 @@ np_status np_rope_append_packed(const np_rope_append_args* args);
  * hold.  Supported: the dtypes, head_dims and groups of the list above; up
  * to 4096 rows; any block_size; tables of up to 2^31 - 257 tokens.
  * out must not overlap q or the pools.  rows or num_tokens 0: a no-op.
- * Three launches (plan, attention, join) on `stream`; results are
- * deterministic.
+ * Three launches (plan, attention, join) on `stream`.  The same call gives
+ * the same bits; a row's last bits depend on the other rows' lengths, which
+ * decide where its work is cut between thread blocks.
  */
 size_t np_paged_prefill_workspace_bytes(int32_t head_dim);
 /* enough for every head_dim */

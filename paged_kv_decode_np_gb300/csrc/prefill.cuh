@@ -9,7 +9,7 @@
 // tokens: nk(m) = max(1, ceil((c - n + min(n, (m + 1) U)) / BN)) tiles.
 //
 // All units, in the order (row, kv head, m), are laid end to end as one
-// stream, nk(m) kv tiles and a fixed cost each, and the stream is cut into one
+// stream, a cost per kv tile and a fixed cost each, and the stream is cut into one
 // equal share per thread block: every SM has the same amount of work whatever
 // the mix of long and short chunks, causal triangles and histories.  A block walks its share; a
 // unit that lies inside one block is normalised and stored directly, a unit
@@ -54,8 +54,9 @@ struct PrefillParams {
   int32_t tile_rows;    // BMT
   int32_t tiles;        // MT
   int32_t bn;           // kv tile
-  int32_t unit_cost;    // what beginning a unit costs a block, in kv tiles
-  int32_t min_share;    // least share a block is given, in kv tiles
+  // what the plan counts: for a kv tile of a unit whose tiles all have tokens,
+  // of one with a single such tile, for beginning a unit; the least share of a block
+  int32_t full_cost, single_cost, unit_cost, min_share;
   int32_t box_tokens;   // tokens per tiled copy
   float qscale;         // |scale| * log2(e)
   int32_t negate;       // scale < 0

@@ -58,15 +58,16 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   return fn;
 }
 
-// A bf16 tensor (dims innermost first, byte strides of dims 1 and 2), copied in
-// boxes of 64 x box1 x box2 in the 128-byte swizzle.
-bool encode_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3],
-                const cuuint64_t (&strides)[2], cuuint32_t box1, cuuint32_t box2) {
+// A bf16 tensor of N dims (innermost first, byte strides of dims 1 ..), copied
+// in the given box in the 128-byte swizzle.
+template <int N>
+bool encode_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[N],
+                const cuuint64_t (&strides)[N - 1], const cuuint32_t (&box)[N]) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
   if (!enc) return false;
-  const cuuint32_t box[3] = {64u, box1, box2};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint32_t estr[N];
+  for (int i = 0; i < N; ++i) estr[i] = 1u;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -80,8 +81,10 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   p.tile_rows = 128;
   p.bn = d == 256 ? 64 : 128;
   p.tile_tokens = p.tile_rows / p.group;
-  p.unit_cost = 2;
-  p.min_share = 4;
+  p.full_cost = d == 256 ? 1 : 3;
+  p.single_cost = d == 256 ? 1 : 2;
+  p.unit_cost = d == 256 ? 2 : 8;
+  p.min_share = d == 256 ? 4 : 8;
   // Tiled copies: boxes of whole 8-row swizzle atoms inside one block, slot
   // coordinates in int32.  box_tokens: the largest power of two that divides
   // the block size, at most a kv tile.
@@ -90,15 +93,18 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   p.box_tokens = bt;
   bool tiled = d >= 64 && bt >= 8 && slots <= INT32_MAX;
   if (tiled) {
-    const cuuint64_t row = (cuuint64_t)p.kv_heads * d * 2, qrow = (cuuint64_t)p.q_heads * d * 2;
-    const cuuint64_t kv_dims[3] = {(cuuint64_t)d, (cuuint64_t)slots, (cuuint64_t)p.kv_heads};
-    const cuuint64_t kv_strides[2] = {row, (cuuint64_t)d * 2};
+    const cuuint64_t row = (cuuint64_t)p.kv_heads * d * 2, head = (cuuint64_t)d * 2;
+    const cuuint32_t slabs = (cuuint32_t)d / 64;
+    // 64 dims, token of 8, slab, group of 8 tokens, kv head
+    const cuuint64_t kv_dims[5] = {64u, 8u, slabs, (cuuint64_t)slots / 8, (cuuint64_t)p.kv_heads};
+    const cuuint64_t kv_strides[4] = {row, 128u, 8 * row, head};
+    const cuuint32_t kv_box[5] = {64u, 8u, slabs, (cuuint32_t)bt / 8, 1u};
     const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)p.q_heads, (cuuint64_t)p.tokens};
-    const cuuint64_t q_strides[2] = {(cuuint64_t)d * 2, qrow};
-    tiled = encode_map(&p.tm_k, p.k_pool, kv_dims, kv_strides, (cuuint32_t)bt, 1u) &&
-            encode_map(&p.tm_v, p.v_pool, kv_dims, kv_strides, (cuuint32_t)bt, 1u) &&
-            encode_map(&p.tm_q, p.q, q_dims, q_strides, (cuuint32_t)p.group,
-                       (cuuint32_t)p.tile_tokens);
+    const cuuint64_t q_strides[2] = {head, (cuuint64_t)p.q_heads * head};
+    const cuuint32_t q_box[3] = {64u, (cuuint32_t)p.group, (cuuint32_t)p.tile_tokens};
+    tiled = encode_map(&p.tm_k, p.k_pool, kv_dims, kv_strides, kv_box) &&
+            encode_map(&p.tm_v, p.v_pool, kv_dims, kv_strides, kv_box) &&
+            encode_map(&p.tm_q, p.q, q_dims, q_strides, q_box);
   }
   np_status rc = npk::launch_prefill_plan(p, s);
   if (rc != NP_OK) return rc;
@@ -197,6 +203,7 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
     p.tile_rows = 64;
     p.bn = 64;
     p.tile_tokens = p.tile_rows / group;
+    p.full_cost = p.single_cost = 1;
     p.unit_cost = 1;
     p.min_share = 3;
     rc = npk::launch_prefill_plan(p, st);

@@ -23,25 +23,30 @@ __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   return s;
 }
 
-// kv tiles of a row's first k units (of one kv head), k <= units
+// what a kv tile of a row's unit a costs
+__device__ __forceinline__ int prefill_tile_cost(const PrefillParams& p, const PrefillRow& g, int a) {
+  return ((int64_t)a * p.tiles + 1) * p.tile_tokens >= g.n ? p.single_cost : p.full_cost;
+}
+
+// cost of a row's first k units (of one kv head), k <= units
 __device__ int64_t prefill_row_prefix(const PrefillParams& p, const PrefillRow& g, int units, int k) {
   if (k <= 0) return 0;
   const int64_t U = (int64_t)p.tile_tokens * p.tiles;
-  int64_t last = 0;
+  int64_t cost = (int64_t)k * p.unit_cost;
   if (k == units) {  // the last unit ends with the chunk, not U tokens on
-    last = prefill_kv_tiles(p, g, g.n);
     --k;
+    cost += (int64_t)prefill_kv_tiles(p, g, g.n) * prefill_tile_cost(p, g, k);
   }
   const int64_t base = (int64_t)g.c - g.n;
   const int64_t z0 = base < 0 ? -base / U : 0;  // units that see nothing: one tile each
   const int z = z0 < k ? (int)z0 : k;
-  return z + floor_sum(k - z, p.bn, U, base + (z + 1) * U + p.bn - 1) + last;
+  return cost + (z + floor_sum(k - z, p.bn, U, base + (z + 1) * U + p.bn - 1)) * p.full_cost;
 }
 
 constexpr int kPlanThreads = 1024;
 
-// One block.  Scans the rows' work -- a unit counts its kv tiles and unit_cost
-// -- cuts the stream into equal shares and writes where each block's begins
+// One block.  Scans the rows' work (costs of kv tiles and of beginning units),
+// cuts the stream into equal shares and writes where each block's begins
 // (row, kv head, unit, kv tile), and which units the shares' ends cut.
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid_constant__
                                                                     PrefillParams p) {
@@ -60,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
     if (i < per && r < p.rows) {
       const PrefillRow g = prefill_row(p, r, true);
       const int units = prefill_units(p, g.n);
-      w[i] = (prefill_row_prefix(p, g, units, units) + (int64_t)units * p.unit_cost) * p.kv_heads;
+      w[i] = prefill_row_prefix(p, g, units, units) * p.kv_heads;
     }
     sum += w[i];
   }
@@ -114,17 +119,18 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
       int a = 0, b = units;  // the last unit that begins at or before `in`
       while (b - a > 1) {
         const int mid = (a + b) >> 1;
-        if (prefill_row_prefix(p, g, units, mid) + (int64_t)mid * p.unit_cost <= in) a = mid;
+        if (prefill_row_prefix(p, g, units, mid) <= in) a = mid;
         else b = mid;
       }
-      const int64_t s0 = prefill_row_prefix(p, g, units, a) + (int64_t)a * p.unit_cost;
+      const int64_t s0 = prefill_row_prefix(p, g, units, a);
       const int nk = prefill_kv_tiles(p, g, (int64_t)(a + 1) * p.tile_tokens * p.tiles);
-      int off = (int)(in - s0) - p.unit_cost;  // < 0: within the fixed cost
+      const int cost = prefill_tile_cost(p, g, a);
+      int off = ((int)(in - s0) - p.unit_cost) / cost;  // <= 0: within the fixed cost
       // an end that lies near a unit's own start or end is moved there: the
       // partials it saves cost more than the imbalance
-      if (off <= 0 || (int64_t)off * 16 <= share) {
+      if (off <= 0 || (int64_t)off * cost * 16 <= share) {
         off = 0;
-      } else if ((int64_t)(nk - off) * 16 <= share) {
+      } else if ((int64_t)(nk - off) * cost * 16 <= share) {
         off = 0;
         // the unit after: of this head, the next head, or the next row
         if (++a >= units) {
@@ -172,26 +178,45 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__
                                                                     PrefillParams p) {
   __shared__ float tile[32][D + 4];
+  __shared__ int piece[kPrefillMaxCtas];  // the partials, in block order
+  __shared__ int pieces;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention is complete
   const int b = blockIdx.x;
   const int4 cut = p.cuts[b];
   if (cut.x < 0) return;
+  if (threadIdx.x < 32) {
+    // a share may be empty: it begins where the next one does and left nothing
+    int n = 0;
+    for (int i0 = b; i0 <= cut.w; i0 += 32) {
+      const int i = i0 + threadIdx.x;
+      bool has = false;
+      if (i <= cut.w) {
+        const int4 s = p.plan[i], e = p.plan[i + 1];
+        has = s.x != e.x || s.y != e.y || s.z != e.z || s.w != e.w;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, has);
+      if (has) piece[n + __popc(m & ((1u << threadIdx.x) - 1u))] = i == b ? 2 * b + 1 : 2 * i;
+      n += __popc(m);
+    }
+    if (threadIdx.x == 0) pieces = n;
+  }
+  __syncthreads();
   const int bm = p.tile_rows * p.tiles;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.y * 32 + lane;  // < bm
   const size_t pf = prefill_part_floats(bm, D);
-  const float* first = p.parts + (size_t)(2 * b + 1) * pf;
-  auto part = [&](int i) { return i == b ? first : p.parts + (size_t)(2 * i) * pf; };
+  auto part = [&](int i) { return p.parts + (size_t)piece[i] * pf; };
+  const int np = pieces;
   float M = -INFINITY;
-  for (int i = b; i <= cut.w; ++i) M = fmaxf(M, part(i)[row]);
+  for (int i = 0; i < np; ++i) M = fmaxf(M, part(i)[row]);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int i = b; i <= cut.w; ++i) L = fmaf(ex2(part(i)[row] - ref), part(i)[bm + row], L);
+  for (int i = 0; i < np; ++i) L = fmaf(ex2(part(i)[row] - ref), part(i)[bm + row], L);
   const float inv = L > 0.f ? 1.f / L : 0.f;
   for (int g = warp; g < D / 4; g += kJoinThreads / 32) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = b; i <= cut.w; ++i) {
+    for (int i = 0; i < np; ++i) {
       const float* q = part(i);
       const float w = ex2(q[row] - ref);
       const float4 o = *reinterpret_cast<const float4*>(q + 2 * bm + ((size_t)g * bm + row) * 4);

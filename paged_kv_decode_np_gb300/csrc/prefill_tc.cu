@@ -24,11 +24,13 @@
 // to bf16 for its product with V (half a step of each weight); l sums the
 // unrounded p.
 //
-// K and V land in shared memory as [64-dim slab][token][128 bytes] in the
-// 128-byte swizzle, which is both K^T's K-major and V's N-major operand
-// layout.  With head_dim a multiple of 64 and block_size a multiple of 8 a
-// tiled copy moves box_tokens of a block (TILED); other shapes take 16-byte
-// asynchronous copies token by token, swizzled by hand.
+// K and V land in shared memory as [8 tokens][64-dim slab][token][128 bytes] in
+// the 128-byte swizzle, which is both K^T's K-major and V's N-major operand
+// layout: 8-token groups are SL KB apart, a group's slabs 1 KB.  With head_dim
+// a multiple of 64 and block_size a multiple of 8 one tiled copy moves
+// box_tokens of a block, all slabs (TILED: the map's dimensions are 64 dims,
+// token of 8, slab, 8-token group, kv head, in the order the box lands); other
+// shapes take 16-byte asynchronous copies token by token, swizzled by hand.
 #include <limits.h>
 
 #include "prefill.cuh"
@@ -85,6 +87,13 @@ __device__ __forceinline__ int tc_tiles(const PrefillParams& p, const PrefillWal
 template <int D>
 __device__ __forceinline__ bool tc_single(const PrefillParams& p, const PrefillWalk& w) {
   return TcCfg<D>::MT == 1 || ((int64_t)w.m * TcCfg<D>::MT + 1) * p.tile_tokens >= w.g.n;
+}
+
+// Byte of 16-byte piece `ch` of token `row` of a K or V tile.
+template <int SL>
+__device__ __forceinline__ uint32_t tc_kv_at(int row, int ch) {
+  return (uint32_t)(((row >> 3) * SL + (ch >> 3)) * 1024 + (row & 7) * 128 +
+                    (((ch & 7) ^ (row & 7)) << 4));
 }
 
 struct RingPos {
@@ -356,11 +365,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     // V rows past the context are zeroed, whatever their slots hold: 0 x NaN is
     // NaN.  (K's only make scores that are masked.)
     auto clear_tail = [&](uint32_t slot, int valid) {
-      const int from = max(valid, 0), rows = BN - from;
+      const int from = max(valid, 0);
       unsigned char* to = smem + C::RING + slot * C::SLOT;
-      for (int slab = 0; slab < SL; ++slab)
-        for (int e = lane; e < rows * 8; e += 32)
-          *reinterpret_cast<uint4*>(to + (slab * BN + from) * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+      for (int e = from * SL * 8 + lane; e < BN * SL * 8; e += 32)
+        *reinterpret_cast<uint4*>(to + tc_kv_at<SL>(e / (SL * 8), e % (SL * 8))) =
+            make_uint4(0u, 0u, 0u, 0u);
     };
     // copies kv tile kt of K or V to position `seq` of the ring; at: look_up(kt)
     auto load_tile = [&](int kt, uint32_t seq, int32_t at) {
@@ -380,13 +389,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const int nbox = valid > 0 ? (valid + bt - 1) / bt : 0;
         if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(nbox * SL * bt) * 128u);
         const CUtensorMap* map = isv ? &p.tm_v : &p.tm_k;
-        for (int i0 = 0; i0 < nbox * SL; i0 += 32) {  // item i: box i / SL, slab i % SL
-          const int i = i0 + lane;
-          const int32_t sl = __shfl_sync(FULL, at, (i / SL) & 31);
-          if (i < nbox * SL)
-            tma_load_3d_plain(dst + (uint32_t)((i % SL) * BN + (i / SL) * bt) * 128u, map,
-                              (i % SL) * 64, sl, w.kvh, fb);
-        }
+        __syncwarp();
+        for (int i = 0; i < nbox; ++i)
+          tma_load_5d_warp(dst + (uint32_t)(i * bt) * (SL * 128u), map,
+                           __shfl_sync(FULL, at, i) >> 3, w.kvh, fb);
         if (tail) {
           ok = __all_sync(FULL, mbar_wait(fb, tails & 1u, abort));
           ++tails;
@@ -414,9 +420,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const int row = r0 + i + sub;
             const int64_t sl = __shfl_sync(FULL, mine, i + sub);
             if (sl >= 0)
-              cp_async16(dst + (uint32_t)((ch >> 3) * BN + row) * 128u +
-                             (uint32_t)(((ch & 7) ^ (row & 7)) << 4),
-                         src + sl * token + ch * 16);
+              cp_async16(dst + tc_kv_at<SL>(row, ch), src + sl * token + ch * 16);
           }
         }
         if (isv && valid < BN) clear_tail(slot, valid);
@@ -443,9 +447,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           if (lane == 0)
             mbar_arrive_expect_tx(bar(B::q_full), (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
           __syncwarp();
-          if (lane < qt * SL)
-            tma_load_3d_plain(base + (uint32_t)lane * 16384u, &p.tm_q, (lane % SL) * 64, w.kvh * G,
-                              w.g.q0 + (w.m * MT + lane / SL) * p.tile_tokens, bar(B::q_full));
+          for (int i = 0; i < qt * SL; ++i)
+            tma_load_3d_warp(base + (uint32_t)i * 16384u, &p.tm_q, (i % SL) * 64, w.kvh * G,
+                             w.g.q0 + (w.m * MT + i / SL) * p.tile_tokens, bar(B::q_full));
         } else {
           constexpr int CH = D / 8;
           for (int e = lane; e < qt * 128 * CH; e += 32) {
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     // ================================================================= mma
     // The whole warp runs the role, its lanes alike; one of them issues.
     constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
-    constexpr uint32_t HI = umma_desc_hi(1024);
+    constexpr uint32_t QHI = umma_desc_hi(1024), KVHI = umma_desc_hi(SL * 1024);
     const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
     RingPos pos{0, 0};
     uint32_t seg = 0;
@@ -519,17 +523,17 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const uint32_t k = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 16);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
-        umma_ss(d, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u,
-                k + ((ks >> 2) * (BN * 128u) + (ks & 3) * 32u) / 16u, HI, QK, ks > 0);
+        umma_ss(d, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u, QHI,
+                k + ((ks >> 2) * 1024u + (ks & 3) * 32u) / 16u, KVHI, QK, ks > 0);
       umma_commit(bar(B::s_full + sb));
     };
     auto issue_pv = [&](int t, int sb, int slot, bool acc) {  // O_t += P V
       tmem_fence_after();
       const uint32_t pa = tmem + (sb ? BN : 0);
-      const uint32_t v = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, BN * 128);
+      const uint32_t v = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 1024);
 #pragma unroll
       for (int ks = 0; ks < BN / 16; ++ks)
-        umma_ts(tmem + C::O0 + t * D, pa + ks * 8, v + ks * 128u, HI, PV,
+        umma_ts(tmem + C::O0 + t * D, pa + ks * 8, v + ks * (SL * 128u), KVHI, PV,
                 ks > 0 ? 1u : (acc ? 1u : 0u));
     };
 

@@ -209,7 +209,11 @@ def test_bad_metadata_is_flagged_and_stays_in_bounds(nplib, dtype, d, bs):
     cap = clean[2]["block_tables"].shape[1] * bs
     e, out, _ = flags(lambda inp: (set_("block_tables", 2, 1)(inp), set_("context_lens", 2, cap + 1)(inp)))
     assert e == nplib.NP_FLAG_CONTEXT
-    assert torch.equal(out[:50], clean[1][:50])
+    # the other rows' values are the same sums; the shares' ends move with the batch's lengths, so
+    # each is within the tolerance of the exact value and not the same bits
+    ref, bound = chunk_reference(clean[2], rows, 0.1)
+    tol = chunk_tolerance(ref, bound, dtype, d, 200)
+    assert ((out.double() - ref).abs() <= tol)[:50].all()
     for v in (-1, 10, 10 ** 9):
         assert flags(set_("query_starts", 2, v))[0] == nplib.NP_FLAG_QUERY
     assert flags(set_("query_starts", 3, 60))[0] == nplib.NP_FLAG_QUERY

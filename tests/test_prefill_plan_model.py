@@ -32,25 +32,34 @@ def units_of(n, U):
     return -(-n // U)
 
 
-def row_prefix(n, c, U, bn, units, k):
+def tile_cost(n, T, mt, costs, a):
+    full, single, _ = costs
+    return single if (a * mt + 1) * T >= n else full
+
+
+def row_prefix(n, c, T, mt, bn, costs, units, k):
+    """Cost of a row's first k units, of mt tiles of T chunk tokens each."""
     if k <= 0:
         return 0
-    last = 0
+    U = T * mt
+    full, _, unit = costs
+    cost = k * unit
     if k == units:
-        last = kv_tiles(n, c, bn, n)
         k -= 1
+        cost += kv_tiles(n, c, bn, n) * tile_cost(n, T, mt, costs, k)
     base = c - n
     z0 = (-base) // U if base < 0 else 0
     z = min(z0, k)
-    return z + floor_sum(k - z, bn, U, base + (z + 1) * U + bn - 1) + last
+    return cost + (z + floor_sum(k - z, bn, U, base + (z + 1) * U + bn - 1)) * full
 
 
-def plan(rows, heads, U, bn, ctas, unit_cost, min_share):
+def plan(rows, heads, T, mt, bn, ctas, costs, min_share):
     """rows: [(n, c)]; returns where each block's share begins (and the end), and the cut units."""
+    U = T * mt
     pre = [0]
     for n, c in rows:
         u = units_of(n, U)
-        pre.append(pre[-1] + (row_prefix(n, c, U, bn, u, u) + u * unit_cost) * heads)
+        pre.append(pre[-1] + row_prefix(n, c, T, mt, bn, costs, u, u) * heads)
     W = pre[-1]
     pe = min(ctas, max(1, -(-W // min_share)))
     pos = []
@@ -74,16 +83,17 @@ def plan(rows, heads, U, bn, ctas, unit_cost, min_share):
             a, e = 0, u
             while e - a > 1:
                 mid = (a + e) // 2
-                if row_prefix(n, c, U, bn, u, mid) + mid * unit_cost <= inn:
+                if row_prefix(n, c, T, mt, bn, costs, u, mid) <= inn:
                     a = mid
                 else:
                     e = mid
-            s0 = row_prefix(n, c, U, bn, u, a) + a * unit_cost
+            s0 = row_prefix(n, c, T, mt, bn, costs, u, a)
+            cost = tile_cost(n, T, mt, costs, a)
             nk = kv_tiles(n, c, bn, (a + 1) * U)
-            off = inn - s0 - unit_cost
-            if off <= 0 or off * 16 <= share:
+            off = (inn - s0 - costs[2]) // cost
+            if off <= 0 or off * cost * 16 <= share:
                 off = 0
-            elif (nk - off) * 16 <= share:
+            elif (nk - off) * cost * 16 <= share:
                 off, a = 0, a + 1
                 if a >= u:
                     a, kvh = 0, kvh + 1
@@ -127,8 +137,9 @@ def walk(rows, heads, U, bn, pos, end):
         m += 1
 
 
-def check(rows, heads, U, bn, ctas, unit_cost, min_share):
-    pos, cuts = plan(rows, heads, U, bn, ctas, unit_cost, min_share)
+def check(rows, heads, T, mt, bn, ctas, costs, min_share):
+    U = T * mt
+    pos, cuts = plan(rows, heads, T, mt, bn, ctas, costs, min_share)
     assert all(x <= y for x, y in zip(pos, pos[1:]))
     pieces = {}
     for b in range(ctas):
@@ -151,8 +162,11 @@ def check(rows, heads, U, bn, ctas, unit_cost, min_share):
         if len(ps) == 1:
             assert key not in named
         else:
-            assert blocks == list(range(blocks[0], blocks[-1] + 1))
-            assert named[key] == (blocks[0], blocks[-1])
+            # the blocks from the first to the one named last, but for empty shares (which begin
+            # where the next one does: the join skips them)
+            first, last = named[key]
+            assert blocks == [b for b in range(first, last + 1) if pos[b] != pos[b + 1]]
+            assert first == blocks[0]
     assert named.keys() == {k for k, v in pieces.items() if len(v) > 1}
 
 
@@ -167,24 +181,26 @@ def test_shares_cover_every_tile_once(seed):
             n = rnd.choice([0, 1, rnd.randint(1, 40), rnd.randint(1, 2000)])
             c = rnd.choice([n, n, rnd.randint(0, 3 * n + 1), n + rnd.randint(0, 9000)])
             rows.append((n, c))
-        check(rows, rnd.choice([1, 2, 3, 8]), tile // G * mt, bn, rnd.choice([1, 4, 148, 152, 160]),
-              rnd.choice([0, 1, 2, 5]), rnd.choice([1, 2, 4, 7]))
+        check(rows, rnd.choice([1, 2, 3, 8]), tile // G, mt, bn, rnd.choice([1, 4, 148, 152, 160]),
+              rnd.choice([(1, 1, 0), (1, 1, 2), (3, 2, 4), (3, 2, 9)]), rnd.choice([1, 2, 4, 8]))
 
 
 def test_prefix_in_closed_form():
     rnd = random.Random(99)
     for _ in range(300):
-        n, U, bn = rnd.randint(1, 700), rnd.choice([8, 14, 50, 64, 85, 256]), rnd.choice([64, 128])
+        n, T, bn = rnd.randint(1, 700), rnd.choice([8, 14, 25, 42, 64, 128]), rnd.choice([64, 128])
+        mt, costs = rnd.choice([1, 2]), rnd.choice([(1, 1, 0), (3, 2, 4)])
         c = rnd.randint(0, 2 * n + 300)
-        u = units_of(n, U)
+        u = units_of(n, T * mt)
         run = 0
         for k in range(u + 1):
-            assert row_prefix(n, c, U, bn, u, k) == run
-            run += kv_tiles(n, c, bn, (k + 1) * U)
+            assert row_prefix(n, c, T, mt, bn, costs, u, k) == run
+            run += kv_tiles(n, c, bn, (k + 1) * T * mt) * tile_cost(n, T, mt, costs, k) + costs[2]
 
 
 def test_far_positions_stay_exact():
     # tiles of a 2^31-token table are counted in 64 bits
-    n, c, U, bn = 5000, 2**31 - 300, 32, 128
-    u = units_of(n, U)
-    assert row_prefix(n, c, U, bn, u, u) == sum(kv_tiles(n, c, bn, (k + 1) * U) for k in range(u))
+    n, c, T, bn = 5000, 2**31 - 300, 16, 128
+    u = units_of(n, 2 * T)
+    assert row_prefix(n, c, T, 2, bn, (1, 1, 0), u, u) == \
+        sum(kv_tiles(n, c, bn, (k + 1) * 2 * T) for k in range(u))
