@@ -54,7 +54,7 @@ struct TcCfg {
   static constexpr int RING = MT * QT;              // offset of the ring
   static constexpr int BARS = RING + NS * SLOT;     // offset of the barriers
   static constexpr int SMEM = 1024 + BARS + 512;    // + up to 1024 of alignment
-  static constexpr int THREADS = 32 * (4 * MT + 3);
+  static constexpr int THREADS = 128 * (MT + 1);    // whole warpgroups: setmaxnreg is theirs
   static constexpr int BM = 128 * MT;
   static constexpr uint32_t O0 = 256;               // tensor memory column of O_0
   static_assert(NS >= 4, "ring");
@@ -143,9 +143,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   bool ok = true;
   PrefillWalk w;
 
-  w.start(p, blockIdx.x);
-
+  // Registers: a softmax thread holds a row of S (BN values).  With 384 threads
+  // each has 168 at launch; 2 x 208 + 88 = 3 x 168.
   if (warp < 4 * MT) {
+    if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    w.start(p, blockIdx.x);
     // ============================================================= softmax
     const int t = warp >> 2;                         // q tile
     const int row = (warp & 3) * 32 + lane;          // its row: tensor memory lane
@@ -184,33 +186,24 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const uint32_t s_at = lanes + (alt ? 1 : t) * BN;
         const int rel = lim - (w.kv0 + j) * BN;  // last visible column
         const bool masked = __any_sync(FULL, rel < BN - 1);
-        // The row's maximum, 32 columns at a time: S is read from tensor memory
-        // again for the exponentials, so a thread holds 2 x 32 values and not
-        // BN (three warps of a scheduler have 168 registers a thread).
-        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
-        uint32_t r[2][32];
-        tmem_ld32(s_at, r[0]);
+        uint32_t r[BN];  // the row of S
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) {
-          tmem_wait_ld();
-          tmem_pin<32>(r[(c >> 5) & 1]);
-          if (c + 32 < BN) tmem_ld32(s_at + c + 32, r[((c >> 5) + 1) & 1]);
-          const uint32_t* s = r[(c >> 5) & 1];
-          if (masked) {
+        for (int c = 0; c < BN; c += 32) tmem_ld32(s_at + c, r + c);
+        tmem_wait_ld();
+        tmem_pin<BN>(r);
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e <= rel) x0 = fmaxf(x0, __uint_as_float(s[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              x0 = fmaxf(x0, __uint_as_float(s[e]));
-              x1 = fmaxf(x1, __uint_as_float(s[e + 1]));
-              x2 = fmaxf(x2, __uint_as_float(s[e + 2]));
-              x3 = fmaxf(x3, __uint_as_float(s[e + 3]));
-            }
-          }
+          for (int c = 0; c < BN; ++c)
+            if (c > rel) r[c] = 0xff800000u;  // -inf
         }
-        tmem_ld32(s_at, r[0]);  // the second pass' first columns
+        float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < BN; c += 8) {
+          x0 = fmaxf(fmaxf(x0, __uint_as_float(r[c])), __uint_as_float(r[c + 1]));
+          x1 = fmaxf(fmaxf(x1, __uint_as_float(r[c + 2])), __uint_as_float(r[c + 3]));
+          x2 = fmaxf(fmaxf(x2, __uint_as_float(r[c + 4])), __uint_as_float(r[c + 5]));
+          x3 = fmaxf(fmaxf(x3, __uint_as_float(r[c + 6])), __uint_as_float(r[c + 7]));
+        }
         const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.qscale;
         const bool grow = mt > m + 8.f;  // also the first visible tile: m = -inf
         if (__any_sync(FULL, grow)) {
@@ -225,17 +218,15 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
               if (!ok) break;
               tmem_fence_after();
             }
-#pragma unroll
-            for (int c = 0; c < D; c += OC) {
-              uint32_t o[OC];
-              if constexpr (OC == 32) tmem_ld32(o_at + c, o);
-              else tmem_ld16(o_at + c, o);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + c, o);
               tmem_wait_ld();
-              tmem_pin<OC>(o);
+              tmem_pin<16>(o);
 #pragma unroll
-              for (int e = 0; e < OC; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              if constexpr (OC == 32) tmem_st32(o_at + c, o);
-              else tmem_st16(o_at + c, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_at + c, o);
             }
             tmem_wait_st();
           }
@@ -244,19 +235,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
         for (int c = 0; c < BN; c += 32) {
-          tmem_wait_ld();
-          tmem_pin<32>(r[(c >> 5) & 1]);
-          if (c + 32 < BN) tmem_ld32(s_at + c + 32, r[((c >> 5) + 1) & 1]);
-          uint32_t* s = r[(c >> 5) & 1];
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e > rel) s[e] = 0xff800000u;  // -inf
-          }
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float a = __uint_as_float(s[e]), b = __uint_as_float(s[e + 1]);
+            float a = __uint_as_float(r[c + e]), b = __uint_as_float(r[c + e + 1]);
             fma2(a, b, p.qscale, ref);
             a = ex2(a);
             b = ex2(b);
@@ -264,7 +246,6 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
             pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          // columns c / 2 .. of S: read already
           tmem_st16(s_at + (c >> 1), pk);
         }
         l += l0 + l1;
@@ -330,7 +311,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       tmem_fence_before();  // O is read before the next unit's first P is reported
       w.advance();
     }
-  } else if (warp == LOAD_K || warp == LOAD_V) {
+  } else {
+   if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   w.start(p, blockIdx.x);
+   if (warp == LOAD_K || warp == LOAD_V) {
     // =============================================================== loads
     // One warp copies q and the K tiles, another the V tiles: a copy costs its
     // issuing thread tens of cycles, and a tile is up to 32 of them.
@@ -502,7 +486,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         cp_async_wait<0>();
       }
     }
-  } else if (warp == ISSUER) {
+   } else if (warp == ISSUER) {
     // ================================================================= mma
     // The whole warp runs the role, its lanes alike; one of them issues.
     constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
@@ -615,6 +599,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     umma_commit(bar(B::drain));
     mbar_wait_drain(bar(B::drain), 0u);
     __syncwarp();
+   }
   }
   if (!ok && lane == 0) set_flag(p.err, NP_FLAG_TIMEOUT);
   __syncwarp();
