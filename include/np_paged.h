@@ -231,7 +231,7 @@ np_status np_rope_append_packed(const np_rope_append_args* args);
  * K and V of the row's c positions must be finite.  Slots past a row's
  * context, in its last block too, are never part of a result, whatever they
  * hold.  Supported: the dtypes, head_dims and groups of the list above; up
- * to 4096 rows; any block_size; tables of up to 2^31 - 257 tokens.
+ * to 4096 rows; any block_size; tables of up to 2^31 - 1025 tokens.
  * out must not overlap q or the pools.  rows or num_tokens 0: a no-op.
  * Three launches (plan, attention, join) on `stream`.  The same call gives
  * the same bits; a row's last bits depend on the other rows' lengths, which

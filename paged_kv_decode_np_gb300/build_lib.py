@@ -50,6 +50,9 @@ def _units(extra: list[str], build_dir: str, csrc: str) -> list[tuple[str, str, 
     for d in HEAD_DIMS:
         units.append((os.path.join(csrc, "prefill_tc.cu"),
                       os.path.join(objdir, f"prefill_tc_d{d}.o"), [f"-DNPK_D={d}"]))
+        if d <= 128:
+            units.append((os.path.join(csrc, "prefill_tc32.cu"),
+                          os.path.join(objdir, f"prefill_tc32_d{d}.o"), [f"-DNPK_D={d}"]))
     return [(s, o, ["-I", csrc] + f + extra) for s, o, f in units]
 
 

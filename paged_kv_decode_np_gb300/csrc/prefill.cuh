@@ -175,6 +175,12 @@ np_status prefill_tc_d64(const PrefillParams& p, bool tiled, cudaStream_t s);
 np_status prefill_tc_d128(const PrefillParams& p, bool tiled, cudaStream_t s);
 np_status prefill_tc_d256(const PrefillParams& p, bool tiled, cudaStream_t s);
 
+// prefill_tc32.cu, per head_dim
+np_status prefill_tc32_d16(const PrefillParams& p, cudaStream_t s);
+np_status prefill_tc32_d32(const PrefillParams& p, cudaStream_t s);
+np_status prefill_tc32_d64(const PrefillParams& p, cudaStream_t s);
+np_status prefill_tc32_d128(const PrefillParams& p, cudaStream_t s);
+
 // The opt-in shared-memory limit of a kernel, a per-device attribute: set at
 // its first launch on a device.  `done`: one word per kernel, bit d for device d.
 template <typename K>

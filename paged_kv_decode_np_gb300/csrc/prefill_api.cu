@@ -118,6 +118,30 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   return NP_ERR_UNSUPPORTED;
 }
 
+// fp32: three bf16 parts on the tensor cores; head_dim 256, whose three parts of
+// q, K and V do not fit in shared memory, on the FMA pipes
+np_status launch_f32(PrefillParams& p, cudaStream_t s) {
+  const bool tc = p.head_dim <= 128;
+  p.tiles = 1;
+  p.tile_rows = tc ? 128 : 64;
+  p.bn = 64;
+  p.tile_tokens = p.tile_rows / p.group;
+  p.full_cost = p.single_cost = 1;
+  p.unit_cost = 1;
+  p.min_share = 3;
+  if (tc) p.qscale = fmaxf(p.qscale, 1e-30f);
+  const np_status rc = npk::launch_prefill_plan(p, s);
+  if (rc != NP_OK) return rc;
+  switch (p.head_dim) {
+    case 16: return npk::prefill_tc32_d16(p, s);
+    case 32: return npk::prefill_tc32_d32(p, s);
+    case 64: return npk::prefill_tc32_d64(p, s);
+    case 128: return npk::prefill_tc32_d128(p, s);
+    case 256: return npk::launch_prefill_simt(p, s);
+  }
+  return NP_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
 extern "C" size_t np_paged_prefill_workspace_bytes(int32_t head_dim) {
@@ -151,8 +175,8 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
       !mul_ok(num_tokens, (int64_t)q_heads * head_dim * es, &qn) ||
       !mul_ok(max_blocks_per_row, block_size, &cap) || !mul_ok(rows, max_blocks_per_row, &tab))
     return NP_ERR_OUT_OF_RANGE;
-  // positions are int32 with a kv tile to spare
-  if (cap > INT32_MAX - 256 || num_tokens > INT32_MAX - 512) return NP_ERR_UNSUPPORTED;
+  // positions are int32 with some kv tiles to spare
+  if (cap > INT32_MAX - 1024 || num_tokens > INT32_MAX - 512) return NP_ERR_UNSUPPORTED;
   if (rows > npk::kPrefillMaxRows) return NP_ERR_UNSUPPORTED;
   if (rows == 0 || num_tokens == 0) return NP_OK;
   if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens || !query_starts)
@@ -199,15 +223,7 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
   if (dtype == NP_BF16) {
     rc = launch_tc(p, slots, st);
   } else {
-    p.tiles = 1;
-    p.tile_rows = 64;
-    p.bn = 64;
-    p.tile_tokens = p.tile_rows / group;
-    p.full_cost = p.single_cost = 1;
-    p.unit_cost = 1;
-    p.min_share = 3;
-    rc = npk::launch_prefill_plan(p, st);
-    if (rc == NP_OK) rc = npk::launch_prefill_simt(p, st);
+    rc = launch_f32(p, st);
   }
   if (rc == NP_OK) rc = npk::launch_prefill_join(p, dtype, st);
   return rc;

@@ -89,13 +89,6 @@ __device__ __forceinline__ bool tc_single(const PrefillParams& p, const PrefillW
   return TcCfg<D>::MT == 1 || ((int64_t)w.m * TcCfg<D>::MT + 1) * p.tile_tokens >= w.g.n;
 }
 
-// Byte of 16-byte piece `ch` of token `row` of a K or V tile.
-template <int SL>
-__device__ __forceinline__ uint32_t tc_kv_at(int row, int ch) {
-  return (uint32_t)(((row >> 3) * SL + (ch >> 3)) * 1024 + (row & 7) * 128 +
-                    (((ch & 7) ^ (row & 7)) << 4));
-}
-
 struct RingPos {
   int slot;
   uint32_t phase;

@@ -152,6 +152,14 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
 }
 
 // ------------------------------------------------------------- various ----
+// Byte of 16-byte piece `ch` of token `row` of a K or V tile laid out as
+// [8 tokens][SL slabs of 64 dims][token][128 bytes], 128-byte swizzle.
+template <int SL>
+__device__ __forceinline__ uint32_t tc_kv_at(int row, int ch) {
+  return (uint32_t)(((row >> 3) * SL + (ch >> 3)) * 1024 + (row & 7) * 128 +
+                    (((ch & 7) ^ (row & 7)) << 4));
+}
+
 // Generic-proxy writes to shared memory, before the async proxy (TMA, mma)
 // reads or writes there.
 __device__ __forceinline__ void fence_async_smem() {
