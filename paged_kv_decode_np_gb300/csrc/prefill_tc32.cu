@@ -15,13 +15,14 @@
 // the sum over a long history is rounded to nearest.
 //
 // A unit is one tile of 128 (token, head) rows; a kv tile is 64 tokens.  Roles:
-//   4 warps of softmax (one thread a row): S from tensor memory, P in three
-//     parts to tensor memory, O of the tile before added up;
-//   4 warps that copy q and K, 4 that copy V: fp32 from global memory to
-//     registers a tile ahead, split, to shared memory in the mma's layout;
+//   4 warps of softmax (one thread a row): q in three parts to tensor memory,
+//     S from there, P in three parts back to it, O of the tile before added up;
+//   4 warps that copy K, 4 that copy V: fp32 from global memory to registers
+//     half a tile ahead, split, to shared memory in the mma's layout;
 //   1 warp that issues:  S(j+1), P V(j), S(j+2), P V(j+1) ...
-// Shared memory (head_dim 128): q 96 KB, K 48 KB, V 48 KB.  Bound: the tensor
-// cores (S reads 6 KB of shared memory for 64 x 128 x 16 products).
+// q and P are the mma's A operands, from tensor memory: only K and V parts are
+// read from shared memory (2 KB for 128 x 64 x 16 products), and q leaves its
+// 96 KB there to a second K and V tile.  Bound: the tensor cores.
 #include <limits.h>
 
 #include "prefill.cuh"
@@ -38,20 +39,20 @@ struct Tc32Cfg {
   static constexpr int SL = D > 64 ? D / 64 : 1;  // 64-dim slabs
   static constexpr int BN = 64;
   static constexpr int PART = SL * BN * 128;      // bytes of a K or V part
-  static constexpr int QPART = SL * 128 * 128;    // bytes of a q part
-  static constexpr int NS = D == 128 ? 1 : 2;     // K tiles, V tiles in shared memory
-  static constexpr int K0 = 3 * QPART, V0 = K0 + NS * 3 * PART;
-  static constexpr int BARS = V0 + NS * 3 * PART;
+  static constexpr int NS = D == 128 ? 2 : 4;     // K tiles, V tiles in shared memory
+  static constexpr int V0 = NS * 3 * PART;
+  static constexpr int BARS = 2 * V0;
   static constexpr int SMEM = 1024 + BARS + 256;
   static constexpr int THREADS = 512;
-  // tensor memory: two S of 64 columns, three P parts of 32, two O
-  static constexpr uint32_t P0 = 128, O0 = 256;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // tensor memory: S (64 columns), P and q (three parts of 32 and of D / 2), O
+  static constexpr uint32_t P0 = 64, Q0 = 160, O0 = 384;
+  static_assert(SMEM <= 227 * 1024 && Q0 + 3 * D / 2 <= O0, "shared and tensor memory");
 };
 
 struct Tc32Bars {
-  static constexpr int q_full = 0, q_empty = 1, k_full = 2, k_empty = 4, v_full = 6, v_empty = 8;
-  static constexpr int s_full = 10, s_empty = 12, p_full = 14, pv_done = 15, drain = 16, count = 17;
+  static constexpr int k_full = 0, k_empty = 4, v_full = 8, v_empty = 12;  // of NS <= 4 slots
+  static constexpr int q_full = 16, s_full = 17, s_empty = 18, p_full = 19, pv_done = 20;
+  static constexpr int drain = 21, count = 22;
 };
 
 // The parts of a product, the small ones first: (a part, b part).
@@ -100,13 +101,12 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tail + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int ISSUER = 12;  // warps 0-3 softmax, 4-7 q and K, 8-11 V
+  constexpr int ISSUER = 12;  // warps 0-3 softmax, 4-7 K, 8-11 V
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i) {
-      const bool warps4 = i == B::q_full || (i >= B::k_full && i < B::k_empty) ||
-                          (i >= B::v_full && i < B::v_empty) ||
-                          (i >= B::s_empty && i < B::s_empty + 2) || i == B::p_full;
+      const bool warps4 = (i >= B::k_full && i < B::k_empty) || (i >= B::v_full && i < B::v_empty) ||
+                          i == B::q_full || i == B::s_empty || i == B::p_full;
       mbar_init(bar(i), warps4 ? 4 : 1);
     }
     *abort = 0;
@@ -126,10 +126,10 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
     return ok;
   };
 
-  // Registers: 512 threads have 128 each at launch; 216 + 2 x 112 + 72 = 4 x 128.
+  // Registers: 512 threads have 128 each at launch; 240 + 2 x 96 + 80 = 4 x 128.
   if (warp < 4) {
     // ============================================================= softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     w.start(p, blockIdx.x);
     const int row = warp * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
@@ -141,16 +141,48 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
       const bool live = tt < p.tile_tokens && tok < w.g.n;
       const bool idle = !__any_sync(FULL, live);  // none of the warp's rows is stored
       const int lim = live ? (int)((int64_t)w.g.c - w.g.n + tok) : INT_MAX;
+      // ---- q of the row, zeros without a token.  The last segment's S are
+      // complete (this warp has waited for each), so its q may go.
+      if (!idle) {
+        const float* q = static_cast<const float*>(p.q) +
+                         ((w.g.q0 + tok) * p.q_heads + (int64_t)w.kvh * p.group + h) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t k[3][8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) x = *reinterpret_cast<const float4*>(q + c + e);
+            uint32_t y[4][3];
+            split3(x.x, y[0][0], y[0][1], y[0][2]);
+            split3(x.y, y[1][0], y[1][1], y[1][2]);
+            split3(x.z, y[2][0], y[2][1], y[2][2]);
+            split3(x.w, y[3][0], y[3][1], y[3][2]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              k[i][e / 2] = upper_halves(y[0][i], y[1][i]);
+              k[i][e / 2 + 1] = upper_halves(y[2][i], y[3][i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) tmem_st8(lanes + C::Q0 + i * (D / 2) + (c >> 1), k[i]);
+        }
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(bar(B::q_full));
+
       float m = -INFINITY, l = 0.f;
       float acc[D];
 #pragma unroll
       for (int c = 0; c < D; ++c) acc[c] = 0.f;
-      // acc = (acc + O of the tile before this one) * f
-      auto add_o = [&](uint32_t tile, float f) {
+      // acc = (acc + O of the tile before) * f
+      auto add_o = [&](float f) {
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           uint32_t o[16];
-          tmem_ld16(lanes + C::O0 + (tile & 1u) * 128 + c, o);
+          tmem_ld16(lanes + C::O0 + c, o);
           tmem_wait_ld();
           tmem_pin<16>(o);
 #pragma unroll
@@ -158,87 +190,77 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
         }
       };
       for (int j = 0; j < n; ++j, ++it) {
-        if (!wait(B::s_full + (it & 1u), (it >> 1) & 1u)) break;
+        if (!wait(B::s_full, it & 1u)) break;
         tmem_fence_after();
-        float f = 1.f;
-        if (!idle) {
-          // S is read twice, 32 columns at a time: with the D values of acc a
-          // thread has no room for a row of it
-          const uint32_t s_at = lanes + (it & 1u) * BN;
-          const int rel = lim - (w.kv0 + j) * BN;  // last visible column
-          const bool masked = __any_sync(FULL, rel < BN - 1);
-          uint32_t r[32];
-          auto read = [&](int c) {
-            tmem_ld32(s_at + c, r);
-            tmem_wait_ld();
-            tmem_pin<32>(r);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e > rel) r[e] = 0xff800000u;  // -inf
-            }
-          };
-          float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < BN; c += 32) {
-            read(c);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              x0 = fmaxf(fmaxf(x0, __uint_as_float(r[e])), __uint_as_float(r[e + 1]));
-              x1 = fmaxf(fmaxf(x1, __uint_as_float(r[e + 2])), __uint_as_float(r[e + 3]));
-            }
-          }
-          const float mn = fmaxf(m, fmaxf(x0, x1) * p.qscale);
-          const float ref = mn == -INFINITY ? 0.f : -mn;
-          f = ex2(m + ref);
-          m = mn;
-          if (j > 0) {  // P V of the tile before has read P
-            if (!wait(B::pv_done, (it - 1) & 1u)) break;
-            tmem_fence_after();
-          }
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < BN; c += 32) {  // 32 weights: 16 columns of each part
-            read(c);
-            uint32_t k0[16], k1[16], k2[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(r[2 * e]), p.qscale, ref));
-              const float b = ex2(fmaf(__uint_as_float(r[2 * e + 1]), p.qscale, ref));
-              l0 += a;
-              l1 += b;
-              uint32_t a0, a1, a2, b0, b1, b2;
-              split3(a, a0, a1, a2);
-              split3(b, b0, b1, b2);
-              k0[e] = upper_halves(a0, b0);
-              k1[e] = upper_halves(a1, b1);
-              k2[e] = upper_halves(a2, b2);
-            }
-            const uint32_t at = lanes + C::P0 + (c >> 1);
-            tmem_st16(at, k0);
-            tmem_st16(at + 32, k1);
-            tmem_st16(at + 64, k2);
-          }
-          l = fmaf(l, f, l0 + l1);
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B::s_empty + (it & 1u)));
-          tmem_wait_st();
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B::p_full));
-          if (j > 0) add_o(it - 1, f);
-        } else {
-          // P of these rows is whatever tensor memory holds: it moves their own O only
-          if (lane == 0) mbar_arrive(bar(B::s_empty + (it & 1u)));
+        if (idle) {  // P of these rows is whatever tensor memory holds: it moves their own O only
+          if (lane == 0) mbar_arrive(bar(B::s_empty));
           if (j > 0 && !wait(B::pv_done, (it - 1) & 1u)) break;
           if (lane == 0) mbar_arrive(bar(B::p_full));
+          continue;
         }
+        uint32_t r[BN];
+        tmem_ld32(lanes, r);
+        tmem_ld32(lanes + 32, r + 32);
+        tmem_wait_ld();
+        tmem_pin<BN>(r);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::s_empty));
+        const int rel = lim - (w.kv0 + j) * BN;  // last visible column
+        if (__any_sync(FULL, rel < BN - 1)) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c > rel) r[c] = 0xff800000u;  // -inf
+        }
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < BN; c += 4) {
+          x0 = fmaxf(fmaxf(x0, __uint_as_float(r[c])), __uint_as_float(r[c + 1]));
+          x1 = fmaxf(fmaxf(x1, __uint_as_float(r[c + 2])), __uint_as_float(r[c + 3]));
+        }
+        const float mn = fmaxf(m, fmaxf(x0, x1) * p.qscale);
+        const float ref = mn == -INFINITY ? 0.f : -mn;
+        const float f = ex2(m + ref);
+        m = mn;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < BN; c += 2) {
+          const float a = ex2(fmaf(__uint_as_float(r[c]), p.qscale, ref));
+          const float b = ex2(fmaf(__uint_as_float(r[c + 1]), p.qscale, ref));
+          l0 += a;
+          l1 += b;
+          r[c] = __float_as_uint(a);
+          r[c + 1] = __float_as_uint(b);
+        }
+        l = fmaf(l, f, l0 + l1);
+        if (j > 0) {  // P V of the tile before is complete: P may go, O is there
+          if (!wait(B::pv_done, (it - 1) & 1u)) break;
+          tmem_fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < BN; c += 16) {  // 16 weights: 8 columns of each part
+          uint32_t k[3][8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t a[3], b[3];
+            split3(__uint_as_float(r[c + 2 * e]), a[0], a[1], a[2]);
+            split3(__uint_as_float(r[c + 2 * e + 1]), b[0], b[1], b[2]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) k[i][e] = upper_halves(a[i], b[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) tmem_st8(lanes + C::P0 + i * 32 + (c >> 1), k[i]);
+        }
+        if (j > 0) add_o(f);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::p_full));
       }
       if (!wait(B::pv_done, (it - 1) & 1u)) break;
       tmem_fence_after();
       if (!idle) {
-        add_o(it - 1, 1.f);
+        add_o(1.f);
         // ---- the row's result: out, or this block's partial of a cut unit
         if (w.whole()) {
           if (live) {
@@ -266,24 +288,25 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
     }
   } else if (warp < ISSUER) {
     // =============================================================== loads
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     w.start(p, blockIdx.x);
     const bool isv = warp >= 8;
     const int wl = warp & 3;                 // warp of its group of four
     constexpr int PT = D / 8;                // 8-dim pieces of a token
     constexpr int TW = 32 / PT;              // tokens a warp takes at a time
     constexpr int NP = PT / 2;               // times: 16 tokens of the 64 are a warp's
+    constexpr int HP = NP > 1 ? NP / 2 : 1;  // as many times at once: half a tile
     const int piece = lane % PT, sub = lane / PT;
     const float* pool = static_cast<const float*>(isv ? p.v_pool : p.k_pool);
     const int64_t token = (int64_t)p.kv_heads * D;
-    const uint32_t to = isv ? C::V0 : C::K0;
     const int full = isv ? B::v_full : B::k_full, empty = isv ? B::v_empty : B::k_empty;
-    uint32_t it = 0, seg = 0;
-    float4 x[NP][2];
+    uint32_t it = 0;
+    float4 x[HP][2];
     // token i of the warp's 16 (i = pass * TW + sub) is row pass * 4 TW + wl TW + sub
     auto row_of = [&](int pass, int s) { return (pass * 4 + wl) * TW + s; };
-    auto fetch = [&](int kt) {  // this warp's tokens of kv tile kt; zeros past the context
-      int64_t at = -1;          // lane i: element offset of the warp's token i
+    // lane i: element offset of the warp's token i of kv tile kt, -1 past the context
+    auto look_up = [&](int kt) {
+      int64_t at = -1;
       if (lane < 16) {
         const int64_t t = (int64_t)kt * BN + row_of(lane / TW, lane % TW);
         if (t < w.g.c) {
@@ -296,9 +319,12 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
           at = (b * p.block_size + ((unsigned)t - j * p.block_size)) * token + (int64_t)w.kvh * D;
         }
       }
+      return at;
+    };
+    auto fetch = [&](int64_t at, int first) {  // passes first .. first + HP - 1; zeros past the context
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int64_t a = __shfl_sync(FULL, at, i * TW + sub);
+      for (int i = 0; i < HP; ++i) {
+        const int64_t a = __shfl_sync(FULL, at, (first + i) * TW + sub);
         x[i][0] = x[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (a >= 0) {
           const float4* src = reinterpret_cast<const float4*>(pool + a + piece * 8);
@@ -309,60 +335,41 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
     };
     while (ok && w.next(p)) {
       const int n = w.kv1 - w.kv0;
-      fetch(w.kv0);
-      if (!isv) {
-        // ---- q: 128 rows, rows without a token zero
-        if (seg > 0 && !wait(B::q_empty, (seg - 1) & 1u)) break;
-        for (int r0 = wl * TW; r0 < 128; r0 += 4 * TW) {
-          const int qrow = r0 + sub;
-          const int tt = qrow / p.group, h = qrow - tt * p.group;
-          const int tok = w.m * p.tile_tokens + tt;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-          if (tt < p.tile_tokens && tok < w.g.n) {
-            const float4* src = reinterpret_cast<const float4*>(
-                static_cast<const float*>(p.q) +
-                ((int64_t)(w.g.q0 + tok) * p.q_heads + w.kvh * p.group + h) * D + piece * 8);
-            a = src[0];
-            b = src[1];
-          }
-          uint4 o[3];
-          split8(a, b, o);
-          unsigned char* dst = smem + (piece >> 3) * 16384 + qrow * 128 + (((piece & 7) ^ (qrow & 7)) << 4);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(dst + k * C::QPART) = o[k];
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B::q_full));
-      }
-      ++seg;
+      int64_t at = look_up(w.kv0);
+      fetch(at, 0);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t slot = it % NS, use = it / NS;
+        const int64_t ahead = j + 1 < n ? look_up(w.kv0 + j + 1) : -1;
         if (use > 0 && !wait(empty + slot, (use - 1) & 1u)) break;
-        unsigned char* dst = smem + to + slot * (3 * C::PART);
+        unsigned char* dst = smem + (isv ? C::V0 : 0) + slot * (3 * C::PART);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          uint4 o[3];
-          split8(x[i][0], x[i][1], o);
-          unsigned char* d = dst + tc_kv_at<SL>(row_of(i, sub), piece);
+        for (int first = 0; first < NP; first += HP) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(d + k * C::PART) = o[k];
+          for (int i = 0; i < HP; ++i) {
+            uint4 o[3];
+            split8(x[i][0], x[i][1], o);
+            unsigned char* d = dst + tc_kv_at<SL>(row_of(first + i, sub), piece);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(d + k * C::PART) = o[k];
+          }
+          if (first + HP < NP) fetch(at, first + HP);
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(full + slot));
-        if (j + 1 < n) fetch(w.kv0 + j + 1);
+        at = ahead;
+        if (j + 1 < n) fetch(at, 0);
       }
       w.advance();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     w.start(p, blockIdx.x);
     if (warp == ISSUER) {
       // =============================================================== mma
       // The whole warp runs the role, its lanes alike; one of them issues.
       constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
-      constexpr uint32_t QHI = umma_desc_hi(1024), KVHI = umma_desc_hi(SL * 1024);
+      constexpr uint32_t KVHI = umma_desc_hi(SL * 1024);
       const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
       uint32_t it = 0, seg = 0;  // kv tiles whose P V is issued; segments
       while (ok && w.next(p)) {
@@ -370,25 +377,21 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
         if (!wait(B::q_full, seg & 1u)) break;
         ++seg;
         for (int j = -1; j < n; ++j) {
-          if (j + 1 < n) {  // S(j + 1)
-            const uint32_t t = it + (j < 0 ? 0u : 1u);
-            const uint32_t slot = t % NS, buf = t & 1u;
+          if (j + 1 < n) {  // S(j + 1), once S(j) has been read
+            const uint32_t t = it + (j < 0 ? 0u : 1u), slot = t % NS;
             if (!wait(B::k_full + slot, (t / NS) & 1u)) break;
-            if (t > 1 && !wait(B::s_empty + buf, ((t >> 1) - 1u) & 1u)) break;
+            if (t > 0 && !wait(B::s_empty, (t - 1u) & 1u)) break;
             tmem_fence_after();
-            const uint32_t q = umma_desc_lo(base, 16);
-            const uint32_t k = umma_desc_lo(base + C::K0 + slot * (3 * C::PART), 16);
+            const uint32_t k = umma_desc_lo(base + slot * (3 * C::PART), 16);
 #pragma unroll
             for (int x = 0; x < 6; ++x)
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
-                umma_ss(tmem + buf * BN,
-                        q + (kPartA[x] * C::QPART + (ks >> 2) * 16384 + (ks & 3) * 32) / 16, QHI,
+                umma_ts(tmem, tmem + C::Q0 + kPartA[x] * (D / 2) + ks * 8,
                         k + (kPartB[x] * C::PART + (ks >> 2) * 1024 + (ks & 3) * 32) / 16, KVHI, QK,
                         x > 0 || ks > 0);
-            umma_commit(bar(B::s_full + buf));
+            umma_commit(bar(B::s_full));
             umma_commit(bar(B::k_empty + slot));
-            if (j + 2 == n) umma_commit(bar(B::q_empty));
           }
           if (j >= 0) {  // O = P(j) V(j)
             const uint32_t slot = it % NS;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
             for (int x = 0; x < 6; ++x)
 #pragma unroll
               for (int ks = 0; ks < BN / 16; ++ks)
-                umma_ts(tmem + C::O0 + (it & 1u) * 128, tmem + C::P0 + kPartA[x] * 32 + ks * 8,
+                umma_ts(tmem + C::O0, tmem + C::P0 + kPartA[x] * 32 + ks * 8,
                         v + (kPartB[x] * C::PART + ks * (2 * SL * 1024)) / 16, KVHI, PV,
                         x > 0 || ks > 0);
             umma_commit(bar(B::pv_done));
