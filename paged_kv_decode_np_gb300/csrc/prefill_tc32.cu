@@ -143,26 +143,29 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
       const int lim = live ? (int)((int64_t)w.g.c - w.g.n + tok) : INT_MAX;
       // ---- q of the row, zeros without a token.  The last segment's S are
       // complete (this warp has waited for each), so its q may go.
+      float acc[D];
       if (!idle) {
         const float* q = static_cast<const float*>(p.q) +
                          ((w.g.q0 + tok) * p.q_heads + (int64_t)w.kvh * p.group + h) * D;
-#pragma unroll 1
+#pragma unroll
+        for (int c = 0; c < D; c += 4) {  // the whole row in flight
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (live) x = *reinterpret_cast<const float4*>(q + c);
+          acc[c] = x.x;
+          acc[c + 1] = x.y;
+          acc[c + 2] = x.z;
+          acc[c + 3] = x.w;
+        }
+#pragma unroll
         for (int c = 0; c < D; c += 16) {
           uint32_t k[3][8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live) x = *reinterpret_cast<const float4*>(q + c + e);
-            uint32_t y[4][3];
-            split3(x.x, y[0][0], y[0][1], y[0][2]);
-            split3(x.y, y[1][0], y[1][1], y[1][2]);
-            split3(x.z, y[2][0], y[2][1], y[2][2]);
-            split3(x.w, y[3][0], y[3][1], y[3][2]);
+          for (int e = 0; e < 8; ++e) {
+            uint32_t x[3], y[3];
+            split3(acc[c + 2 * e], x[0], x[1], x[2]);
+            split3(acc[c + 2 * e + 1], y[0], y[1], y[2]);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              k[i][e / 2] = upper_halves(y[0][i], y[1][i]);
-              k[i][e / 2 + 1] = upper_halves(y[2][i], y[3][i]);
-            }
+            for (int i = 0; i < 3; ++i) k[i][e] = upper_halves(x[i], y[i]);
           }
 #pragma unroll
           for (int i = 0; i < 3; ++i) tmem_st8(lanes + C::Q0 + i * (D / 2) + (c >> 1), k[i]);
@@ -174,19 +177,24 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
       if (lane == 0) mbar_arrive(bar(B::q_full));
 
       float m = -INFINITY, l = 0.f;
-      float acc[D];
 #pragma unroll
       for (int c = 0; c < D; ++c) acc[c] = 0.f;
       // acc = (acc + O of the tile before) * f
       auto add_o = [&](float f) {
+        constexpr int OC = D < 32 ? 16 : (D < 64 ? 32 : 64);  // columns at a time
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(lanes + C::O0 + c, o);
+        for (int c = 0; c < D; c += OC) {
+          uint32_t o[OC];
+          if constexpr (OC == 16) {
+            tmem_ld16(lanes + C::O0 + c, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < OC; e += 32) tmem_ld32(lanes + C::O0 + c + e, o + e);
+          }
           tmem_wait_ld();
-          tmem_pin<16>(o);
+          tmem_pin<OC>(o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[c + e] = (acc[c + e] + __uint_as_float(o[e])) * f;
+          for (int e = 0; e < OC; ++e) acc[c + e] = (acc[c + e] + __uint_as_float(o[e])) * f;
         }
       };
       for (int j = 0; j < n; ++j, ++it) {
