@@ -5,22 +5,32 @@
 namespace npk {
 
 // sum over i < n of floor((a i + b) / m), for a, b >= 0, m > 0: the lattice
-// points under a line, counted by Euclid's reduction of (a, m).
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// points under a line, counted by Euclid's reduction of (a, m).  T holds
+// a n + b; a 64-bit division takes several times a 32-bit one.
+template <typename T>
+__device__ int64_t floor_sum_in(T n, T m, T a, T b) {
   int64_t s = 0;
   while (n > 0) {
-    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t y = a * n + b;
+    const T qa = a / m, qb = b / m;
+    s += (int64_t)n * (n - 1) / 2 * qa + (int64_t)n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const T y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
-    const int64_t t = m;
+    b = y - n * m;
+    const T t = m;
     m = a;
     a = t;
   }
   return s;
+}
+
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  // the first step leaves a < m and b < m; later ones only shrink
+  if (n < (1 << 20) && m <= 1024 && a <= 1024 && b < (1ll << 31))
+    return floor_sum_in<uint32_t>((uint32_t)n, (uint32_t)m, (uint32_t)a, (uint32_t)b);
+  return floor_sum_in<int64_t>(n, m, a, b);
 }
 
 // what a kv tile of a row's unit a costs
@@ -43,7 +53,7 @@ __device__ int64_t prefill_row_prefix(const PrefillParams& p, const PrefillRow& 
   return cost + (z + floor_sum(k - z, p.bn, U, base + (z + 1) * U + p.bn - 1)) * p.full_cost;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 
 // One block.  Scans the rows' work (costs of kv tiles and of beginning units),
 // cuts the stream into equal shares and writes where each block's begins
@@ -51,23 +61,22 @@ constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid_constant__
                                                                     PrefillParams p) {
   __shared__ int64_t pre[kPrefillMaxRows + 1];  // work before each row
-  __shared__ int64_t warp_sum[32];
+  __shared__ int64_t warp_sum[kPlanThreads / 32];
   __shared__ int4 pos[kPrefillMaxCtas + 1];
   constexpr unsigned FULL = 0xffffffffu;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int PER = kPrefillMaxRows / kPlanThreads;
-  const int per = (p.rows + kPlanThreads - 1) / kPlanThreads;  // <= PER rows a thread
-  int64_t w[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
+  // the attention may become resident: it waits for this block before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per = (p.rows + kPlanThreads - 1) / kPlanThreads;  // rows a thread
+  int64_t sum = 0;
+  for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
-    w[i] = 0;
-    if (i < per && r < p.rows) {
+    if (r < p.rows) {
       const PrefillRow g = prefill_row(p, r, true);
       const int units = prefill_units(p, g.n);
-      w[i] = prefill_row_prefix(p, g, units, units) * p.kv_heads;
+      pre[r] = sum;  // within the thread's rows for now
+      sum += prefill_row_prefix(p, g, units, units) * p.kv_heads;
     }
-    sum += w[i];
   }
   int64_t x = sum;
 #pragma unroll
@@ -78,23 +87,22 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
   if (lane == 31) warp_sum[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int64_t y = warp_sum[lane];
+    constexpr int WARPS = kPlanThreads / 32;
+    int64_t y = lane < WARPS ? warp_sum[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < WARPS; o <<= 1) {
       const int64_t u = __shfl_up_sync(FULL, y, o);
       if (lane >= o) y += u;
     }
-    warp_sum[lane] = y;
+    if (lane < WARPS) warp_sum[lane] = y;
   }
   __syncthreads();
-  int64_t run = x - sum + (warp > 0 ? warp_sum[warp - 1] : 0);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
+  const int64_t run = x - sum + (warp > 0 ? warp_sum[warp - 1] : 0);
+  for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
-    if (i < per && r < p.rows) pre[r] = run;
-    run += w[i];
+    if (r < p.rows) pre[r] += run;
   }
-  if (tid == 0) pre[p.rows] = warp_sum[31];
+  if (tid == 0) pre[p.rows] = warp_sum[kPlanThreads / 32 - 1];
   __syncthreads();
   const int64_t W = pre[p.rows];
   // blocks that share the work: a share holds min_share at least
@@ -168,22 +176,33 @@ np_status launch_prefill_plan(const PrefillParams& p, cudaStream_t s) {
 
 // The join: block (b, y) merges rows [32 y, 32 y + 32) of the unit that block
 // b's share began and its end cuts.  Piece b lies in b's slot 1, the pieces
-// of blocks b + 1 .. last in their slot 0.  A thread holds one row's 4 dims at
-// a time; consecutive lanes hold consecutive rows, so partial loads are
-// coalesced; the result goes through shared memory so that the stores are
-// too.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// of blocks b + 1 .. last in their slot 0.
+//     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
+// Bound by latency (a unit's partials are some hundred KB in L2), so it is a
+// few rounds of independent loads: the pieces' list, then every (piece, row)'s
+// m and l, then the O -- a thread holds one row's 4 dims of D / 32 groups,
+// consecutive lanes consecutive rows, four pieces in flight.  The result goes
+// through shared memory so that the stores are coalesced.
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__
                                                                     PrefillParams p) {
-  __shared__ float tile[32][D + 4];
+  // every (piece, row)'s m and l; then the results [32][D + 4]
+  __shared__ __align__(16) float buf[2 * kPrefillMaxCtas * 32];
+  static_assert(32 * (D + 4) <= 2 * kPrefillMaxCtas * 32, "results fit");
+  float(*ms)[32] = reinterpret_cast<float(*)[32]>(buf);
+  float(*ls)[32] = ms + kPrefillMaxCtas;
   __shared__ int piece[kPrefillMaxCtas];  // the partials, in block order
   __shared__ int pieces;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention is complete
+  // the plan is complete: the attention, which waited for it, let this launch start
   const int b = blockIdx.x;
   const int4 cut = p.cuts[b];
-  if (cut.x < 0) return;
+  if (cut.x < 0) {
+    // (this launch must not end before the attention: what comes after waits for it)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   if (threadIdx.x < 32) {
     // a share may be empty: it begins where the next one does and left nothing
     int n = 0;
@@ -200,36 +219,58 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
     }
     if (threadIdx.x == 0) pieces = n;
   }
+  const PrefillRow gr = prefill_row(p, cut.x);
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention is complete
   const int bm = p.tile_rows * p.tiles;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int WARPS = kJoinThreads / 32;
   const int row = blockIdx.y * 32 + lane;  // < bm
   const size_t pf = prefill_part_floats(bm, D);
-  auto part = [&](int i) { return p.parts + (size_t)piece[i] * pf; };
   const int np = pieces;
-  float M = -INFINITY;
-  for (int i = 0; i < np; ++i) M = fmaxf(M, part(i)[row]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int i = 0; i < np; ++i) L = fmaf(ex2(part(i)[row] - ref), part(i)[bm + row], L);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  for (int g = warp; g < D / 4; g += kJoinThreads / 32) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-      const float* q = part(i);
-      const float w = ex2(q[row] - ref);
-      const float4 o = *reinterpret_cast<const float4*>(q + 2 * bm + ((size_t)g * bm + row) * 4);
-      acc.x = fmaf(w, o.x, acc.x);
-      acc.y = fmaf(w, o.y, acc.y);
-      acc.z = fmaf(w, o.z, acc.z);
-      acc.w = fmaf(w, o.w, acc.w);
-    }
-    *reinterpret_cast<float4*>(&tile[lane][4 * g]) =
-        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  for (int i = warp; i < np; i += WARPS) {
+    const float* q = p.parts + (size_t)piece[i] * pf;
+    ms[i][lane] = q[row];
+    ls[i][lane] = q[bm + row];
   }
   __syncthreads();
-  const PrefillRow gr = prefill_row(p, cut.x);
+  float M = -INFINITY;
+  for (int i = 0; i < np; ++i) M = fmaxf(M, ms[i][lane]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int i = 0; i < np; ++i) L = fmaf(ex2(ms[i][lane] - ref), ls[i][lane], L);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  constexpr int GW = D / 4 < WARPS ? 1 : D / 4 / WARPS;  // groups of 4 dims a warp
+  const bool some = warp * GW < D / 4;
+  float acc[GW][4];
+#pragma unroll
+  for (int g = 0; g < GW; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[g][e] = 0.f;
+  if (some) {
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      const float* q = p.parts + (size_t)piece[i] * pf + 2 * bm + ((size_t)(warp * GW) * bm + row) * 4;
+      const float w = ex2(ms[i][lane] - ref);
+#pragma unroll
+      for (int g = 0; g < GW; ++g) {
+        const float4 o = *reinterpret_cast<const float4*>(q + (size_t)g * bm * 4);
+        acc[g][0] = fmaf(w, o.x, acc[g][0]);
+        acc[g][1] = fmaf(w, o.y, acc[g][1]);
+        acc[g][2] = fmaf(w, o.z, acc[g][2]);
+        acc[g][3] = fmaf(w, o.w, acc[g][3]);
+      }
+    }
+  }
+  __syncthreads();  // m and l are no longer read
+  float(*tile)[D + 4] = reinterpret_cast<float(*)[D + 4]>(buf);
+  if (some) {
+#pragma unroll
+    for (int g = 0; g < GW; ++g)
+      *reinterpret_cast<float4*>(&tile[lane][4 * (warp * GW + g)]) =
+          make_float4(acc[g][0] * inv, acc[g][1] * inv, acc[g][2] * inv, acc[g][3] * inv);
+  }
+  __syncthreads();
   for (int e = threadIdx.x; e < 32 * (D / 4); e += kJoinThreads) {
     const int rr = e / (D / 4), d = (e % (D / 4)) * 4;
     const int urow = blockIdx.y * 32 + rr;           // row of the unit

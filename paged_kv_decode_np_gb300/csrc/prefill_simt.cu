@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
   const float qscale = p.negate ? -p.qscale : p.qscale;
   const int G = p.group;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is complete
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may wait
   PrefillWalk w;
   w.start(p, blockIdx.x);
   while (w.next(p)) {

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   tmem_fence_after();
   const uint32_t tmem = *tail;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is complete
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may wait
 
   bool ok = true;
   PrefillWalk w;
