@@ -7,8 +7,8 @@
 // nine bf16 products, exact in fp32; the three smallest (below 2^-22 of the
 // whole) are left out:
 //     a b = a0 b0 + (a0 b1 + a1 b0) + (a1 b1 + a0 b2 + a2 b0)
-// so S = Q K^T and O = P V are six tensor-core products each, added to one
-// fp32 accumulator, the small ones first (an accumulator's rounding is
+// so S = Q K^T and O = P V are six tensor-core products each, added in fp32,
+// the small ones first (an accumulator's rounding is
 // relative to what it holds).  Six times the work of bf16 is still several
 // times the rate of the FMA pipes.  O is accumulated over the kv tiles in
 // registers: a tile's P V is 24 steps of the tensor cores' accumulator, and
@@ -20,9 +20,13 @@
 //   4 warps that copy K, 4 that copy V: fp32 from global memory to registers
 //     half a tile ahead, split, to shared memory in the mma's layout;
 //   1 warp that issues:  S(j+1), P V(j), S(j+2), P V(j+1) ...
-// q and P are the mma's A operands, from tensor memory: only K and V parts are
-// read from shared memory (2 KB for 128 x 64 x 16 products), and q leaves its
-// 96 KB there to a second K and V tile.  Bound: the tensor cores.
+// A 128 x 64 mma takes as long as a 128 x 128 one, so S has 128 columns: a kv
+// tile's parts lie one after the other, and q_i times [K_0; K_1] gives q_i K_0 in
+// the first 64 columns and q_i K_1 in the others (q_2 K_1 comes for nothing);
+// q_0 K_2 joins the latter, and the softmax adds the two.  Four mma a 16-dim
+// step instead of six.  P and q's first two parts are A operands in tensor
+// memory, which has no room for q's third: that one is in shared memory.
+// Bound: the tensor cores.
 #include <limits.h>
 
 #include "prefill.cuh"
@@ -40,13 +44,14 @@ struct Tc32Cfg {
   static constexpr int BN = 64;
   static constexpr int PART = SL * BN * 128;      // bytes of a K or V part
   static constexpr int NS = D == 128 ? 2 : 4;     // K tiles, V tiles in shared memory
-  static constexpr int V0 = NS * 3 * PART;
-  static constexpr int BARS = 2 * V0;
+  static constexpr int K0 = SL * 128 * 128;       // after q's third part
+  static constexpr int V0 = K0 + NS * 3 * PART;
+  static constexpr int BARS = V0 + NS * 3 * PART;
   static constexpr int SMEM = 1024 + BARS + 256;
   static constexpr int THREADS = 512;
-  // tensor memory: S (64 columns), P and q (three parts of 32 and of D / 2), O
-  static constexpr uint32_t P0 = 64, Q0 = 160, O0 = 384;
-  static_assert(SMEM <= 227 * 1024 && Q0 + 3 * D / 2 <= O0, "shared and tensor memory");
+  // tensor memory: S (128 columns), P (three parts of 32), q (two of D / 2), O
+  static constexpr uint32_t P0 = 128, Q0 = 224, O0 = 384;
+  static_assert(SMEM <= 227 * 1024 && Q0 + D <= O0, "shared and tensor memory");
 };
 
 struct Tc32Bars {
@@ -169,10 +174,16 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
             for (int i = 0; i < 3; ++i) k[i][e] = upper_halves(x[i], y[i]);
           }
 #pragma unroll
-          for (int i = 0; i < 3; ++i) tmem_st8(lanes + C::Q0 + i * (D / 2) + (c >> 1), k[i]);
+          for (int i = 0; i < 2; ++i) tmem_st8(lanes + C::Q0 + i * (D / 2) + (c >> 1), k[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)  // the third part: 16-byte pieces c / 8 + i
+            *reinterpret_cast<uint4*>(smem + (c >> 6) * 16384 + row * 128 +
+                                      ((((c >> 3) + i) & 7) ^ (row & 7)) * 16) =
+                make_uint4(k[2][4 * i], k[2][4 * i + 1], k[2][4 * i + 2], k[2][4 * i + 3]);
         }
         tmem_wait_st();
         tmem_fence_before();
+        fence_async_smem();
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(bar(B::q_full));
@@ -208,10 +219,20 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
           continue;
         }
         uint32_t r[BN];
-        tmem_ld32(lanes, r);
+        tmem_ld32(lanes, r);  // q K_0 of all parts; q K_1 and q K_2 are BN columns on
         tmem_ld32(lanes + 32, r + 32);
         tmem_wait_ld();
         tmem_pin<BN>(r);
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t y[32];
+          tmem_ld32(lanes + BN + c, y);
+          tmem_wait_ld();
+          tmem_pin<32>(y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            r[c + e] = __float_as_uint(__uint_as_float(r[c + e]) + __uint_as_float(y[e]));
+        }
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::s_empty));
@@ -350,7 +371,7 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
         const uint32_t slot = it % NS, use = it / NS;
         const int64_t ahead = j + 1 < n ? look_up(w.kv0 + j + 1) : -1;
         if (use > 0 && !wait(empty + slot, (use - 1) & 1u)) break;
-        unsigned char* dst = smem + (isv ? C::V0 : 0) + slot * (3 * C::PART);
+        unsigned char* dst = smem + (isv ? C::V0 : C::K0) + slot * (3 * C::PART);
 #pragma unroll
         for (int first = 0; first < NP; first += HP) {
 #pragma unroll
@@ -378,8 +399,9 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
       // =============================================================== mma
       // The whole warp runs the role, its lanes alike; one of them issues.
       constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
-      constexpr uint32_t KVHI = umma_desc_hi(SL * 1024);
-      const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
+      constexpr uint32_t QHI = umma_desc_hi(1024), KVHI = umma_desc_hi(SL * 1024);
+      const uint32_t QK1 = umma_idesc_bf16(128, BN, false, p.negate != 0);      // one part of K
+      const uint32_t QK2 = umma_idesc_bf16(128, 2 * BN, false, p.negate != 0);  // two
       uint32_t it = 0, seg = 0;  // kv tiles whose P V is issued; segments
       while (ok && w.next(p)) {
         const int n = w.kv1 - w.kv0;
@@ -391,14 +413,24 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
             if (!wait(B::k_full + slot, (t / NS) & 1u)) break;
             if (t > 0 && !wait(B::s_empty, (t - 1u) & 1u)) break;
             tmem_fence_after();
-            const uint32_t k = umma_desc_lo(base + slot * (3 * C::PART), 16);
+            const uint32_t k = umma_desc_lo(base + C::K0 + slot * (3 * C::PART), 16);
+            const uint32_t q2 = umma_desc_lo(base, 16);
+            // 16 dims of K parts from `part` on
+            auto kd = [&](int part, int ks) {
+              return k + (uint32_t)(part * C::PART + (ks >> 2) * 1024 + (ks & 3) * 32) / 16;
+            };
 #pragma unroll
-            for (int x = 0; x < 6; ++x)
+            for (int ks = 0; ks < D / 16; ++ks)  // q2 [K0; K1]
+              umma_ss(tmem, q2 + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, QHI, kd(0, ks), KVHI, QK2,
+                      ks > 0);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)  // q0 K2
+              umma_ts(tmem + BN, tmem + C::Q0 + ks * 8, kd(2, ks), KVHI, QK1, 1);
+#pragma unroll
+            for (int i = 1; i >= 0; --i)  // q1 [K0; K1], q0 [K0; K1]
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
-                umma_ts(tmem, tmem + C::Q0 + kPartA[x] * (D / 2) + ks * 8,
-                        k + (kPartB[x] * C::PART + (ks >> 2) * 1024 + (ks & 3) * 32) / 16, KVHI, QK,
-                        x > 0 || ks > 0);
+                umma_ts(tmem, tmem + C::Q0 + i * (D / 2) + ks * 8, kd(0, ks), KVHI, QK2, 1);
             umma_commit(bar(B::s_full));
             umma_commit(bar(B::k_empty + slot));
           }
