@@ -285,11 +285,20 @@ def _device_now() -> int:
     return cur if cur >= 0 else -2
 
 
-def _at(t: torch.Tensor, name: str, cur: int) -> int:
-    """_dev's address and refusals, the usual case first."""
-    if t.get_device() == cur and t.is_contiguous():
-        return t.data_ptr()
-    return _dev(t, name, cur)
+class _Codes(dict):
+    def __missing__(self, dt):
+        return _dtype_code(dt)  # raises
+
+
+_CODES = _Codes({torch.float32: NP_F32, torch.bfloat16: NP_BF16})
+
+
+def _refuse(cur: int, **tensors) -> None:
+    """_dev's refusal of the first tensor that is not a contiguous one on
+    device ``cur`` (the calls below look at all of theirs in one condition)."""
+    for name, t in tensors.items():
+        if t is not None:
+            _dev(t, name, cur)
 
 
 def _stream_now(stream, cur: int) -> int:
@@ -352,9 +361,10 @@ def np_rope_append(q_out, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin
             raise ValueError(f"{name}: q_out must match q")
         if hq == 0:
             raise ValueError(f"{name}: q has no heads; pass q and q_out as None")
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype is not dt or w.shape != (d,)):
-            raise ValueError(f"{name}: {what} must be [head_dim] of the pools' dtype")
+    if q_weight is not None and (q_weight.dtype is not dt or q_weight.shape != (d,)):
+        raise ValueError(f"{name}: q_weight must be [head_dim] of the pools' dtype")
+    if k_weight is not None and (k_weight.dtype is not dt or k_weight.shape != (d,)):
+        raise ValueError(f"{name}: k_weight must be [head_dim] of the pools' dtype")
     if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,):
         raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
     if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2:
@@ -373,15 +383,25 @@ def np_rope_append(q_out, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin
     kp, ks = _token_rows(k_new, "k_new", cur, n, hk, d)
     vp, vs = _token_rows(v_new, "v_new", cur, n, hk, d)
     max_pos, rot = cos_sin.shape
+    if not (slot_mapping.get_device() == k_pool.get_device() == v_pool.get_device() ==
+            cos_sin.get_device() == positions.get_device() == cur and
+            (q_out is None or (q_out.get_device() == cur and q_out.is_contiguous())) and
+            (q_weight is None or (q_weight.get_device() == cur and q_weight.is_contiguous())) and
+            (k_weight is None or (k_weight.get_device() == cur and k_weight.is_contiguous())) and
+            (err_word is None or (err_word.get_device() == cur and err_word.is_contiguous())) and
+            slot_mapping.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous() and
+            cos_sin.is_contiguous() and positions.is_contiguous()):
+        _refuse(cur, q_out=q_out, slot_mapping=slot_mapping, k_pool=k_pool, v_pool=v_pool,
+                cos_sin=cos_sin, positions=positions, q_weight=q_weight, k_weight=k_weight,
+                err_word=err_word)
     st = load().np_rope_append_packed(_pack(
-        _ROPE_ARGS, name, 0 if q_out is None else _at(q_out, "q_out", cur), qp, kp, vp,
-        _at(slot_mapping, "slot_mapping", cur), _at(k_pool, "k_pool", cur),
-        _at(v_pool, "v_pool", cur), _at(cos_sin, "cos_sin", cur), _at(positions, "positions", cur),
-        0 if q_weight is None else _at(q_weight, "q_weight", cur),
-        0 if k_weight is None else _at(k_weight, "k_weight", cur),
-        0 if err_word is None else _at(err_word, "err_word", cur), _stream_now(stream, cur),
-        qs, ks, vs, nb, _dtype_code(dt), bs, hq, hk, d, max_pos, rot, axes, 1 if interleaved else 0,
-        n, 0 if sections is None else 1, *sec, eps))
+        _ROPE_ARGS, name, 0 if q_out is None else q_out.data_ptr(), qp, kp, vp,
+        slot_mapping.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), cos_sin.data_ptr(),
+        positions.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
+        0 if k_weight is None else k_weight.data_ptr(),
+        0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur),
+        qs, ks, vs, nb, _CODES[dt], bs, hq, hk, d, max_pos, rot, axes,
+        1 if interleaved else 0, n, 0 if sections is None else 1, *sec, eps))
     if st != NP_OK:
         raise NPError(st, name)
 
@@ -422,14 +442,24 @@ def np_paged_prefill(out, q, k_pool, v_pool, block_tables, context_lens, query_s
     if query_starts.dtype is not torch.int32 or query_starts.shape != (rows + 1,):
         raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
     cur = _device_now()
+    if not (out.get_device() == q.get_device() == k_pool.get_device() == v_pool.get_device() ==
+            block_tables.get_device() == context_lens.get_device() ==
+            query_starts.get_device() == cur and
+            (workspace is None or (workspace.get_device() == cur and workspace.is_contiguous())) and
+            (err_word is None or (err_word.get_device() == cur and err_word.is_contiguous())) and
+            out.is_contiguous() and q.is_contiguous() and k_pool.is_contiguous() and
+            v_pool.is_contiguous() and block_tables.is_contiguous() and
+            context_lens.is_contiguous() and query_starts.is_contiguous()):
+        _refuse(cur, out=out, q=q, k_pool=k_pool, v_pool=v_pool, block_tables=block_tables,
+                context_lens=context_lens, query_starts=query_starts, workspace=workspace,
+                err_word=err_word)
     st = load().np_paged_prefill_packed(_pack(
-        _PREFILL_ARGS, name, _at(out, "out", cur), _at(q, "q", cur), _at(k_pool, "k_pool", cur),
-        _at(v_pool, "v_pool", cur), _at(block_tables, "block_tables", cur),
-        _at(context_lens, "context_lens", cur), _at(query_starts, "query_starts", cur),
-        0 if workspace is None else _at(workspace, "workspace", cur),
-        0 if err_word is None else _at(err_word, "err_word", cur), _stream_now(stream, cur), nb,
-        0 if workspace is None else workspace.nbytes, _dtype_code(dt), bs, hk, d, mb, rows, tokens,
-        hq, scale))
+        _PREFILL_ARGS, name, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), query_starts.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(),
+        0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur), nb,
+        0 if workspace is None else workspace.nbytes, _CODES[dt], bs, hk, d, mb, rows,
+        tokens, hq, scale))
     if st != NP_OK:
         raise NPError(st, name)
 

@@ -182,6 +182,10 @@ def test_binding_refusals():
                      (dict(query_starts=qs[:2]), "query_starts"), (dict(query_starts=qs.long()), "query")]:
         with pytest.raises(ValueError, match=what):
             prefill(**kw)
+    if torch.cuda.is_available():  # a dtype the library does not store: refused once on a device
+        h = lambda t: t.half().cuda()  # noqa: E731
+        with pytest.raises(TypeError, match="dtype"):
+            npg.np_paged_prefill(h(q), h(q), h(pool), h(pool), bt.cuda(), cl.cuda(), qs.cuda(), 0.1, None)
     with pytest.raises(ValueError, match="cos_sin"):
         npg.prefill_step(q.clone(), q, k, k, slots, pool, pool, bt, cl, qs, 0.1, None, positions=pos)
     with pytest.raises(ValueError, match="rot_dim/2"):
