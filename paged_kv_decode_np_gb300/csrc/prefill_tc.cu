@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           if (j + 1 < n) pos.template step<NS>();
           bool have_k = false;
           if (j < n0) {
-            if (!wait(B::p_full, done0 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
+            if (!wait(B::kv_full + vslot, vphase) || !wait(B::p_full, done0 & 1u)) break;
             ++done0;
             issue_pv(0, 0, vslot, j > 0);
             if (j + 1 < n0) {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
               umma_commit(bar(B::o_full));
             }
           }
-          if (!wait(B::p_full + 1, done1 & 1u) || !wait(B::kv_full + vslot, vphase)) break;
+          if (!wait(B::kv_full + vslot, vphase) || !wait(B::p_full + 1, done1 & 1u)) break;
           ++done1;
           issue_pv(1, 1, vslot, j > 0);
           umma_commit(bar(B::kv_empty + vslot));
@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const int slot = pos.slot;
             const uint32_t phase = pos.phase;
             pos.template step<NS>();
-            if (!wait(B::p_full + (j & 1 ? 2 : 0), (j & 1 ? done2 : done0) & 1u) ||
-                !wait(B::kv_full + slot, phase))
+            if (!wait(B::kv_full + slot, phase) ||
+                !wait(B::p_full + (j & 1 ? 2 : 0), (j & 1 ? done2 : done0) & 1u))
               break;
             if (j & 1) ++done2;
             else ++done0;

@@ -363,16 +363,29 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
         }
       }
     };
+    // brings this warp's tokens of a tile into L2: the registers hold half a tile
+    // ahead, too little for HBM's latency.  Lines of 128 bytes, two a lane.
+    auto prefetch = [&](int64_t at) {
+      constexpr int LINES = D / 32 > 0 ? D / 32 : 1;  // of a token
+#pragma unroll
+      for (int i = 0; i < (16 * LINES + 31) / 32; ++i) {
+        const int x = i * 32 + lane;
+        const int64_t a = __shfl_sync(FULL, at, (x / LINES) & 15);
+        if (x < 16 * LINES && a >= 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(pool + a + (x % LINES) * 32));
+      }
+    };
     while (ok && w.next(p)) {
       const int n = w.kv1 - w.kv0;
       int64_t at = look_up(w.kv0);
+      int64_t ahead = n > 1 ? look_up(w.kv0 + 1) : -1;
       fetch(at, 0);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t slot = it % NS, use = it / NS;
-        const int64_t ahead = j + 1 < n ? look_up(w.kv0 + j + 1) : -1;
+        const int64_t ahead2 = j + 2 < n ? look_up(w.kv0 + j + 2) : -1;
         if (use > 0 && !wait(empty + slot, (use - 1) & 1u)) break;
         unsigned char* dst = smem + (isv ? C::V0 : C::K0) + slot * (3 * C::PART);
-#pragma unroll
+#pragma unroll 1
         for (int first = 0; first < NP; first += HP) {
 #pragma unroll
           for (int i = 0; i < HP; ++i) {
@@ -388,7 +401,9 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(full + slot));
         at = ahead;
+        ahead = ahead2;
         if (j + 1 < n) fetch(at, 0);
+        if (j + 2 < n) prefetch(ahead);
       }
       w.advance();
     }
