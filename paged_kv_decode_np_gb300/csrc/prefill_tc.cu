@@ -9,8 +9,8 @@
 //     P_w = 2^(c S_w - m)      fp32 -> bf16, into the tensor memory of S_w
 //     O_w += P_w V             tcgen05.mma, A = P_w from tensor memory
 // Roles: MT warpgroups of softmax (one thread a row: no shuffles), one warp
-// that issues the mma, one that loads q and K, one that loads V.  With two q tiles (head_dim <= 128)
-// the tensor cores work on one while the other's softmax runs:
+// that issues the mma, one that loads q and K, one that loads V.  With two q
+// tiles (head_dim <= 128) the tensor cores work on one while the other's softmax runs:
 //     ... PV_0(j), S_0(j+1) | PV_1(j), S_1(j+1) ...
 // and the two share every K and V tile, 128 operations a byte of it in
 // shared memory.  A unit of one tile (a row with few tokens; always at
@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
    if (warp == LOAD_K || warp == LOAD_V) {
     // =============================================================== loads
     // One warp copies q and the K tiles, another the V tiles: a copy costs its
-    // issuing thread tens of cycles, and a tile is up to 32 of them.
+    // issuing thread tens of cycles, and a tile is up to 16 of them (2048 16-byte
+    // ones token by token).
     const bool isv = warp == LOAD_V;
     const int G = p.group;
     uint32_t seg = 0, seq0 = 0;  // segments; ring tiles before this segment
@@ -331,8 +332,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     };
     // TILED: the pool slot of lane i's box of kv tile kt, read a tile ahead
     auto look_up = [&](int kt) {
-      const int tok = kt * BN + lane * p.box_tokens;
-      return lane * p.box_tokens < BN && tok < w.g.c ? (int32_t)pool_slot((unsigned)tok) : 0;
+      const int off = lane * p.box_tokens;
+      return off < BN && kt * BN + off < w.g.c ? (int32_t)pool_slot((unsigned)(kt * BN + off)) : 0;
     };
     // token by token: the pending tile's copies are complete, for the mma too
     auto report = [&]() {

@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
       int64_t at = look_up(w.kv0);
       int64_t ahead = n > 1 ? look_up(w.kv0 + 1) : -1;
       fetch(at, 0);
+      if (n > 1) prefetch(ahead);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t slot = it % NS, use = it / NS;
         const int64_t ahead2 = j + 2 < n ? look_up(w.kv0 + j + 2) : -1;

@@ -135,6 +135,29 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, ws=FAKE + 8 * MB + 128) == 3
 
 
+def test_packed_calls_check_the_same(lib):
+    assert lib.np_rope_append_packed(None) == 1
+    assert lib.np_paged_prefill_packed(None) == 1
+    import paged_kv_decode_np_gb300 as npg
+    # rows 0: nothing to do; a q_heads that kv_heads does not divide: refused
+    form = npg._PREFILL_ARGS
+    args = [FAKE, FAKE + MB, FAKE + 2 * MB, FAKE + 3 * MB, FAKE, FAKE, FAKE, FAKE + 8 * MB, 0, 0, 16,
+            1 << 30, 1, 16, 2, 128, 4, 0, 5, 4, 0.1]
+    assert lib.np_paged_prefill_packed(form.pack(*args)) == 0
+    args[-2] = 3
+    assert lib.np_paged_prefill_packed(form.pack(*args)) == 1
+    args[-2], args[17], args[11] = 4, 2, -5
+    assert lib.np_paged_prefill_packed(form.pack(*args)) == 3  # a negative workspace size
+    form = npg._ROPE_ARGS
+    args = [FAKE, FAKE + MB, FAKE + 2 * MB, FAKE + 3 * MB, FAKE, FAKE + 4 * MB, FAKE + 5 * MB, FAKE, FAKE,
+            0, 0, 0, 0, 512, 256, 256, 16, 1, 16, 4, 2, 128, 100, 128, 3, 0, 0, 1, 16, 24, 24, 0, 1e-6]
+    assert lib.np_rope_append_packed(form.pack(*args)) == 0    # no tokens
+    args[29] = 23
+    assert lib.np_rope_append_packed(form.pack(*args)) == 1    # sections do not add up
+    args[29], args[24] = 24, 5
+    assert lib.np_rope_append_packed(form.pack(*args)) == 2    # five axes
+
+
 def test_prefill_workspace(lib):
     import paged_kv_decode_np_gb300 as npg
     f = lib.np_paged_prefill_workspace_bytes

@@ -74,6 +74,15 @@ def test_tokens_and_heads(nplib, t, hq, hk):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,hq,hk", [(16, 5, 1), (32, 3, 2), (64, 6, 2), (128, 7, 3), (256, 2, 1)])
+@pytest.mark.parametrize("t", [511, 512, 2047, 2048, 2500])
+def test_every_block_size(nplib, dtype, d, hq, hk, t):
+    # the launcher chooses the block by the number of tokens: both sides of each border, heads that
+    # do not fill a block
+    _check(nplib, _case(dtype, t, hq, hk, d, d, norm=d != 32, fused=d == 64, seed=t + d), t % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("axes,rot,sections", [(3, 128, (16, 24, 24)), (3, 64, (5, 14, 13)),
                                                (2, 32, (0, 16)), (4, 64, (1, 0, 30, 1)),
