@@ -97,20 +97,22 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   int bt = 1;
   while (bt < p.bn && p.block_size % (2 * bt) == 0) bt *= 2;
   p.box_tokens = bt;
-  bool tiled = d >= 64 && bt >= 8 && slots <= INT32_MAX;
-  if (tiled) {
+  bool tiled = bt >= 8 && slots <= INT32_MAX;
+  if (d >= 64) {
     const cuuint64_t row = (cuuint64_t)p.kv_heads * d * 2, head = (cuuint64_t)d * 2;
     const cuuint32_t slabs = (cuuint32_t)d / 64;
+    const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)p.q_heads, (cuuint64_t)p.tokens};
+    const cuuint64_t q_strides[2] = {head, (cuuint64_t)p.q_heads * head};
+    const cuuint32_t q_box[3] = {64u, (cuuint32_t)p.group, (cuuint32_t)p.tile_tokens};
+    if (!encode_map(&p.tm_q, p.q, q_dims, q_strides, q_box)) return NP_ERR_CUDA;
     // 64 dims, token of 8, slab, group of 8 tokens, kv head
     const cuuint64_t kv_dims[5] = {64u, 8u, slabs, (cuuint64_t)slots / 8, (cuuint64_t)p.kv_heads};
     const cuuint64_t kv_strides[4] = {row, 128u, 8 * row, head};
     const cuuint32_t kv_box[5] = {64u, 8u, slabs, (cuuint32_t)bt / 8, 1u};
-    const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)p.q_heads, (cuuint64_t)p.tokens};
-    const cuuint64_t q_strides[2] = {head, (cuuint64_t)p.q_heads * head};
-    const cuuint32_t q_box[3] = {64u, (cuuint32_t)p.group, (cuuint32_t)p.tile_tokens};
-    tiled = encode_map(&p.tm_k, p.k_pool, kv_dims, kv_strides, kv_box) &&
-            encode_map(&p.tm_v, p.v_pool, kv_dims, kv_strides, kv_box) &&
-            encode_map(&p.tm_q, p.q, q_dims, q_strides, q_box);
+    tiled = tiled && encode_map(&p.tm_k, p.k_pool, kv_dims, kv_strides, kv_box) &&
+            encode_map(&p.tm_v, p.v_pool, kv_dims, kv_strides, kv_box);
+  } else {
+    tiled = false;
   }
   np_status rc = npk::launch_prefill_plan(p, s);
   if (rc != NP_OK) return rc;

@@ -57,7 +57,7 @@ struct TcCfg {
   static constexpr int THREADS = 128 * (MT + 1);    // whole warpgroups: setmaxnreg is theirs
   static constexpr int BM = 128 * MT;
   static constexpr uint32_t O0 = 256;               // tensor memory column of O_0
-  static_assert(NS >= 4, "ring");
+  static_assert(NS >= 4, "ring");  // (loaders wait for a slot's last use only: see kv_empty)
 };
 
 // Barriers, by index from the barrier area's start (8 bytes each).
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tail + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int LOAD_K = 4 * MT, LOAD_V = 4 * MT + 1, ISSUER = 4 * MT + 2;
+  constexpr int LOAD = 4 * MT, ISSUER = 4 * MT + 3;  // three warps load, or two (TILED)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i)
@@ -308,12 +308,13 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   } else {
    if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
    w.start(p, blockIdx.x);
-   if (warp == LOAD_K || warp == LOAD_V) {
+   if (warp < LOAD + (TILED ? 2 : 3)) {
     // =============================================================== loads
-    // One warp copies q and the K tiles, another the V tiles: a copy costs its
-    // issuing thread tens of cycles, and a tile is up to 16 of them (2048 16-byte
-    // ones token by token).
-    const bool isv = warp == LOAD_V;
+    // TILED: one warp copies q and the K tiles, another the V tiles (a copy costs
+    // its issuing thread tens of cycles, and a tile is up to 16 of them).  Token
+    // by token, 64 copies of the whole warp a tile and some 70 cycles each: three
+    // warps take the tiles in turn, the first one q too.
+    const int id = warp - LOAD;
     const int G = p.group;
     uint32_t seg = 0, seq0 = 0;  // segments; ring tiles before this segment
     int64_t last = -1;  // the last tile's ring position (for the drain)
@@ -351,13 +352,31 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             make_uint4(0u, 0u, 0u, 0u);
     };
     // copies kv tile kt of K or V to position `seq` of the ring; at: look_up(kt)
-    auto load_tile = [&](int kt, uint32_t seq, int32_t at) {
+    auto load_tile = [&](bool isv, int kt, uint32_t seq, int32_t at) {
       const uint32_t slot = seq % NS;
+      const int valid = min(BN, w.g.c - kt * BN);  // <= 0: a row without history
+      // token by token: byte offsets of tokens lane, 32 + lane, ..., on their way
+      // while the slot is waited for
+      constexpr int TOK = TILED ? 1 : BN / 32;
+      int64_t mine[TOK];
+      if constexpr (!TILED) {
+#pragma unroll
+        for (int x = 0; x < TOK; ++x)
+          mine[x] = x * 32 + lane < valid
+                        ? pool_slot((unsigned)(kt * BN + x * 32 + lane)) * p.kv_heads * (D * 2)
+                        : -1;
+      }
       if (seq >= NS) {
-        ok = __all_sync(FULL, mbar_wait(bar(B::kv_empty + slot), (seq / NS - 1u) & 1u, abort));
+        const uint32_t phase = (seq / NS - 1u) & 1u;
+        if (!TILED && pending >= 0 &&
+            !__all_sync(FULL, mbar_try_wait(bar(B::kv_empty + slot), phase))) {
+          cp_async_wait<0>();  // not yet: the mma may need the pending tile first
+          report();
+          pending = -1;
+        }
+        ok = __all_sync(FULL, mbar_wait(bar(B::kv_empty + slot), phase, abort));
         if (!ok) return;
       }
-      const int valid = min(BN, w.g.c - kt * BN);  // <= 0: a row without history
       const uint32_t dst = ring + slot * C::SLOT;
       if constexpr (TILED) {
         // a context's last V tile lands on a barrier of this warp's, which
@@ -389,18 +408,27 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         constexpr int CH = D / 8;      // 16-byte pieces of a token
         constexpr int PER = 32 / CH;   // tokens a warp copies at a time
         static_assert(CH <= 32, "a token's pieces fit a warp");
-        const char* src = static_cast<const char*>(isv ? p.v_pool : p.k_pool) + (int64_t)w.kvh * D * 2;
-        const int64_t token = (int64_t)p.kv_heads * D * 2;
+        const char* src = static_cast<const char*>(isv ? p.v_pool : p.k_pool) + (int64_t)w.kvh * D * 2 +
+                          lane % CH * 16;
+        // lane: piece ch of the tokens sub, sub + PER, ...; where token 8 a + b + sub
+        // (b a multiple of PER) goes, tc_kv_at, is a sum of what depends on a, on
+        // b and on the lane, but for the swizzle: b's bits flip the lane's
         const int ch = lane % CH, sub = lane / CH;
+        const uint32_t to = dst + (uint32_t)(((sub >> 3) * SL + (ch >> 3)) * 1024 + (sub & 7) * 128);
+        const uint32_t swz = (uint32_t)(((ch & 7) ^ (sub & 7)) << 4);
+        // (rolled: four roles share the instruction caches)
+#pragma unroll 1
         for (int r0 = 0; r0 < valid; r0 += 32) {
-          const int64_t mine = r0 + lane < valid ? pool_slot((unsigned)(kt * BN + r0 + lane)) : -1;
-#pragma unroll 4
+#pragma unroll 8
           for (int i = 0; i < 32; i += PER) {
-            const int row = r0 + i + sub;
-            const int64_t sl = __shfl_sync(FULL, mine, i + sub);
-            if (sl >= 0)
-              cp_async16(dst + tc_kv_at<SL>(row, ch), src + sl * token + ch * 16);
+            const int64_t at = __shfl_sync(FULL, mine[0], i + sub);
+            if (at >= 0)
+              cp_async16(to + (uint32_t)(((r0 + i) >> 3) * (SL * 1024) + (i & 7) * 128) +
+                             (swz ^ (uint32_t)((i & 7) << 4)),
+                         src + at);
           }
+#pragma unroll
+          for (int x = 0; x + 1 < TOK; ++x) mine[x] = mine[x + 1];
         }
         if (isv && valid < BN) clear_tail(slot, valid);
         cp_async_commit();
@@ -415,14 +443,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     while (ok && w.next(p)) {
       int32_t ahead = TILED ? look_up(w.kv0) : 0;
       const bool single = tc_single<D>(p, w);
-      if (!isv) {
+      if (id == 0) {
         // ---- q
         if (seg > 0) {
           ok = __all_sync(FULL, mbar_wait(bar(B::q_empty), (seg - 1) & 1u, abort));
           if (!ok) break;
         }
         const int qt = single ? 1 : 2;
-        if constexpr (TILED) {
+        if constexpr (D >= 64) {  // (tiled copies whatever the pools take)
           if (lane == 0)
             mbar_arrive_expect_tx(bar(B::q_full), (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
           __syncwarp();
@@ -453,14 +481,28 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       // ---- this warp's tiles, at their positions in the order the mma takes
       // them: K0 V0 K1 V1 ... with two q tiles, K0 K1 V0 K2 V1 ... V with one
       const int n = w.kv1 - w.kv0;
-      for (int j = 0; j < n && ok; ++j) {
-        const int32_t at = ahead;
-        if (TILED && j + 1 < n) ahead = look_up(w.kv0 + j + 1);
-        uint32_t seq;
-        if (!single) seq = 2u * j + (isv ? 1u : 0u);
-        else if (isv) seq = j + 1 < n ? 2u * j + 2u : 2u * n - 1u;
-        else seq = j == 0 ? 0u : 2u * j - 1u;
-        load_tile(w.kv0 + j, seq0 + seq, at);
+      if constexpr (TILED) {
+        const bool isv = id == 1;
+        for (int j = 0; j < n && ok; ++j) {
+          const int32_t at = ahead;
+          if (j + 1 < n) ahead = look_up(w.kv0 + j + 1);
+          uint32_t seq;
+          if (!single) seq = 2u * j + (isv ? 1u : 0u);
+          else if (isv) seq = j + 1 < n ? 2u * j + 2u : 2u * n - 1u;
+          else seq = j == 0 ? 0u : 2u * j - 1u;
+          load_tile(isv, w.kv0 + j, seq0 + seq, at);
+        }
+      } else {
+        for (int s = 0; s < 2 * n && ok; ++s) {
+          if ((seq0 + (uint32_t)s) % 3u != (uint32_t)id) continue;
+          bool isv = s & 1;
+          int j = s >> 1;
+          if (single) {
+            isv = s == 2 * n - 1 || (s > 0 && !isv);
+            j = s == 0 ? 0 : (s == 2 * n - 1 ? n - 1 : (isv ? s / 2 - 1 : (s + 1) / 2));
+          }
+          load_tile(isv, w.kv0 + j, seq0 + (uint32_t)s, 0);
+        }
       }
       seq0 += 2u * n;
       if constexpr (!TILED) {  // all of it is reported before the next q waits for it
@@ -471,8 +513,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       w.advance();
     }
     if (*abort) {  // never leave copies in flight (bounded)
+      if (D >= 64 && id == 0 && seg > 0) mbar_wait_drain(bar(B::q_full), (seg - 1) & 1u);
       if constexpr (TILED) {
-        if (!isv && seg > 0) mbar_wait_drain(bar(B::q_full), (seg - 1) & 1u);
         // the last NS positions up to this warp's last tile: those of the other
         // warp's that never came run into the wait's limit
         for (int64_t q = last > NS ? last - NS : 0; q <= last; ++q)
