@@ -26,6 +26,17 @@ same buffers again and again can check and convert the arguments once::
     step = npg.PreparedStep(out, q, k_new, v_new, slot_mapping, k_pool, v_pool,
                             block_tables, context_lens, scale, S, ws)
     step.launch()   # the same library calls, ~4 us of host time
+
+A prompt, or a chunk of one, of several rows (rotated, appended, attended)::
+
+    table = npg.rope_table(max_positions, head_dim)
+    ws = npg.prefill_workspace(head_dim)
+    npg.prefill_step(out, q, k_new, v_new, slot_mapping, k_pool, v_pool,
+                     block_tables, context_lens, query_starts, scale, ws,
+                     cos_sin=table, positions=positions)
+
+The new tokens of a decode step are rotated and appended by np_rope_append,
+then read by np_paged_decode.
 """
 from __future__ import annotations
 

@@ -1,11 +1,14 @@
-// prefill_simt.cu -- np_paged_prefill on the FMA pipes: fp32 pools, every
-// head_dim and block size.
+// prefill_simt.cu -- np_paged_prefill on the FMA pipes: fp32 pools of head_dim
+// 256, whose three bf16 parts of q, K and V do not fit in shared memory beside
+// one another (narrower heads: prefill_tc32.cu).
 //
 // A unit is one tile of 64 (token, head) rows; a kv tile is 64 tokens.  256
 // threads form S = Q K^T as 4 x 4 microtiles from shared memory (rows 4 ty +
 // i, tokens tx + 16 j), run the online softmax with each row spread over the
 // 16 lanes of its ty, and add P V as 4 rows x (D / 16) dims.  Everything is
-// fp32.
+// fp32.  Bound: the FMA pipes behind shared memory (8 16-byte reads for 64
+// products); eight chunks of 71-184 tokens over 833-2031 positions, 8 / 1
+// heads: 447 us, 27 TFLOP/s.
 #include "prefill.cuh"
 
 namespace npk {
@@ -14,7 +17,7 @@ constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 64;
 constexpr int kSimtBn = 64;
 
-template <typename T, int D>
+template <int D>
 struct SimtSmem {
   static constexpr int LD = D + 4;        // rows start on different banks
   static constexpr int LP = kSimtBn + 4;
@@ -22,11 +25,12 @@ struct SimtSmem {
   static constexpr size_t bytes = floats * 4 + kSimtBn * 8;
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __grid_constant__
                                                                        PrefillParams p) {
+  using T = float;
   using S = Storage<T>;
-  using M = SimtSmem<T, D>;
+  using M = SimtSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int NG = (D + 63) / 64;   // groups of 4 dims a thread owns: 4 tx + 64 j
@@ -231,30 +235,13 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
   }
 }
 
-template <typename T, int D>
-static np_status launch_simt(const PrefillParams& p, cudaStream_t s) {
-  constexpr size_t bytes = SimtSmem<T, D>::bytes;
+np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s) {
+  constexpr size_t bytes = SimtSmem<256>::bytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
   static unsigned long long allowed = 0;
-  const np_status rc = allow_smem(prefill_simt_kernel<T, D>, bytes, &allowed);
+  const np_status rc = allow_smem(prefill_simt_kernel<256>, bytes, &allowed);
   if (rc != NP_OK) return rc;
-  return launch_dependent(prefill_simt_kernel<T, D>, p.ctas, 1, kSimtThreads, bytes, s, p);
-}
-
-template <typename T>
-static np_status launch_simt_dim(const PrefillParams& p, cudaStream_t s) {
-  switch (p.head_dim) {
-    case 16: return launch_simt<T, 16>(p, s);
-    case 32: return launch_simt<T, 32>(p, s);
-    case 64: return launch_simt<T, 64>(p, s);
-    case 128: return launch_simt<T, 128>(p, s);
-    case 256: return launch_simt<T, 256>(p, s);
-  }
-  return NP_ERR_UNSUPPORTED;
-}
-
-np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s) {
-  return launch_simt_dim<float>(p, s);
+  return launch_dependent(prefill_simt_kernel<256>, p.ctas, 1, kSimtThreads, bytes, s, p);
 }
 
 }  // namespace npk
