@@ -259,6 +259,26 @@ def test_same_bits_every_time_on_any_stream_and_in_graphs(nplib, dtype, d):
     assert ((outs[0].double() - ref).abs() <= chunk_tolerance(ref, bound, dtype, d, 900)).all()
 
 
+@pytest.mark.parametrize("a,b", [((BF, 32), (F32, 16)), ((BF, 16), (F32, 32)), ((F32, 16), (F32, 16)),
+                                 ((BF, 128), (F32, 64)), ((BF, 256), (F32, 256))])
+def test_two_different_calls_at_once(nplib, a, b):
+    # narrow heads leave room on an SM for a block of each call: both want its tensor memory
+    rows = [(300, 900), (1, 2000), (65, 65)]
+    calls = [_check(nplib, dtype, d, 4, 4, 16, rows, seed=9 + i) for i, (dtype, d) in enumerate((a, b))]
+    outs = [torch.zeros_like(want) for _, want in calls]
+    ws = [nplib.prefill_workspace(inp["q"].shape[2]).fill_(255) for inp, _ in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for o in outs:
+        o.fill_(77.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (inp, _), o, w, st in zip(calls, outs, ws, streams):
+            _run(nplib, inp, inp["q"].shape[2] ** -0.5, out=o, ws=w, stream=st)
+    torch.cuda.synchronize()
+    for (_, want), o in zip(calls, outs):
+        assert torch.equal(o, want)
+
+
 @pytest.mark.parametrize("dtype,hk,d,bs", [(BF, 8, 128, 16), (BF, 8, 128, 7), (F32, 8, 128, 16)])
 def test_pool_offsets_past_32_bits(nplib, dtype, hk, d, bs):
     nb = (2 ** 31 // (hk * d) + 8192) // bs  # more than 2^31 elements
