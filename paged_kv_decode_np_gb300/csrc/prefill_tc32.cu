@@ -24,7 +24,10 @@
 // tile's parts lie one after the other, and q_i times [K_0; K_1] gives q_i K_0 in
 // the first 64 columns and q_i K_1 in the others (q_2 K_1 comes for nothing);
 // q_0 K_2 joins the latter, and the softmax adds the two.  Four mma a 16-dim
-// step instead of six.  P and q's first two parts are A operands in tensor
+// step instead of six.  Successive mma run in order only where they share their
+// accumulator and their shape, and q_0 K_2 is 64 wide over half of the columns:
+// it is issued once the others are complete (their own commit), and the next
+// tile's first mma once the softmax has read these (s_empty).  P and q's first two parts are A operands in tensor
 // memory, which has no room for q's third: that one is in shared memory.
 //
 // Bound: the softmax warps, one a scheduler (~5500 cycles a kv tile), and behind
@@ -61,7 +64,8 @@ struct Tc32Cfg {
 struct Tc32Bars {
   static constexpr int k_full = 0, k_empty = 4, v_full = 8, v_empty = 12;  // of NS <= 4 slots
   static constexpr int q_full = 16, s_full = 17, s_empty = 18, p_full = 19, pv_done = 20;
-  static constexpr int drain = 21, count = 22;
+  static constexpr int s_part = 21;  // the products with [K_0; K_1] are complete
+  static constexpr int drain = 22, count = 23;
 };
 
 // The parts of a product, the small ones first: (a part, b part).
@@ -444,13 +448,16 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
               umma_ss(tmem, q2 + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, QHI, kd(0, ks), KVHI, QK2,
                       ks > 0);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)  // q0 K2
-              umma_ts(tmem + BN, tmem + C::Q0 + ks * 8, kd(2, ks), KVHI, QK1, 1);
-#pragma unroll
             for (int i = 1; i >= 0; --i)  // q1 [K0; K1], q0 [K0; K1]
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
                 umma_ts(tmem, tmem + C::Q0 + i * (D / 2) + ks * 8, kd(0, ks), KVHI, QK2, 1);
+            umma_commit(bar(B::s_part));  // another shape follows on their columns
+            if (!wait(B::s_part, t & 1u)) break;
+            tmem_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)  // q0 K2
+              umma_ts(tmem + BN, tmem + C::Q0 + ks * 8, kd(2, ks), KVHI, QK1, 1);
             umma_commit(bar(B::s_full));
             umma_commit(bar(B::k_empty + slot));
           }
