@@ -6,16 +6,25 @@
 // and V serves G heads and a one-token row fills G rows.  Per kv tile of BN
 // tokens and q tile w:
 //     S_w = Q_w K^T            tcgen05.mma, both operands in shared memory
-//     P_w = 2^(c S_w - m)      fp32 -> bf16, into the tensor memory of S_w
+//     P_w = 2^(c S_w - m)      fp32 -> bf16, into tensor memory
 //     O_w += P_w V             tcgen05.mma, A = P_w from tensor memory
 // Roles: MT warpgroups of softmax (one thread a row: no shuffles), one warp
 // that issues the mma, one that loads q and K, one that loads V.  With two q
 // tiles (head_dim <= 128) the tensor cores work on one while the other's softmax runs:
 //     ... PV_0(j), S_0(j+1) | PV_1(j), S_1(j+1) ...
 // and the two share every K and V tile, 128 operations a byte of it in
-// shared memory.  A unit of one tile (a row with few tokens; always at
-// head_dim 256, whose O takes 256 of the 512 columns) uses both S buffers for
-// it: S(j+1) runs under softmax j.
+// shared memory.  In a unit of one tile (a row with few tokens; always at
+// head_dim 256, whose O takes 256 of the 512 columns) S(j+1) runs under softmax j.
+//
+// Tensor memory: one S, two P, O.  mma of different shapes or accumulators have
+// no order among themselves, so none may write what an earlier one still reads:
+// - S is free once the softmax has read it, into registers, at its beginning
+//   (s_read; the issuing warp waits for that of the S before, whichever tile's);
+// - a P (a q tile's; of one tile alone, that of every other kv tile) is written
+//   after its tile's S(j) is complete, whose commit covers every P V that was
+//   issued before S(j) and with that all uses of this P.
+// (With P over its S, as one buffer a tile, S(j+1) has to wait for P V(j): mixed
+// batch 254 us, chunk 1024 of 131072 3490 us, prompts 267 us; so 242, 3250, 240.)
 //
 // The running maximum is replaced only where it would grow by more than 2^8
 // (m need not be the maximum, only near it: p <= 256 keeps its relative
@@ -64,7 +73,8 @@ struct TcCfg {
   static constexpr int SMEM = 1024 + BARS + 512;    // + up to 1024 of alignment
   static constexpr int THREADS = 128 * (MT + 1);    // whole warpgroups: setmaxnreg is theirs
   static constexpr int BM = 128 * MT;
-  static constexpr uint32_t O0 = 256;               // tensor memory column of O_0
+  // tensor memory columns: S at 0 (BN), the two P (BN / 2 each), O
+  static constexpr uint32_t P0 = BN, O0 = 256;
   // A loader waits for the slot's last use only, and skips the other loaders'
   // phases: its tile before, at most 3 positions back, waited for a slot that was
   // freed after the use before that.
@@ -76,10 +86,14 @@ template <int D>
 struct TcBars {
   static constexpr int NS = TcCfg<D>::NS;
   static constexpr int q_full = 0, q_empty = 1, kv_full = 2, kv_empty = 2 + NS;
-  // of an S buffer: 0 and 1 by their q tiles, 2 buffer 1 lent to q tile 0.  A
-  // warp waits on all phases of a barrier or on none: one that skips some
+  // s_*, o_full: by q tile; p_full: by P buffer.  Four warps arrive on s_read and
+  // p_full, each once a phase: what a warp arrives for next was issued after a
+  // wait for the phase before (S(j+1) after s_read of S(j); the S of a P buffer's
+  // next use after the P V of this one).
+  // A warp waits on all phases of a barrier or on none: one that skips some
   // could take an earlier phase of the same parity for its own.
-  static constexpr int s_full = 2 + 2 * NS, p_full = s_full + 3, o_full = p_full + 3;
+  static constexpr int s_full = 2 + 2 * NS, s_read = s_full + 2, p_full = s_read + 2;
+  static constexpr int o_full = p_full + 2;
   static constexpr int pv_done = o_full + 2;  // one-tile units: one phase a kv tile
   static constexpr int drain = pv_done + 1, tail_full = drain + 1, count = tail_full + 1;
 };
@@ -133,7 +147,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i)
-      mbar_init(bar(i), i >= B::p_full && i < B::p_full + 3 ? 4 : 1);
+      mbar_init(bar(i), i >= B::s_read && i < B::o_full ? 4 : 1);  // s_read, p_full: four warps
     *abort = 0;
     fence_mbar_init();
   }
@@ -160,7 +174,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const uint32_t o_at = lanes + C::O0 + t * D;
     const int tt = row / p.group, h = row - tt * p.group;
     constexpr int OC = D < 32 ? 16 : 32;             // columns of O at a time
-    uint32_t used = 0, lent = 0;  // S tiles so far in the tile's own buffer; in the lent one
+    uint32_t used = 0;            // S tiles so far
     uint32_t pv = 0, oc = 0;      // phases of pv_done; of this tile's o_full
     while (ok && w.next(p)) {
       const int64_t first = ((int64_t)w.m * MT + t) * p.tile_tokens;
@@ -177,25 +191,29 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const int lim = live ? (int)((int64_t)w.g.c - w.g.n + tok) : INT_MAX;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        const bool alt = single && (j & 1);  // in the lent buffer
-        const int sb = alt ? 2 : t;          // barrier index
-        ok = __all_sync(FULL, mbar_wait(bar(B::s_full + sb), (alt ? lent : used) & 1u, abort));
+        const int pb = single ? (j & 1) : t;  // P buffer
+        ok = __all_sync(FULL, mbar_wait(bar(B::s_full + t), used & 1u, abort));
         if (!ok) break;
-        if (alt) ++lent;
-        else ++used;
-        if (idle) {  // P of these rows is whatever S left: it moves their own O only
-          if (lane == 0) mbar_arrive(bar(B::p_full + sb));
+        ++used;
+        if (idle) {  // P of these rows is whatever is there: it moves their own O only
+          if (lane == 0) {
+            mbar_arrive(bar(B::s_read + t));
+            mbar_arrive(bar(B::p_full + pb));
+          }
           continue;
         }
         tmem_fence_after();
-        const uint32_t s_at = lanes + (alt ? 1 : t) * BN;
+        const uint32_t p_at = lanes + C::P0 + pb * (BN / 2);
         const int rel = lim - (w.kv0 + j) * BN;  // last visible column
         const bool masked = __any_sync(FULL, rel < BN - 1);
         uint32_t r[BN];  // the row of S
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) tmem_ld32(s_at + c, r + c);
+        for (int c = 0; c < BN; c += 32) tmem_ld32(lanes + c, r + c);
         tmem_wait_ld();
         tmem_pin<BN>(r);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::s_read + t));
         if (masked) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
@@ -251,13 +269,13 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
             pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          tmem_st16(s_at + (c >> 1), pk);
+          tmem_st16(p_at + (c >> 1), pk);
         }
         l += l0 + l1;
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B::p_full + sb));
+        if (lane == 0) mbar_arrive(bar(B::p_full + pb));
       }
       if (!ok) break;
       if (n > 0) {
@@ -284,7 +302,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         part[urow] = m;
         part[C::BM + urow] = l;
       }
-#pragma unroll
+      // (rolled, as is the mma's loop over all of a unit: four roles share the
+      // instruction caches.  Prompts 260 us unrolled, 240 so)
+#pragma unroll 1
       for (int c = 0; c < D; c += OC) {
         uint32_t o[OC];
         if (n > 0) {
@@ -542,26 +562,31 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
     RingPos pos{0, 0};
     uint32_t seg = 0;
-    uint32_t done0 = 0, done1 = 0, done2 = 0;  // phases of each p_full so far
+    uint32_t done0 = 0, done1 = 0;  // phases of each p_full so far
+    int s_bar = -1;                 // s_read of the last S issued, and its phase
+    uint32_t s_phase = 0, issued0 = 0, issued1 = 0;
 
     auto wait = [&](int b, uint32_t phase) {
       ok = ok && __all_sync(FULL, mbar_wait(bar(b), phase, abort));
       return ok;
     };
-    // S = Q_t K^T into buffer sb (2: buffer 1, lent)
-    auto issue_s = [&](int t, int sb, int slot) {
-      const uint32_t d = tmem + (sb ? BN : 0);
+    auto issue_s = [&](int t, int slot) {  // S = Q_t K^T, once the S before has been read
+      if (s_bar >= 0 && !wait(s_bar, s_phase)) return false;
+      s_bar = B::s_read + t;
+      s_phase = (t ? issued1++ : issued0++) & 1u;
+      tmem_fence_after();
       const uint32_t q = umma_desc_lo(base + (uint32_t)t * C::QT, 16);
       const uint32_t k = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 16);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
-        umma_ss(d, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u, QHI,
+        umma_ss(tmem, q + ((ks >> 2) * 16384u + (ks & 3) * 32u) / 16u, QHI,
                 k + ((ks >> 2) * 1024u + (ks & 3) * 32u) / 16u, KVHI, QK, ks > 0);
-      umma_commit(bar(B::s_full + sb));
+      umma_commit(bar(B::s_full + t));
+      return true;
     };
-    auto issue_pv = [&](int t, int sb, int slot, bool acc) {  // O_t += P V
+    auto issue_pv = [&](int t, int pb, int slot, bool acc) {  // O_t += P V, P in buffer pb
       tmem_fence_after();
-      const uint32_t pa = tmem + (sb ? BN : 0);
+      const uint32_t pa = tmem + C::P0 + pb * (BN / 2);
       const uint32_t v = umma_desc_lo(ring + (uint32_t)slot * C::SLOT, 1024);
 #pragma unroll
       for (int ks = 0; ks < BN / 16; ++ks)
@@ -575,40 +600,34 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       ++seg;
       if (!tc_single<D>(p, w)) {
         const int n0 = tc_tiles<D>(p, w, 0);  // <= n: the unit's last tokens see the most
-        int kslot = pos.slot;
-        if (!wait(B::kv_full + kslot, pos.phase)) break;
-        pos.template step<NS>();
-        if (n0 > 0) issue_s(0, 0, kslot);
-        issue_s(1, 1, kslot);
-        umma_commit(bar(B::kv_empty + kslot));
-        if (n == 1) umma_commit(bar(B::q_empty));
-        for (int j = 0; j < n; ++j) {
+#pragma unroll 1
+        for (int j = -1; j < n; ++j) {  // P V_t(j), S_t(j + 1)
           const int vslot = pos.slot;
           const uint32_t vphase = pos.phase;
-          pos.template step<NS>();
-          kslot = pos.slot;
+          if (j >= 0) pos.template step<NS>();
+          const int kslot = pos.slot;
           const uint32_t kphase = pos.phase;
           if (j + 1 < n) pos.template step<NS>();
-          bool have_k = false;
           if (j < n0) {
-            if (!wait(B::kv_full + vslot, vphase) || !wait(B::p_full, done0 & 1u)) break;
-            ++done0;
-            issue_pv(0, 0, vslot, j > 0);
+            if (j >= 0) {
+              if (!wait(B::kv_full + vslot, vphase) || !wait(B::p_full, done0 & 1u)) break;
+              ++done0;
+              issue_pv(0, 0, vslot, j > 0);
+            }
             if (j + 1 < n0) {
-              if (!wait(B::kv_full + kslot, kphase)) break;
-              have_k = true;
-              issue_s(0, 0, kslot);
-            } else {
+              if (!wait(B::kv_full + kslot, kphase) || !issue_s(0, kslot)) break;
+            } else if (j >= 0) {
               umma_commit(bar(B::o_full));
             }
           }
-          if (!wait(B::kv_full + vslot, vphase) || !wait(B::p_full + 1, done1 & 1u)) break;
-          ++done1;
-          issue_pv(1, 1, vslot, j > 0);
-          umma_commit(bar(B::kv_empty + vslot));
+          if (j >= 0) {
+            if (!wait(B::kv_full + vslot, vphase) || !wait(B::p_full + 1, done1 & 1u)) break;
+            ++done1;
+            issue_pv(1, 1, vslot, j > 0);
+            umma_commit(bar(B::kv_empty + vslot));
+          }
           if (j + 1 < n) {
-            if (!have_k && !wait(B::kv_full + kslot, kphase)) break;
-            issue_s(1, 1, kslot);
+            if (!wait(B::kv_full + kslot, kphase) || !issue_s(1, kslot)) break;
             umma_commit(bar(B::kv_empty + kslot));
             if (j + 2 == n) umma_commit(bar(B::q_empty));
           } else {
@@ -617,11 +636,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         }
       } else {
         for (int j = -1; j < n; ++j) {
-          if (j + 1 < n) {  // S(j + 1), into the buffer that P(j - 1) has left
+          if (j + 1 < n) {  // S(j + 1)
             const int slot = pos.slot;
-            if (!wait(B::kv_full + slot, pos.phase)) break;
+            if (!wait(B::kv_full + slot, pos.phase) || !issue_s(0, slot)) break;
             pos.template step<NS>();
-            issue_s(0, (j + 1) & 1 ? 2 : 0, slot);
             umma_commit(bar(B::kv_empty + slot));
             if (j + 2 == n) umma_commit(bar(B::q_empty));
           }
@@ -630,11 +648,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const uint32_t phase = pos.phase;
             pos.template step<NS>();
             if (!wait(B::kv_full + slot, phase) ||
-                !wait(B::p_full + (j & 1 ? 2 : 0), (j & 1 ? done2 : done0) & 1u))
+                !wait(B::p_full + (j & 1), (j & 1 ? done1 : done0) & 1u))
               break;
-            if (j & 1) ++done2;
+            if (j & 1) ++done1;
             else ++done0;
-            issue_pv(0, j & 1 ? 2 : 0, slot, j > 0);
+            issue_pv(0, j & 1, slot, j > 0);
             umma_commit(bar(B::pv_done));
             umma_commit(bar(B::kv_empty + slot));
             if (j + 1 == n) umma_commit(bar(B::o_full));
