@@ -114,6 +114,31 @@ __device__ __forceinline__ bool tc_single(const PrefillParams& p, const PrefillW
   return TcCfg<D>::MT == 1 || ((int64_t)w.m * TcCfg<D>::MT + 1) * p.tile_tokens >= w.g.n;
 }
 
+// mbar_wait of a warp that may have nothing to do for a long while beside a block
+// that works on: the limit runs from the last tile the block has made.
+__device__ __forceinline__ bool tc_wait_beside(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               volatile uint32_t* tiles) {
+  if (mbar_try_wait(bar, parity)) return true;
+  long long t0 = clock64();
+  uint32_t seen = *tiles;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      const long long t = clock64();
+      if (t - t0 > kWaitLimitCycles) {
+        const uint32_t now = *tiles;
+        if (now == seen) {
+          *abort = 1;
+          return false;
+        }
+        seen = now;
+        t0 = t;
+      }
+    }
+  }
+}
+
 struct RingPos {
   int slot;
   uint32_t phase;
@@ -141,6 +166,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   volatile uint32_t* tail = reinterpret_cast<volatile uint32_t*>(smem + C::BARS + 8 * B::count);
   volatile int* abort = reinterpret_cast<volatile int*>(tail + 1);
+  volatile uint32_t* tiles = tail + 2;  // kv tiles of one-tile units so far (tc_wait_beside)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int LOAD = 4 * MT, ISSUER = 4 * MT + 3;  // three warps load, or two (TILED)
@@ -149,6 +175,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     for (int i = 0; i < B::count; ++i)
       mbar_init(bar(i), i >= B::s_read && i < B::o_full ? 4 : 1);  // s_read, p_full: four warps
     *abort = 0;
+    *tiles = 0;
     fence_mbar_init();
   }
   if (warp == ISSUER) tmem_alloc(smem_u32(const_cast<uint32_t*>(tail)), 512);
@@ -192,7 +219,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int pb = single ? (j & 1) : t;  // P buffer
-        ok = __all_sync(FULL, mbar_wait(bar(B::s_full + t), used & 1u, abort));
+        // (tile 1's warps pass over the units of one tile before, a share's worth of them)
+        ok = __all_sync(FULL, tc_wait_beside(bar(B::s_full + t), used & 1u, abort, tiles));
         if (!ok) break;
         ++used;
         if (idle) {  // P of these rows is whatever is there: it moves their own O only
@@ -655,6 +683,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             issue_pv(0, j & 1, slot, j > 0);
             umma_commit(bar(B::pv_done));
             umma_commit(bar(B::kv_empty + slot));
+            if (MT == 2 && lane == 0) *tiles = *tiles + 1u;
             if (j + 1 == n) umma_commit(bar(B::o_full));
           }
         }
