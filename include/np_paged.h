@@ -273,6 +273,12 @@ typedef struct np_paged_prefill_args {
 
 np_status np_paged_prefill_packed(const np_paged_prefill_args* args);
 
+/* What np_paged_prefill_packed would return before its first launch: NP_OK
+ * where it would launch (or has nothing to do).  Launches nothing, reads no
+ * device memory: a step that appends before it attends asks first, so that a
+ * refusal leaves the pools and q as they were. */
+np_status np_paged_prefill_check(const np_paged_prefill_args* args);
+
 /*
  * np_paged_decode_plan -- the schedule the library recommends, as a
  * num_splits value for np_paged_decode.  Pure host arithmetic on STATIC

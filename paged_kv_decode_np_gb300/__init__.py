@@ -152,7 +152,7 @@ def _declare_prompt(lib: ctypes.CDLL) -> None:
                                    _I32, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32,
                                    ctypes.POINTER(_I32), _I32, _P, _P, ctypes.c_float, _I32, _P,
                                    _P]
-    for name in ("np_rope_append_packed", "np_paged_prefill_packed"):
+    for name in ("np_rope_append_packed", "np_paged_prefill_packed", "np_paged_prefill_check"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.c_char_p]
@@ -435,6 +435,19 @@ def np_paged_prefill(out, q, k_pool, v_pool, block_tables, context_lens, query_s
     np_paged.h).  q/out [tokens, q_heads, head_dim]; query_starts int32
     [rows + 1]; row r's chunk q[query_starts[r]:query_starts[r + 1]] holds its
     newest positions, already appended to the pools."""
+    _launch_prefill(_prefill_args(out, q, k_pool, v_pool, block_tables, context_lens, query_starts,
+                                  scale, workspace, err_word, stream))
+
+
+def _launch_prefill(packed: bytes) -> None:
+    st = load().np_paged_prefill_packed(packed)
+    if st != NP_OK:
+        raise NPError(st, "np_paged_prefill")
+
+
+def _prefill_args(out, q, k_pool, v_pool, block_tables, context_lens, query_starts, scale,
+                  workspace, err_word, stream) -> bytes:
+    """np_paged_prefill's packed arguments, after the binding's checks."""
     name = "np_paged_prefill"
     if q.dim() != 3 or k_pool.dim() != 4:
         raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim]")
@@ -464,15 +477,13 @@ def np_paged_prefill(out, q, k_pool, v_pool, block_tables, context_lens, query_s
         _refuse(cur, out=out, q=q, k_pool=k_pool, v_pool=v_pool, block_tables=block_tables,
                 context_lens=context_lens, query_starts=query_starts, workspace=workspace,
                 err_word=err_word)
-    st = load().np_paged_prefill_packed(_pack(
+    return _pack(
         _PREFILL_ARGS, name, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
         block_tables.data_ptr(), context_lens.data_ptr(), query_starts.data_ptr(),
         0 if workspace is None else workspace.data_ptr(),
         0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur), nb,
         0 if workspace is None else workspace.nbytes, _CODES[dt], bs, hk, d, mb, rows,
-        tokens, hq, scale))
-    if st != NP_OK:
-        raise NPError(st, name)
+        tokens, hq, scale)
 
 
 def prefill_step(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, block_tables, context_lens,
@@ -483,18 +494,24 @@ def prefill_step(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, block_table
     their attention.  With ``cos_sin`` and ``positions`` np_rope_append rotates
     (and, with weights, normalises) q and k on the way: the rotated q goes to
     ``q_rotated`` (default: back into q, which must then be dense).  Without
-    them np_kv_append copies k_new and v_new as they are."""
+    them np_kv_append copies k_new and v_new as they are.  What either call
+    refuses is refused before the first launch: nothing is written, and the
+    step may be called again."""
+    if cos_sin is None and any(x is not None for x in (positions, sections, q_weight, k_weight,
+                                                       q_rotated)):
+        raise ValueError("prefill_step: positions, sections, weights and q_rotated need cos_sin")
+    qr = q if q_rotated is None else q_rotated
+    attend = _prefill_args(out, qr, k_pool, v_pool, block_tables, context_lens, query_starts, scale,
+                           workspace, err_word, stream)
+    st = load().np_paged_prefill_check(attend)
+    if st != NP_OK:
+        raise NPError(st, "np_paged_prefill")
     if cos_sin is not None:
-        qr = q if q_rotated is None else q_rotated
         np_rope_append(qr, q, k_new, v_new, slot_mapping, k_pool, v_pool, cos_sin, positions,
                        sections, interleaved, q_weight, k_weight, eps, err_word, stream)
     else:
-        if any(x is not None for x in (positions, sections, q_weight, k_weight, q_rotated)):
-            raise ValueError("prefill_step: positions, sections, weights and q_rotated need cos_sin")
-        qr = q
         np_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, err_word, stream)
-    np_paged_prefill(out, qr, k_pool, v_pool, block_tables, context_lens, query_starts, scale,
-                     workspace, err_word, stream)
+    _launch_prefill(attend)
 
 
 def np_paged_decode_plan(rows, q_heads, kv_heads, head_dim, block_size, max_blocks_per_row,

@@ -162,6 +162,92 @@ extern "C" size_t np_paged_prefill_workspace_bytes(int32_t head_dim) {
          2 * npk::kPrefillMaxCtas * npk::prefill_part_floats(unit_rows(head_dim), head_dim) * 4;
 }
 
+namespace {
+
+// The checks of a call; *run: whether there is something to launch.
+np_status check_prefill(const np_paged_prefill_args& a, bool* run) {
+  *run = false;
+  const int es = a.dtype == NP_F32 ? 4 : (a.dtype == NP_BF16 ? 2 : 0);
+  if (es == 0) return NP_ERR_UNSUPPORTED;
+  if (a.rows < 0 || a.num_tokens < 0 || a.q_heads <= 0 || a.kv_heads <= 0 ||
+      a.q_heads % a.kv_heads != 0 || a.num_blocks <= 0 || a.block_size <= 0 ||
+      a.max_blocks_per_row <= 0 || a.head_dim <= 0 || !isfinite(a.scale))
+    return NP_ERR_INVALID_ARG;
+  const int d = a.head_dim;
+  if (d != 16 && d != 32 && d != 64 && d != 128 && d != 256) return NP_ERR_UNSUPPORTED;
+  if (a.q_heads / a.kv_heads > (a.dtype == NP_BF16 ? 16 : 8)) return NP_ERR_UNSUPPORTED;
+  int64_t slots = 0, pool = 0, cap = 0, qn = 0, tab = 0;
+  if (!mul_ok(a.num_blocks, a.block_size, &slots) ||
+      !mul_ok(slots, (int64_t)a.kv_heads * d * es, &pool) ||
+      !mul_ok(a.num_tokens, (int64_t)a.q_heads * d * es, &qn) ||
+      !mul_ok(a.max_blocks_per_row, a.block_size, &cap) || !mul_ok(a.rows, a.max_blocks_per_row, &tab))
+    return NP_ERR_OUT_OF_RANGE;
+  // positions are int32 with some kv tiles to spare
+  if (cap > INT32_MAX - 1024 || a.num_tokens > INT32_MAX - 512) return NP_ERR_UNSUPPORTED;
+  if (a.rows > npk::kPrefillMaxRows) return NP_ERR_UNSUPPORTED;
+  if (a.rows == 0 || a.num_tokens == 0) return NP_OK;
+  if (!a.out || !a.q || !a.k_pool || !a.v_pool || !a.block_tables || !a.context_lens || !a.query_starts)
+    return NP_ERR_INVALID_ARG;
+  if (!aligned(a.out, 16) || !aligned(a.q, 16) || !aligned(a.k_pool, 16) || !aligned(a.v_pool, 16) ||
+      !aligned(a.block_tables, 4) || !aligned(a.context_lens, 4) || !aligned(a.query_starts, 4) ||
+      (a.err_word && !aligned(a.err_word, 4)))
+    return NP_ERR_INVALID_ARG;
+  if (overlap(a.out, qn, a.q, qn) || overlap(a.out, qn, a.k_pool, pool) ||
+      overlap(a.out, qn, a.v_pool, pool))
+    return NP_ERR_INVALID_ARG;
+  if (!a.workspace || a.workspace_bytes < 0 ||
+      (size_t)a.workspace_bytes < np_paged_prefill_workspace_bytes(d) || !aligned(a.workspace, 256))
+    return NP_ERR_WORKSPACE;
+  *run = true;
+  return NP_OK;
+}
+
+}  // namespace
+
+extern "C" np_status np_paged_prefill_check(const np_paged_prefill_args* a) {
+  bool run;
+  return a ? check_prefill(*a, &run) : NP_ERR_INVALID_ARG;
+}
+
+extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
+  if (!a) return NP_ERR_INVALID_ARG;
+  bool run;
+  const np_status st = check_prefill(*a, &run);
+  if (st != NP_OK || !run) return st;
+  const int sms = sm_count();
+  if (sms <= 0) return NP_ERR_CUDA;
+
+  PrefillParams p{};
+  p.out = a->out;
+  p.q = a->q;
+  p.k_pool = a->k_pool;
+  p.v_pool = a->v_pool;
+  p.block_tables = a->block_tables;
+  p.context_lens = a->context_lens;
+  p.query_starts = a->query_starts;
+  p.err = a->err_word;
+  p.plan = static_cast<int4*>(a->workspace);
+  p.cuts = p.plan + npk::kPrefillMaxCtas + 1;
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + round_up(kPlanBytes, 256));
+  p.num_blocks = a->num_blocks;
+  p.block_size = a->block_size;
+  p.kv_heads = a->kv_heads;
+  p.q_heads = a->q_heads;
+  p.group = a->q_heads / a->kv_heads;
+  p.max_blocks_per_row = a->max_blocks_per_row;
+  p.rows = a->rows;
+  p.tokens = a->num_tokens;
+  p.ctas = sms < npk::kPrefillMaxCtas ? sms : npk::kPrefillMaxCtas;
+  p.head_dim = a->head_dim;
+  p.qscale = fabsf(a->scale) * 1.4426950408889634f;  // log2(e)
+  p.negate = a->scale < 0.f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
+  const np_dtype dtype = static_cast<np_dtype>(a->dtype);
+  const np_status rc =
+      dtype == NP_BF16 ? launch_tc(p, a->num_blocks * a->block_size, s) : launch_f32(p, s);
+  return rc == NP_OK ? npk::launch_prefill_join(p, dtype, s) : rc;
+}
+
 extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_pool,
                                       const void* v_pool, np_dtype dtype, int64_t num_blocks,
                                       int32_t block_size, int32_t kv_heads, int32_t head_dim,
@@ -170,82 +256,27 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
                                       int32_t rows, int32_t num_tokens, int32_t q_heads,
                                       float scale, void* workspace, size_t workspace_bytes,
                                       int32_t* err_word, np_stream_t stream) {
-  const int es = dtype == NP_F32 ? 4 : (dtype == NP_BF16 ? 2 : 0);
-  if (es == 0) return NP_ERR_UNSUPPORTED;
-  if (rows < 0 || num_tokens < 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 ||
-      num_blocks <= 0 || block_size <= 0 || max_blocks_per_row <= 0 || head_dim <= 0 ||
-      !isfinite(scale))
-    return NP_ERR_INVALID_ARG;
-  if (head_dim != 16 && head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
-    return NP_ERR_UNSUPPORTED;
-  const int group = q_heads / kv_heads;
-  if (group > (dtype == NP_BF16 ? 16 : 8)) return NP_ERR_UNSUPPORTED;
-  int64_t slots = 0, pool = 0, cap = 0, qn = 0, tab = 0;
-  if (!mul_ok(num_blocks, block_size, &slots) ||
-      !mul_ok(slots, (int64_t)kv_heads * head_dim * es, &pool) ||
-      !mul_ok(num_tokens, (int64_t)q_heads * head_dim * es, &qn) ||
-      !mul_ok(max_blocks_per_row, block_size, &cap) || !mul_ok(rows, max_blocks_per_row, &tab))
-    return NP_ERR_OUT_OF_RANGE;
-  // positions are int32 with some kv tiles to spare
-  if (cap > INT32_MAX - 1024 || num_tokens > INT32_MAX - 512) return NP_ERR_UNSUPPORTED;
-  if (rows > npk::kPrefillMaxRows) return NP_ERR_UNSUPPORTED;
-  if (rows == 0 || num_tokens == 0) return NP_OK;
-  if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens || !query_starts)
-    return NP_ERR_INVALID_ARG;
-  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
-      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_starts, 4) ||
-      (err_word && !aligned(err_word, 4)))
-    return NP_ERR_INVALID_ARG;
-  if (overlap(out, qn, q, qn) || overlap(out, qn, k_pool, pool) || overlap(out, qn, v_pool, pool))
-    return NP_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < np_paged_prefill_workspace_bytes(head_dim) ||
-      !aligned(workspace, 256))
-    return NP_ERR_WORKSPACE;
-  const int sms = sm_count();
-  if (sms <= 0) return NP_ERR_CUDA;
-
-  PrefillParams p{};
-  p.out = out;
-  p.q = q;
-  p.k_pool = k_pool;
-  p.v_pool = v_pool;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.query_starts = query_starts;
-  p.err = err_word;
-  p.plan = static_cast<int4*>(workspace);
-  p.cuts = p.plan + npk::kPrefillMaxCtas + 1;
-  p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(kPlanBytes, 256));
-  p.num_blocks = num_blocks;
-  p.block_size = block_size;
-  p.kv_heads = kv_heads;
-  p.q_heads = q_heads;
-  p.group = group;
-  p.max_blocks_per_row = max_blocks_per_row;
-  p.rows = rows;
-  p.tokens = num_tokens;
-  p.ctas = sms < npk::kPrefillMaxCtas ? sms : npk::kPrefillMaxCtas;
-  p.head_dim = head_dim;
-  p.qscale = fabsf(scale) * 1.4426950408889634f;  // log2(e)
-  p.negate = scale < 0.f;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-
-  np_status rc;
-  if (dtype == NP_BF16) {
-    rc = launch_tc(p, slots, st);
-  } else {
-    rc = launch_f32(p, st);
-  }
-  if (rc == NP_OK) rc = npk::launch_prefill_join(p, dtype, st);
-  return rc;
-}
-
-extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
-  if (!a) return NP_ERR_INVALID_ARG;
-  return np_paged_prefill(a->out, a->q, a->k_pool, a->v_pool, static_cast<np_dtype>(a->dtype),
-                          a->num_blocks, a->block_size, a->kv_heads, a->head_dim, a->block_tables,
-                          a->max_blocks_per_row, a->context_lens, a->query_starts, a->rows,
-                          a->num_tokens, a->q_heads, a->scale, a->workspace,
-                          a->workspace_bytes < 0 ? 0 : (size_t)a->workspace_bytes, a->err_word,
-                          a->stream);
+  np_paged_prefill_args a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_starts = query_starts;
+  a.workspace = workspace;
+  a.err_word = err_word;
+  a.stream = stream;
+  a.num_blocks = num_blocks;
+  a.workspace_bytes = workspace_bytes > (size_t)INT64_MAX ? INT64_MAX : (int64_t)workspace_bytes;
+  a.dtype = dtype;
+  a.block_size = block_size;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.max_blocks_per_row = max_blocks_per_row;
+  a.rows = rows;
+  a.num_tokens = num_tokens;
+  a.q_heads = q_heads;
+  a.scale = scale;
+  return np_paged_prefill_packed(&a);
 }
