@@ -224,7 +224,12 @@ np_status np_rope_append_packed(const np_rope_append_args* args);
  *   block_tables, context_lens, pools, err_word: as np_paged_decode.  A chunk
  *                  token whose row has fewer positions than its chunk has
  *                  tokens, so that it sees nothing, gets zeros.
- *   scale          finite, any sign
+ *   scale          any sign; scale * log2(e) finite (|scale| < 2.35e38).
+ *                  |scale q.k| has to stay below 2^30: a row's maximum is
+ *                  rounded to fp32, and the weights are taken from the exact
+ *                  distance to that.  Below 1e-30 in size the scale counts as
+ *                  1e-30 (but for fp32 at head_dim 256): the weights are equal
+ *                  to within fp32's rounding as long as |q.k| < 1e22
  *   workspace      >= np_paged_prefill_workspace_bytes(head_dim) bytes,
  *                  256-byte aligned, not shared by calls that may overlap;
  *                  contents need no initialisation and mean nothing after

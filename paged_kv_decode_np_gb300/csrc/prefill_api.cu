@@ -24,6 +24,8 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
   return p && q && n > 0 && m > 0 && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Plan and cut list, then the partials of kPrefillMaxCtas blocks.
 constexpr size_t kPlanBytes = (2 * npk::kPrefillMaxCtas + 1) * sizeof(int4);
 
@@ -171,7 +173,7 @@ np_status check_prefill(const np_paged_prefill_args& a, bool* run) {
   if (es == 0) return NP_ERR_UNSUPPORTED;
   if (a.rows < 0 || a.num_tokens < 0 || a.q_heads <= 0 || a.kv_heads <= 0 ||
       a.q_heads % a.kv_heads != 0 || a.num_blocks <= 0 || a.block_size <= 0 ||
-      a.max_blocks_per_row <= 0 || a.head_dim <= 0 || !isfinite(a.scale))
+      a.max_blocks_per_row <= 0 || a.head_dim <= 0 || !isfinite(a.scale * kLog2e))
     return NP_ERR_INVALID_ARG;
   const int d = a.head_dim;
   if (d != 16 && d != 32 && d != 64 && d != 128 && d != 256) return NP_ERR_UNSUPPORTED;
@@ -239,7 +241,7 @@ extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
   p.tokens = a->num_tokens;
   p.ctas = sms < npk::kPrefillMaxCtas ? sms : npk::kPrefillMaxCtas;
   p.head_dim = a->head_dim;
-  p.qscale = fabsf(a->scale) * 1.4426950408889634f;  // log2(e)
+  p.qscale = fabsf(a->scale) * kLog2e;
   p.negate = a->scale < 0.f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
   const np_dtype dtype = static_cast<np_dtype>(a->dtype);
