@@ -79,20 +79,7 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   const int d = p.head_dim;
   // a masked score is -inf before it is scaled: no 0 x inf
   p.qscale = fmaxf(p.qscale, 1e-30f);
-  p.tiles = d == 256 ? 1 : 2;
-  p.tile_rows = 128;
-  p.bn = d == 256 ? 64 : 128;
-  p.tile_tokens = p.tile_rows / p.group;
-  // Measured, us, {full, single, unit cost, least share}.  Two q tiles: a batch
-  // of 62 one-token rows and two chunks of 512 takes 242 with {3, 2, 8, 8}, 304
-  // with {1, 1, 2, 4}, 275 with {2, 1, 6, 6}; six prompts of 581-2750 tokens 227,
-  // 230, 227, and 239 with {1, 1, 1, 3}; 16 tokens over 1000 positions 16.7, with
-  // a least share of 16 20.5.  One q tile (head_dim 256, 16 chunks): {1, 1, 2, 4}
-  // 72, {1, 1, 1, 3} 75, {3, 2, 8, 8} 89.
-  p.full_cost = d == 256 ? 1 : 3;
-  p.single_cost = d == 256 ? 1 : 2;
-  p.unit_cost = d == 256 ? 2 : 8;
-  p.min_share = d == 256 ? 4 : 8;
+  npk::prefill_tiling(p, NP_BF16);
   // Tiled copies: boxes of whole 8-row swizzle atoms inside one block, slot
   // coordinates in int32.  box_tokens: the largest power of two that divides
   // the block size, at most a kv tile.
@@ -131,18 +118,8 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
 // fp32: three bf16 parts on the tensor cores; head_dim 256, whose three parts of
 // q, K and V do not fit in shared memory, on the FMA pipes
 np_status launch_f32(PrefillParams& p, cudaStream_t s) {
-  const bool tc = p.head_dim <= 128;
-  p.tiles = 1;
-  p.tile_rows = tc ? 128 : 64;
-  p.bn = 64;
-  p.tile_tokens = p.tile_rows / p.group;
-  // measured (head_dim 128; eight chunks of 71-184 over 833-2031 positions, and
-  // 32 over 900): unit_cost 3 183 us, 1 187 us, 8 tiles 190 us; min_share 2 23 us,
-  // 4 28 us, 6 31 us
-  p.full_cost = p.single_cost = 1;
-  p.unit_cost = 3;
-  p.min_share = 2;
-  if (tc) p.qscale = fmaxf(p.qscale, 1e-30f);
+  npk::prefill_tiling(p, NP_F32);
+  if (p.head_dim <= 128) p.qscale = fmaxf(p.qscale, 1e-30f);
   const np_status rc = npk::launch_prefill_plan(p, s);
   if (rc != NP_OK) return rc;
   switch (p.head_dim) {

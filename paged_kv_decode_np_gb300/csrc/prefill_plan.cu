@@ -4,55 +4,6 @@
 
 namespace npk {
 
-// sum over i < n of floor((a i + b) / m), for a, b >= 0, m > 0: the lattice
-// points under a line, counted by Euclid's reduction of (a, m).  T holds
-// a n + b; a 64-bit division takes several times a 32-bit one.
-template <typename T>
-__device__ int64_t floor_sum_in(T n, T m, T a, T b) {
-  int64_t s = 0;
-  while (n > 0) {
-    const T qa = a / m, qb = b / m;
-    s += (int64_t)n * (n - 1) / 2 * qa + (int64_t)n * qb;
-    a -= qa * m;
-    b -= qb * m;
-    const T y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y - n * m;
-    const T t = m;
-    m = a;
-    a = t;
-  }
-  return s;
-}
-
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  // the first step leaves a < m and b < m; later ones only shrink
-  if (n < (1 << 20) && m <= 1024 && a <= 1024 && b < (1ll << 31))
-    return floor_sum_in<uint32_t>((uint32_t)n, (uint32_t)m, (uint32_t)a, (uint32_t)b);
-  return floor_sum_in<int64_t>(n, m, a, b);
-}
-
-// what a kv tile of a row's unit a costs
-__device__ __forceinline__ int prefill_tile_cost(const PrefillParams& p, const PrefillRow& g, int a) {
-  return ((int64_t)a * p.tiles + 1) * p.tile_tokens >= g.n ? p.single_cost : p.full_cost;
-}
-
-// cost of a row's first k units (of one kv head), k <= units
-__device__ int64_t prefill_row_prefix(const PrefillParams& p, const PrefillRow& g, int units, int k) {
-  if (k <= 0) return 0;
-  const int64_t U = (int64_t)p.tile_tokens * p.tiles;
-  int64_t cost = (int64_t)k * p.unit_cost;
-  if (k == units) {  // the last unit ends with the chunk, not U tokens on
-    --k;
-    cost += (int64_t)prefill_kv_tiles(p, g, g.n) * prefill_tile_cost(p, g, k);
-  }
-  const int64_t base = (int64_t)g.c - g.n;
-  const int64_t z0 = base < 0 ? -base / U : 0;  // units that see nothing: one tile each
-  const int z = z0 < k ? (int)z0 : k;
-  return cost + (z + floor_sum(k - z, p.bn, U, base + (z + 1) * U + p.bn - 1)) * p.full_cost;
-}
-
 constexpr int kPlanThreads = 256;
 
 // One block.  Scans the rows' work (costs of kv tiles and of beginning units),
@@ -72,10 +23,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r < p.rows) {
-      const PrefillRow g = prefill_row(p, r, true);
-      const int units = prefill_units(p, g.n);
       pre[r] = sum;  // within the thread's rows for now
-      sum += prefill_row_prefix(p, g, units, units) * p.kv_heads;
+      sum += prefill_row_cost(p, r);
     }
   }
   int64_t x = sum;
@@ -104,69 +53,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
   }
   if (tid == 0) pre[p.rows] = warp_sum[kPlanThreads / 32 - 1];
   __syncthreads();
-  const int64_t W = pre[p.rows];
-  // blocks that share the work: a share holds min_share at least
-  const int64_t want = (W + p.min_share - 1) / p.min_share;
-  const int Pe = (int)(want < 1 ? 1 : (want < p.ctas ? want : p.ctas));
-  if (tid <= p.ctas) {
-    const int64_t share = W / Pe;
-    const int64_t x = tid >= Pe ? W : share * tid + (W % Pe) * tid / Pe;
-    int4 q = make_int4(p.rows, 0, 0, 0);
-    if (x < W) {
-      int lo = 0, hi = p.rows;  // the last row with pre[row] <= x: it has work there
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= x) lo = mid;
-        else hi = mid;
-      }
-      const PrefillRow g = prefill_row(p, lo);
-      const int units = prefill_units(p, g.n);
-      const int64_t wh = (pre[lo + 1] - pre[lo]) / p.kv_heads;
-      int kvh = (int)((x - pre[lo]) / wh);
-      const int64_t in = (x - pre[lo]) - kvh * wh;
-      int a = 0, b = units;  // the last unit that begins at or before `in`
-      while (b - a > 1) {
-        const int mid = (a + b) >> 1;
-        if (prefill_row_prefix(p, g, units, mid) <= in) a = mid;
-        else b = mid;
-      }
-      const int64_t s0 = prefill_row_prefix(p, g, units, a);
-      const int nk = prefill_kv_tiles(p, g, (int64_t)(a + 1) * p.tile_tokens * p.tiles);
-      const int cost = prefill_tile_cost(p, g, a);
-      int off = ((int)(in - s0) - p.unit_cost) / cost;  // <= 0: within the fixed cost
-      // an end that lies near a unit's own start or end is moved there: the
-      // partials it saves cost more than the imbalance
-      if (off <= 0 || (int64_t)off * cost * 16 <= share) {
-        off = 0;
-      } else if ((int64_t)(nk - off) * cost * 16 <= share) {
-        off = 0;
-        // the unit after: of this head, the next head, or the next row
-        if (++a >= units) {
-          a = 0;
-          if (++kvh >= p.kv_heads) {
-            kvh = 0;
-            ++lo;
-          }
-        }
-      }
-      q = make_int4(lo, kvh, a, off);
-    }
-    pos[tid] = q;
-    p.plan[tid] = q;
-  }
+  if (tid <= p.ctas) p.plan[tid] = pos[tid] = prefill_share_start(p, pre, tid);
   __syncthreads();
-  if (tid < p.ctas) {
-    // the unit that this share's end cuts, if the share holds its first tile
-    int4 cut = make_int4(-1, 0, 0, 0);
-    const int4 s = pos[tid], e = pos[tid + 1];
-    auto same = [](int4 u, int4 v) { return u.x == v.x && u.y == v.y && u.z == v.z; };
-    if (e.w > 0 && (!same(s, e) || s.w == 0)) {
-      int last = tid + 1;  // the last block whose share begins in the unit
-      while (last + 1 <= p.ctas && same(pos[last + 1], e)) ++last;
-      cut = make_int4(e.x, e.y, e.z, last);
-    }
-    p.cuts[tid] = cut;
-  }
+  if (tid < p.ctas) p.cuts[tid] = prefill_share_cut(p, pos, tid);
 }
 
 np_status launch_prefill_plan(const PrefillParams& p, cudaStream_t s) {
