@@ -79,6 +79,8 @@ struct TcCfg {
   // phases: its tile before, at most 3 positions back, waited for a slot that was
   // freed after the use before that.
   static_assert(NS >= 4, "ring");
+  // One block an SM: a second would wait for the first's tensor memory.
+  static_assert(2 * (SMEM + 1024) > 228 * 1024, "one block an SM");
 };
 
 // Barriers, by index from the barrier area's start (8 bytes each).
@@ -90,8 +92,13 @@ struct TcBars {
   // p_full, each once a phase: what a warp arrives for next was issued after a
   // wait for the phase before (S(j+1) after s_read of S(j); the S of a P buffer's
   // next use after the P V of this one).
-  // A warp waits on all phases of a barrier or on none: one that skips some
-  // could take an earlier phase of the same parity for its own.
+  // A wait that skips phases could take an earlier one of the same parity for its
+  // own.  q_*, s_*, p_full, o_full and tail_full: who waits, waits for every phase.
+  // The two others are never two phases behind what is waited for:
+  // - kv_empty: a loader skips the others' tiles of a slot (the lag: TcCfg::NS);
+  // - pv_done, waited for only where O is rescaled: phase j - 1 at tile j, whose
+  //   S(j) is complete; S(j) was issued after P V(j - 2), so that phase j - 2 is
+  //   complete with it, and P V(j) is not issued before this warp's P(j).
   static constexpr int s_full = 2 + 2 * NS, s_read = s_full + 2, p_full = s_read + 2;
   static constexpr int o_full = p_full + 2;
   static constexpr int pv_done = o_full + 2;  // one-tile units: one phase a kv tile

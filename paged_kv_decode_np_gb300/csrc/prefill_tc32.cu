@@ -59,6 +59,7 @@ struct Tc32Cfg {
   // tensor memory: S (128 columns), P (three parts of 32), q (two of D / 2), O
   static constexpr uint32_t P0 = 128, Q0 = 224, O0 = 384;
   static_assert(SMEM <= 227 * 1024 && Q0 + D <= O0, "shared and tensor memory");
+  static_assert(2 * (SMEM + 1024) > 228 * 1024, "one block an SM");
 };
 
 struct Tc32Bars {

@@ -111,8 +111,8 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn, 
 // operands; one elected lane issues.  (The election is part of each: where a
 // branch on a lane's predicate guards them instead, their operands go from
 // vector to uniform registers one by one, about 100 cycles an mma; and where
-// that predicate was an earlier election's, kept in a register, small guarded
-// blocks faulted.)
+// that predicate was an earlier election's, kept in a register, a guarded block
+// of a single mma raised an illegal address.  Why is not known.)
 
 // D (tensor memory) = A B (+ D where acc)
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
