@@ -115,8 +115,7 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   return NP_ERR_UNSUPPORTED;
 }
 
-// fp32: three bf16 parts on the tensor cores; head_dim 256, whose three parts of
-// q, K and V do not fit in shared memory, on the FMA pipes
+// fp32: three bf16 parts on the tensor cores; head_dim 256 on the FMA pipes
 np_status launch_f32(PrefillParams& p, cudaStream_t s) {
   npk::prefill_tiling(p, NP_F32);
   if (p.head_dim <= 128) p.qscale = fmaxf(p.qscale, 1e-30f);

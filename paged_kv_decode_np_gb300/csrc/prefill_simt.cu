@@ -1,6 +1,7 @@
 // prefill_simt.cu -- np_paged_prefill on the FMA pipes: fp32 pools of head_dim
-// 256, whose three bf16 parts of q, K and V do not fit in shared memory beside
-// one another (narrower heads: prefill_tc32.cu).
+// 256.  (Narrower heads: prefill_tc32.cu, whose tiles of 128 rows and 64 tokens do
+// not fit in shared memory in three bf16 parts at this width.  Smaller ones
+// would: 64 rows and 32 tokens, 192 KB; not built.)
 //
 // A unit is one tile of 64 (token, head) rows; a kv tile is 64 tokens.  256
 // threads form S = Q K^T as 4 x 4 microtiles from shared memory (rows 4 ty +
@@ -13,11 +14,11 @@
 
 namespace npk {
 
+constexpr int D = 256;
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 64;
 constexpr int kSimtBn = 64;
 
-template <int D>
 struct SimtSmem {
   static constexpr int LD = D + 4;        // rows start on different banks
   static constexpr int LP = kSimtBn + 4;
@@ -25,15 +26,13 @@ struct SimtSmem {
   static constexpr size_t bytes = floats * 4 + kSimtBn * 8;
 };
 
-template <int D>
 __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __grid_constant__
                                                                        PrefillParams p) {
-  using T = float;
-  using S = Storage<T>;
-  using M = SimtSmem<D>;
+  using S = Storage<float>;
+  using M = SimtSmem;
   constexpr unsigned FULL = 0xffffffffu;
-  constexpr int V = 16 / (int)sizeof(T);
-  constexpr int NG = (D + 63) / 64;   // groups of 4 dims a thread owns: 4 tx + 64 j
+  constexpr int V = 4;        // floats of a 16-byte access
+  constexpr int NG = D / 64;  // groups of 4 dims a thread owns: 4 tx + 64 j
   extern __shared__ __align__(16) unsigned char smem[];
   float* qs = reinterpret_cast<float*>(smem);
   float* ks = qs + kSimtRows * M::LD;
@@ -59,7 +58,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 #pragma unroll
       for (int k = 0; k < V; ++k) x[k] = 0.f;
       if (tt < p.tile_tokens && tok0 + tt < w.g.n)
-        S::template load<V>(static_cast<const T*>(p.q) +
+        S::template load<V>(static_cast<const float*>(p.q) +
                                 ((int64_t)(w.g.q0 + tok0 + tt) * p.q_heads + w.kvh * G + h) * D + d,
                             x);
 #pragma unroll
@@ -105,8 +104,8 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
         for (int k = 0; k < V; ++k) x[k] = y[k] = 0.f;
         if (sl >= 0) {
           const int64_t at = (sl * p.kv_heads + w.kvh) * D + d;
-          S::template load<V>(static_cast<const T*>(p.k_pool) + at, x);
-          S::template load<V>(static_cast<const T*>(p.v_pool) + at, y);
+          S::template load<V>(static_cast<const float*>(p.k_pool) + at, x);
+          S::template load<V>(static_cast<const float*>(p.v_pool) + at, y);
         }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -179,7 +178,6 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int d = 4 * tx + 64 * j;
-          if (D < 64 && d >= D) continue;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const float4 v = *reinterpret_cast<const float4*>(&vs[(k + kk) * M::LD + d]);
@@ -204,12 +202,11 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
       if (w.whole()) {
         if (tt >= p.tile_tokens || tok0 + tt >= w.g.n) continue;
         const float inv = l_run[i] > 0.f ? 1.f / l_run[i] : 0.f;
-        T* out = static_cast<T*>(p.out) +
-                 ((int64_t)(w.g.q0 + tok0 + tt) * p.q_heads + w.kvh * G + h) * D;
+        float* out = static_cast<float*>(p.out) +
+                     ((int64_t)(w.g.q0 + tok0 + tt) * p.q_heads + w.kvh * G + h) * D;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int d = 4 * tx + 64 * j;
-          if (d >= D) continue;
           float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = o[i][j][e] * inv;
@@ -225,9 +222,8 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int g = tx + 16 * j;  // dims 4 g .. 4 g + 3
-          if (4 * g < D)
-            *reinterpret_cast<float4*>(part + 2 * kSimtRows + ((size_t)g * kSimtRows + row) * 4) =
-                make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
+          *reinterpret_cast<float4*>(part + 2 * kSimtRows + ((size_t)g * kSimtRows + row) * 4) =
+              make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
         }
       }
     }
@@ -236,12 +232,12 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 }
 
 np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s) {
-  constexpr size_t bytes = SimtSmem<256>::bytes;
+  constexpr size_t bytes = SimtSmem::bytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
   static unsigned long long allowed = 0;
-  const np_status rc = allow_smem(prefill_simt_kernel<256>, bytes, &allowed);
+  const np_status rc = allow_smem(prefill_simt_kernel, bytes, &allowed);
   if (rc != NP_OK) return rc;
-  return launch_dependent(prefill_simt_kernel<256>, p.ctas, 1, kSimtThreads, bytes, s, p);
+  return launch_dependent(prefill_simt_kernel, p.ctas, 1, kSimtThreads, bytes, s, p);
 }
 
 }  // namespace npk
