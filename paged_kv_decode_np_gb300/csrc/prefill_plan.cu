@@ -84,9 +84,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
   float(*ls)[32] = ms + kPrefillMaxCtas;
   __shared__ int piece[kPrefillMaxCtas];  // the partials, in block order
   __shared__ int pieces;
-  // the plan is complete: the attention, which waited for it, let this launch start
+  // The plan is complete: every block of the attention waited for it before it let
+  // this launch start.  Its results are read from L2, where they are: this block
+  // has not waited for anything yet that would make an older line in L1 go.
   const int b = blockIdx.x;
-  const int4 cut = p.cuts[b];
+  const int4 cut = __ldcg(p.cuts + b);
   if (cut.x < 0) {
     // (this launch must not end before the attention: what comes after waits for it)
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
       const int i = i0 + threadIdx.x;
       bool has = false;
       if (i <= cut.w) {
-        const int4 s = p.plan[i], e = p.plan[i + 1];
+        const int4 s = __ldcg(p.plan + i), e = __ldcg(p.plan + i + 1);
         has = s.x != e.x || s.y != e.y || s.z != e.z || s.w != e.w;
       }
       const unsigned m = __ballot_sync(0xffffffffu, has);
