@@ -165,7 +165,9 @@ np_status np_kv_append(void* k_pool, void* v_pool, np_dtype dtype,
  * Arithmetic is fp32; each result is rounded to dtype once.  v is copied bit
  * for bit.  q_heads == 0 with q, q_out and q_weight NULL: k and v only.
  * q_out may be q itself where q is dense; else what is written (q_out, the
- * pools) must not overlap what is read: NP_ERR_INVALID_ARG.  Pointers 16-byte
+ * pools) must not overlap q, k_new or v_new, nor one another:
+ * NP_ERR_INVALID_ARG.  It must lie apart from the other arrays too, which is
+ * not checked.  Pointers 16-byte
  * aligned; strides a multiple of 16 bytes, at least a token's heads.  Any
  * kv_heads and q_heads up to 4096 (q_heads need not be a multiple here);
  * head_dim as in the list above.  num_tokens == 0 is a no-op.
@@ -233,6 +235,11 @@ np_status np_rope_append_packed(const np_rope_append_args* args);
  *   workspace      >= np_paged_prefill_workspace_bytes(head_dim) bytes,
  *                  256-byte aligned, not shared by calls that may overlap;
  *                  contents need no initialisation and mean nothing after
+ * Arithmetic: sums, the softmax and its statistics in fp32.  bf16: the weights
+ * are rounded to bf16 for their product with V (as np_paged_decode's are), the
+ * result once.  fp32 to head_dim 128: each product is six of the nine products
+ * of three bf16 parts, what is left out is below 2^-22 of it; head_dim 256:
+ * fp32 products.
  * K and V of the row's c positions must be finite.  Slots past a row's
  * context, in its last block too, are never part of a result, whatever they
  * hold.  Supported: the dtypes, head_dims and groups of the list above; up
