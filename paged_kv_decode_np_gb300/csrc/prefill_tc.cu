@@ -41,13 +41,14 @@
 // token of 8, slab, 8-token group, kv head, in the order the box lands); other
 // shapes take 16-byte asynchronous copies token by token, swizzled by hand.
 //
-// Bound: the chain S -> softmax -> P V of a q tile, ~2760 cycles a kv tile
-// against 2048 of mma for the pair (head_dim 128).  1024 tokens over 131072
-// positions, 64 / 8 heads: 3.1-3.4 ms, 1290-1420 TFLOP/s, the tensor pipe 71 %
-// active; six prompts of 581-2750 tokens, 40 / 8 heads: 226-240 us, 760-800
-// TFLOP/s; 64 one-token rows over 1024-8192 positions: 208 us, 5.8 TB/s.  The
-// roles' code is kept small on purpose: unrolling a loader's loop or another
-// copy of the mma sequence cost 5 to 20 % in instruction fetch.
+// Bound: the chain S -> softmax -> P V of a q tile, ~3200 cycles a kv tile (1500
+// of them the softmax) against 2048 of mma for the pair (head_dim 128).  1024
+// tokens over 131072 positions, 64 / 8 heads: 3.2-3.46 ms by the box, 1270-1370
+// TFLOP/s; a shorter one under the profiler has the tensor pipe 65 % active.  Six
+// prompts of 581-2750 tokens, 40 / 8 heads: 240-256 us, 710-760 TFLOP/s; 62
+// one-token rows and two chunks of 512 over 1024-8192 positions: 240-246 us, 5.0
+// TB/s.  The roles' code is kept small on purpose: unrolling a loader's loop or
+// another copy of the mma sequence cost 5 to 20 % in instruction fetch.
 #include <limits.h>
 
 #include "prefill.cuh"

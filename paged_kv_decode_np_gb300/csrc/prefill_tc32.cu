@@ -30,10 +30,12 @@
 // tile's first mma once the softmax has read these (s_empty).  P and q's first two parts are A operands in tensor
 // memory, which has no room for q's third: that one is in shared memory.
 //
-// Bound: the softmax warps, one a scheduler (~5500 cycles a kv tile), and behind
-// them the mma (56 of them, 64 cycles each: ~3600).  Eight chunks of 71-184 tokens over
-// 833-2031 positions, 32 / 8 heads of 128: 162 us, 148 TFLOP/s of fp32 products
-// (950 us on the FMA pipes); error against exact values 3e-7 of their norm.
+// Bound: the softmax warps, one a scheduler (~5400 cycles of work in ~6600 a kv
+// tile), and behind them the mma (56 of them, 64 cycles each, and ~420 for the
+// wait between the shapes: ~4000).  Eight chunks of 71-184 tokens over 833-2031
+// positions, 32 / 8 heads of 128: 167 us, 143 TFLOP/s of fp32 products (950 us on
+// the FMA pipes); without the wait 162; with all products 64 columns wide, no
+// wait and half the adding up, 173.  Error against exact values 3e-7 of their norm.
 #include <limits.h>
 
 #include "prefill.cuh"

@@ -223,8 +223,13 @@ static np_status launch_rope(RopeParams& p, cudaStream_t stream) {
   // with 256 threads, 3.4 with 64, 5.0 with 32).  Many: one warp a token, which
   // walks its heads with the token's cosines, sines, slot and position read
   // once by few threads (16384 tokens of 80 heads: 102 us, 6.6 TB/s, with 32;
-  // 114 with 128; 136 with 256).  1000 tokens: 4.6 us with 128, 5.5 with 256,
-  // 5.9 with 32.
+  // 114 with 128; 136 with 256).  At the borders, us with 32 / 128 / 256 threads,
+  // bf16, 128 dims, 80 heads: 511 tokens 12.5 / 7.1 / 6.6, 1000 14.0 / 9.7 / 11.2,
+  // 2048 18.4 / 17.2 / 20.4, 4096 29.2 / 32.0 / 37.7; 10 heads: 511 3.2 / 2.7 / 2.8,
+  // 2048 5.3 / 6.0 / 6.3, 4096 6.8 / 9.3 / 9.6; with norms, 80 heads: 2048 21.3 /
+  // 21.7 / 32.1, 16384 123 / 145 / 236 (86 registers: 23 blocks of a warp an SM).
+  // Three heads leave lanes idle in a warp a token: 2048 3.1 / 2.7 / 2.9, 16384
+  // 13.1 / 11.2 / 12.2, where 128 threads would be right.
   const int cap = p.tokens >= 2048 ? 32 : (p.tokens >= 512 ? 128 : kRopeThreads);
   // heads a token's threads take at a time: all of them in the fewest equal
   // rounds that fit a block
