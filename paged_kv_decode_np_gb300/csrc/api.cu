@@ -196,10 +196,16 @@ bool encode_pool_map(CUtensorMap* m, const void* pool, int64_t slots, int32_t kv
   cuuint32_t box[4] = {64u, (cuuint32_t)box_tokens, (cuuint32_t)head_group,
                        (cuuint32_t)(head_dim / 64)};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  CUresult rc = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    NPK_TMAP_L2_PROMO, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return rc == CUDA_SUCCESS;
+  auto encode = [&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, NPK_TMAP_L2_PROMO,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // A host thread that has launched nothing yet has no context, which the driver's
+  // encoder wants: the runtime binds the current device's, and it is tried again.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 // Small per-thread cache: the same pools are read step after step.
