@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define NP_ABI_VERSION 3
+#define NP_ABI_VERSION 4
 
 /* Same type as cudaStream_t / CUstream, without pulling in CUDA headers. */
 typedef struct CUstream_st* np_stream_t;
@@ -87,6 +87,10 @@ typedef enum np_status {
 } np_status;
 
 typedef enum np_dtype { NP_F32 = 0, NP_BF16 = 1 } np_dtype;
+
+/* 8-bit cache forms (the np_*_q8 calls): e4m3 (OCP FP8, largest value 448) or
+ * signed whole numbers from -127 to 127. */
+typedef enum np_form8 { NP_E4M3 = 0, NP_INT8 = 1 } np_form8;
 
 /* Bits OR-ed into *err_word by the kernels. */
 #define NP_FLAG_BLOCK_ID 0x1 /* a block-table entry the walk needed was outside
@@ -103,8 +107,13 @@ typedef enum np_dtype { NP_F32 = 0, NP_BF16 = 1 } np_dtype;
                                 inconsistent and did nothing (never expected) */
 #define NP_FLAG_POSITION 0x20 /* np_rope_append: a position outside [0,
                                 max_positions); the nearest one was used */
-#define NP_FLAG_QUERY 0x40   /* np_paged_prefill: query_starts not ascending
-                                within [0, num_tokens]; clamped into it */
+#define NP_FLAG_QUERY 0x40   /* np_paged_prefill(_q8): query_starts not ascending
+                                within [0, num_tokens]; clamped into it.
+                                np_block_map: a negative new or kept length
+                                (taken as 0), or more new tokens than num_tokens */
+#define NP_FLAG_VALUE 0x80   /* np_kv_append_q8: a new element was not finite */
+#define NP_FLAG_BLOCKS 0x100 /* np_block_map: the free list ran out, or its count
+                                does not fit its length */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* np_status_string(np_status status);
@@ -290,6 +299,221 @@ np_status np_paged_prefill_packed(const np_paged_prefill_args* args);
  * device memory: a step that appends before it attends asks first, so that a
  * refusal leaves the pools and q as they were. */
 np_status np_paged_prefill_check(const np_paged_prefill_args* args);
+
+/*
+ * ---- The cache in 8 bits.
+ * The pools are [num_blocks, block_size, kv_heads, head_dim] bytes of an
+ * np_form8, with k_scale and v_scale [num_blocks, kv_heads] fp32: an element of
+ * block b and kv head h stands for its code times scale[b][h].  A scale is a
+ * power of two from 2^-60 to 2^60: reading, any other bits count as the power
+ * of two of their exponent field, clamped into that range (zeros, too, of
+ * blocks that were never written).  With QMAX the form's largest code (448,
+ * 127), np_kv_append_q8 chooses the least scale 2^e with max |x| <= QMAX 2^e.
+ * A power of two costs e4m3 nothing (its steps are relative) and int8 half a
+ * bit on average, and makes a code times its scale exact in bf16 and a code
+ * moved to a larger scale exact but for the bits that fall off its end.
+ */
+
+/*
+ * np_block_map -- one step of a batch's bookkeeping: block tables, slot
+ * mapping, positions and query starts from the requests' lengths, with blocks
+ * taken from and given back to a free list, all on the device (so a captured
+ * step needs no host in between).
+ * Row r holds c = context_lens[r] positions.  It keeps the first
+ * b = min(c, kept_lens[r]) of them (kept_lens NULL: all) and gets new_lens[r]
+ * more.  With have = ceil(c / block_size) and need = ceil((b + new) / block_size):
+ *   - have > need: table entries need .. have - 1 are put at the free list's end and
+ *     become -1; over the batch in the order (last row first, last block first);
+ *   - need > have: entries have .. need - 1 are taken from the list's end, after
+ *     everything that is put there; in the order (first row first, first block
+ *     first), so that a step that takes back what the step before took leaves
+ *     the list as it was.
+ * A finished request keeps 0 and gets 0; a rejected draft's tail is not kept.
+ *   block_tables   [rows, max_blocks_per_row] int32, updated
+ *   context_lens   [rows] int32, updated to b + new
+ *   new_lens       [rows] int32
+ *   kept_lens      [rows] int32 or NULL; may be context_lens itself
+ *   free_blocks    [num_blocks] int32: the list, entries 0 .. *free_count - 1
+ *   free_count     device int32, updated
+ *   query_starts   [rows + 1] int32 (written): where each row's new tokens
+ *                  begin among the step's tokens, then their number
+ *   slot_mapping   [num_tokens] int64 (written), token by token: the pool slot
+ *                  of its position; -1 past the step's last token.  NULL with
+ *                  num_tokens 0: the tables only
+ *   positions      [num_tokens] int32 (written) or NULL: the token's position in
+ *                  its row; 0 past the last
+ * What does not fit is refused row by row and flagged: a row whose table is too
+ * short for its new tokens gets none (NP_FLAG_CONTEXT), nor do the row that the
+ * free list or num_tokens has no room for and the rows after it
+ * (NP_FLAG_BLOCKS, NP_FLAG_QUERY); such a row still keeps min(c, kept).  A list
+ * entry outside [0, num_blocks) becomes -1 in the table and its slots -1
+ * (NP_FLAG_BLOCK_ID).  Up to 4096 rows; tables of up to 2^31 - 1025 tokens.  The
+ * arrays must not overlap but for kept_lens.  rows 0 with tokens: all of them
+ * are past the last.
+ */
+np_status np_block_map(int32_t* block_tables, int32_t max_blocks_per_row,
+                       int32_t* context_lens, const int32_t* new_lens,
+                       const int32_t* kept_lens, int32_t rows,
+                       int32_t block_size, int32_t* free_blocks,
+                       int32_t* free_count, int64_t num_blocks,
+                       int32_t* query_starts, int64_t* slot_mapping,
+                       int32_t* positions, int32_t num_tokens,
+                       int32_t* err_word, np_stream_t stream);
+
+/*
+ * np_kv_append_q8 -- np_kv_append into 8-bit pools: the new tokens' K and V are
+ * rounded to the form (to nearest, ties to even) under their block's scale.
+ *   k_pool, v_pool, k_scale, v_scale   as above (updated)
+ *   k_new, v_new    [num_tokens, kv_heads, head_dim] of `dtype`, k_stride and
+ *                   v_stride elements between tokens (kv_heads * head_dim when
+ *                   dense; a fused projection's rows otherwise)
+ *   slot_mapping    [num_tokens] int64, as in np_kv_append (negative: padding,
+ *                   skipped; past the pool: skipped, NP_FLAG_SLOT).  The tokens
+ *                   of one block stand side by side in it, as np_block_map's do
+ *                   (else that block's contents and scales mean nothing).  Two
+ *                   tokens with the same slot leave a mixture of theirs.
+ * For each block and kv head, with A the largest |x| of the call's tokens there
+ * and e(A) the least e in [-60, 60] with A <= QMAX 2^e: a call that writes the
+ * block's first slot begins it anew, its scale is 2^e(A); another leaves the
+ * larger of 2^e(A) and the scale it finds, and where that one grows, the codes
+ * of the block's other slots are rounded to the new scale.  (Scales at least
+ * double as they grow, so what a code loses that way adds up to less than the
+ * one half step of the last rounding again.)
+ * Values past QMAX 2^60 become the largest code; so do infinities, which do
+ * not count in A; NaN becomes NaN in e4m3 and 0 in int8 (all three but the
+ * first: NP_FLAG_VALUE).
+ * dtype NP_F32 or NP_BF16; head_dim as in the list above; any block_size and
+ * kv_heads.  Pointers 16-byte aligned, strides a multiple of 16 bytes, at least
+ * a token's heads.  The pools and scales must not overlap one another, nor what is
+ * read.  num_tokens == 0 is a no-op.
+ */
+np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
+                          float* v_scale, np_form8 form, int64_t num_blocks,
+                          int32_t block_size, int32_t kv_heads,
+                          int32_t head_dim, const void* k_new,
+                          const void* v_new, np_dtype dtype, int64_t k_stride,
+                          int64_t v_stride, const int64_t* slot_mapping,
+                          int32_t num_tokens, int32_t* err_word,
+                          np_stream_t stream);
+
+/*
+ * np_paged_decode_q8 -- np_paged_decode of an 8-bit cache: query_len newest
+ * positions of every row attend causally over the row's history.
+ *   out, q         [rows, query_len, q_heads, head_dim] dtype
+ *   k_pool, v_pool, k_scale, v_scale, form   as above
+ *   block_tables, context_lens, scale, err_word   as in np_paged_decode
+ *                  (scale: any finite value whose product with log2(e) is; |scale
+ *                  q.k| has to stay below 2^30)
+ *   workspace      >= np_paged_decode_q8_workspace_bytes(head_dim) bytes, 256-byte
+ *                  aligned, not shared by calls that may overlap; needs no
+ *                  initialisation
+ * One schedule: the balanced one (equal shares of all rows' history, cut rows
+ * joined by a second launch; the same call gives the same bits).  q, K, V and the
+ * weights are multiplied in fp16 with fp32 sums: codes are exact in fp16, q is
+ * scaled by a power of two first (bf16 is then exact but below 2^-28 of the
+ * row's largest element); a weight is rounded to fp16 for its product with V,
+ * bf16 out; for fp32, q and the weights are two fp16 parts each (22 bits).  The
+ * softmax and its sums are fp32.
+ * Slots past a row's context are never part of a result.  Supported: dtype
+ * NP_F32 (g * query_len <= 8) or NP_BF16 (<= 16), g = q_heads / kv_heads; head_dim
+ * of the list above; any block_size; any kv_heads; rows up to 65535; tables of up to
+ * 2^31 - 1025 tokens.  A row without history gets zeros.  rows 0: a no-op.
+ */
+size_t np_paged_decode_q8_workspace_bytes(int32_t head_dim);
+/* enough for every head_dim */
+#define NP_DECODE_Q8_WORKSPACE_BYTES (64u << 20)
+
+np_status np_paged_decode_q8(void* out, const void* q, np_dtype dtype,
+                             const void* k_pool, const void* v_pool,
+                             const float* k_scale, const float* v_scale,
+                             np_form8 form, int64_t num_blocks,
+                             int32_t block_size, int32_t kv_heads,
+                             int32_t head_dim, const int32_t* block_tables,
+                             int32_t max_blocks_per_row,
+                             const int32_t* context_lens, int32_t rows,
+                             int32_t query_len, int32_t q_heads, float scale,
+                             void* workspace, size_t workspace_bytes,
+                             int32_t* err_word, np_stream_t stream);
+
+/*
+ * np_paged_prefill_q8 -- np_paged_prefill over an 8-bit cache: ragged chunks of
+ * new tokens, already appended (np_kv_append_q8), attend causally over their
+ * rows' histories.  out and q of `dtype`; pools, scales and form as above; the
+ * other arguments, limits and errors as np_paged_prefill's.
+ */
+np_status np_paged_prefill_q8(void* out, const void* q, np_dtype dtype,
+                              const void* k_pool, const void* v_pool,
+                              const float* k_scale, const float* v_scale,
+                              np_form8 form, int64_t num_blocks,
+                              int32_t block_size, int32_t kv_heads,
+                              int32_t head_dim, const int32_t* block_tables,
+                              int32_t max_blocks_per_row,
+                              const int32_t* context_lens,
+                              const int32_t* query_starts, int32_t rows,
+                              int32_t num_tokens, int32_t q_heads, float scale,
+                              void* workspace, size_t workspace_bytes,
+                              int32_t* err_word, np_stream_t stream);
+
+/* The q8 calls with their arguments in a struct (see np_rope_append_args). */
+typedef struct np_block_map_args {
+  int32_t* block_tables;
+  int32_t* context_lens;
+  const int32_t* new_lens;
+  const int32_t* kept_lens;
+  int32_t* free_blocks;
+  int32_t* free_count;
+  int32_t* query_starts;
+  int64_t* slot_mapping;
+  int32_t* positions;
+  int32_t* err_word;
+  np_stream_t stream;
+  int64_t num_blocks;
+  int32_t max_blocks_per_row, rows, block_size, num_tokens;
+} np_block_map_args;
+
+np_status np_block_map_packed(const np_block_map_args* args);
+
+typedef struct np_kv_append_q8_args {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  const void* k_new;
+  const void* v_new;
+  const int64_t* slot_mapping;
+  int32_t* err_word;
+  np_stream_t stream;
+  int64_t num_blocks, k_stride, v_stride;
+  int32_t form, dtype, block_size, kv_heads, head_dim, num_tokens;
+} np_kv_append_q8_args;
+
+np_status np_kv_append_q8_packed(const np_kv_append_q8_args* args);
+
+/* np_paged_decode_q8 (query_starts NULL, num_tokens = rows * query_len) and
+ * np_paged_prefill_q8 (query_len 0). */
+typedef struct np_read_q8_args {
+  void* out;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_starts;
+  void* workspace;
+  int32_t* err_word;
+  np_stream_t stream;
+  int64_t num_blocks, workspace_bytes;
+  int32_t form, dtype, block_size, kv_heads, head_dim, max_blocks_per_row;
+  int32_t rows, query_len, num_tokens, q_heads;
+  float scale;
+} np_read_q8_args;
+
+np_status np_paged_decode_q8_packed(const np_read_q8_args* args);
+np_status np_paged_prefill_q8_packed(const np_read_q8_args* args);
+/* as np_paged_prefill_check */
+np_status np_paged_prefill_q8_check(const np_read_q8_args* args);
 
 /*
  * np_paged_decode_plan -- the schedule the library recommends, as a

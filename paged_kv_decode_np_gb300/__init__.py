@@ -58,7 +58,10 @@ __all__ = [
     "NP_ERR_UNSUPPORTED",
     "NP_ERR_WORKSPACE", "NP_ERR_OUT_OF_RANGE", "NP_ERR_CUDA", "NP_F32", "NP_BF16",
     "NP_FLAG_BLOCK_ID", "NP_FLAG_CONTEXT", "NP_FLAG_SLOT", "NP_FLAG_TIMEOUT", "NP_FLAG_CONFIG",
-    "NP_FLAG_POSITION", "NP_FLAG_QUERY",
+    "NP_FLAG_POSITION", "NP_FLAG_QUERY", "NP_FLAG_VALUE", "NP_FLAG_BLOCKS", "NP_E4M3", "NP_INT8",
+    "np_block_map", "np_kv_append_q8", "np_paged_decode_q8", "np_paged_decode_q8_workspace_bytes",
+    "np_paged_prefill_q8", "q8_pools", "decode_q8_workspace", "decode_step_q8", "prefill_step_q8",
+    "NP_DECODE_Q8_WORKSPACE_BYTES",
 ]
 
 NP_OK = 0
@@ -78,9 +81,15 @@ NP_FLAG_TIMEOUT = 0x8
 NP_FLAG_CONFIG = 0x10
 NP_FLAG_POSITION = 0x20
 NP_FLAG_QUERY = 0x40
+NP_FLAG_VALUE = 0x80
+NP_FLAG_BLOCKS = 0x100
+
+NP_E4M3 = 0
+NP_INT8 = 1
 
 NP_NOALLOC_SCRATCH_BYTES = 32 << 20
 NP_PREFILL_WORKSPACE_BYTES = 64 << 20
+NP_DECODE_Q8_WORKSPACE_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libnp_paged.so")
@@ -141,6 +150,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.np_selftest_bounded_wait.argtypes = [_P, _I64, _P]
     if hasattr(lib, "np_rope_append"):  # a library of ABI version 2 has no prompt side
         _declare_prompt(lib)
+    if hasattr(lib, "np_block_map"):  # a library of ABI version 3 has no 8-bit cache
+        _declare_q8(lib)
     if path is None:
         _LIB = lib
     return lib
@@ -162,6 +173,16 @@ def _declare_prompt(lib: ctypes.CDLL) -> None:
     lib.np_paged_prefill.argtypes = [_P, _P, _P, _P, ctypes.c_int, _I64, _I32, _I32, _I32, _P, _I32,
                                      _P, _P, _I32, _I32, _I32, ctypes.c_float, _P, ctypes.c_size_t,
                                      _P, _P]
+
+
+def _declare_q8(lib: ctypes.CDLL) -> None:
+    for name in ("np_block_map_packed", "np_kv_append_q8_packed", "np_paged_decode_q8_packed",
+                 "np_paged_prefill_q8_packed", "np_paged_prefill_q8_check"):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.c_char_p]
+    lib.np_paged_decode_q8_workspace_bytes.restype = ctypes.c_size_t
+    lib.np_paged_decode_q8_workspace_bytes.argtypes = [_I32]
 
 
 def _check(status: int, call: str) -> None:
@@ -512,6 +533,235 @@ def prefill_step(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, block_table
     else:
         np_kv_append(k_pool, v_pool, k_new, v_new, slot_mapping, err_word, stream)
     _launch_prefill(attend)
+
+
+# ------------------------------------------------------- the cache in 8 bits --
+# np_block_map_args, np_kv_append_q8_args and np_read_q8_args (np_paged.h)
+_MAP_ARGS = struct.Struct("@11Pq4i")
+_APPEND_Q8_ARGS = struct.Struct("@9P3q6i")
+_READ_Q8_ARGS = struct.Struct("@12P2q10if")
+
+_FORMS = {torch.float8_e4m3fn: NP_E4M3, torch.int8: NP_INT8}
+
+
+def q8_pools(num_blocks, block_size, kv_heads, head_dim, form=torch.float8_e4m3fn, device="cuda"):
+    """(k_pool, v_pool, k_scale, v_scale) of an empty 8-bit cache: pools
+    [num_blocks, block_size, kv_heads, head_dim] of torch.float8_e4m3fn or torch.int8, and a
+    power-of-two fp32 scale per block and kv head.  An element stands for code * scale."""
+    if form not in _FORMS:
+        raise TypeError(f"unsupported form {form}; the cache holds float8_e4m3fn or int8")
+    pools = [torch.zeros((num_blocks, block_size, kv_heads, head_dim), dtype=torch.uint8,
+                         device=device).view(form) for _ in range(2)]
+    scales = [torch.zeros((num_blocks, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return (*pools, *scales)
+
+
+def _q8_shape(name, k_pool, v_pool, k_scale, v_scale):
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape:
+        raise ValueError(f"{name}: pools must be [blocks, block_size, kv_heads, head_dim]")
+    form = _FORMS.get(k_pool.dtype)
+    if form is None or v_pool.dtype is not k_pool.dtype:
+        raise TypeError(f"{name}: pools must be float8_e4m3fn or int8, both the same")
+    nb, bs, hk, d = k_pool.shape
+    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or \
+            k_scale.shape != (nb, hk) or v_scale.shape != (nb, hk):
+        raise ValueError(f"{name}: scales must be float32 [blocks, kv_heads]")
+    return form, nb, bs, hk, d
+
+
+def _on(cur: int, *tensors) -> bool:
+    """Whether all of them (None aside) are contiguous on device ``cur``."""
+    return all(t is None or (t.get_device() == cur and t.is_contiguous()) for t in tensors)
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, query_starts,
+                 slot_mapping, positions, block_size, kept_lens=None, err_word=None, stream=None):
+    """One step of a batch's bookkeeping on the GPU (see np_paged.h): every row keeps its first
+    min(context_lens, kept_lens) positions (all, without ``kept_lens``) and gets ``new_lens`` more;
+    blocks go back to and come from the end of ``free_blocks``.  Updates block_tables, context_lens,
+    free_blocks and free_count; writes query_starts, slot_mapping and positions (both None: the
+    tables only).
+
+    block_tables int32 [rows, max_blocks]; context_lens, new_lens, kept_lens int32 [rows];
+    free_blocks int32 [num_blocks]; free_count int32 [1]; query_starts int32 [rows + 1];
+    slot_mapping int64 [tokens]; positions int32 [tokens]."""
+    name = "np_block_map"
+    if block_tables.dtype is not torch.int32 or block_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
+    rows, mb = block_tables.shape
+    for t, what in ((context_lens, "context_lens"), (new_lens, "new_lens"), (kept_lens, "kept_lens")):
+        if t is not None and (t.dtype is not torch.int32 or t.shape != (rows,)):
+            raise ValueError(f"{name}: {what} must be int32 [rows]")
+    if free_blocks.dtype is not torch.int32 or free_blocks.dim() != 1:
+        raise ValueError(f"{name}: free_blocks must be int32 [num_blocks]")
+    if free_count.dtype is not torch.int32 or free_count.numel() != 1:
+        raise ValueError(f"{name}: free_count must be one int32")
+    if query_starts.dtype is not torch.int32 or query_starts.shape != (rows + 1,):
+        raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
+    if slot_mapping is not None and (slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1):
+        raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
+    if positions is not None and (slot_mapping is None or positions.dtype is not torch.int32 or
+                                  positions.shape != slot_mapping.shape):
+        raise ValueError(f"{name}: positions must be int32 [tokens], beside a slot_mapping")
+    cur = _device_now()
+    if not _on(cur, block_tables, context_lens, new_lens, kept_lens, free_blocks, free_count,
+               query_starts, slot_mapping, positions, err_word):
+        _refuse(cur, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
+                kept_lens=kept_lens, free_blocks=free_blocks, free_count=free_count,
+                query_starts=query_starts, slot_mapping=slot_mapping, positions=positions,
+                err_word=err_word)
+    n = 0 if slot_mapping is None else slot_mapping.shape[0]
+    st = load().np_block_map_packed(_pack(
+        _MAP_ARGS, name, block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(),
+        _ptr(kept_lens), free_blocks.data_ptr(), free_count.data_ptr(), query_starts.data_ptr(),
+        _ptr(slot_mapping) if n else 0, _ptr(positions) if n else 0, _ptr(err_word),
+        _stream_now(stream, cur), free_blocks.shape[0], mb, rows, block_size, n))
+    if st != NP_OK:
+        raise NPError(st, name)
+
+
+def np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, err_word=None,
+                    stream=None):
+    """New K/V [T, kv_heads, head_dim] (bf16 or fp32; tokens may be strided) rounded into the 8-bit
+    pools at ``slot_mapping`` (int64 [T]), with a power-of-two scale per block and kv head (see
+    np_paged.h).  The tokens of a block stand side by side in ``slot_mapping``."""
+    name = "np_kv_append_q8"
+    form, nb, bs, hk, d = _q8_shape(name, k_pool, v_pool, k_scale, v_scale)
+    if k_new.dim() != 3 or v_new.shape != k_new.shape or k_new.shape[1] != hk or k_new.shape[2] != d:
+        raise ValueError(f"{name}: k_new/v_new must be [tokens, kv_heads, head_dim] of the pools")
+    if v_new.dtype is not k_new.dtype:
+        raise ValueError(f"{name}: k_new and v_new must share a dtype")
+    n = k_new.shape[0]
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,):
+        raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
+    cur = _device_now()
+    kp, ks = _token_rows(k_new, "k_new", cur, n, hk, d)
+    vp, vs = _token_rows(v_new, "v_new", cur, n, hk, d)
+    if not _on(cur, k_pool, v_pool, k_scale, v_scale, slot_mapping, err_word):
+        _refuse(cur, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
+                slot_mapping=slot_mapping, err_word=err_word)
+    st = load().np_kv_append_q8_packed(_pack(
+        _APPEND_Q8_ARGS, name, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), kp, vp, slot_mapping.data_ptr(), _ptr(err_word),
+        _stream_now(stream, cur), nb, ks, vs, form, _CODES[k_new.dtype], bs, hk, d, n))
+    if st != NP_OK:
+        raise NPError(st, name)
+
+
+def _read_q8_args(name, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                  query_starts, scale, workspace, err_word, stream, query_len, tokens) -> bytes:
+    """np_read_q8_args after the binding's checks; q's shape is the caller's to check."""
+    form, nb, bs, hk, d = _q8_shape(name, k_pool, v_pool, k_scale, v_scale)
+    if q.shape[-1] != d:
+        raise ValueError(f"{name}: q/pool shape mismatch")
+    if out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError(f"{name}: out must match q")
+    if block_tables.dtype is not torch.int32 or block_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
+    rows, mb = block_tables.shape
+    if context_lens.dtype is not torch.int32 or context_lens.shape != (rows,):
+        raise ValueError(f"{name}: context_lens must be int32 [rows]")
+    if query_starts is not None and (query_starts.dtype is not torch.int32 or
+                                     query_starts.shape != (rows + 1,)):
+        raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
+    cur = _device_now()
+    if not _on(cur, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+               query_starts, workspace, err_word):
+        _refuse(cur, out=out, q=q, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
+                block_tables=block_tables, context_lens=context_lens, query_starts=query_starts,
+                workspace=workspace, err_word=err_word)
+    return _pack(
+        _READ_Q8_ARGS, name, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        _ptr(query_starts), _ptr(workspace), _ptr(err_word), _stream_now(stream, cur), nb,
+        0 if workspace is None else workspace.nbytes, form, _CODES[q.dtype], bs, hk, d, mb, rows,
+        query_len, tokens, q.shape[-2], scale)
+
+
+def np_paged_decode_q8_workspace_bytes(head_dim) -> int:
+    return load().np_paged_decode_q8_workspace_bytes(head_dim)
+
+
+def decode_q8_workspace(head_dim, device="cuda") -> torch.Tensor:
+    """A workspace for np_paged_decode_q8 (its contents need no initialisation)."""
+    n = np_paged_decode_q8_workspace_bytes(head_dim)
+    if n == 0:
+        raise ValueError(f"unsupported head_dim {head_dim}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def np_paged_decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                       workspace, err_word=None, stream=None):
+    """The decode read of an 8-bit cache (see np_paged.h): q/out [rows, q_heads, head_dim], or
+    [rows, query_len, q_heads, head_dim] (the rows' last query_len positions), bf16 or fp32."""
+    name = "np_paged_decode_q8"
+    rows, qn, _, _ = _q_shape(q)
+    if block_tables.dim() == 2 and block_tables.shape[0] != rows:
+        raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
+    st = load().np_paged_decode_q8_packed(_read_q8_args(
+        name, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, None, scale,
+        workspace, err_word, stream, qn, rows * qn))
+    if st != NP_OK:
+        raise NPError(st, name)
+
+
+def np_paged_prefill_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                        query_starts, scale, workspace, err_word=None, stream=None):
+    """Attention of ragged chunks over an 8-bit cache (see np_paged.h): as np_paged_prefill, with
+    np_kv_append_q8's pools and scales; q/out [tokens, q_heads, head_dim] bf16 or fp32."""
+    _launch_prefill_q8(_prefill_q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                                        context_lens, query_starts, scale, workspace, err_word,
+                                        stream))
+
+
+def _prefill_q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                     query_starts, scale, workspace, err_word, stream) -> bytes:
+    name = "np_paged_prefill_q8"
+    if q.dim() != 3:
+        raise ValueError(f"{name}: q must be [tokens, q_heads, head_dim]")
+    if query_starts is None:
+        raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
+    return _read_q8_args(name, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                         query_starts, scale, workspace, err_word, stream, 0, q.shape[0])
+
+
+def _launch_prefill_q8(packed: bytes) -> None:
+    st = load().np_paged_prefill_q8_packed(packed)
+    if st != NP_OK:
+        raise NPError(st, "np_paged_prefill_q8")
+
+
+def decode_step_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                   workspace, *, k_new=None, v_new=None, slot_mapping=None, err_word=None,
+                   stream=None):
+    """One decode step of an 8-bit cache: the rows' new K/V ([rows, kv_heads, head_dim], or
+    [rows, query_len, kv_heads, head_dim] with slots [rows, query_len]) appended, if given, then
+    the read."""
+    if k_new is not None:
+        if k_new.dim() == 4:
+            k_new, v_new = k_new.flatten(0, 1), v_new.flatten(0, 1)
+        np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping.flatten(),
+                        err_word, stream)
+    np_paged_decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                       workspace, err_word, stream)
+
+
+def prefill_step_q8(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, k_scale, v_scale,
+                    block_tables, context_lens, query_starts, scale, workspace, *, err_word=None,
+                    stream=None):
+    """One layer's prompt step of an 8-bit cache: the new tokens' k and v rounded into the pools,
+    then their attention.  What the attention refuses is refused before the append."""
+    attend = _prefill_q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                              query_starts, scale, workspace, err_word, stream)
+    st = load().np_paged_prefill_q8_check(attend)
+    if st != NP_OK:
+        raise NPError(st, "np_paged_prefill_q8")
+    np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, err_word, stream)
+    _launch_prefill_q8(attend)
 
 
 def np_paged_decode_plan(rows, q_heads, kv_heads, head_dim, block_size, max_blocks_per_row,

@@ -41,7 +41,16 @@ def _units(extra: list[str], build_dir: str, csrc: str) -> list[tuple[str, str, 
         (os.path.join(csrc, "prefill_api.cu"), os.path.join(objdir, "prefill_api.o"), []),
         (os.path.join(csrc, "prefill_plan.cu"), os.path.join(objdir, "prefill_plan.o"), []),
         (os.path.join(csrc, "prefill_simt.cu"), os.path.join(objdir, "prefill_simt.o"), []),
+        (os.path.join(csrc, "block_map.cu"), os.path.join(objdir, "block_map.o"), []),
+        (os.path.join(csrc, "append_q8.cu"), os.path.join(objdir, "append_q8.o"), []),
+        (os.path.join(csrc, "decode_q8_api.cu"), os.path.join(objdir, "decode_q8_api.o"), []),
+        (os.path.join(csrc, "prefill_q8_simt.cu"), os.path.join(objdir, "prefill_q8_simt.o"), []),
     ]
+    for d in HEAD_DIMS:
+        for form, name in enumerate(("e4m3", "int8")):
+            units.append((os.path.join(csrc, "decode_q8.cu"),
+                          os.path.join(objdir, f"decode_q8_d{d}_{name}.o"),
+                          [f"-DNPK_D={d}", f"-DNPK_FORM={form}"]))
     for bf16 in (0, 1):
         for d in HEAD_DIMS:
             name = f"decode_{'bf16' if bf16 else 'f32'}_d{d}.o"

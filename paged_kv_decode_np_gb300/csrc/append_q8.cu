@@ -1,0 +1,304 @@
+// append_q8.cu -- np_kv_append_q8: new tokens' K and V rounded into the 8-bit
+// pools, with one power-of-two scale per (block of tokens, kv head).
+//
+// A run is the call's tokens of one block, side by side in the slot mapping.
+// For a run, a kv head and K or V:
+//   A  = max |x|,  e = least with A <= QMAX 2^e
+//   e' = e where the run holds the block's first slot, else max(e_old, e)
+//   older codes of the block: rne(code 2^(e_old - e')) where e' > e_old
+//   new codes: rne(x 2^-e')
+// One warp does that: it reads the run's values (a 16-byte vector a lane and
+// step), keeps them in registers where they fit (16 tokens of 128 bf16 dims),
+// takes the maximum, and writes the codes.  No two warps touch the same block
+// and head, so there is nothing to wait for and nothing atomic.
+//
+// Bound: HBM for prompts, latency for decode batches.  A block of the grid takes
+// `window` tokens: its warps find which of them begin runs and deal out
+// (run, head, K or V).
+#include "cache8.cuh"
+#include "decode_launch.h"
+#include "host_checks.h"
+
+namespace npk {
+
+constexpr int kAppend8Warps = 8;
+
+struct Append8Params {
+  uint8_t* pool[2];
+  float* scale[2];
+  const void* src[2];
+  int64_t stride[2];  // elements between tokens
+  const int64_t* slots;
+  int32_t* err;
+  int64_t num_slots;
+  int32_t block_size, kv_heads, tokens, window;
+};
+
+__device__ __forceinline__ int64_t block_of(const Append8Params& p, int64_t slot) {
+  return p.num_slots <= 0x7fffffffll ? (int64_t)((uint32_t)slot / (uint32_t)p.block_size)
+                                     : slot / p.block_size;
+}
+
+template <typename T, int D, int FORM>
+__device__ __forceinline__ void append8_run(const Append8Params& p, int t0, int64_t blk, int h, int kv,
+                                            int lane) {
+  constexpr unsigned FULL = 0xffffffffu;
+  using F = Form8<FORM>;
+  constexpr int V = 16 / (int)sizeof(T);         // values of a vector
+  constexpr int LT = D / V;                      // lanes of a token (1 to 64)
+  constexpr int PT = LT <= 32 ? 1 : LT / 32;     // vectors of a lane and token
+  constexpr int TP = LT <= 32 ? 32 / LT : 1;     // tokens of a step
+  constexpr int U = 8 / PT;                      // steps whose values stay in registers
+  const int sub = LT <= 32 ? lane / LT : 0;
+  const int col = (LT <= 32 ? lane % LT : lane) * V;
+
+  // the run's length, and whether it holds the block's first slot
+  int n = 0;
+  bool anew = false;
+  const int64_t first = blk * p.block_size;
+  for (int i0 = 0;; i0 += 32) {
+    const int64_t s = t0 + i0 + lane < p.tokens ? p.slots[t0 + i0 + lane] : -1;
+    const bool in = s >= first && s < first + p.block_size && s < p.num_slots;
+    const unsigned m = __ballot_sync(FULL, in);
+    const int run = m == FULL ? 32 : __ffs(~m) - 1;
+    anew |= __any_sync(FULL, in && lane < run && s == first);
+    n += run;
+    if (run < 32) break;
+  }
+
+  const T* src = static_cast<const T*>(p.src[kv]) + (int64_t)h * D + col;
+  const int64_t stride = p.stride[kv];
+  uint4 held[U][PT];
+  uint32_t top = 0;  // the largest |x| that is finite, as bits
+  bool odd = false;
+  auto load = [&](int i, uint4* r) {  // token i + sub of the run
+#pragma unroll
+    for (int k = 0; k < PT; ++k)
+      r[k] = i + sub < n
+                 ? *reinterpret_cast<const uint4*>(src + (t0 + i + sub) * stride + k * 32 * V)
+                 : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto widen = [&](const uint4& r, float* x) {
+    Storage<T>::template load<V>(reinterpret_cast<const T*>(&r), x);
+  };
+  auto look = [&](const uint4& r) {
+    float x[V];
+    widen(r, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
+      if (a >= 0x7f800000u) odd = true;
+      else top = max(top, a);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u * TP, held[u]);
+  // the scale found, on its way meanwhile
+  float* sp = p.scale[kv] + blk * p.kv_heads + h;
+  const int e_old = scale_exp(__float_as_uint(*sp));
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int k = 0; k < PT; ++k) look(held[u][k]);
+  for (int i = U * TP; i < n; i += TP) {
+    uint4 r[PT];
+    load(i, r);
+#pragma unroll
+    for (int k = 0; k < PT; ++k) look(r[k]);
+  }
+  top = __reduce_max_sync(FULL, top);
+  if (odd) set_flag(p.err, NP_FLAG_VALUE);
+  int e = top < 0x00800000u ? kScaleMin : min(max(F::need(top), kScaleMin), kScaleMax);
+  if (!anew) e = max(e, e_old);
+
+  uint8_t* pool = p.pool[kv] + (int64_t)h * D;
+  const int64_t row = (int64_t)p.kv_heads * D;  // bytes of a slot, all heads
+  if (!anew && e > e_old) {
+    // the codes of the block's other slots, to the new scale
+    const float f = pow2f(max(e_old - e, -126));
+    for (int o = 0; o < p.block_size; ++o) {
+      if (first + o >= p.num_slots) break;
+      bool mine = false;  // written by this run
+      for (int i = lane; i < n; i += 32) mine |= p.slots[t0 + i] == first + o;
+      if (__any_sync(FULL, mine)) continue;
+      uint8_t* at = pool + (first + o) * row;
+      for (int d = 4 * lane; d < D; d += 128) {
+        float x[4];
+        widen8x4<FORM>(*reinterpret_cast<const uint32_t*>(at + d), x);
+        *reinterpret_cast<uint32_t*>(at + d) =
+            F::code2(x[0] * f, x[1] * f) | (F::code2(x[2] * f, x[3] * f) << 16);
+      }
+    }
+  }
+  if (lane == 0) *sp = pow2f(e);
+
+  const float f = pow2f(-e);
+  auto store = [&](int i, const uint4* r) {
+    if (i + sub >= n) return;
+    uint8_t* at = pool + p.slots[t0 + i + sub] * row + col;
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      float x[V];
+      widen(r[k], x);
+      uint32_t w[V / 4];
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q)
+        w[q] = F::code2(x[4 * q] * f, x[4 * q + 1] * f) | (F::code2(x[4 * q + 2] * f, x[4 * q + 3] * f) << 16);
+      if constexpr (V == 8) *reinterpret_cast<uint2*>(at + k * 32 * V) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(at + k * 32 * V) = w[0];
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) store(u * TP, held[u]);
+  for (int i = U * TP; i < n; i += TP) {
+    uint4 r[PT];
+    load(i, r);
+    store(i, r);
+  }
+}
+
+template <typename T, int D, int FORM>
+__global__ void __launch_bounds__(32 * kAppend8Warps) append8_kernel(const __grid_constant__
+                                                                     Append8Params p) {
+  __shared__ int64_t run_block[32];
+  __shared__ int run_token[32];
+  __shared__ int runs;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w0 = blockIdx.x * p.window;  // this block's tokens
+  if (warp == 0) {
+    const int t = w0 + lane;
+    const bool live = lane < p.window && t < p.tokens;
+    const int64_t s = live ? p.slots[t] : -1;
+    const int64_t before = live && t > 0 ? p.slots[t - 1] : -1;
+    if (s >= p.num_slots && blockIdx.y == 0) set_flag(p.err, NP_FLAG_SLOT);
+    const bool in = s >= 0 && s < p.num_slots;
+    const int64_t b = in ? block_of(p, s) : -1;
+    const bool joined = before >= 0 && before < p.num_slots && block_of(p, before) == b;
+    const bool lead = in && !joined;
+    const unsigned m = __ballot_sync(0xffffffffu, lead);
+    if (lead) {
+      const int k = __popc(m & ((1u << lane) - 1u));
+      run_block[k] = b;
+      run_token[k] = t;
+    }
+    if (lane == 0) runs = __popc(m);
+  }
+  __syncthreads();
+  const int tasks = runs * 2 * p.kv_heads;
+  for (int i = blockIdx.y * kAppend8Warps + warp; i < tasks; i += gridDim.y * kAppend8Warps) {
+    // neighbouring warps: neighbouring heads of the same tokens
+    const int h = i % p.kv_heads, x = i / p.kv_heads;
+    append8_run<T, D, FORM>(p, run_token[x >> 1], run_block[x >> 1], h, x & 1, lane);
+  }
+}
+
+template <typename T, int D, int FORM>
+static np_status launch_append8(Append8Params& p, cudaStream_t s) {
+  // few tokens: few of them a block, so that all warps find work
+  p.window = p.tokens >= 4096 ? 32 : p.tokens >= 512 ? 8 : 1;
+  const unsigned x = (unsigned)((p.tokens + p.window - 1) / p.window);
+  const int tasks = 2 * p.kv_heads;  // of one run
+  unsigned y = (unsigned)((tasks + kAppend8Warps - 1) / kAppend8Warps);
+  if (y > 64) y = 64;
+  append8_kernel<T, D, FORM><<<dim3(x, y), 32 * kAppend8Warps, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? NP_OK : NP_ERR_CUDA;
+}
+
+template <typename T, int FORM>
+static np_status launch_append8_dim(Append8Params& p, int32_t d, cudaStream_t s) {
+  switch (d) {
+    case 16: return launch_append8<T, 16, FORM>(p, s);
+    case 32: return launch_append8<T, 32, FORM>(p, s);
+    case 64: return launch_append8<T, 64, FORM>(p, s);
+    case 128: return launch_append8<T, 128, FORM>(p, s);
+    case 256: return launch_append8<T, 256, FORM>(p, s);
+  }
+  return NP_ERR_UNSUPPORTED;
+}
+
+}  // namespace npk
+
+extern "C" np_status np_kv_append_q8_packed(const np_kv_append_q8_args* a) {
+  using namespace npk;
+  if (!a) return NP_ERR_INVALID_ARG;
+  const int es = a->dtype == NP_F32 ? 4 : (a->dtype == NP_BF16 ? 2 : 0);
+  if (es == 0 || (a->form != NP_E4M3 && a->form != NP_INT8)) return NP_ERR_UNSUPPORTED;
+  const int d = a->head_dim;
+  if (a->num_blocks <= 0 || a->block_size <= 0 || a->kv_heads <= 0 || a->num_tokens < 0 || d <= 0)
+    return NP_ERR_INVALID_ARG;
+  if (d != 16 && d != 32 && d != 64 && d != 128 && d != 256) return NP_ERR_UNSUPPORTED;
+  const int64_t row = (int64_t)a->kv_heads * d;
+  int64_t slots = 0, pool = 0, scales = 0, kn = 0, vn = 0;
+  if (!mul_fits(a->num_blocks, a->block_size, &slots) || !mul_fits(slots, row, &pool) ||
+      !mul_fits(a->num_blocks, 4ll * a->kv_heads, &scales))
+    return NP_ERR_OUT_OF_RANGE;
+  if (a->num_tokens == 0) return NP_OK;
+  if (a->k_stride < 0 || a->v_stride < 0) return NP_ERR_INVALID_ARG;
+  if (!mul_fits(a->num_tokens - 1, a->k_stride, &kn) || !mul_fits(a->num_tokens - 1, a->v_stride, &vn) ||
+      !mul_fits(kn, es, &kn) || !mul_fits(vn, es, &vn))
+    return NP_ERR_OUT_OF_RANGE;
+  kn += row * es;
+  vn += row * es;
+  if (!a->k_pool || !a->v_pool || !a->k_scale || !a->v_scale || !a->k_new || !a->v_new || !a->slot_mapping)
+    return NP_ERR_INVALID_ARG;
+  if (a->num_tokens > 1 && (a->k_stride < row || a->k_stride * es % 16 != 0 || a->v_stride < row ||
+                            a->v_stride * es % 16 != 0))
+    return NP_ERR_INVALID_ARG;
+  for (const void* x : {static_cast<const void*>(a->k_pool), static_cast<const void*>(a->v_pool),
+                        static_cast<const void*>(a->k_scale), static_cast<const void*>(a->v_scale), a->k_new,
+                        a->v_new})
+    if (!aligned_to(x, 16)) return NP_ERR_INVALID_ARG;
+  if (!aligned_to(a->slot_mapping, 8) || !aligned_to(a->err_word, 4)) return NP_ERR_INVALID_ARG;
+  const Span spans[] = {{a->k_pool, pool}, {a->v_pool, pool}, {a->k_scale, scales}, {a->v_scale, scales},
+                        {a->k_new, kn},    {a->v_new, vn},    {a->slot_mapping, 8ll * a->num_tokens}};
+  if (any_overlap(spans, 4)) return NP_ERR_INVALID_ARG;
+  Append8Params p{};
+  p.pool[0] = static_cast<uint8_t*>(a->k_pool);
+  p.pool[1] = static_cast<uint8_t*>(a->v_pool);
+  p.scale[0] = a->k_scale;
+  p.scale[1] = a->v_scale;
+  p.src[0] = a->k_new;
+  p.src[1] = a->v_new;
+  p.stride[0] = a->k_stride;
+  p.stride[1] = a->v_stride;
+  p.slots = a->slot_mapping;
+  p.err = a->err_word;
+  p.num_slots = slots;
+  p.block_size = a->block_size;
+  p.kv_heads = a->kv_heads;
+  p.tokens = a->num_tokens;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
+  if (a->form == NP_E4M3)
+    return a->dtype == NP_BF16 ? launch_append8_dim<__nv_bfloat16, NP_E4M3>(p, d, s)
+                               : launch_append8_dim<float, NP_E4M3>(p, d, s);
+  return a->dtype == NP_BF16 ? launch_append8_dim<__nv_bfloat16, NP_INT8>(p, d, s)
+                             : launch_append8_dim<float, NP_INT8>(p, d, s);
+}
+
+extern "C" np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                     np_form8 form, int64_t num_blocks, int32_t block_size,
+                                     int32_t kv_heads, int32_t head_dim, const void* k_new,
+                                     const void* v_new, np_dtype dtype, int64_t k_stride,
+                                     int64_t v_stride, const int64_t* slot_mapping, int32_t num_tokens,
+                                     int32_t* err_word, np_stream_t stream) {
+  np_kv_append_q8_args a{};
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.slot_mapping = slot_mapping;
+  a.err_word = err_word;
+  a.stream = stream;
+  a.num_blocks = num_blocks;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.form = form;
+  a.dtype = dtype;
+  a.block_size = block_size;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.num_tokens = num_tokens;
+  return np_kv_append_q8_packed(&a);
+}

@@ -1,0 +1,726 @@
+// decode_q8.cu -- np_paged_decode_q8: the decode read of an 8-bit cache, compiled
+// once per head_dim and form (-DNPK_D, -DNPK_FORM).
+//
+// Per row, kv head and its MR = G Q (query token, head) rows, with codes k, v and
+// exponents a, b of their scales:
+//     x_j = c (q . k_j) 2^a_j + b_j                (log2 units; c = scale log2 e)
+//     O  = sum_j 2^(x_j - M) v_j,   l = sum_j 2^(x_j - M - b_j),   out = O / l
+// so V's scale is an addition to the exponent, and its product stays a product
+// of codes.  M is set 6 below the largest x seen, and again only where an x passes it by
+// more than 14: weights stay within fp16's 2^15, and what is too small for its
+// subnormals is below 2^-30 of the largest.
+//
+// The products are m16n8k16 mma (fp16 in, fp32 out) with the cache as the A
+// operand -- 16 tokens x 16 dims of K, 16 dims x 16 tokens of V -- and the rows
+// as B's 8 columns, so that a code is widened once for 8 rows.  Codes are exact
+// in fp16; q is scaled by a power of two; fp32 q and weights take two fp16
+// parts each, two mma to a sum.  S comes out with a lane's values on tokens
+// lane/4, lane/4 + 8 and rows 2 (lane%4), + 1; movmatrix turns it into B of the
+// second product.
+//
+// A warp is a reader of its own: it owns a ring of stages in shared memory, a
+// stage holding the K, V and scales of CT tokens of one kv head, filled by its own
+// 16-byte asynchronous copies (which zero what lies past the context) and waited for
+// by nobody else.  No barrier is on the way but the join of a head's warps at a
+// row's end.  A block's HG kv heads have WPH warps each, which take the block's
+// chunks of CT tokens in turn.
+//
+// The work: rows (times groups of HG kv heads) laid end to end in chunks, an
+// equal share per block, one block an SM, from the context lengths on the device.
+// A row inside one block is stored directly; one that is cut leaves partials
+// that a second launch joins in block order.
+#include "cache8.cuh"
+#include "decode_q8.cuh"
+#include "tcgen05.cuh"  // cp_async_*
+
+#ifndef NPK_D
+#error "compiled per head_dim and form"
+#endif
+
+namespace npk {
+
+// Geometry of a stage.  Rows of D bytes; 128-byte lines; 16-byte pieces of a line are
+// swizzled so that both products' reads are free of bank conflicts.
+template <int D, int NT>
+struct Q8Geo {
+  static constexpr int WARPS = q8_warps(D, NT);
+  static constexpr int CT = 16 * NT;              // tokens of a stage
+  static constexpr int MR = 8 * NT;               // rows of the exchange at a row's end
+  static constexpr int LD = D + 4;                // floats of an exchanged O row
+  static constexpr int DATA = 2 * CT * D + 8 * CT;
+  static constexpr int SWAP = (MR * LD + 2 * MR) * 4;
+  static constexpr int STAGE = ((DATA > SWAP ? DATA : SWAP) + 127) / 128 * 128;
+  static constexpr int FIT = 224 * 1024 / (WARPS * STAGE);
+  static constexpr int NS = FIT < 8 ? FIT : 8;    // stages of a warp's ring
+  static constexpr int SMEM = WARPS * NS * STAGE;
+  static_assert(NS >= 3, "ring");
+  // byte of piece `ch` of row `r`
+  __device__ __forceinline__ static uint32_t at(int r, int ch) {
+    if constexpr (D >= 128) return (uint32_t)(r * D + ((ch ^ (r & 7)) << 4));
+    else if constexpr (D == 16) return (uint32_t)(r << 4);
+    else {
+      constexpr int PL = 128 / D, PP = D / 16;  // rows of a line, pieces of a row
+      const int line = r / PL, c = (r % PL) * PP + ch;
+      return (uint32_t)(line * 128 + ((c ^ (2 * (line & 3))) << 4));
+    }
+  }
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// the part of (lo, hi) that `packed` leaves
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t packed) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+  return pack_half(lo - f.x, hi - f.y);
+}
+
+// 16 bytes to shared memory, zeros where !live
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+}
+
+__device__ __forceinline__ int32_t q8_len(const DecodeQ8Params& p, int r) {
+  const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+  const int32_t c = p.lens[r];
+  return c < 0 ? 0 : (c > cap ? (int32_t)cap : c);
+}
+
+// A block's walk over its share, by each of its warps: segment by segment (a run of
+// one row's chunks), in each the chunks that are this warp's.
+template <int CT>
+struct Q8Walk {
+  int hgi, r;          // the segment's kv head group and row
+  int32_t c;           // its context
+  int32_t c0;          // its first chunk (of the row)
+  int64_t g0, g1;      // its chunks among the block's
+  int64_t total;       // the block's chunks
+
+  __device__ __forceinline__ void fill(const DecodeQ8Params& p) {
+    c = q8_len(p, r);
+    const int64_t n = (c + CT - 1) / CT - c0;
+    g1 = min(total, g0 + n);
+  }
+  __device__ __forceinline__ void start(const DecodeQ8Params& p, int hgi_, int r_, int32_t c0_, int64_t n) {
+    hgi = hgi_;
+    r = r_;
+    c0 = c0_;
+    g0 = 0;
+    g1 = 0;
+    total = n;
+    if (total > 0) fill(p);
+  }
+  __device__ __forceinline__ bool live() const { return g0 < total; }
+  __device__ __forceinline__ void next(const DecodeQ8Params& p) {  // the next segment with chunks
+    g0 = g1;
+    c0 = 0;
+    while (g0 < total && g1 == g0) {
+      if (++r == p.rows) {
+        r = 0;
+        ++hgi;
+      }
+      fill(p);
+    }
+  }
+};
+
+template <typename T, int D, int FORM, int NT>
+__global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
+    decode_q8_kernel(const __grid_constant__ DecodeQ8Params p) {
+  using Geo = Q8Geo<D, NT>;
+  using F = Form8<FORM>;
+  constexpr unsigned FULL = 0xffffffffu;
+  constexpr int WARPS = Geo::WARPS, CT = Geo::CT, NS = Geo::NS, MR = Geo::MR, LD = Geo::LD;
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int PARTS = F32 ? 2 : 1;            // fp16 parts of q and of the weights
+  static_assert(!F32 || NT == 1, "fp32 rows fit one tile");
+  constexpr int KW = D >= 64 ? 4 : D / 16;      // 4-byte words of a K read
+  constexpr int KJ = D / 16 / KW;               // K reads of a token
+  constexpr int VB = D >= 128 ? 16 : D / 8;     // bytes of a V read
+  constexpr int VJ = D == 256 ? 2 : 1;          // V reads of a token
+  extern __shared__ __align__(128) unsigned char q8_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int HG = p.head_group, WPH = WARPS / HG;
+  const int hl = warp % HG, wi = warp / HG;     // kv head of the group, warp of the head
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this block's share: chunks [u0, u1) of all rows' chunks, which each thread
+  // counts for a run of rows
+  __shared__ int64_t warp_sum[WARPS];
+  __shared__ int64_t found[6];  // first row, first chunk, chunks; W, Pe, u0
+  {
+    const int per = (p.rows + 32 * WARPS - 1) / (32 * WARPS);
+    const int ra = min(p.rows, (int)threadIdx.x * per), rb = min(p.rows, ra + per);
+    const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+    int64_t own = 0;
+    for (int r = ra; r < rb; ++r) {
+      const int32_t c = p.lens[r];
+      if (blockIdx.x == 0 && (c < 0 || c > cap)) set_flag(p.err, NP_FLAG_CONTEXT);
+      own += (q8_len(p, r) + CT - 1) / CT;
+    }
+    int64_t x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int64_t before = x - own, all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    const int64_t W = all * (p.kv_heads / HG);
+    const int64_t want = (W + p.least - 1) / p.least;
+    const int64_t Pe = want < 1 ? 1 : min(want, (int64_t)gridDim.x);
+    const int b = blockIdx.x;
+    const int64_t u0 = b < Pe ? b * W / Pe : W, u1 = b + 1 < Pe ? (b + 1) * W / Pe : W;
+    if (threadIdx.x == 0) {
+      found[0] = 0;
+      found[1] = 0;
+      found[2] = u1 - u0;
+      found[3] = W;
+      found[4] = Pe;
+      found[5] = u0;
+    }
+    __syncthreads();
+    if (u1 > u0) {
+      const int64_t at = u0 % all;
+      if (own > 0 && before <= at && at < before + own) {  // one thread's
+        int64_t run = before;
+        int r = ra;
+        for (;; ++r) {
+          const int64_t n = (q8_len(p, r) + CT - 1) / CT;
+          if (at < run + n) break;
+          run += n;
+        }
+        found[0] = r + (u0 / all) * p.rows;
+        found[1] = at - run;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) p.cuts[b] = make_int4(-1, 0, 0, 0);  // (unless its last row is cut, below)
+  }
+  const int64_t chunks = found[2];
+  const int64_t v0 = found[0];
+
+  // rows without history
+  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    if (q8_len(p, r) != 0) continue;
+    T* o = static_cast<T*>(p.out) + (int64_t)r * p.query_len * p.q_heads * D;
+    for (int64_t i = threadIdx.x; i < (int64_t)p.query_len * p.q_heads * D; i += 32 * WARPS) o[i] = T(0.f);
+  }
+  if (wi >= WPH || chunks == 0) return;  // (warps beyond the heads' have nothing to do)
+
+  unsigned char* ring = q8_smem + (size_t)warp * NS * Geo::STAGE;
+  const uint32_t ring_u = smem_u32(ring);
+  const int rows_used = p.group * p.query_len;  // MR at most
+
+  // ---- loads: chunk by chunk ahead of the reads.  Lane i < CT looks after token i.
+  Q8Walk<CT> ld;
+  ld.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
+  int64_t lg = wi;         // the next chunk to load, of the block's
+  int32_t block = 0;       // the block of its token `lane`, looked up ahead
+  int32_t inner = 0;       // and the token's place in it
+  bool held = false;       // (a token of the row)
+  auto look_up = [&]() {
+    while (ld.live() && lg >= ld.g1) ld.next(p);
+    held = false;
+    if (!ld.live()) return;
+    const int32_t t = (int32_t)(ld.c0 + (lg - ld.g0)) * CT + (lane % CT);
+    held = t < ld.c;
+    if (held) {
+      const int32_t j = (int32_t)((uint32_t)t / (uint32_t)p.block_size);
+      inner = t - j * p.block_size;
+      block = p.tables[(int64_t)ld.r * p.max_blocks + j];
+    }
+  };
+  auto issue = [&](int slot) {
+    if (ld.live()) {
+      const uint32_t st = ring_u + (uint32_t)slot * Geo::STAGE;
+      if (!held) block = inner = 0;
+      if (block < 0 || block >= p.num_blocks) {
+        set_flag(p.err, NP_FLAG_BLOCK_ID);
+        block = 0;
+      }
+      const int kvh = ld.hgi * HG + hl;
+      const int64_t at = ((int64_t)block * p.block_size + inner) * p.kv_heads + kvh;
+      if (lane < CT) {  // NT 1: 16 lanes; their scales
+        const int64_t sc = (int64_t)block * p.kv_heads + kvh;
+        copy4(st + 2 * CT * D + 4 * lane, p.k_scale + sc, held);
+        copy4(st + 2 * CT * D + 4 * (CT + lane), p.v_scale + sc, held);
+      }
+      constexpr int LT = D / 16;                    // lanes of a token
+      constexpr int TP = 32 / LT < CT ? 32 / LT : CT;  // tokens of a step
+      const int sub = lane / LT, ch = lane % LT;
+#pragma unroll
+      for (int i = 0; i < CT; i += TP) {
+        const int tok = (i + sub) % CT;             // (D 16, NT 1: half the lanes repeat)
+        const int64_t off = __shfl_sync(FULL, at, tok) * D + ch * 16;
+        const bool on = __shfl_sync(FULL, (int)held, tok) != 0;
+        if (TP * LT == 32 || lane < TP * LT) {
+          copy16(st + Geo::at(tok, ch), p.k_pool + off, on);
+          copy16(st + CT * D + Geo::at(tok, ch), p.v_pool + off, on);
+        }
+      }
+      lg += WPH;
+      look_up();
+    }
+    cp_async_commit();
+  };
+  look_up();
+#pragma unroll 1
+  for (int s = 0; s < NS - 1; ++s) issue(s);
+
+  // ---- reads
+  Q8Walk<CT> w;
+  w.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
+  int64_t cg = wi;  // this warp's next chunk
+  int slot = 0;     // its stage
+  bool first = true;
+  for (; w.live(); w.next(p)) {
+    const int kvh = w.hgi * HG + hl;
+    // q: column n of tile nt is row n + 8 nt of the head's (query token, head) rows; a
+    // lane holds dims 16 (piece) + 4 word .. + 3 of column g
+    uint32_t qf[NT][PARTS][KJ * KW][2];
+    float qs[NT][2];  // scale of rows 2 t4, + 1
+    int32_t lim[NT][2];  // the first position each does not see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = nt * 8 + g;
+      const bool on = row < rows_used;
+      const int qi = on ? row / p.group : 0, h = on ? row - qi * p.group : 0;
+      const T* src = static_cast<const T*>(p.q) +
+                     (((int64_t)w.r * p.query_len + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+      float x[KJ * KW][4];
+      float big = 0.f;
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+          const int d = D >= 128 ? 16 * (2 * t4 + (j & 1) + 8 * (j >> 1)) + 4 * k : t4 * (4 * KW) + 4 * k;
+          float* y = x[j * KW + k];
+          Storage<T>::template load<4>(src + d, y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!on) y[e] = 0.f;
+            big = fmaxf(big, fabsf(y[e]));
+          }
+        }
+      big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
+      // the row's largest element to [2^14, 2^15)
+      const int e = min(14 + 127 - (int)(__float_as_uint(big) >> 23), 120);
+      const float f = pow2f(e);
+      const float s = on ? p.qscale * pow2f(-e) : 0.f;
+      qs[nt][0] = __shfl_sync(FULL, s, 8 * t4);
+      qs[nt][1] = __shfl_sync(FULL, s, 8 * t4 + 4);
+#pragma unroll
+      for (int i = 0; i < KJ * KW; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float a = x[i][2 * c] * f, b = x[i][2 * c + 1] * f;
+          qf[nt][0][i][c] = pack_half(a, b);
+          if constexpr (F32) qf[nt][1][i][c] = pack_rest(a, b, qf[nt][0][i][c]);
+        }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row2 = nt * 8 + 2 * t4 + c;
+        lim[nt][c] = row2 < rows_used ? w.c - p.query_len + row2 / p.group + 1 : w.c;
+      }
+    }
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    int last = -1;  // the stage read last in this segment
+    const int32_t all_see = w.c - p.query_len + 1;  // positions before it: every row
+
+    for (; cg < w.g1; cg += WPH) {
+      cp_async_wait<NS - 2>();
+      __syncwarp();
+      issue(slot == 0 ? NS - 1 : slot - 1);  // into the stage read before
+      const uint32_t st = ring_u + (uint32_t)slot * Geo::STAGE;
+      last = slot;
+      slot = slot + 1 == NS ? 0 : slot + 1;
+      const int32_t t0 = (int32_t)(w.c0 + (cg - w.g0)) * CT;
+#pragma unroll
+      for (int sub = 0; sub < CT; sub += 16) {
+        if (sub > 0 && t0 + sub >= w.c) break;  // uniform
+        // ---- S
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+          uint32_t a[KW], b[KW];
+          if constexpr (D >= 128) {
+            const int ch = 2 * t4 + (j & 1) + 8 * (j >> 1);
+            lds<KW>(st + Geo::at(sub + g, ch), a);
+            lds<KW>(st + Geo::at(sub + g + 8, ch), b);
+          } else {
+            const int ch = t4 * KW / 4, in = t4 * KW % 4 * 4;
+            lds<KW>(st + Geo::at(sub + g, ch) + in, a);
+            lds<KW>(st + Geo::at(sub + g + 8, ch) + in, b);
+          }
+#pragma unroll
+          for (int k = 0; k < KW; ++k) {
+            const uint32_t a0 = F::half_lo(a[k]), a2 = F::half_hi(a[k]);
+            const uint32_t a1 = F::half_lo(b[k]), a3 = F::half_hi(b[k]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int pt = 0; pt < PARTS; ++pt)
+                mma_f16(s[nt], a0, a1, a2, a3, qf[nt][pt][j * KW + k][0], qf[nt][pt][j * KW + k][1]);
+          }
+        }
+        // ---- softmax: rows of S are tokens g and g + 8
+        uint32_t sc[4];
+        lds<1>(st + 2 * CT * D + 4 * (sub + g), &sc[0]);
+        lds<1>(st + 2 * CT * D + 4 * (sub + g + 8), &sc[1]);
+        lds<1>(st + 2 * CT * D + 4 * (CT + sub + g), &sc[2]);
+        lds<1>(st + 2 * CT * D + 4 * (CT + sub + g + 8), &sc[3]);
+        const float ka = pow2f(scale_exp(sc[0])), kb = pow2f(scale_exp(sc[1]));
+        const int ea = scale_exp(sc[2]), eb = scale_exp(sc[3]);
+        const float va = (float)ea, vb = (float)eb, ia = pow2f(-ea), ib = pow2f(-eb);
+        const bool edge = t0 + sub + 16 > all_see;  // uniform
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], va);
+            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], vb);
+            if (edge) {
+              if (t0 + sub + g >= lim[nt][c]) s[nt][c] = -INFINITY;
+              if (t0 + sub + g + 8 >= lim[nt][c]) s[nt][2 + c] = -INFINITY;
+            }
+            grow |= fmaxf(s[nt][c], s[nt][2 + c]) > m[nt][c] + 14.f;
+          }
+        }
+        if (__any_sync(FULL, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float x = fmaxf(s[nt][c], s[nt][2 + c]);
+              x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
+              if (x > m[nt][c] + 14.f) {
+                const float f = ex2(m[nt][c] - (x - 6.f));
+                m[nt][c] = x - 6.f;
+                l[nt][c] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  o[nt][i][c] *= f;
+                  o[nt][i][2 + c] *= f;
+                }
+              }
+            }
+          }
+        }
+        uint32_t pf[NT][PARTS][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float ref = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+            s[nt][c] = ex2(s[nt][c] - ref);
+            s[nt][2 + c] = ex2(s[nt][2 + c] - ref);
+            l[nt][c] = fmaf(s[nt][c], ia, fmaf(s[nt][2 + c], ib, l[nt][c]));
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t x = pack_half(s[nt][2 * k], s[nt][2 * k + 1]);
+            pf[nt][0][k] = transpose8(x);
+            if constexpr (F32) pf[nt][1][k] = transpose8(pack_rest(s[nt][2 * k], s[nt][2 * k + 1], x));
+          }
+        }
+        // ---- O += V^T P: a lane's dims are VB bytes of tokens 2 t4, + 1, + 8, + 9
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) {
+          uint32_t x[4][(VB + 3) / 4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tok = sub + 2 * t4 + (k & 1) + 8 * (k >> 1);
+            const int byte = j * 128 + g * VB;
+            const uint32_t at = st + CT * D + Geo::at(tok, byte >> 4) + (byte & 15);
+            if constexpr (VB == 2) {
+              uint16_t y;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(y) : "r"(at));
+              x[k][0] = y;
+            } else {
+              lds<VB / 4>(at, x[k]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < (VB + 3) / 4; ++k) {
+            const uint32_t p01 = __byte_perm(x[0][k], x[1][k], 0x5140), p23 = __byte_perm(x[2][k], x[3][k], 0x5140);
+            const uint32_t a0 = F::half_lo(p01), a1 = F::half_hi(p01);
+            const uint32_t a2 = F::half_lo(p23), a3 = F::half_hi(p23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int pt = 0; pt < PARTS; ++pt)
+                mma_f16(o[nt][j * (VB / 2) + 2 * k], a0, a1, a2, a3, pf[nt][pt][0], pf[nt][pt][1]);
+            if constexpr (VB >= 4) {
+              const uint32_t q01 = __byte_perm(x[0][k], x[1][k], 0x7362),
+                             q23 = __byte_perm(x[2][k], x[3][k], 0x7362);
+              const uint32_t b0 = F::half_lo(q01), b1 = F::half_hi(q01);
+              const uint32_t b2 = F::half_lo(q23), b3 = F::half_hi(q23);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int pt = 0; pt < PARTS; ++pt)
+                  mma_f16(o[nt][j * (VB / 2) + 2 * k + 1], b0, b1, b2, b3, pf[nt][pt][0], pf[nt][pt][1]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the segment's end: each of the head's warps puts m, l and O into the stage it
+    // read last (which nothing is on its way into), then each joins some of the rows
+    __syncwarp();
+    if (last >= 0) {
+      float* e = reinterpret_cast<float*>(ring + (size_t)last * Geo::STAGE);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = l[nt][c];
+          x += __shfl_xor_sync(FULL, x, 4);
+          x += __shfl_xor_sync(FULL, x, 8);
+          x += __shfl_xor_sync(FULL, x, 16);
+          const int row = nt * 8 + 2 * t4 + c;
+          if (g == 0) {
+            e[row] = m[nt][c];
+            e[MR + row] = x;
+          }
+          float* orow = e + 2 * MR + row * LD;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int j = i / (VB / 2), d = j * 128 + g * VB + 2 * (i % (VB / 2));
+            *reinterpret_cast<float2*>(orow + d) = make_float2(o[nt][i][c], o[nt][i][2 + c]);
+          }
+        }
+    }
+    const bool many = WPH > 1;
+    if (many) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
+    else __syncwarp();
+    {
+      const bool whole = w.c0 == 0 && (w.g1 - w.g0) * CT >= w.c;
+      float* part = p.parts + (((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * HG + hl) * q8_entry_floats(D);
+      // the stage that warp i of the head read last, if it has a chunk here
+      auto entry = [&](int i) -> const float* {
+        if (w.g1 <= i) return nullptr;
+        const int64_t k = (w.g1 - 1 - i) / WPH;  // its chunks before its last one
+        if (i + k * WPH < w.g0) return nullptr;
+        return reinterpret_cast<const float*>(q8_smem +
+                                              ((size_t)(hl + i * HG) * NS + (size_t)(k % NS)) * Geo::STAGE);
+      };
+      for (int row = wi; row < rows_used; row += WPH) {
+        float M = -INFINITY;
+        for (int i = 0; i < WPH; ++i) {
+          const float* e = entry(i);
+          if (e) M = fmaxf(M, e[row]);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        constexpr int DL = D >= 32 ? D / 32 : 1;  // dims of a lane, 32 apart
+        float L = 0.f, acc[DL];
+#pragma unroll
+        for (int k = 0; k < DL; ++k) acc[k] = 0.f;
+        for (int i = 0; i < WPH; ++i) {
+          const float* e = entry(i);
+          if (!e) continue;
+          const float f = ex2(e[row] - ref);
+          L = fmaf(f, e[MR + row], L);
+#pragma unroll
+          for (int k = 0; k < DL; ++k)
+            if (D >= 32 || lane < D) acc[k] = fmaf(f, e[2 * MR + row * LD + lane + 32 * k], acc[k]);
+        }
+        if (D < 32 && lane >= D) continue;
+        if (whole) {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const int qi = row / p.group, h = row - qi * p.group;
+          T* out = static_cast<T*>(p.out) +
+                   (((int64_t)w.r * p.query_len + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+#pragma unroll
+          for (int k = 0; k < DL; ++k) {
+            const float y = acc[k] * inv;
+            Storage<T>::template store<1>(out + lane + 32 * k, &y);
+          }
+        } else {
+          if (lane == 0) {
+            part[row] = M;
+            part[kQ8Rows + row] = L;
+          }
+#pragma unroll
+          for (int k = 0; k < DL; ++k) part[2 * kQ8Rows + row * D + lane + 32 * k] = acc[k];
+        }
+      }
+    }
+    if (threadIdx.x == 0 && w.g1 == w.total && w.c0 == 0) {
+      // The share ends in this row, which begins here: cut, if chunks of it are left,
+      // and its last block is the one with its last chunk.
+      const int64_t n = (w.c + CT - 1) / CT, end = found[5] + w.g0 + n;
+      if (n > w.g1 - w.g0)
+        p.cuts[blockIdx.x] = make_int4(w.hgi * p.rows + w.r, blockIdx.x,
+                                       (int)((end * found[4] - 1) / found[3]), first ? 0 : 1);
+    }
+    if (many) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
+    else __syncwarp();
+    first = false;
+  }
+  cp_async_wait<0>();
+}
+
+// The join: one warp per (cut row, kv head, (query token, head) row), over the blocks
+// that hold a piece, in block order; eight pieces' loads at a time.
+constexpr int kQ8JoinThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __grid_constant__
+                                                                        DecodeQ8Params p) {
+  __shared__ int4 list[kQ8MaxCtas];
+  __shared__ int cuts;
+  constexpr int WARPS = kQ8JoinThreads / 32, U = 8;
+  constexpr int DL = D >= 32 ? D / 32 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int HG = p.head_group, rows_used = p.group * p.query_len;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    int n = 0;
+    for (int b0 = 0; b0 < p.ctas; b0 += 32) {
+      const int4 c = b0 + lane < p.ctas ? __ldcg(p.cuts + b0 + lane) : make_int4(-1, 0, 0, 0);
+      const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
+      if (c.x >= 0) list[n + __popc(m & ((1u << lane) - 1u))] = c;
+      n += __popc(m);
+    }
+    if (lane == 0) cuts = n;
+  }
+  __syncthreads();
+  const int tasks = cuts * HG * rows_used;
+  for (int task = blockIdx.x + warp * gridDim.x; task < tasks; task += WARPS * gridDim.x) {
+    const int row = task % rows_used, hl = task / rows_used % HG;
+    const int4 c = list[task / rows_used / HG];
+    auto entry = [&](int b) {
+      return p.parts + (((size_t)b * 2 + (b == c.y ? c.w : 0)) * HG + hl) * q8_entry_floats(D);
+    };
+    float M = -INFINITY, L = 0.f, acc[DL];
+#pragma unroll
+    for (int k = 0; k < DL; ++k) acc[k] = 0.f;
+    for (int b0 = c.y; b0 <= c.z; b0 += U) {
+      float m[U], l[U], o[U][DL];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = b0 + u <= c.z;
+        const float* e = entry(in ? b0 + u : c.y);
+        m[u] = in ? __ldcg(e + row) : -INFINITY;
+        l[u] = __ldcg(e + kQ8Rows + row);
+#pragma unroll
+        for (int k = 0; k < DL; ++k)
+          o[u][k] = D >= 32 || lane < D ? __ldcg(e + 2 * kQ8Rows + row * D + lane + 32 * k) : 0.f;
+      }
+      float mx = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) mx = fmaxf(mx, m[u]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      const float f = ex2(M - ref);
+      L *= f;
+#pragma unroll
+      for (int k = 0; k < DL; ++k) acc[k] *= f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float a = ex2(m[u] - ref);
+        L = fmaf(a, l[u], L);
+#pragma unroll
+        for (int k = 0; k < DL; ++k) acc[k] = fmaf(a, o[u][k], acc[k]);
+      }
+      M = mx;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int r = c.x % p.rows, kvh = c.x / p.rows * HG + hl;
+    const int qi = row / p.group, h = row - qi * p.group;
+    T* out = static_cast<T*>(p.out) +
+             (((int64_t)r * p.query_len + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+    if (D < 32 && lane >= D) continue;
+#pragma unroll
+    for (int k = 0; k < DL; ++k) {
+      const float y = acc[k] * inv;
+      Storage<T>::template store<1>(out + lane + 32 * k, &y);
+    }
+  }
+}
+
+template <typename T, int D, int FORM, int NT>
+static np_status launch(const DecodeQ8Params& p, cudaStream_t s) {
+  using Geo = Q8Geo<D, NT>;
+  static unsigned long long allowed = 0;
+  np_status rc = allow_smem(decode_q8_kernel<T, D, FORM, NT>, Geo::SMEM, &allowed);
+  if (rc != NP_OK) return rc;
+  decode_q8_kernel<T, D, FORM, NT><<<p.ctas, 32 * Geo::WARPS, Geo::SMEM, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return NP_ERR_CUDA;
+  return launch_dependent(decode_q8_join_kernel<T, D>, p.ctas, 1, kQ8JoinThreads, 0, s, p);
+}
+
+#define NPK_CAT2(a, b) a##b
+#define NPK_CAT(a, b) NPK_CAT2(a, b)
+
+#if NPK_FORM == 0
+#define NPK_NAME NPK_CAT(NPK_CAT(decode_q8_d, NPK_D), _e4m3)
+#else
+#define NPK_NAME NPK_CAT(NPK_CAT(decode_q8_d, NPK_D), _int8)
+#endif
+
+np_status NPK_NAME(const DecodeQ8Params& p, np_dtype dtype, cudaStream_t s) {
+  if (dtype == NP_F32) return launch<float, NPK_D, NPK_FORM, 1>(p, s);
+  return p.group * p.query_len <= 8 ? launch<__nv_bfloat16, NPK_D, NPK_FORM, 1>(p, s)
+                                    : launch<__nv_bfloat16, NPK_D, NPK_FORM, 2>(p, s);
+}
+
+}  // namespace npk

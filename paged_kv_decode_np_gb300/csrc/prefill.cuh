@@ -40,6 +40,8 @@ struct PrefillParams {
   const void* q;
   const void* k_pool;
   const void* v_pool;
+  const float* k_scale;  // 8-bit pools: [num_blocks, kv_heads]
+  const float* v_scale;
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_starts;
@@ -316,6 +318,8 @@ np_status launch_prefill_plan(const PrefillParams& p, cudaStream_t s);
 np_status launch_prefill_join(const PrefillParams& p, np_dtype dtype, cudaStream_t s);
 // prefill_simt.cu
 np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s);
+// prefill_q8_simt.cu
+np_status launch_prefill_q8_simt(const PrefillParams& p, np_dtype dtype, np_form8 form, cudaStream_t s);
 
 // prefill_tc.cu, per head_dim
 np_status prefill_tc_d16(const PrefillParams& p, bool tiled, cudaStream_t s);

@@ -138,6 +138,19 @@ np_status launch_f32(PrefillParams& p, cudaStream_t s) {
   return NP_ERR_UNSUPPORTED;
 }
 
+// an 8-bit cache
+np_status launch_q8(PrefillParams& p, np_dtype dtype, np_form8 form, cudaStream_t s) {
+  p.tiles = 1;
+  p.tile_rows = 64;
+  p.bn = 64;
+  p.tile_tokens = p.tile_rows / p.group;
+  p.full_cost = p.single_cost = 1;
+  p.unit_cost = 3;
+  p.min_share = 2;
+  const np_status rc = npk::launch_prefill_plan(p, s);
+  return rc == NP_OK ? npk::launch_prefill_q8_simt(p, dtype, form, s) : rc;
+}
+
 }  // namespace
 
 extern "C" size_t np_paged_prefill_workspace_bytes(int32_t head_dim) {
@@ -149,8 +162,9 @@ extern "C" size_t np_paged_prefill_workspace_bytes(int32_t head_dim) {
 
 namespace {
 
-// The checks of a call; *run: whether there is something to launch.
-np_status check_prefill(const np_paged_prefill_args& a, bool* run) {
+// The checks of a call; *run: whether there is something to launch.  pool_es: bytes of
+// a pool's element (0: the dtype's).
+np_status check_prefill(const np_paged_prefill_args& a, bool* run, int pool_es = 0) {
   *run = false;
   const int es = a.dtype == NP_F32 ? 4 : (a.dtype == NP_BF16 ? 2 : 0);
   if (es == 0) return NP_ERR_UNSUPPORTED;
@@ -163,7 +177,7 @@ np_status check_prefill(const np_paged_prefill_args& a, bool* run) {
   if (a.q_heads / a.kv_heads > (a.dtype == NP_BF16 ? 16 : 8)) return NP_ERR_UNSUPPORTED;
   int64_t slots = 0, pool = 0, cap = 0, qn = 0, tab = 0;
   if (!mul_ok(a.num_blocks, a.block_size, &slots) ||
-      !mul_ok(slots, (int64_t)a.kv_heads * d * es, &pool) ||
+      !mul_ok(slots, (int64_t)a.kv_heads * d * (pool_es ? pool_es : es), &pool) ||
       !mul_ok(a.num_tokens, (int64_t)a.q_heads * d * es, &qn) ||
       !mul_ok(a.max_blocks_per_row, a.block_size, &cap) || !mul_ok(a.rows, a.max_blocks_per_row, &tab))
     return NP_ERR_OUT_OF_RANGE;
@@ -194,15 +208,12 @@ extern "C" np_status np_paged_prefill_check(const np_paged_prefill_args* a) {
   return a ? check_prefill(*a, &run) : NP_ERR_INVALID_ARG;
 }
 
-extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
-  if (!a) return NP_ERR_INVALID_ARG;
-  bool run;
-  const np_status st = check_prefill(*a, &run);
-  if (st != NP_OK || !run) return st;
-  const int sms = sm_count();
-  if (sms <= 0) return NP_ERR_CUDA;
+namespace {
 
-  PrefillParams p{};
+// A checked call's parameters, but for the tiling; false: no device.
+bool fill_params(const np_paged_prefill_args* a, PrefillParams& p) {
+  const int sms = sm_count();
+  if (sms <= 0) return false;
   p.out = a->out;
   p.q = a->q;
   p.k_pool = a->k_pool;
@@ -226,6 +237,18 @@ extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
   p.head_dim = a->head_dim;
   p.qscale = fabsf(a->scale) * kLog2e;
   p.negate = a->scale < 0.f;
+  return true;
+}
+
+}  // namespace
+
+extern "C" np_status np_paged_prefill_packed(const np_paged_prefill_args* a) {
+  if (!a) return NP_ERR_INVALID_ARG;
+  bool run;
+  const np_status st = check_prefill(*a, &run);
+  if (st != NP_OK || !run) return st;
+  PrefillParams p{};
+  if (!fill_params(a, p)) return NP_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
   const np_dtype dtype = static_cast<np_dtype>(a->dtype);
   const np_status rc =
@@ -264,4 +287,108 @@ extern "C" np_status np_paged_prefill(void* out, const void* q, const void* k_po
   a.q_heads = q_heads;
   a.scale = scale;
   return np_paged_prefill_packed(&a);
+}
+
+// ---------------------------------------------------------- 8-bit caches --
+namespace {
+
+np_paged_prefill_args plain_args(const np_read_q8_args& a) {
+  np_paged_prefill_args b{};
+  b.out = a.out;
+  b.q = a.q;
+  b.k_pool = a.k_pool;
+  b.v_pool = a.v_pool;
+  b.block_tables = a.block_tables;
+  b.context_lens = a.context_lens;
+  b.query_starts = a.query_starts;
+  b.workspace = a.workspace;
+  b.err_word = a.err_word;
+  b.stream = a.stream;
+  b.num_blocks = a.num_blocks;
+  b.workspace_bytes = a.workspace_bytes;
+  b.dtype = a.dtype;
+  b.block_size = a.block_size;
+  b.kv_heads = a.kv_heads;
+  b.head_dim = a.head_dim;
+  b.max_blocks_per_row = a.max_blocks_per_row;
+  b.rows = a.rows;
+  b.num_tokens = a.num_tokens;
+  b.q_heads = a.q_heads;
+  b.scale = a.scale;
+  return b;
+}
+
+np_status check_prefill_q8(const np_read_q8_args& a, bool* run) {
+  *run = false;
+  if (a.form != NP_E4M3 && a.form != NP_INT8) return NP_ERR_UNSUPPORTED;
+  if (a.query_len != 0) return NP_ERR_INVALID_ARG;
+  const np_status st = check_prefill(plain_args(a), run, 1);
+  if (st != NP_OK || !*run) return st;
+  *run = false;
+  int64_t scales = 0;
+  if (!mul_ok(a.num_blocks, 4ll * a.kv_heads, &scales)) return NP_ERR_OUT_OF_RANGE;
+  if (!a.k_scale || !a.v_scale || !aligned(a.k_scale, 16) || !aligned(a.v_scale, 16)) return NP_ERR_INVALID_ARG;
+  const int64_t out = (int64_t)a.num_tokens * a.q_heads * a.head_dim * (a.dtype == NP_BF16 ? 2 : 4);
+  if (overlap(a.out, out, a.k_scale, scales) || overlap(a.out, out, a.v_scale, scales)) return NP_ERR_INVALID_ARG;
+  *run = true;
+  return NP_OK;
+}
+
+}  // namespace
+
+extern "C" np_status np_paged_prefill_q8_check(const np_read_q8_args* a) {
+  bool run;
+  return a ? check_prefill_q8(*a, &run) : NP_ERR_INVALID_ARG;
+}
+
+extern "C" np_status np_paged_prefill_q8_packed(const np_read_q8_args* a) {
+  if (!a) return NP_ERR_INVALID_ARG;
+  bool run;
+  const np_status st = check_prefill_q8(*a, &run);
+  if (st != NP_OK || !run) return st;
+  const np_paged_prefill_args b = plain_args(*a);
+  PrefillParams p{};
+  if (!fill_params(&b, p)) return NP_ERR_CUDA;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
+  const np_dtype dtype = static_cast<np_dtype>(a->dtype);
+  const np_status rc = launch_q8(p, dtype, static_cast<np_form8>(a->form), s);
+  return rc == NP_OK ? npk::launch_prefill_join(p, dtype, s) : rc;
+}
+
+extern "C" np_status np_paged_prefill_q8(void* out, const void* q, np_dtype dtype, const void* k_pool,
+                                         const void* v_pool, const float* k_scale, const float* v_scale,
+                                         np_form8 form, int64_t num_blocks, int32_t block_size,
+                                         int32_t kv_heads, int32_t head_dim, const int32_t* block_tables,
+                                         int32_t max_blocks_per_row, const int32_t* context_lens,
+                                         const int32_t* query_starts, int32_t rows, int32_t num_tokens,
+                                         int32_t q_heads, float scale, void* workspace,
+                                         size_t workspace_bytes, int32_t* err_word, np_stream_t stream) {
+  np_read_q8_args a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_starts = query_starts;
+  a.workspace = workspace;
+  a.err_word = err_word;
+  a.stream = stream;
+  a.num_blocks = num_blocks;
+  a.workspace_bytes = workspace_bytes > (size_t)INT64_MAX ? INT64_MAX : (int64_t)workspace_bytes;
+  a.form = form;
+  a.dtype = dtype;
+  a.block_size = block_size;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.max_blocks_per_row = max_blocks_per_row;
+  a.rows = rows;
+  a.num_tokens = num_tokens;
+  a.q_heads = q_heads;
+  a.scale = scale;
+  return np_paged_prefill_q8_packed(&a);
 }
