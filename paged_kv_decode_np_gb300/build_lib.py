@@ -59,6 +59,8 @@ def _units(extra: list[str], build_dir: str, csrc: str) -> list[tuple[str, str, 
     for d in HEAD_DIMS:
         units.append((os.path.join(csrc, "prefill_tc.cu"),
                       os.path.join(objdir, f"prefill_tc_d{d}.o"), [f"-DNPK_D={d}"]))
+        units.append((os.path.join(csrc, "prefill_tc.cu"),
+                      os.path.join(objdir, f"prefill_tcq8_d{d}.o"), [f"-DNPK_D={d}", "-DNPK_Q8"]))
         if d <= 128:
             units.append((os.path.join(csrc, "prefill_tc32.cu"),
                           os.path.join(objdir, f"prefill_tc32_d{d}.o"), [f"-DNPK_D={d}"]))

@@ -76,6 +76,79 @@ struct Form8<NP_INT8> {
   }
 };
 
+// Four codes times their block's scale as bf16: exact, for a code has four (e4m3)
+// or at most seven significant bits and the scale is a power of two.
+template <int FORM>
+struct Scaled8;
+
+__device__ __forceinline__ uint32_t bf16_twice(int e) {  // 2^e in both halves, e in [-126, 127]
+  return (uint32_t)(e + 127) * 0x00800080u;
+}
+__device__ __forceinline__ uint32_t bf16_mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <>
+struct Scaled8<NP_E4M3> {
+  // A code's exponent and mantissa as bf16's are the value times 2^-120, subnormals
+  // too.  2^(120 + e) is bf16's up to e = 7; larger scales take two factors.
+  uint32_t f, more;
+  __device__ __forceinline__ explicit Scaled8(int e) : f(bf16_twice(min(120 + e, 127))), more(bf16_twice(max(e - 7, 0))) {}
+  __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+    lo = bf16_mul2(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), f);
+    hi = bf16_mul2(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), f);
+  }
+  // (the same for all of a token's codes: the caller asks once)
+  __device__ __forceinline__ bool large() const { return more != 0x3f803f80u; }
+  __device__ __forceinline__ void widen_large(uint32_t& lo, uint32_t& hi) const {
+    lo = bf16_mul2(lo, more);
+    hi = bf16_mul2(hi, more);
+  }
+};
+
+template <>
+struct Scaled8<NP_INT8> {
+  // Under 0x43 the low seven bits are the bf16 128 + them, and the sign bit alone
+  // 128 or 256: their difference is the code.
+  uint32_t f;
+  __device__ __forceinline__ explicit Scaled8(int e) : f(bf16_twice(e)) {}
+  __device__ __forceinline__ static uint32_t code(uint32_t t) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t & 0xff7fff7fu), "r"(t & 0xff80ff80u));
+    return r;
+  }
+  __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+    lo = bf16_mul2(code(__byte_perm(w, 0x43434343u, 0x4140)), f);
+    hi = bf16_mul2(code(__byte_perm(w, 0x43434343u, 0x4342)), f);
+  }
+  __device__ __forceinline__ bool large() const { return false; }
+  __device__ __forceinline__ void widen_large(uint32_t&, uint32_t&) const {}
+};
+
+// 16 bytes to shared memory, zeros where !live
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+}
+
 // four codes as fp32
 template <int FORM>
 __device__ __forceinline__ void widen8x4(uint32_t w, float* x) {

@@ -92,27 +92,6 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t packe
   return pack_half(lo - f.x, hi - f.y);
 }
 
-// 16 bytes to shared memory, zeros where !live
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0)
-               : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(at));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
-  else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
-}
-
 __device__ __forceinline__ int32_t q8_len(const DecodeQ8Params& p, int r) {
   const int64_t cap = (int64_t)p.max_blocks * p.block_size;
   const int32_t c = p.lens[r];

@@ -81,6 +81,15 @@ bool encode_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[N],
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
+// q's map of the tensor-core kernel, head_dim a multiple of 64
+bool encode_q(PrefillParams& p) {
+  const cuuint64_t d = (cuuint64_t)p.head_dim, head = d * 2;
+  const cuuint64_t q_dims[3] = {d, (cuuint64_t)p.q_heads, (cuuint64_t)p.tokens};
+  const cuuint64_t q_strides[2] = {head, (cuuint64_t)p.q_heads * head};
+  const cuuint32_t q_box[3] = {64u, (cuuint32_t)p.group, (cuuint32_t)p.tile_tokens};
+  return encode_map(&p.tm_q, p.q, q_dims, q_strides, q_box);
+}
+
 // bf16: the tensor-core kernel of this head_dim
 np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   const int d = p.head_dim;
@@ -97,10 +106,7 @@ np_status launch_tc(PrefillParams& p, int64_t slots, cudaStream_t s) {
   if (d >= 64) {
     const cuuint64_t row = (cuuint64_t)p.kv_heads * d * 2, head = (cuuint64_t)d * 2;
     const cuuint32_t slabs = (cuuint32_t)d / 64;
-    const cuuint64_t q_dims[3] = {(cuuint64_t)d, (cuuint64_t)p.q_heads, (cuuint64_t)p.tokens};
-    const cuuint64_t q_strides[2] = {head, (cuuint64_t)p.q_heads * head};
-    const cuuint32_t q_box[3] = {64u, (cuuint32_t)p.group, (cuuint32_t)p.tile_tokens};
-    if (!encode_map(&p.tm_q, p.q, q_dims, q_strides, q_box)) return NP_ERR_CUDA;
+    if (!encode_q(p)) return NP_ERR_CUDA;
     // 64 dims, token of 8, slab, group of 8 tokens, kv head
     const cuuint64_t kv_dims[5] = {64u, 8u, slabs, (cuuint64_t)slots / 8, (cuuint64_t)p.kv_heads};
     const cuuint64_t kv_strides[4] = {row, 128u, 8 * row, head};
@@ -138,17 +144,32 @@ np_status launch_f32(PrefillParams& p, cudaStream_t s) {
   return NP_ERR_UNSUPPORTED;
 }
 
-// an 8-bit cache
+// An 8-bit cache: bf16 on the tensor cores, fp32 on the FMA pipes.
 np_status launch_q8(PrefillParams& p, np_dtype dtype, np_form8 form, cudaStream_t s) {
-  p.tiles = 1;
-  p.tile_rows = 64;
-  p.bn = 64;
-  p.tile_tokens = p.tile_rows / p.group;
-  p.full_cost = p.single_cost = 1;
-  p.unit_cost = 3;
-  p.min_share = 2;
+  if (dtype == NP_F32) {
+    p.tiles = 1;
+    p.tile_rows = 64;
+    p.bn = 64;
+    p.tile_tokens = p.tile_rows / p.group;
+    p.full_cost = p.single_cost = 1;
+    p.unit_cost = 3;
+    p.min_share = 2;
+    const np_status rc = npk::launch_prefill_plan(p, s);
+    return rc == NP_OK ? npk::launch_prefill_q8_simt(p, form, s) : rc;
+  }
+  p.qscale = fmaxf(p.qscale, 1e-30f);  // (as above)
+  npk::prefill_tiling(p, NP_BF16);
+  if (p.head_dim >= 64 && !encode_q(p)) return NP_ERR_CUDA;
   const np_status rc = npk::launch_prefill_plan(p, s);
-  return rc == NP_OK ? npk::launch_prefill_q8_simt(p, dtype, form, s) : rc;
+  if (rc != NP_OK) return rc;
+  switch (p.head_dim) {
+    case 16: return npk::prefill_tcq8_d16(p, form, s);
+    case 32: return npk::prefill_tcq8_d32(p, form, s);
+    case 64: return npk::prefill_tcq8_d64(p, form, s);
+    case 128: return npk::prefill_tcq8_d128(p, form, s);
+    case 256: return npk::prefill_tcq8_d256(p, form, s);
+  }
+  return NP_ERR_UNSUPPORTED;
 }
 
 }  // namespace

@@ -41,6 +41,11 @@
 // token of 8, slab, 8-token group, kv head, in the order the box lands); other
 // shapes take 16-byte asynchronous copies token by token, swizzled by hand.
 //
+// An 8-bit cache (Q8, compiled apart) is widened to the same bf16 tiles on the way,
+// its scales multiplied in, which is exact: six warps take the 8-token groups of the
+// tiles in turn, each group through a ring of the warp's own in shared memory, filled by
+// asynchronous copies of which every lane reads back its own alone.
+//
 // Bound: the chain S -> softmax -> P V of a q tile, ~3200 cycles a kv tile (1500
 // of them the softmax) against 2048 of mma for the pair (head_dim 128).  1024
 // tokens over 131072 positions, 64 / 8 heads: 3.2-3.46 ms by the box, 1270-1370
@@ -51,6 +56,7 @@
 // another copy of the mma sequence cost 5 to 20 % in instruction fetch.
 #include <limits.h>
 
+#include "cache8.cuh"
 #include "prefill.cuh"
 #include "tcgen05.cuh"
 
@@ -60,19 +66,30 @@
 
 namespace npk {
 
-template <int D>
+// How K and V come: bf16 token by token, bf16 by tiled copies, 8 bits (Q8 + form)
+constexpr int kTokens = 0, kTiled = 1, kQ8 = 2;
+
+template <int D, bool Q8 = false>
 struct TcCfg {
   static constexpr int SL = D > 64 ? D / 64 : 1;    // 64-dim slabs
   static constexpr int MT = D == 256 ? 1 : 2;       // q tiles of a unit
   static constexpr int BN = D == 256 ? 64 : 128;    // kv tile
   static constexpr int SLOT = SL * BN * 128;        // bytes of a K or V tile
   static constexpr int QT = SL * 128 * 128;         // bytes of a q tile
-  static constexpr int FIT = (227 * 1024 - 2048 - MT * QT) / SLOT;
+  // Q8: warps that widen, the lanes' 16-byte pieces of an 8-token group, bytes of a group
+  // (and its scales) and how many of them a warp's ring holds
+  static constexpr int CONV = 6;
+  static constexpr int PI = D >= 64 ? D / 64 : 1;
+  static constexpr int GB = PI * 512 + 128;
+  static constexpr int SG = D == 256 ? 2 : D == 128 ? 4 : 8;
+  static constexpr int STG = Q8 ? CONV * SG * GB : 0;
+  static constexpr int FIT = (227 * 1024 - 2048 - MT * QT - STG) / SLOT;
   static constexpr int NS = FIT < 8 ? FIT : 8;      // slots of the K/V ring
   static constexpr int RING = MT * QT;              // offset of the ring
   static constexpr int BARS = RING + NS * SLOT;     // offset of the barriers
-  static constexpr int SMEM = 1024 + BARS + 512;    // + up to 1024 of alignment
-  static constexpr int THREADS = 128 * (MT + 1);    // whole warpgroups: setmaxnreg is theirs
+  static constexpr int RAW = BARS + 512;            // offset of the widening warps' rings
+  static constexpr int SMEM = 1024 + RAW + STG;     // + up to 1024 of alignment
+  static constexpr int THREADS = 128 * (MT + (Q8 ? 2 : 1));  // whole warpgroups: setmaxnreg is theirs
   static constexpr int BM = 128 * MT;
   // tensor memory columns: S at 0 (BN), the two P (BN / 2 each), O
   static constexpr uint32_t P0 = BN, O0 = 256;
@@ -85,9 +102,9 @@ struct TcCfg {
 };
 
 // Barriers, by index from the barrier area's start (8 bytes each).
-template <int D>
+template <int D, bool Q8 = false>
 struct TcBars {
-  static constexpr int NS = TcCfg<D>::NS;
+  static constexpr int NS = TcCfg<D, Q8>::NS;
   static constexpr int q_full = 0, q_empty = 1, kv_full = 2, kv_empty = 2 + NS;
   // s_*, o_full: by q tile; p_full: by P buffer.  Four warps arrive on s_read and
   // p_full, each once a phase: what a warp arrives for next was issued after a
@@ -96,7 +113,8 @@ struct TcBars {
   // A wait that skips phases could take an earlier one of the same parity for its
   // own.  q_*, s_*, p_full, o_full and tail_full: who waits, waits for every phase.
   // The two others are never two phases behind what is waited for:
-  // - kv_empty: a loader skips the others' tiles of a slot (the lag: TcCfg::NS);
+  // - kv_empty: a loader skips the others' tiles of a slot (the lag: TcCfg::NS; Q8:
+  //   each of the six warps has groups of every tile, and waits for every phase);
   // - pv_done, waited for only where O is rescaled: phase j - 1 at tile j, whose
   //   S(j) is complete; S(j) was issued after P V(j - 2), so that phase j - 2 is
   //   complete with it, and P V(j) is not issued before this warp's P(j).
@@ -159,11 +177,12 @@ struct RingPos {
   }
 };
 
-template <int D, bool TILED>
-__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+template <int D, int KV>
+__global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
     prefill_tc_kernel(const __grid_constant__ PrefillParams p) {
-  using C = TcCfg<D>;
-  using B = TcBars<D>;
+  constexpr bool TILED = KV == kTiled, Q8 = KV >= kQ8;
+  using C = TcCfg<D, Q8>;
+  using B = TcBars<D, Q8>;
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int MT = C::MT, BN = C::BN, SL = C::SL, NS = C::NS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -177,11 +196,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   volatile uint32_t* tiles = tail + 2;  // kv tiles of one-tile units so far (tc_wait_beside)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int LOAD = 4 * MT, ISSUER = 4 * MT + 3;  // three warps load, or two (TILED)
+  // three warps load, or two (TILED); Q8: six widen, one loads q
+  constexpr int LOAD = 4 * MT, ISSUER = C::THREADS / 32 - 1;
+  constexpr int CONV = Q8 ? C::CONV : 0, LOADERS = Q8 ? 1 : TILED ? 2 : 3;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i)
-      mbar_init(bar(i), i >= B::s_read && i < B::o_full ? 4 : 1);  // s_read, p_full: four warps
+      mbar_init(bar(i), i >= B::s_read && i < B::o_full ? 4  // s_read, p_full: four warps
+                        : Q8 && i >= B::kv_full && i < B::kv_empty ? BN / 8 : 1);
     *abort = 0;
     *tiles = 0;
     fence_mbar_init();
@@ -198,9 +220,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   PrefillWalk w;
 
   // Registers: a softmax thread holds a row of S (BN values).  With 384 threads
-  // each has 168 at launch; 2 x 208 + 88 = 3 x 168.
+  // each has 168 at launch; 2 x 208 + 88 = 3 x 168.  512 threads (Q8): 128 each, 2 x 192 +
+  // 2 x 64 = 4 x 128.
   if (warp < 4 * MT) {
-    if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (MT == 2 && !Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (MT == 2 && Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     w.start(p, blockIdx.x);
     // ============================================================= softmax
     const int t = warp >> 2;                         // q tile
@@ -373,15 +397,118 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       w.advance();
     }
   } else {
-   if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   if constexpr (MT == 2 && !Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   if constexpr (MT == 2 && Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
    w.start(p, blockIdx.x);
-   if (warp < LOAD + (TILED ? 2 : 3)) {
+   if (warp < LOAD + CONV) {
+    // =============================================================== widen
+    if constexpr (Q8) {
+      constexpr int GPT = BN / 8;       // groups of a tile
+      constexpr int CPT = D / 16;       // 16-byte pieces of a token
+      constexpr int SG = C::SG, PI = C::PI, FORM = KV - kQ8;
+      const int wc = warp - LOAD;
+      const int tok = lane & 7, c0 = lane >> 3;  // token of a group; its pieces c0, c0 + 4, ..
+      const uint32_t raw = base + C::RAW + (uint32_t)(wc * SG) * C::GB;
+      const int64_t row = (int64_t)p.kv_heads * D;
+      uint32_t seq0 = 0;                // ring tiles before this segment
+      while (ok && w.next(p)) {
+        const bool single = tc_single<D>(p, w);
+        const int n = w.kv1 - w.kv0, NG = 2 * n * GPT;
+        // position s of the segment's tiles, in the order the mma takes them (see below)
+        auto tile = [&](int s, bool& isv) {
+          isv = s & 1;
+          if (!single) return s >> 1;
+          isv = s == 2 * n - 1 || (s > 0 && !isv);
+          return s == 0 ? 0 : (s == 2 * n - 1 ? n - 1 : (isv ? s / 2 - 1 : (s + 1) / 2));
+        };
+        // the group to copy next: its tokens' blocks are looked up a group ahead
+        int xl = wc, put = 0;
+        bool on = false, isv = false;
+        int32_t block = 0, inner = 0;
+        auto look_up = [&]() {
+          const int j = tile(xl / GPT, isv);
+          const int t = (w.kv0 + j) * BN + xl % GPT * 8 + tok;
+          on = t < w.g.c;
+          block = inner = 0;
+          if (on) {
+            const int b = (int)((unsigned)t / (unsigned)p.block_size);
+            inner = t - b * p.block_size;
+            block = p.block_tables[(int64_t)w.r * p.max_blocks_per_row + b];
+          }
+        };
+        auto issue = [&]() {
+          if (xl < NG) {
+            if (block < 0 || block >= p.num_blocks) {
+              set_flag(p.err, NP_FLAG_BLOCK_ID);
+              block = 0;
+            }
+            const uint32_t to = raw + (uint32_t)put * C::GB;
+            const char* src = static_cast<const char*>(isv ? p.v_pool : p.k_pool) +
+                              ((int64_t)block * p.block_size + inner) * row + w.kvh * D;
+#pragma unroll
+            for (int i = 0; i < PI; ++i)
+              if (CPT >= 4 || c0 < CPT) copy16(to + i * 512 + lane * 16, src + (c0 + 4 * i) * 16, on);
+            copy4(to + PI * 512 + lane * 4,
+                  (isv ? p.v_scale : p.k_scale) + (int64_t)block * p.kv_heads + w.kvh, on);
+            put = put + 1 == SG ? 0 : put + 1;
+            xl += CONV;
+            if (xl < NG) look_up();
+          }
+          cp_async_commit();
+        };
+        look_up();  // (a segment has two tiles at least, a tile more groups than warps)
+#pragma unroll 1
+        for (int i = 0; i < SG - 1; ++i) issue();
+        int get = 0, was = -1;
+        for (int x = wc; x < NG; x += CONV) {
+          cp_async_wait<SG - 2>();
+          issue();  // to where the group before lay
+          const int s = x / GPT;
+          const uint32_t seq = seq0 + (uint32_t)s, slot = seq % NS;
+          if (s != was) {
+            was = s;
+            if (seq >= NS) {
+              ok = __all_sync(FULL, mbar_wait(bar(B::kv_empty + slot), (seq / NS - 1u) & 1u, abort));
+              if (!ok) break;
+            }
+          }
+          const uint32_t from = raw + (uint32_t)get * C::GB;
+          get = get + 1 == SG ? 0 : get + 1;
+          uint32_t bits;
+          lds<1>(from + PI * 512 + lane * 4, &bits);
+          const Scaled8<FORM> sc(scale_exp(bits));
+          unsigned char* dst = smem + C::RING + slot * C::SLOT;
+#pragma unroll
+          for (int i = 0; i < PI; ++i) {
+            if (CPT < 4 && c0 >= CPT) break;
+            uint32_t q[4], y[8];
+            lds<4>(from + i * 512 + lane * 16, q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc.widen(q[k], y[2 * k], y[2 * k + 1]);
+            if (sc.large()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sc.widen_large(y[2 * k], y[2 * k + 1]);
+            }
+            const int r = x % GPT * 8 + tok, ch = 2 * (c0 + 4 * i);
+            *reinterpret_cast<uint4*>(dst + tc_kv_at<SL>(r, ch)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + tc_kv_at<SL>(r, ch + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B::kv_full + slot));
+        }
+        cp_async_wait<0>();
+        seq0 += 2u * n;
+        w.advance();
+      }
+    }
+   } else if (warp < LOAD + CONV + LOADERS) {
     // =============================================================== loads
     // TILED: one warp copies q and the K tiles, another the V tiles (a copy costs
     // its issuing thread tens of cycles, and a tile is up to 16 of them).  Token
     // by token, 64 copies of the whole warp a tile and some 70 cycles each: three
     // warps take the tiles in turn, the first one q too.
-    const int id = warp - LOAD;
+    const int id = warp - LOAD - CONV;
     const int G = p.group;
     uint32_t seg = 0, seq0 = 0;  // segments; ring tiles before this segment
     int64_t last = -1;  // the last tile's ring position (for the drain)
@@ -548,7 +675,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       // ---- this warp's tiles, at their positions in the order the mma takes
       // them: K0 V0 K1 V1 ... with two q tiles, K0 K1 V0 K2 V1 ... V with one
       const int n = w.kv1 - w.kv0;
-      if constexpr (TILED) {
+      if constexpr (Q8) {
+      } else if constexpr (TILED) {
         const bool isv = id == 1;
         for (int j = 0; j < n && ok; ++j) {
           const int32_t at = ahead;
@@ -572,7 +700,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         }
       }
       seq0 += 2u * n;
-      if constexpr (!TILED) {  // all of it is reported before the next q waits for it
+      if constexpr (!TILED && !Q8) {  // all of it is reported before the next q waits for it
         cp_async_wait<0>();
         if (pending >= 0) report();
         pending = -1;
@@ -714,23 +842,29 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool TILED>
+template <int D, int KV>
 static np_status launch(const PrefillParams& p, cudaStream_t s) {
   static unsigned long long allowed = 0;
-  const np_status rc = allow_smem(prefill_tc_kernel<D, TILED>, TcCfg<D>::SMEM, &allowed);
+  using C = TcCfg<D, (KV >= kQ8)>;
+  const np_status rc = allow_smem(prefill_tc_kernel<D, KV>, C::SMEM, &allowed);
   if (rc != NP_OK) return rc;
-  return launch_dependent(prefill_tc_kernel<D, TILED>, p.ctas, 1, TcCfg<D>::THREADS, TcCfg<D>::SMEM, s,
-                          p);
+  return launch_dependent(prefill_tc_kernel<D, KV>, p.ctas, 1, C::THREADS, C::SMEM, s, p);
 }
 
 #define NPK_CAT2(a, b) a##b
 #define NPK_CAT(a, b) NPK_CAT2(a, b)
 
+#ifdef NPK_Q8
+np_status NPK_CAT(prefill_tcq8_d, NPK_D)(const PrefillParams& p, np_form8 form, cudaStream_t s) {
+  return form == NP_E4M3 ? launch<NPK_D, kQ8 + NP_E4M3>(p, s) : launch<NPK_D, kQ8 + NP_INT8>(p, s);
+}
+#else
 np_status NPK_CAT(prefill_tc_d, NPK_D)(const PrefillParams& p, bool tiled, cudaStream_t s) {
 #if NPK_D >= 64
-  if (tiled) return launch<NPK_D, true>(p, s);
+  if (tiled) return launch<NPK_D, kTiled>(p, s);
 #endif
-  return launch<NPK_D, false>(p, s);
+  return launch<NPK_D, kTokens>(p, s);
 }
+#endif
 
 }  // namespace npk

@@ -105,6 +105,26 @@ def test_scales_of_blocks_of_any_size(nplib, dtype):
     assert torch.equal(_run(nplib, inp, 0.1), _run(nplib, same, 0.1))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("form", [E4M3, INT8], ids=["e4m3", "int8"])
+@pytest.mark.parametrize("e", [-60, -5, 0, 7, 8, 60])
+def test_every_code_under_small_and_large_scales(nplib, form, dtype, e):
+    """One position a row, so that its V comes out as it is: exactly."""
+    codes = torch.arange(256, dtype=torch.int16).to(torch.uint8)
+    skip = codes == 0x80 if form is INT8 else (codes & 0x7f) == 0x7f
+    codes = torch.where(skip, torch.zeros_like(codes), codes)
+    d = 64
+    v = codes.view(4, 1, 1, d).view(form).cuda()
+    q = torch.ones(4, 1, d, dtype=dtype, device="cuda")
+    scale = torch.full((4, 1), 2.0 ** e, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    inp = dict(q=q, k_pool=v, v_pool=v, k_scale=torch.ones_like(scale), v_scale=scale,
+               block_tables=torch.arange(4, **i32)[:, None].contiguous(), context_lens=torch.ones(4, **i32),
+               query_starts=torch.arange(5, **i32))
+    out = _run(nplib, inp, 0.01)
+    assert torch.equal(out.double().flatten(), v.float().double().flatten() * 2.0 ** e)
+
+
 def test_many_rows(nplib):
     gen = torch.Generator().manual_seed(2)
     rows = [(1 + int(x) % 3, 3 + int(x)) for x in torch.randint(0, 60, (600,), generator=gen)]
