@@ -128,6 +128,50 @@ struct Scaled8<NP_INT8> {
   __device__ __forceinline__ void widen_large(uint32_t&, uint32_t&) const {}
 };
 
+// Four codes as fp16, times 2^-d (d >= 0): exact where the result is no finer than fp16's
+// 2^-24.
+template <int FORM>
+struct Below8;
+
+__device__ __forceinline__ uint32_t half_twice_below(uint32_t d) {  // 2^-d in both halves; 0 past 24
+  return d <= 14u ? 0x3c003c00u - d * 0x04000400u : d <= 24u ? 0x04000400u >> (d - 14u) : 0u;
+}
+
+template <>
+struct Below8<NP_E4M3> {
+  __half2 f;
+  __device__ __forceinline__ explicit Below8(uint32_t d) {
+    const uint32_t w = half_twice_below(d);
+    f = *reinterpret_cast<const __half2*>(&w);
+  }
+  __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+    const uint32_t a = Form8<NP_E4M3>::half_lo(w), b = Form8<NP_E4M3>::half_hi(w);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
+
+template <>
+struct Below8<NP_INT8> {
+  // (1152 + code) 2^-d - 1152 2^-d
+  __half2 f, off;
+  __device__ __forceinline__ explicit Below8(uint32_t d) {
+    const uint32_t w = half_twice_below(d), c = 0xe480e480u;  // -1152
+    f = *reinterpret_cast<const __half2*>(&w);
+    off = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
+  }
+  __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+    const uint32_t t = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(t, 0x64646464u, 0x4140), b = __byte_perm(t, 0x64646464u, 0x4342);
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&a), f, off);
+    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b), f, off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
+
 // 16 bytes to shared memory, zeros where !live
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
@@ -147,6 +191,11 @@ __device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
   else if constexpr (N == 2)
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
   else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+}
+
+__device__ __forceinline__ void sts4(uint32_t at, const uint32_t* w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
 }
 
 // four codes as fp32

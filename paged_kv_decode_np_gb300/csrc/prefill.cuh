@@ -329,11 +329,11 @@ np_status prefill_tc_d128(const PrefillParams& p, bool tiled, cudaStream_t s);
 np_status prefill_tc_d256(const PrefillParams& p, bool tiled, cudaStream_t s);
 
 // the same for an 8-bit cache
-np_status prefill_tcq8_d16(const PrefillParams& p, np_form8 form, cudaStream_t s);
-np_status prefill_tcq8_d32(const PrefillParams& p, np_form8 form, cudaStream_t s);
-np_status prefill_tcq8_d64(const PrefillParams& p, np_form8 form, cudaStream_t s);
-np_status prefill_tcq8_d128(const PrefillParams& p, np_form8 form, cudaStream_t s);
-np_status prefill_tcq8_d256(const PrefillParams& p, np_form8 form, cudaStream_t s);
+np_status prefill_tcq8_d16(const PrefillParams& p, np_form8 form, bool tiled, cudaStream_t s);
+np_status prefill_tcq8_d32(const PrefillParams& p, np_form8 form, bool tiled, cudaStream_t s);
+np_status prefill_tcq8_d64(const PrefillParams& p, np_form8 form, bool tiled, cudaStream_t s);
+np_status prefill_tcq8_d128(const PrefillParams& p, np_form8 form, bool tiled, cudaStream_t s);
+np_status prefill_tcq8_d256(const PrefillParams& p, np_form8 form, bool tiled, cudaStream_t s);
 
 // prefill_tc32.cu, per head_dim
 np_status prefill_tc32_d16(const PrefillParams& p, cudaStream_t s);

@@ -60,18 +60,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   return fn;
 }
 
-// A bf16 tensor of N dims (innermost first, byte strides of dims 1 ..), copied
-// in the given box in the 128-byte swizzle.
+// A tensor of N dims (innermost first, byte strides of dims 1 ..) of bf16 or of another
+// type, copied in the given box in the 128-byte swizzle or another.
 template <int N>
 bool encode_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[N],
-                const cuuint64_t (&strides)[N - 1], const cuuint32_t (&box)[N]) {
+                const cuuint64_t (&strides)[N - 1], const cuuint32_t (&box)[N],
+                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
   if (!enc) return false;
   cuuint32_t estr[N];
   for (int i = 0; i < N; ++i) estr[i] = 1u;
   auto encode = [&] {
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void*>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return enc(m, type, N, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (encode()) return true;
@@ -159,15 +161,34 @@ np_status launch_q8(PrefillParams& p, np_dtype dtype, np_form8 form, cudaStream_
   }
   p.qscale = fmaxf(p.qscale, 1e-30f);  // (as above)
   npk::prefill_tiling(p, NP_BF16);
-  if (p.head_dim >= 64 && !encode_q(p)) return NP_ERR_CUDA;
+  const int d = p.head_dim;
+  bool tiled = false;
+  if (d >= 64) {
+    if (!encode_q(p)) return NP_ERR_CUDA;
+    // Tiled copies: boxes of whole 8-token groups inside one block, slots in int32.
+    int bt = 1;
+    while (bt < p.bn && p.block_size % (2 * bt) == 0) bt *= 2;
+    p.box_tokens = bt;
+    const int64_t slots = p.num_blocks * p.block_size;
+    if (bt >= 8 && slots <= INT32_MAX) {
+      // up to 128 bytes of a token, slot, 128-byte slab, kv head
+      const cuuint64_t wide = d < 128 ? d : 128, slabs = d / wide;
+      const cuuint64_t dims[4] = {wide, (cuuint64_t)slots, slabs, (cuuint64_t)p.kv_heads};
+      const cuuint64_t strides[3] = {(cuuint64_t)p.kv_heads * d, 128u, (cuuint64_t)d};
+      const cuuint32_t box[4] = {(cuuint32_t)wide, (cuuint32_t)bt, (cuuint32_t)slabs, 1u};
+      const CUtensorMapSwizzle swizzle = d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+      tiled = encode_map(&p.tm_k, p.k_pool, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, swizzle) &&
+              encode_map(&p.tm_v, p.v_pool, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, swizzle);
+    }
+  }
   const np_status rc = npk::launch_prefill_plan(p, s);
   if (rc != NP_OK) return rc;
-  switch (p.head_dim) {
-    case 16: return npk::prefill_tcq8_d16(p, form, s);
-    case 32: return npk::prefill_tcq8_d32(p, form, s);
-    case 64: return npk::prefill_tcq8_d64(p, form, s);
-    case 128: return npk::prefill_tcq8_d128(p, form, s);
-    case 256: return npk::prefill_tcq8_d256(p, form, s);
+  switch (d) {
+    case 16: return npk::prefill_tcq8_d16(p, form, tiled, s);
+    case 32: return npk::prefill_tcq8_d32(p, form, tiled, s);
+    case 64: return npk::prefill_tcq8_d64(p, form, tiled, s);
+    case 128: return npk::prefill_tcq8_d128(p, form, tiled, s);
+    case 256: return npk::prefill_tcq8_d256(p, form, tiled, s);
   }
   return NP_ERR_UNSUPPORTED;
 }

@@ -41,10 +41,20 @@
 // token of 8, slab, 8-token group, kv head, in the order the box lands); other
 // shapes take 16-byte asynchronous copies token by token, swizzled by hand.
 //
-// An 8-bit cache (Q8, compiled apart) is widened to the same bf16 tiles on the way,
-// its scales multiplied in, which is exact: six warps take the 8-token groups of the
-// tiles in turn, each group through a ring of the warp's own in shared memory, filled by
-// asynchronous copies of which every lane reads back its own alone.
+// An 8-bit cache (Q8, compiled apart) comes in one of two ways.
+// Tiled copies (Q8T): a tile's bytes land in rings of their own, one for K and one for V,
+// from which four warps widen a quarter of each tile to fp16, which holds every code:
+// two or three instructions for four codes, where bf16 takes ten.  A tile's largest
+// exponents (of its blocks' scales; one for K, one for V) stay apart from its values: K's
+// is a factor of the tile's scores, V's is added to the exponents of its weights and
+// taken back in l, as 2^(x + b) v and 2^x are a weight's two shares.  Blocks of smaller
+// scales are multiplied by what they are below the largest: exact down to 2^-15 (e4m3;
+// int8 2^-24) and beyond that to 2^-33 of the tile's largest value.  q is fp16 as well,
+// each row times a power of two that brings its largest element to 2^14 .. 2^15; the same
+// four warps turn it in place.
+// Token by token, six warps widen to bf16 with the scales multiplied in, exactly: they
+// take the 8-token groups of the tiles in turn, each group through a ring of the warp's
+// own, filled by asynchronous copies of which every lane reads back its own alone.
 //
 // Bound: the chain S -> softmax -> P V of a q tile, ~3200 cycles a kv tile (1500
 // of them the softmax) against 2048 of mma for the pair (head_dim 128).  1024
@@ -66,29 +76,39 @@
 
 namespace npk {
 
-// How K and V come: bf16 token by token, bf16 by tiled copies, 8 bits (Q8 + form)
-constexpr int kTokens = 0, kTiled = 1, kQ8 = 2;
+// How K and V come: bf16 token by token, bf16 by tiled copies; 8 bits (+ form) the same two ways
+enum : int { kTokens = 0, kTiled = 1, kQ8 = 2, kQ8Tiled = 4 };
+// 0: bf16, 1: 8 bits token by token, 2: 8 bits by tiled copies
+__host__ __device__ constexpr int tc_kind(int kv) { return kv >= kQ8Tiled ? 2 : kv >= kQ8 ? 1 : 0; }
 
-template <int D, bool Q8 = false>
+template <int D, int KIND = 0>
 struct TcCfg {
+  static constexpr bool Q8 = KIND > 0;
   static constexpr int SL = D > 64 ? D / 64 : 1;    // 64-dim slabs
   static constexpr int MT = D == 256 ? 1 : 2;       // q tiles of a unit
   static constexpr int BN = D == 256 ? 64 : 128;    // kv tile
   static constexpr int SLOT = SL * BN * 128;        // bytes of a K or V tile
   static constexpr int QT = SL * 128 * 128;         // bytes of a q tile
-  // Q8: warps that widen, the lanes' 16-byte pieces of an 8-token group, bytes of a group
-  // (and its scales) and how many of them a warp's ring holds
-  static constexpr int CONV = 6;
+  // Q8: warps that widen, the lanes' 16-byte pieces of an 8-token group; token by token:
+  // bytes of a group (and its scales) and how many of them a warp's ring holds; tiled:
+  // bytes of a raw tile (and its scales), tiles of the raw ring
+  static constexpr int CONV = KIND == 2 ? 4 : 6;
   static constexpr int PI = D >= 64 ? D / 64 : 1;
   static constexpr int GB = PI * 512 + 128;
   static constexpr int SG = D == 256 ? 2 : D == 128 ? 4 : 8;
-  static constexpr int STG = Q8 ? CONV * SG * GB : 0;
+  static constexpr int RT = BN * D, RS = 2;  // (of K, and as many of V)
+  static constexpr int STG = KIND == 2 ? 2 * RS * RT : KIND == 1 ? CONV * SG * GB : 0;
   static constexpr int FIT = (227 * 1024 - 2048 - MT * QT - STG) / SLOT;
   static constexpr int NS = FIT < 8 ? FIT : 8;      // slots of the K/V ring
   static constexpr int RING = MT * QT;              // offset of the ring
-  static constexpr int BARS = RING + NS * SLOT;     // offset of the barriers
+  static constexpr int RAW_T = RING + NS * SLOT;    // offset of the raw rings
+  static constexpr int BARS = RAW_T + (KIND == 2 ? STG : 0);  // offset of the barriers
   static constexpr int RAW = BARS + 512;            // offset of the widening warps' rings
-  static constexpr int SMEM = 1024 + RAW + STG;     // + up to 1024 of alignment
+  // Q8T: raw rings (1024-byte aligned: swizzled copies), then barriers, a ring of the
+  // tiles' exponents (TE bytes a tile), the exponents of q's rows by segment parity
+  static constexpr int TE = 48, TILES = 16;
+  static constexpr int EXPS = BARS + 512, QEXP = EXPS + TILES * TE;
+  static constexpr int SMEM = 1024 + (KIND == 2 ? QEXP + 2 * 128 * MT : RAW + STG);  // + up to 1024 of alignment
   static constexpr int THREADS = 128 * (MT + (Q8 ? 2 : 1));  // whole warpgroups: setmaxnreg is theirs
   static constexpr int BM = 128 * MT;
   // tensor memory columns: S at 0 (BN), the two P (BN / 2 each), O
@@ -96,15 +116,17 @@ struct TcCfg {
   // A loader waits for the slot's last use only, and skips the other loaders'
   // phases: its tile before, at most 3 positions back, waited for a slot that was
   // freed after the use before that.
-  static_assert(NS >= 4, "ring");
+  // (Q8: all widening warps take part in every tile.)
+  static_assert(NS >= (KIND == 2 ? 3 : 4), "ring");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
   // One block an SM: a second would wait for the first's tensor memory.
   static_assert(2 * (SMEM + 1024) > 228 * 1024, "one block an SM");
 };
 
 // Barriers, by index from the barrier area's start (8 bytes each).
-template <int D, bool Q8 = false>
+template <int D, int KIND = 0>
 struct TcBars {
-  static constexpr int NS = TcCfg<D, Q8>::NS;
+  static constexpr int NS = TcCfg<D, KIND>::NS;
   static constexpr int q_full = 0, q_empty = 1, kv_full = 2, kv_empty = 2 + NS;
   // s_*, o_full: by q tile; p_full: by P buffer.  Four warps arrive on s_read and
   // p_full, each once a phase: what a warp arrives for next was issued after a
@@ -121,7 +143,10 @@ struct TcBars {
   static constexpr int s_full = 2 + 2 * NS, s_read = s_full + 2, p_full = s_read + 2;
   static constexpr int o_full = p_full + 2;
   static constexpr int pv_done = o_full + 2;  // one-tile units: one phase a kv tile
-  static constexpr int drain = pv_done + 1, tail_full = drain + 1, count = tail_full + 1;
+  static constexpr int drain = pv_done + 1, tail_full = drain + 1;
+  // Q8T: raw tiles, K's ring and V's; q as it came.  Who waits, waits for every phase.
+  static constexpr int raw_full = tail_full + 1, raw_empty = raw_full + 4, q_raw = raw_empty + 4;
+  static constexpr int count = KIND == 2 ? q_raw + 1 : raw_full;
 };
 
 // kv tiles of the current segment that q tile t sees, from kv0 on
@@ -132,6 +157,15 @@ __device__ __forceinline__ int tc_tiles(const PrefillParams& p, const PrefillWal
   const int nk = prefill_kv_tiles(p, w.g, first + p.tile_tokens);
   const int end = nk < w.kv1 ? nk : w.kv1;
   return end > w.kv0 ? end - w.kv0 : 0;
+}
+
+// The kv tile at position s of a segment's 2 n tiles, in the order the mma takes them:
+// K0 V0 K1 V1 ... with two q tiles, K0 K1 V0 K2 V1 ... V with one.
+__device__ __forceinline__ int tc_tile_at(int s, int n, bool single, bool& isv) {
+  isv = s & 1;
+  if (!single) return s >> 1;
+  isv = s == 2 * n - 1 || (s > 0 && !isv);
+  return s == 0 ? 0 : (s == 2 * n - 1 ? n - 1 : (isv ? s / 2 - 1 : (s + 1) / 2));
 }
 
 // The current segment's unit has one q tile with tokens.
@@ -178,11 +212,11 @@ struct RingPos {
 };
 
 template <int D, int KV>
-__global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
+__global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
     prefill_tc_kernel(const __grid_constant__ PrefillParams p) {
-  constexpr bool TILED = KV == kTiled, Q8 = KV >= kQ8;
-  using C = TcCfg<D, Q8>;
-  using B = TcBars<D, Q8>;
+  constexpr bool TILED = KV == kTiled, Q8 = KV >= kQ8, Q8T = KV >= kQ8Tiled;
+  using C = TcCfg<D, tc_kind(KV)>;
+  using B = TcBars<D, tc_kind(KV)>;
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int MT = C::MT, BN = C::BN, SL = C::SL, NS = C::NS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -196,14 +230,17 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
   volatile uint32_t* tiles = tail + 2;  // kv tiles of one-tile units so far (tc_wait_beside)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // three warps load, or two (TILED); Q8: six widen, one loads q
+  // three warps load, or two (TILED); Q8: six widen, one loads q; Q8T: four widen, one
+  // loads K, one V, one q
   constexpr int LOAD = 4 * MT, ISSUER = C::THREADS / 32 - 1;
-  constexpr int CONV = Q8 ? C::CONV : 0, LOADERS = Q8 ? 1 : TILED ? 2 : 3;
+  constexpr int CONV = Q8 ? C::CONV : 0, RAWER = LOAD + CONV, LOADERS = Q8 ? 1 : TILED ? 2 : 3;
+  constexpr int Q0 = RAWER + (Q8T ? 2 : 0);  // the first loader
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B::count; ++i)
       mbar_init(bar(i), i >= B::s_read && i < B::o_full ? 4  // s_read, p_full: four warps
-                        : Q8 && i >= B::kv_full && i < B::kv_empty ? BN / 8 : 1);
+                        : Q8 && i >= B::kv_full && i < B::kv_empty ? (Q8T ? CONV : BN / 8)
+                        : Q8T && ((i >= B::raw_empty && i < B::q_raw) || i == B::q_full) ? CONV : 1);
     *abort = 0;
     *tiles = 0;
     fence_mbar_init();
@@ -234,9 +271,13 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
     const int tt = row / p.group, h = row - tt * p.group;
     constexpr int OC = D < 32 ? 16 : 32;             // columns of O at a time
     uint32_t used = 0;            // S tiles so far
+    uint32_t seen = 0, segs = 0;  // Q8T: kv tiles and segments so far, whosever they were
     uint32_t pv = 0, oc = 0;      // phases of pv_done; of this tile's o_full
     while (ok && w.next(p)) {
       const int64_t first = ((int64_t)w.m * MT + t) * p.tile_tokens;
+      const uint32_t tile0 = seen;
+      seen += (uint32_t)(w.kv1 - w.kv0);
+      ++segs;
       if (first >= w.g.n) {  // no tokens in this tile
         w.advance();
         continue;
@@ -249,6 +290,9 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
       // the last position the row sees; rows that are not stored need no mask
       const int lim = live ? (int)((int64_t)w.g.c - w.g.n + tok) : INT_MAX;
       float m = -INFINITY, l = 0.f;
+      // Q8T: x = c S + b, weights 2^(x - m) with m 6 below the largest x (fp16's range)
+      constexpr float ABOVE = Q8T ? 14.f : 8.f, BELOW = Q8T ? 6.f : 0.f;
+      float row_scale = p.qscale;
       for (int j = 0; j < n; ++j) {
         const int pb = single ? (j & 1) : t;  // P buffer
         // (tile 1's warps pass over the units of one tile before, a share's worth of them)
@@ -272,26 +316,40 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
         tmem_wait_ld();
         tmem_pin<BN>(r);
         tmem_fence_before();
+        // (before S is given back: the next segment's exponents may come after that)
+        if (Q8T && j == 0)
+          row_scale *= pow2f(-(int)*reinterpret_cast<volatile signed char*>(
+              smem + C::QEXP + (segs & 1u) * (128 * MT) + t * 128 + row));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::s_read + t));
+        float c = row_scale, b = 0.f, back = 1.f;
+        if constexpr (Q8T) {
+          const short te = *reinterpret_cast<volatile short*>(
+              smem + C::EXPS + (tile0 + (uint32_t)j) % C::TILES * C::TE + 2 * (BN / 8));
+          const int ke = (signed char)(te & 0xff), ve = te >> 8;
+          c = fmaxf(c * pow2f(ke), 1.2e-38f);  // (a masked score is -inf before it is scaled)
+          b = (float)ve;
+          back = pow2f(-ve);
+        }
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c > rel) r[c] = 0xff800000u;  // -inf
+          for (int e = 0; e < BN; ++e)
+            if (e > rel) r[e] = 0xff800000u;  // -inf
         }
         float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < BN; c += 8) {
-          x0 = fmaxf(fmaxf(x0, __uint_as_float(r[c])), __uint_as_float(r[c + 1]));
-          x1 = fmaxf(fmaxf(x1, __uint_as_float(r[c + 2])), __uint_as_float(r[c + 3]));
-          x2 = fmaxf(fmaxf(x2, __uint_as_float(r[c + 4])), __uint_as_float(r[c + 5]));
-          x3 = fmaxf(fmaxf(x3, __uint_as_float(r[c + 6])), __uint_as_float(r[c + 7]));
+        for (int e = 0; e < BN; e += 8) {
+          x0 = fmaxf(fmaxf(x0, __uint_as_float(r[e])), __uint_as_float(r[e + 1]));
+          x1 = fmaxf(fmaxf(x1, __uint_as_float(r[e + 2])), __uint_as_float(r[e + 3]));
+          x2 = fmaxf(fmaxf(x2, __uint_as_float(r[e + 4])), __uint_as_float(r[e + 5]));
+          x3 = fmaxf(fmaxf(x3, __uint_as_float(r[e + 6])), __uint_as_float(r[e + 7]));
         }
-        const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.qscale;
-        const bool grow = mt > m + 8.f;  // also the first visible tile: m = -inf
+        const float most = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+        const float mt = Q8T ? fmaf(most, c, b) : most * c;
+        const bool grow = mt > m + ABOVE;  // also the first visible tile: m = -inf
         if (__any_sync(FULL, grow)) {
-          const float f = grow ? ex2(m - mt) : 1.f;
-          if (grow) m = mt;
+          const float f = grow ? ex2(m - (mt - BELOW)) : 1.f;
+          if (grow) m = mt - BELOW;
           l *= f;
           if (j > 0) {
             // PV(j - 1) must be complete.  With two q tiles it is: S(j) was
@@ -302,36 +360,41 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
               tmem_fence_after();
             }
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int d = 0; d < D; d += 16) {
               uint32_t o[16];
-              tmem_ld16(o_at + c, o);
+              tmem_ld16(o_at + d, o);
               tmem_wait_ld();
               tmem_pin<16>(o);
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(o_at + c, o);
+              tmem_st16(o_at + d, o);
             }
             tmem_wait_st();
           }
         }
-        const float ref = m == -INFINITY ? 0.f : -m;
+        const float ref = m == -INFINITY ? 0.f : b - m;
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) {
+        for (int k = 0; k < BN; k += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float a = __uint_as_float(r[c + e]), b = __uint_as_float(r[c + e + 1]);
-            fma2(a, b, p.qscale, ref);
-            a = ex2(a);
-            b = ex2(b);
-            add2(l0, l1, a, b);
-            const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
-            pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+            float u = __uint_as_float(r[k + e]), v = __uint_as_float(r[k + e + 1]);
+            fma2(u, v, c, ref);
+            u = ex2(u);
+            v = ex2(v);
+            add2(l0, l1, u, v);
+            if constexpr (Q8T) {
+              const __half2 hh = __floats2half2_rn(u, v);
+              pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+            } else {
+              const __nv_bfloat162 hh = __floats2bfloat162_rn(u, v);
+              pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
           }
-          tmem_st16(p_at + (c >> 1), pk);
+          tmem_st16(p_at + (k >> 1), pk);
         }
-        l += l0 + l1;
+        l = Q8T ? fmaf(l0 + l1, back, l) : l + (l0 + l1);
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
@@ -402,7 +465,114 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
    w.start(p, blockIdx.x);
    if (warp < LOAD + CONV) {
     // =============================================================== widen
-    if constexpr (Q8) {
+    if constexpr (Q8T) {
+      // q of each segment, then tile by tile, a quarter of the rows and tokens each.
+      // Bytes past the context are whatever they are.  K's only make scores that are
+      // masked; V's meet weights of 0, which e4m3's NaN would not stand: zeros instead.
+      constexpr int GW = BN / 8 / CONV;  // 8-token groups of a warp
+      constexpr int RS = C::RS, PI = C::PI, FORM = KV - kQ8Tiled;
+      const int wc = warp - LOAD, tok = lane & 7, c0 = lane >> 3;
+      uint32_t seq = 0, tile = 0, segs = 0;  // positions in the ring; kv tiles; segments
+      while (ok && w.next(p)) {
+        const bool single = tc_single<D>(p, w);
+        const int n = w.kv1 - w.kv0;
+        ok = __all_sync(FULL, mbar_wait(bar(B::q_raw), segs & 1u, abort));
+        if (!ok) break;
+        ++segs;
+        for (int t = 0; t < (single ? 1 : 2); ++t) {
+          // a lane's row; rows that hold no (token, head) are left as they are
+          const int row = wc * 32 + lane;
+          const int64_t first = ((int64_t)w.m * MT + t) * p.tile_tokens;
+          const int live = (int)min((int64_t)p.tile_tokens, w.g.n - first) * p.group;
+          if (wc * 32 >= live) continue;
+          const uint32_t at = base + (uint32_t)t * C::QT + (uint32_t)row * 128u;
+          auto piece = [&](int i) { return at + (uint32_t)((i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)); };
+          uint32_t big = 0;
+#pragma unroll 2
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t x[4];
+            lds<4>(piece(i), x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) big = __vmaxu2(big, x[e] & 0x7fff7fffu);
+          }
+          big = max(big & 0xffffu, big >> 16);
+          const int e = min(14 + 127 - (int)(big >> 7), 120);
+          const float f = pow2f(e);
+#pragma unroll 1
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t x[4];
+            lds<4>(piece(i), x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float lo, hi;
+              widen_bf16x2(x[k], lo, hi);
+              const __half2 h = __floats2half2_rn(lo * f, hi * f);
+              x[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            sts4(piece(i), x);
+          }
+          smem[C::QEXP + (segs & 1u) * (128 * MT) + t * 128 + row] = (unsigned char)(signed char)e;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B::q_full));
+#pragma unroll 1
+        for (int s = 0; s < 2 * n; ++s, ++seq) {
+          bool isv;
+          const int j = tc_tile_at(s, n, single, isv);
+          const uint32_t slot = seq % NS, te = (tile + (uint32_t)j) % C::TILES;
+          const uint32_t own = tile + (uint32_t)j, rs = own % RS + (isv ? RS : 0);
+          ok = mbar_wait(bar(B::raw_full + rs), (own / RS) & 1u, abort);
+          if (ok && seq >= NS) ok = mbar_wait(bar(B::kv_empty + slot), (seq / NS - 1u) & 1u, abort);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          const uint32_t from = base + C::RAW_T + rs * (uint32_t)C::RT;
+          const uint32_t below = base + C::EXPS + te * C::TE + (isv ? BN / 8 : 0);
+          const uint32_t to = ring + slot * C::SLOT;
+          // (rolled: four roles share the instruction caches)
+          auto piece = [&](int i, uint32_t* q, uint32_t& d) {  // piece i of the warp's GW x PI
+            const int g = wc * GW + i / PI, r = g * 8 + tok, ch = c0 + 4 * (i % PI);
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(d) : "r"(below + g));
+            // the boxes' layout: box_tokens tokens, in slabs of 128 bytes, swizzled
+            uint32_t at;
+            if constexpr (D == 64) at = (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+            else if constexpr (D == 128) at = (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
+            else {
+              const int b = r & ~(p.box_tokens - 1), in = r - b;
+              at = (uint32_t)(b * 256 + ((ch >> 3) * p.box_tokens + in) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+            }
+            lds<4>(from + at, q);
+          };
+          uint32_t q[4], d;
+          piece(0, q, d);
+          const int valid = FORM == NP_E4M3 && isv ? w.g.c - (w.kv0 + j) * BN : BN;
+#pragma unroll 1
+          for (int i = 0; i < GW * PI; ++i) {
+            uint32_t q1[4], d1;
+            piece(min(i + 1, GW * PI - 1), q1, d1);  // on its way meanwhile
+            const Below8<FORM> f(d);
+            uint32_t y[8];
+            const int r = (wc * GW + i / PI) * 8 + tok, ch = 2 * (c0 + 4 * (i % PI));
+            if (FORM == NP_E4M3 && r >= valid) q[0] = q[1] = q[2] = q[3] = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f.widen(q[e], y[2 * e], y[2 * e + 1]);
+            sts4(to + tc_kv_at<SL>(r, ch), y);
+            sts4(to + tc_kv_at<SL>(r, ch + 1), y + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = q1[e];
+            d = d1;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(B::raw_empty + rs));
+            mbar_arrive(bar(B::kv_full + slot));
+          }
+        }
+        tile += (uint32_t)n;
+        w.advance();
+      }
+    } else if constexpr (Q8) {
       constexpr int GPT = BN / 8;       // groups of a tile
       constexpr int CPT = D / 16;       // 16-byte pieces of a token
       constexpr int SG = C::SG, PI = C::PI, FORM = KV - kQ8;
@@ -414,19 +584,12 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
       while (ok && w.next(p)) {
         const bool single = tc_single<D>(p, w);
         const int n = w.kv1 - w.kv0, NG = 2 * n * GPT;
-        // position s of the segment's tiles, in the order the mma takes them (see below)
-        auto tile = [&](int s, bool& isv) {
-          isv = s & 1;
-          if (!single) return s >> 1;
-          isv = s == 2 * n - 1 || (s > 0 && !isv);
-          return s == 0 ? 0 : (s == 2 * n - 1 ? n - 1 : (isv ? s / 2 - 1 : (s + 1) / 2));
-        };
         // the group to copy next: its tokens' blocks are looked up a group ahead
         int xl = wc, put = 0;
         bool on = false, isv = false;
         int32_t block = 0, inner = 0;
         auto look_up = [&]() {
-          const int j = tile(xl / GPT, isv);
+          const int j = tc_tile_at(xl / GPT, n, single, isv);
           const int t = (w.kv0 + j) * BN + xl % GPT * 8 + tok;
           on = t < w.g.c;
           block = inner = 0;
@@ -502,13 +665,114 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
         w.advance();
       }
     }
-   } else if (warp < LOAD + CONV + LOADERS) {
+   } else if (Q8T && warp < Q0) {
+    // ============================================================ raw tiles
+    // One warp copies K's tiles, the other V's; lane i looks after 8-token group i, whose
+    // block is looked up two tiles ahead.  K's warp also brings the tile's exponents, of
+    // K and V, a tile ahead: ring entry {how far each group's is below the tile's, K and
+    // V; the tile's}.  An entry is written TILES tiles after the one it replaces, whose
+    // readers are done: K's tile is at most RS + NS tiles before one whose scores have been
+    // read, and the softmax of the tile two before that is over.
+    if constexpr (Q8T) {
+      constexpr int RS = C::RS;
+      static_assert(RS + NS + 3 <= C::TILES, "ring of exponents");
+      const bool isv = warp != RAWER;
+      const CUtensorMap* map = isv ? &p.tm_v : &p.tm_k;
+      const int ring0 = isv ? RS : 0;
+      const int per = p.box_tokens / 8;  // groups of a box
+      const int bs = p.block_size, step = BN / bs, rest = BN % bs;
+      const bool mine = lane < BN / 8;
+      uint32_t tile = 0;  // kv tiles so far
+      while (ok && w.next(p)) {
+        const int n = w.kv1 - w.kv0;
+        // the lane's group: position, its place among the row's blocks and in its block, two
+        // tiles ahead of the copies
+        int t = w.kv0 * BN + lane * 8;
+        int j = (int)((unsigned)t / (unsigned)bs), in = t - j * bs;
+        const int32_t* row = p.block_tables + (int64_t)w.r * p.max_blocks_per_row;
+        auto look_up = [&]() -> int32_t {
+          const int32_t b = mine && t < w.g.c ? row[j] : 0;
+          t += BN;
+          j += step;
+          in += rest;
+          if (in >= bs) {
+            in -= bs;
+            ++j;
+          }
+          return b;
+        };
+        auto checked = [&](int32_t b) {
+          if (b < 0 || b >= p.num_blocks) {
+            set_flag(p.err, NP_FLAG_BLOCK_ID);
+            b = 0;
+          }
+          return b;
+        };
+        auto scale = [&](const float* s, int32_t b) { return __float_as_uint(s[(int64_t)b * p.kv_heads + w.kvh]); };
+        int in0 = in;
+        int32_t b0 = checked(look_up());
+        int in1 = in;
+        int32_t b1 = look_up();
+        uint32_t ks = 0, vs = 0;
+        if (!isv) {
+          ks = scale(p.k_scale, b0);
+          vs = scale(p.v_scale, b0);
+        }
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, ++tile) {
+          const int in2 = in;
+          const int32_t b2 = look_up();
+          b1 = checked(b1);
+          const uint32_t ks0 = ks, vs0 = vs;
+          if (!isv) {
+            ks = scale(p.k_scale, b1);
+            vs = scale(p.v_scale, b1);
+          }
+          const uint32_t rs = tile % RS + ring0;
+          if (tile >= RS) {
+            ok = __all_sync(FULL, mbar_wait(bar(B::raw_empty + rs), (tile / RS - 1u) & 1u, abort));
+            if (!ok) break;
+          }
+          const int valid = min(w.g.c - (w.kv0 + i) * BN, BN);  // <= 0: a row without history
+          if (!isv) {
+            const bool on = mine && lane * 8 < valid;
+            const int ke = on ? scale_exp(ks0) : kScaleMin, ve = on ? scale_exp(vs0) : kScaleMin;
+            const int kt = __reduce_max_sync(FULL, ke), vt = __reduce_max_sync(FULL, ve);
+            unsigned char* te = smem + C::EXPS + tile % C::TILES * C::TE;
+            if (mine) {
+              te[lane] = (unsigned char)(kt - ke);
+              te[BN / 8 + lane] = (unsigned char)(vt - ve);
+            }
+            if (lane == 0) *reinterpret_cast<short*>(te + 2 * (BN / 8)) = (short)((kt & 0xff) | (vt * 256));
+            __syncwarp();
+          }
+          const int nbox = valid <= 0 ? 0 : (valid + p.box_tokens - 1) / p.box_tokens;
+          if (lane == 0) mbar_arrive_expect_tx(bar(B::raw_full + rs), (uint32_t)(nbox * p.box_tokens * D));
+          __syncwarp();
+          const int32_t at = b0 * bs + in0;
+          const uint32_t to = base + C::RAW_T + rs * (uint32_t)C::RT;
+#pragma unroll 1
+          for (int x = 0; x < nbox; ++x)
+            tma_load_4d_warp(to + (uint32_t)(x * p.box_tokens * D), map, __shfl_sync(FULL, at, x * per), w.kvh,
+                             bar(B::raw_full + rs));
+          b0 = b1;
+          b1 = b2;
+          in0 = in1;
+          in1 = in2;
+        }
+        w.advance();
+      }
+      if (*abort)  // never leave copies in flight (bounded)
+        for (uint32_t q = tile > RS ? tile - RS : 0; q < tile; ++q)
+          mbar_wait_drain(bar(B::raw_full + (int)(q % RS) + ring0), (q / RS) & 1u);
+    }
+   } else if (warp < Q0 + LOADERS) {
     // =============================================================== loads
     // TILED: one warp copies q and the K tiles, another the V tiles (a copy costs
     // its issuing thread tens of cycles, and a tile is up to 16 of them).  Token
     // by token, 64 copies of the whole warp a tile and some 70 cycles each: three
     // warps take the tiles in turn, the first one q too.
-    const int id = warp - LOAD - CONV;
+    const int id = warp - Q0;
     const int G = p.group;
     uint32_t seg = 0, seq0 = 0;  // segments; ring tiles before this segment
     int64_t last = -1;  // the last tile's ring position (for the drain)
@@ -645,12 +909,12 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
         }
         const int qt = single ? 1 : 2;
         if constexpr (D >= 64) {  // (tiled copies whatever the pools take)
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar(B::q_full), (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
+          const uint32_t qb = bar(Q8T ? B::q_raw : B::q_full);
+          if (lane == 0) mbar_arrive_expect_tx(qb, (uint32_t)(qt * SL * G * p.tile_tokens) * 128u);
           __syncwarp();
           for (int i = 0; i < qt * SL; ++i)
             tma_load_3d_warp(base + (uint32_t)i * 16384u, &p.tm_q, (i % SL) * 64, w.kvh * G,
-                             w.g.q0 + (w.m * MT + i / SL) * p.tile_tokens, bar(B::q_full));
+                             w.g.q0 + (w.m * MT + i / SL) * p.tile_tokens, qb);
         } else {
           constexpr int CH = D / 8;
           for (int e = lane; e < qt * 128 * CH; e += 32) {
@@ -708,7 +972,7 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
       w.advance();
     }
     if (*abort) {  // never leave copies in flight (bounded)
-      if (D >= 64 && id == 0 && seg > 0) mbar_wait_drain(bar(B::q_full), (seg - 1) & 1u);
+      if (D >= 64 && id == 0 && seg > 0) mbar_wait_drain(bar(Q8T ? B::q_raw : B::q_full), (seg - 1) & 1u);
       if constexpr (TILED) {
         // the last NS positions up to this warp's last tile: those of the other
         // warp's that never came run into the wait's limit
@@ -721,9 +985,9 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
    } else if (warp == ISSUER) {
     // ================================================================= mma
     // The whole warp runs the role, its lanes alike; one of them issues.
-    constexpr uint32_t PV = umma_idesc_bf16(128, D, true);
+    constexpr uint32_t PV = umma_idesc_bf16(128, D, true, false, Q8T);
     constexpr uint32_t QHI = umma_desc_hi(1024), KVHI = umma_desc_hi(SL * 1024);
-    const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0);
+    const uint32_t QK = umma_idesc_bf16(128, BN, false, p.negate != 0, Q8T);
     RingPos pos{0, 0};
     uint32_t seg = 0;
     uint32_t done0 = 0, done1 = 0;  // phases of each p_full so far
@@ -845,7 +1109,7 @@ __global__ void __launch_bounds__(TcCfg<D, (KV >= kQ8)>::THREADS, 1)
 template <int D, int KV>
 static np_status launch(const PrefillParams& p, cudaStream_t s) {
   static unsigned long long allowed = 0;
-  using C = TcCfg<D, (KV >= kQ8)>;
+  using C = TcCfg<D, tc_kind(KV)>;
   const np_status rc = allow_smem(prefill_tc_kernel<D, KV>, C::SMEM, &allowed);
   if (rc != NP_OK) return rc;
   return launch_dependent(prefill_tc_kernel<D, KV>, p.ctas, 1, C::THREADS, C::SMEM, s, p);
@@ -855,7 +1119,11 @@ static np_status launch(const PrefillParams& p, cudaStream_t s) {
 #define NPK_CAT(a, b) NPK_CAT2(a, b)
 
 #ifdef NPK_Q8
-np_status NPK_CAT(prefill_tcq8_d, NPK_D)(const PrefillParams& p, np_form8 form, cudaStream_t s) {
+np_status NPK_CAT(prefill_tcq8_d, NPK_D)(const PrefillParams& p, np_form8 form, bool tiled, cudaStream_t s) {
+#if NPK_D >= 64
+  if (tiled)
+    return form == NP_E4M3 ? launch<NPK_D, kQ8Tiled + NP_E4M3>(p, s) : launch<NPK_D, kQ8Tiled + NP_INT8>(p, s);
+#endif
   return form == NP_E4M3 ? launch<NPK_D, kQ8 + NP_E4M3>(p, s) : launch<NPK_D, kQ8 + NP_INT8>(p, s);
 }
 #else

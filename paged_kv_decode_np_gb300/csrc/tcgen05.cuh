@@ -100,10 +100,12 @@ __device__ __forceinline__ constexpr uint32_t umma_desc_hi(uint32_t stride) {
   return (stride >> 4) | (1u << 14) | (2u << 29);
 }
 
-// bf16 x bf16 -> fp32, M x N; b_mn: B's N extent is contiguous; neg_a: -A
-__host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn, bool neg_a = false) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((neg_a ? 1u : 0u) << 13) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// bf16 x bf16 -> fp32, M x N; b_mn: B's N extent is contiguous; neg_a: -A.  f16: fp16
+// operands instead.
+__host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn, bool neg_a = false,
+                                                       bool f16 = false) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((neg_a ? 1u : 0u) << 13) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // ----------------------------------------------------------------- mma ----
@@ -178,6 +180,16 @@ __device__ __forceinline__ void tma_load_5d_warp(uint32_t dst, const CUtensorMap
       "@e cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%5, %5, %5, %2, %3}], [%4];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c3), "r"(c4), "r"(bar), "r"(0)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_warp(uint32_t dst, const CUtensorMap* map, int32_t c1,
+                                                 int32_t c3, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%5, %2, %5, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c1), "r"(c3), "r"(bar), "r"(0)
       : "memory");
 }
 

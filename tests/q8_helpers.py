@@ -5,7 +5,7 @@ import math
 
 import torch
 
-from prompt_helpers import HALF
+from prompt_helpers import HALF, chunk_tolerance
 
 FORMS = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 QMAX = {torch.float8_e4m3fn: 448.0, torch.int8: 127.0}
@@ -141,3 +141,31 @@ def decode_tolerance(ref, bound, dtype, d, longest, vtop):
     tol = tol + mass * (2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22)
     tol = tol + longest * 2.0 ** -31 * vtop
     return 1.1 * (tol + HALF[dtype] * ref.abs()) + 1e-30
+
+
+def prefill_tolerance(inp, ref, bound, dtype, d, longest, scale):
+    """How far np_paged_prefill_q8 may be off, per element: prompt_helpers.chunk_tolerance, and for
+    bf16 with tiled copies what fp16 adds at its small end.
+
+    A weight below fp16's normals is off by at most 2^-25 where the largest is 2^6 or more: 2^-31 of
+    the largest value, for each of `longest` positions (a value of 0 under the largest weight leaves
+    nothing else to compare with).  A V element whose block's scale is far below its tile's is off by at
+    most 2^-25 of the tile's scale, 2^-31 of the largest value and less; weights add up to 1.  A K
+    element, likewise, by 2^-25 of the tile's scale: a score by that times the sum of |q|, and the output
+    by twice that, relative."""
+    tol = chunk_tolerance(ref, bound, dtype, d, longest)
+    bs = inp["k_pool"].shape[1]
+    if dtype != torch.bfloat16 or d < 64 or bs % 8 or longest == 0:
+        return tol
+    used = inp["block_tables"][inp["block_tables"] >= 0].long()
+    if used.numel() == 0:
+        return tol
+    top = {k: float(inp[k][used].clamp(2.0 ** -60, 2.0 ** 60).max()) for k in ("k_scale", "v_scale")}
+    vtop = top["v_scale"] * QMAX[inp["v_pool"].dtype]
+    inside = ~ref.isnan()
+    q = inp["q"].double().abs().sum(-1, keepdim=True).expand(inp["q"].shape)
+    if q.shape != ref.shape:  # (the caller left out tokens of no row)
+        starts = inp["query_starts"].tolist()
+        q = q[starts[0]:starts[-1]]
+    e = q * abs(scale) * 2.0 ** -25 * top["k_scale"]
+    return tol + torch.where(inside, 1.1 * (2 * e * bound[0] + (longest + 1) * 2.0 ** -31 * vtop), 0.0)

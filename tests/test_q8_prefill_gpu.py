@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import q8_helpers as h
-from prompt_helpers import chunk_reference, chunk_tolerance
+from prompt_helpers import chunk_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -33,7 +33,8 @@ def _check(npg, dtype, form, d, hk, g, bs, rows, scale=None, **kw):
     assert (out[~inside] == 77.0).all()  # tokens of no row are left as they were
     got, ref = out[inside].double(), ref[inside]
     assert got.isfinite().all()
-    tol = chunk_tolerance(ref, tuple(b[inside] for b in bound), dtype, d, max([1] + [c for _, c in rows]))
+    tol = h.prefill_tolerance(inp, ref, tuple(b[inside] for b in bound), dtype, d, max([1] + [c for _, c in rows]),
+                              scale)
     off = (got - ref).abs()
     assert (off <= tol).all(), f"worst {(off / tol).max().item():.2f} of the tolerance"
     return inp, out
