@@ -133,17 +133,15 @@ struct Scaled8<NP_INT8> {
 template <int FORM>
 struct Below8;
 
-__device__ __forceinline__ uint32_t half_twice_below(uint32_t d) {  // 2^-d in both halves; 0 past 24
-  return d <= 14u ? 0x3c003c00u - d * 0x04000400u : d <= 24u ? 0x04000400u >> (d - 14u) : 0u;
+// 2^-d in both halves, d <= 126; 0 past 24
+__device__ __forceinline__ __half2 half_twice_below(uint32_t d) {
+  return __float2half2_rn(__uint_as_float((127u - d) << 23));
 }
 
 template <>
 struct Below8<NP_E4M3> {
   __half2 f;
-  __device__ __forceinline__ explicit Below8(uint32_t d) {
-    const uint32_t w = half_twice_below(d);
-    f = *reinterpret_cast<const __half2*>(&w);
-  }
+  __device__ __forceinline__ explicit Below8(uint32_t d) : f(half_twice_below(d)) {}
   __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {
     const uint32_t a = Form8<NP_E4M3>::half_lo(w), b = Form8<NP_E4M3>::half_hi(w);
     const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
@@ -157,9 +155,8 @@ template <>
 struct Below8<NP_INT8> {
   // (1152 + code) 2^-d - 1152 2^-d
   __half2 f, off;
-  __device__ __forceinline__ explicit Below8(uint32_t d) {
-    const uint32_t w = half_twice_below(d), c = 0xe480e480u;  // -1152
-    f = *reinterpret_cast<const __half2*>(&w);
+  __device__ __forceinline__ explicit Below8(uint32_t d) : f(half_twice_below(d)) {
+    const uint32_t c = 0xe480e480u;  // -1152
     off = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
   }
   __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {

@@ -526,41 +526,60 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
           if (ok && seq >= NS) ok = mbar_wait(bar(B::kv_empty + slot), (seq / NS - 1u) & 1u, abort);
           ok = __all_sync(FULL, ok);
           if (!ok) break;
+          // The lane's piece k of group i of the warp's: token r, 16-byte piece ch = c0 + 4 k.
+          // In the raw tile groups are 8 D bytes apart (in boxes: box_tokens tokens, in
+          // slabs of 128 bytes, swizzled), in the widened one SL KB.
+          const int r0 = wc * GW * 8 + tok;
           const uint32_t from = base + C::RAW_T + rs * (uint32_t)C::RT;
-          const uint32_t below = base + C::EXPS + te * C::TE + (isv ? BN / 8 : 0);
-          const uint32_t to = ring + slot * C::SLOT;
-          // (rolled: four roles share the instruction caches)
-          auto piece = [&](int i, uint32_t* q, uint32_t& d) {  // piece i of the warp's GW x PI
-            const int g = wc * GW + i / PI, r = g * 8 + tok, ch = c0 + 4 * (i % PI);
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(d) : "r"(below + g));
-            // the boxes' layout: box_tokens tokens, in slabs of 128 bytes, swizzled
-            uint32_t at;
-            if constexpr (D == 64) at = (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-            else if constexpr (D == 128) at = (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
-            else {
-              const int b = r & ~(p.box_tokens - 1), in = r - b;
-              at = (uint32_t)(b * 256 + ((ch >> 3) * p.box_tokens + in) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+          const uint32_t to = ring + slot * C::SLOT + (uint32_t)(wc * GW * SL * 1024 + tok * 128);
+          auto raw = [&](int i, uint32_t (&q)[PI][4]) {
+            const int r = r0 + 8 * i;
+#pragma unroll
+            for (int k = 0; k < PI; ++k) {
+              const int ch = c0 + 4 * k;
+              uint32_t at;
+              if constexpr (D == 64) at = (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+              else if constexpr (D == 128) at = (uint32_t)(r * 128 + ((ch ^ tok) << 4));
+              else {
+                const int b = r & ~(p.box_tokens - 1);
+                at = (uint32_t)(b * 256 + ((k >> 1) * p.box_tokens + r - b) * 128 + (((ch & 7) ^ tok) << 4));
+              }
+              lds<4>(from + at, q[k]);
             }
-            lds<4>(from + at, q);
           };
-          uint32_t q[4], d;
-          piece(0, q, d);
+          uint32_t below;  // how far the groups' scales are below the tile's, a byte each
+          {
+            const uint32_t at = base + C::EXPS + te * C::TE + (isv ? BN / 8 : 0) + wc * GW;
+            if constexpr (GW == 4) lds<1>(at, &below);
+            else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(below) : "r"(at));
+          }
           const int valid = FORM == NP_E4M3 && isv ? w.g.c - (w.kv0 + j) * BN : BN;
+          uint32_t q[PI][4];
+          raw(0, q);
+          // (a group's pieces unrolled, the groups rolled: four roles share the instruction
+          // caches.  Chunk 1024 of 65536 2073 us with the pieces rolled too)
 #pragma unroll 1
-          for (int i = 0; i < GW * PI; ++i) {
-            uint32_t q1[4], d1;
-            piece(min(i + 1, GW * PI - 1), q1, d1);  // on its way meanwhile
-            const Below8<FORM> f(d);
-            uint32_t y[8];
-            const int r = (wc * GW + i / PI) * 8 + tok, ch = 2 * (c0 + 4 * (i % PI));
-            if (FORM == NP_E4M3 && r >= valid) q[0] = q[1] = q[2] = q[3] = 0u;
+          for (int i = 0; i < GW; ++i) {
+            uint32_t q1[PI][4];
+            raw(min(i + 1, GW - 1), q1);  // on its way meanwhile
+            const Below8<FORM> f(below & 0xffu);
+            below >>= 8;
+            if (FORM == NP_E4M3 && r0 + 8 * i >= valid) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f.widen(q[e], y[2 * e], y[2 * e + 1]);
-            sts4(to + tc_kv_at<SL>(r, ch), y);
-            sts4(to + tc_kv_at<SL>(r, ch + 1), y + 4);
+              for (int k = 0; k < PI; ++k) q[k][0] = q[k][1] = q[k][2] = q[k][3] = 0u;
+            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = q1[e];
-            d = d1;
+            for (int k = 0; k < PI; ++k) {
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f.widen(q[k][e], y[2 * e], y[2 * e + 1]);
+              const int ch = 2 * (c0 + 4 * k);  // 16-byte piece of the widened token
+              const uint32_t at = to + (uint32_t)(i * SL * 1024 + k * 1024) + (((ch & 7) ^ tok) << 4);
+              sts4(at, y);
+              sts4(at ^ 16u, y + 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) q[k][e] = q1[k][e];
+            }
           }
           fence_async_smem();
           __syncwarp();
@@ -749,12 +768,11 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
           const int nbox = valid <= 0 ? 0 : (valid + p.box_tokens - 1) / p.box_tokens;
           if (lane == 0) mbar_arrive_expect_tx(bar(B::raw_full + rs), (uint32_t)(nbox * p.box_tokens * D));
           __syncwarp();
-          const int32_t at = b0 * bs + in0;
-          const uint32_t to = base + C::RAW_T + rs * (uint32_t)C::RT;
-#pragma unroll 1
-          for (int x = 0; x < nbox; ++x)
-            tma_load_4d_warp(to + (uint32_t)(x * p.box_tokens * D), map, __shfl_sync(FULL, at, x * per), w.kvh,
-                             bar(B::raw_full + rs));
+          // (each by the lane of its first group: a loop of elected copies takes twice the time)
+          if (mine && lane % per == 0 && lane * 8 < valid)
+            tma_load_4d_lane(base + C::RAW_T + rs * (uint32_t)C::RT + (uint32_t)(lane * 8 * D), map,
+                             b0 * bs + in0, w.kvh, bar(B::raw_full + rs));
+          __syncwarp();
           b0 = b1;
           b1 = b2;
           in0 = in1;

@@ -183,12 +183,12 @@ __device__ __forceinline__ void tma_load_5d_warp(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d_warp(uint32_t dst, const CUtensorMap* map, int32_t c1,
+// A tiled copy of this thread's, at (0, c1, 0, c3).
+__device__ __forceinline__ void tma_load_4d_lane(uint32_t dst, const CUtensorMap* map, int32_t c1,
                                                  int32_t c3, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%5, %2, %5, %3}], [%4];\n\t}" ::"r"(dst),
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%5, %2, %5, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c1), "r"(c3), "r"(bar), "r"(0)
       : "memory");
 }
