@@ -92,9 +92,23 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t packe
   return pack_half(lo - f.x, hi - f.y);
 }
 
+// Row r's query tokens: the first one's place in q and out, how many, and whether the
+// row is read here at all.
+struct Q8Row {
+  int32_t q0, n;
+};
+__device__ __forceinline__ Q8Row q8_row(const DecodeQ8Params& p, int r) {
+  if (p.query_starts == nullptr) return {r * p.query_len, p.query_len};
+  const int32_t a = min(max(p.query_starts[r], 0), p.tokens);
+  const int32_t n = min(max(p.query_starts[r + 1], a), p.tokens) - a;
+  return {a, n <= p.query_len ? n : 0};
+}
+
+// Row r's context, 0 where it is not read here.
 __device__ __forceinline__ int32_t q8_len(const DecodeQ8Params& p, int r) {
   const int64_t cap = (int64_t)p.max_blocks * p.block_size;
   const int32_t c = p.lens[r];
+  if (p.query_starts != nullptr && q8_row(p, r).n == 0) return 0;
   return c < 0 ? 0 : (c > cap ? (int32_t)cap : c);
 }
 
@@ -168,7 +182,13 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
     int64_t own = 0;
     for (int r = ra; r < rb; ++r) {
       const int32_t c = p.lens[r];
-      if (blockIdx.x == 0 && (c < 0 || c > cap)) set_flag(p.err, NP_FLAG_CONTEXT);
+      if (blockIdx.x == 0) {
+        if (c < 0 || c > cap) set_flag(p.err, NP_FLAG_CONTEXT);
+        if (p.query_starts != nullptr) {
+          const int32_t a = p.query_starts[r], b = p.query_starts[r + 1];
+          if (a < 0 || b < a || b > p.tokens) set_flag(p.err, NP_FLAG_QUERY);
+        }
+      }
       own += (q8_len(p, r) + CT - 1) / CT;
     }
     int64_t x = own;
@@ -222,15 +242,14 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   // rows without history
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     if (q8_len(p, r) != 0) continue;
-    T* o = static_cast<T*>(p.out) + (int64_t)r * p.query_len * p.q_heads * D;
-    for (int64_t i = threadIdx.x; i < (int64_t)p.query_len * p.q_heads * D; i += 32 * WARPS) o[i] = T(0.f);
+    const Q8Row qr = q8_row(p, r);
+    T* o = static_cast<T*>(p.out) + (int64_t)qr.q0 * p.q_heads * D;
+    for (int64_t i = threadIdx.x; i < (int64_t)qr.n * p.q_heads * D; i += 32 * WARPS) o[i] = T(0.f);
   }
   if (wi >= WPH || chunks == 0) return;  // (warps beyond the heads' have nothing to do)
 
   unsigned char* ring = q8_smem + (size_t)warp * NS * Geo::STAGE;
   const uint32_t ring_u = smem_u32(ring);
-  const int rows_used = p.group * p.query_len;  // MR at most
-
   // ---- loads: chunk by chunk ahead of the reads.  Lane i < CT looks after token i.
   Q8Walk<CT> ld;
   ld.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
@@ -295,6 +314,8 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   bool first = true;
   for (; w.live(); w.next(p)) {
     const int kvh = w.hgi * HG + hl;
+    const Q8Row qr = q8_row(p, w.r);
+    const int rows_used = p.group * qr.n;  // MR at most
     // q: column n of tile nt is row n + 8 nt of the head's (query token, head) rows; a
     // lane holds dims 16 (piece) + 4 word .. + 3 of column g
     uint32_t qf[NT][PARTS][KJ * KW][2];
@@ -306,7 +327,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       const bool on = row < rows_used;
       const int qi = on ? row / p.group : 0, h = on ? row - qi * p.group : 0;
       const T* src = static_cast<const T*>(p.q) +
-                     (((int64_t)w.r * p.query_len + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+                     ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
       float x[KJ * KW][4];
       float big = 0.f;
 #pragma unroll
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int row2 = nt * 8 + 2 * t4 + c;
-        lim[nt][c] = row2 < rows_used ? w.c - p.query_len + row2 / p.group + 1 : w.c;
+        lim[nt][c] = row2 < rows_used ? w.c - qr.n + row2 / p.group + 1 : w.c;
       }
     }
     float o[NT][D / 16][4];
@@ -356,7 +377,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       l[nt][0] = l[nt][1] = 0.f;
     }
     int last = -1;  // the stage read last in this segment
-    const int32_t all_see = w.c - p.query_len + 1;  // positions before it: every row
+    const int32_t all_see = w.c - qr.n + 1;  // positions before it: every row
 
     for (; cg < w.g1; cg += WPH) {
       cp_async_wait<NS - 2>();
@@ -567,7 +588,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           const float inv = L > 0.f ? 1.f / L : 0.f;
           const int qi = row / p.group, h = row - qi * p.group;
           T* out = static_cast<T*>(p.out) +
-                   (((int64_t)w.r * p.query_len + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+                   ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
 #pragma unroll
           for (int k = 0; k < DL; ++k) {
             const float y = acc[k] * inv;
@@ -610,7 +631,7 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
   constexpr int WARPS = kQ8JoinThreads / 32, U = 8;
   constexpr int DL = D >= 32 ? D / 32 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int HG = p.head_group, rows_used = p.group * p.query_len;
+  const int HG = p.head_group, MR = p.group * p.query_len;  // rows at most
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
     int n = 0;
@@ -623,10 +644,13 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
     if (lane == 0) cuts = n;
   }
   __syncthreads();
-  const int tasks = cuts * HG * rows_used;
+  const int tasks = cuts * HG * MR;
   for (int task = blockIdx.x + warp * gridDim.x; task < tasks; task += WARPS * gridDim.x) {
-    const int row = task % rows_used, hl = task / rows_used % HG;
-    const int4 c = list[task / rows_used / HG];
+    const int row = task % MR, hl = task / MR % HG;
+    const int4 c = list[task / MR / HG];
+    const int r = c.x % p.rows, kvh = c.x / p.rows * HG + hl;
+    const Q8Row qr = q8_row(p, r);
+    if (row >= p.group * qr.n) continue;
     auto entry = [&](int b) {
       return p.parts + (((size_t)b * 2 + (b == c.y ? c.w : 0)) * HG + hl) * q8_entry_floats(D);
     };
@@ -663,10 +687,9 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
       M = mx;
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int r = c.x % p.rows, kvh = c.x / p.rows * HG + hl;
     const int qi = row / p.group, h = row - qi * p.group;
     T* out = static_cast<T*>(p.out) +
-             (((int64_t)r * p.query_len + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+             ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
     if (D < 32 && lane >= D) continue;
 #pragma unroll
     for (int k = 0; k < DL; ++k) {

@@ -27,6 +27,11 @@ struct DecodeQ8Params {
   int4* cuts;    // [ctas] {row of the stream, first block, last block, slot}; x = -1: none
   int64_t num_blocks;
   int32_t block_size, kv_heads, q_heads, group, max_blocks;
+  // Chunks (np_paged_prefill_q8): row r's query tokens are query_starts[r] .. [r + 1] of
+  // `tokens`, and only rows with at most query_len of them are read; else NULL, and
+  // every row has query_len.
+  const int32_t* query_starts;
+  int32_t tokens;
   int32_t rows, query_len, head_group, ctas;
   int32_t least;  // chunks a block takes at least
   float qscale;   // scale * log2(e)
@@ -42,6 +47,11 @@ NPK_Q8_DECLARE(64)
 NPK_Q8_DECLARE(128)
 NPK_Q8_DECLARE(256)
 #undef NPK_Q8_DECLARE
+
+// The launches for a head_dim and form, after everything that they need but head_group,
+// least and ctas is in p (decode_q8_api.cu).
+np_status launch_decode_q8(DecodeQ8Params& p, int32_t head_dim, np_dtype dtype, np_form8 form, int sms,
+                           cudaStream_t s);
 
 // the warps of a thread block, which bound the kv heads it takes (head_group)
 __host__ __device__ constexpr int q8_warps(int d, int tiles) {

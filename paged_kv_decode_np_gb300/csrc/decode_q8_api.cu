@@ -66,6 +66,31 @@ np_status check_decode_q8(const np_read_q8_args& a, bool* run) {
 
 }  // namespace
 
+namespace npk {
+
+np_status launch_decode_q8(DecodeQ8Params& p, int32_t head_dim, np_dtype t, np_form8 form, int sms,
+                           cudaStream_t s) {
+  p.ctas = sms < kQ8MaxCtas ? sms : kQ8MaxCtas;
+  // kv heads of a block: the largest divisor that its warps have room for
+  const int tiles = t == NP_BF16 && p.group * p.query_len > 8 ? 2 : 1;
+  const int warps = q8_warps(head_dim, tiles);
+  p.head_group = 1;
+  for (int h = 2; h <= 8 && h <= warps; ++h)
+    if (p.kv_heads % h == 0) p.head_group = h;
+  p.least = 2 * (warps / p.head_group);
+  const bool e4m3 = form == NP_E4M3;
+  switch (head_dim) {
+    case 16: return e4m3 ? decode_q8_d16_e4m3(p, t, s) : decode_q8_d16_int8(p, t, s);
+    case 32: return e4m3 ? decode_q8_d32_e4m3(p, t, s) : decode_q8_d32_int8(p, t, s);
+    case 64: return e4m3 ? decode_q8_d64_e4m3(p, t, s) : decode_q8_d64_int8(p, t, s);
+    case 128: return e4m3 ? decode_q8_d128_e4m3(p, t, s) : decode_q8_d128_int8(p, t, s);
+    case 256: return e4m3 ? decode_q8_d256_e4m3(p, t, s) : decode_q8_d256_int8(p, t, s);
+  }
+  return NP_ERR_UNSUPPORTED;
+}
+
+}  // namespace npk
+
 extern "C" size_t np_paged_decode_q8_workspace_bytes(int32_t head_dim) {
   return head_dim_ok(head_dim) ? npk::q8_workspace_bytes(head_dim) : 0;
 }
@@ -97,26 +122,9 @@ extern "C" np_status np_paged_decode_q8_packed(const np_read_q8_args* a) {
   p.max_blocks = a->max_blocks_per_row;
   p.rows = a->rows;
   p.query_len = a->query_len;
-  p.ctas = sms < npk::kQ8MaxCtas ? sms : npk::kQ8MaxCtas;
   p.qscale = a->scale * kLog2e;
-  // kv heads of a block: the largest divisor that its warps have room for
-  const int tiles = a->dtype == NP_BF16 && p.group * p.query_len > 8 ? 2 : 1;
-  const int warps = npk::q8_warps(a->head_dim, tiles);
-  p.head_group = 1;
-  for (int h = 2; h <= 8 && h <= warps; ++h)
-    if (p.kv_heads % h == 0) p.head_group = h;
-  p.least = 2 * (warps / p.head_group);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
-  const np_dtype t = static_cast<np_dtype>(a->dtype);
-  const bool e4m3 = a->form == NP_E4M3;
-  switch (a->head_dim) {
-    case 16: return e4m3 ? npk::decode_q8_d16_e4m3(p, t, s) : npk::decode_q8_d16_int8(p, t, s);
-    case 32: return e4m3 ? npk::decode_q8_d32_e4m3(p, t, s) : npk::decode_q8_d32_int8(p, t, s);
-    case 64: return e4m3 ? npk::decode_q8_d64_e4m3(p, t, s) : npk::decode_q8_d64_int8(p, t, s);
-    case 128: return e4m3 ? npk::decode_q8_d128_e4m3(p, t, s) : npk::decode_q8_d128_int8(p, t, s);
-    case 256: return e4m3 ? npk::decode_q8_d256_e4m3(p, t, s) : npk::decode_q8_d256_int8(p, t, s);
-  }
-  return NP_ERR_UNSUPPORTED;
+  return npk::launch_decode_q8(p, a->head_dim, static_cast<np_dtype>(a->dtype), static_cast<np_form8>(a->form),
+                               sms, reinterpret_cast<cudaStream_t>(a->stream));
 }
 
 extern "C" np_status np_paged_decode_q8(void* out, const void* q, np_dtype dtype, const void* k_pool,

@@ -60,6 +60,7 @@ struct PrefillParams {
   // of one with a single such tile, for beginning a unit; the least share of a block
   int32_t full_cost, single_cost, unit_cost, min_share;
   int32_t box_tokens;   // tokens per tiled copy
+  int32_t skip_tokens;  // rows with this many chunk tokens or fewer are another launch's
   float qscale;         // |scale| * log2(e)
   int32_t negate;       // scale < 0
 };
@@ -120,7 +121,7 @@ NPK_HD PrefillRow prefill_row(const PrefillParams& p, int r, bool flag = false) 
     c = c < 0 ? 0 : (int32_t)cap;
   }
   g.q0 = a2;
-  g.n = b2 - a2;
+  g.n = b2 - a2 <= p.skip_tokens ? 0 : b2 - a2;
   g.c = c;
   return g;
 }

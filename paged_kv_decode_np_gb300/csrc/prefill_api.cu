@@ -7,6 +7,7 @@
 
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled_v12000
 
+#include "decode_q8.cuh"
 #include "prefill.cuh"
 
 namespace {
@@ -28,6 +29,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Plan and cut list, then the partials of kPrefillMaxCtas blocks.
 constexpr size_t kPlanBytes = (2 * npk::kPrefillMaxCtas + 1) * sizeof(int4);
+// The decode read's partials and cuts use the same workspace (np_paged_prefill_q8).
+static_assert(npk::kQ8MaxCtas <= npk::kPrefillMaxCtas && 8 * npk::kQ8Rows <= 128 &&
+                  npk::kQ8MaxCtas * sizeof(int4) <= kPlanBytes,
+              "workspace");
 
 // rows of the largest unit any kernel of this head_dim takes
 int unit_rows(int32_t head_dim) { return head_dim == 256 ? 128 : 256; }
@@ -395,7 +400,40 @@ extern "C" np_status np_paged_prefill_q8_packed(const np_read_q8_args* a) {
   p.v_scale = a->v_scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(a->stream);
   const np_dtype dtype = static_cast<np_dtype>(a->dtype);
-  const np_status rc = launch_q8(p, dtype, static_cast<np_form8>(a->form), s);
+  const np_form8 form = static_cast<np_form8>(a->form);
+  // Rows with few tokens go to the decode read's kernel: their (token, head) rows fit
+  // one fetch of its tile.  Two launches more, so where rows are short on average.
+  const int few = (p.group <= 8 ? 8 : 16) / p.group;
+  if (p.rows > 1 ? p.tokens < 64ll * p.rows : p.tokens <= few) {
+    p.skip_tokens = few;
+    npk::DecodeQ8Params d{};
+    d.out = p.out;
+    d.q = p.q;
+    d.k_pool = static_cast<const uint8_t*>(p.k_pool);
+    d.v_pool = static_cast<const uint8_t*>(p.v_pool);
+    d.k_scale = p.k_scale;
+    d.v_scale = p.v_scale;
+    d.tables = p.block_tables;
+    d.lens = p.context_lens;
+    d.err = p.err;
+    // (the workspace is the attention's after the join: the plan is launched when that is over)
+    d.parts = static_cast<float*>(a->workspace);
+    d.cuts = reinterpret_cast<int4*>(static_cast<char*>(a->workspace) + npk::q8_parts_bytes(p.head_dim));
+    d.num_blocks = p.num_blocks;
+    d.block_size = p.block_size;
+    d.kv_heads = p.kv_heads;
+    d.q_heads = p.q_heads;
+    d.group = p.group;
+    d.max_blocks = p.max_blocks_per_row;
+    d.query_starts = p.query_starts;
+    d.tokens = p.tokens;
+    d.rows = p.rows;
+    d.query_len = few;
+    d.qscale = a->scale * kLog2e;
+    const np_status rc = npk::launch_decode_q8(d, p.head_dim, dtype, form, p.ctas, s);
+    if (rc != NP_OK || p.tokens <= few) return rc;  // (no row has more than all the tokens)
+  }
+  const np_status rc = launch_q8(p, dtype, form, s);
   return rc == NP_OK ? npk::launch_prefill_join(p, dtype, s) : rc;
 }
 

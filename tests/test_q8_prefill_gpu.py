@@ -110,7 +110,8 @@ def test_scales_of_blocks_of_any_size(nplib, dtype):
 @pytest.mark.parametrize("form", [E4M3, INT8], ids=["e4m3", "int8"])
 @pytest.mark.parametrize("e", [-60, -5, 0, 7, 8, 60])
 def test_every_code_under_small_and_large_scales(nplib, form, dtype, e):
-    """One position a row, so that its V comes out as it is: exactly."""
+    """One position a row, so that its V comes out as it is: a weight over itself (as the two fp16
+    parts of the decode read's kernel, 2^-22 off, where q is fp32; l and the quotient rounded)."""
     codes = torch.arange(256, dtype=torch.int16).to(torch.uint8)
     skip = codes == 0x80 if form is INT8 else (codes & 0x7f) == 0x7f
     codes = torch.where(skip, torch.zeros_like(codes), codes)
@@ -123,13 +124,55 @@ def test_every_code_under_small_and_large_scales(nplib, form, dtype, e):
                block_tables=torch.arange(4, **i32)[:, None].contiguous(), context_lens=torch.ones(4, **i32),
                query_starts=torch.arange(5, **i32))
     out = _run(nplib, inp, 0.01)
-    assert torch.equal(out.double().flatten(), v.float().double().flatten() * 2.0 ** e)
+    want = v.float().double().flatten() * 2.0 ** e
+    off = (out.double().flatten() - want).abs()
+    assert (off <= want.abs() * (0.0 if dtype is BF else 2.0 ** -22 + 3 * 2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("form", [E4M3, INT8], ids=["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("bs", [1, 16])
+def test_every_code_exactly(nplib, form, dtype, n, bs):
+    """As above with keys of zero, so that the weight is a power of two: in every way that V comes (the
+    first n - 1 tokens see nothing)."""
+    codes = torch.arange(256, dtype=torch.int16).to(torch.uint8)
+    skip = codes == 0x80 if form is INT8 else (codes & 0x7f) == 0x7f
+    codes = torch.where(skip, torch.zeros_like(codes), codes)
+    d = 64
+    v = torch.full((4, bs, 1, d), 0x7f if form is E4M3 else 0x80, dtype=torch.uint8)
+    v[:, 0] = codes.view(4, 1, d)
+    v = v.view(form).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    scale = torch.tensor([[2.0 ** -60], [2.0 ** -3], [2.0 ** 9], [2.0 ** 60]], device="cuda")
+    inp = dict(q=torch.ones(4 * n, 1, d, dtype=dtype, device="cuda"),
+               k_pool=torch.zeros(4, bs, 1, d, dtype=torch.uint8, device="cuda").view(form), v_pool=v,
+               k_scale=torch.ones_like(scale), v_scale=scale,
+               block_tables=torch.arange(4, **i32)[:, None].contiguous(), context_lens=torch.ones(4, **i32),
+               query_starts=torch.arange(5, **i32) * n)
+    out = _run(nplib, inp, 0.01).view(4, n, d).double()
+    assert torch.equal(out[:, -1], v[:, 0, 0].float().double() * scale.double()) and (out[:, :-1] == 0).all()
 
 
 def test_many_rows(nplib):
     gen = torch.Generator().manual_seed(2)
     rows = [(1 + int(x) % 3, 3 + int(x)) for x in torch.randint(0, 60, (600,), generator=gen)]
     _check(nplib, BF, INT8, 64, 1, 4, 16, rows, seed=5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("g", [1, 3, 8, 16])
+@pytest.mark.parametrize("d", [32, 128])
+def test_short_rows_among_long_ones(nplib, dtype, g, d):
+    """Rows whose tokens fit one fetch are another kernel's: every count around that border, with and
+    without a history, among chunks; and such rows alone."""
+    if g == 16 and dtype is F32:
+        g = 7
+    rows = [(n, c) for n in (0, 1, 2, 3, 4, 7, 8, 9, 17) for c in (0, 1, n, 100, 1111)]
+    _check(nplib, dtype, E4M3, d, 2, g, 16, rows + [(130, 300)], seed=g, before=2, behind=3)
+    _check(nplib, dtype, INT8, d, 3, g, 8, [(1, c) for c in (5, 0, 700, 64, 2000)], seed=g, behind=1)
+    _check(nplib, dtype, INT8, d, 1, g, 5, [(1, 3000)], seed=g)
+    _check(nplib, dtype, INT8, d, 1, g, 16, [(0, 30), (1, 3000), (0, 0)], seed=g)
 
 
 def test_bad_metadata_is_flagged(nplib):
