@@ -29,6 +29,8 @@
 // equal share per block, one block an SM, from the context lengths on the device.
 // A row inside one block is stored directly; one that is cut leaves partials
 // that a second launch joins in block order.
+#include <type_traits>
+
 #include "cache8.cuh"
 #include "decode_q8.cuh"
 #include "tcgen05.cuh"  // cp_async_*
@@ -112,6 +114,12 @@ __device__ __forceinline__ int32_t q8_len(const DecodeQ8Params& p, int r) {
   return c < 0 ? 0 : (c > cap ? (int32_t)cap : c);
 }
 
+// a / b for a >= 0, b > 0: a 64-bit division takes several times a 32-bit one
+__device__ __forceinline__ int64_t q8_div(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // A block's walk over its share, by each of its warps: segment by segment (a run of
 // one row's chunks), in each the chunks that are this warp's.
 template <int CT>
@@ -119,15 +127,14 @@ struct Q8Walk {
   int hgi, r;          // the segment's kv head group and row
   int32_t c;           // its context
   int32_t c0;          // its first chunk (of the row)
-  int64_t g0, g1;      // its chunks among the block's
-  int64_t total;       // the block's chunks
+  int32_t g0, g1;      // its chunks among the block's
+  int32_t total;       // the block's chunks
 
   __device__ __forceinline__ void fill(const DecodeQ8Params& p) {
     c = q8_len(p, r);
-    const int64_t n = (c + CT - 1) / CT - c0;
-    g1 = min(total, g0 + n);
+    g1 = min(total, g0 + (c + CT - 1) / CT - c0);
   }
-  __device__ __forceinline__ void start(const DecodeQ8Params& p, int hgi_, int r_, int32_t c0_, int64_t n) {
+  __device__ __forceinline__ void start(const DecodeQ8Params& p, int hgi_, int r_, int32_t c0_, int32_t n) {
     hgi = hgi_;
     r = r_;
     c0 = c0_;
@@ -174,6 +181,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   // ---- this block's share: chunks [u0, u1) of all rows' chunks, which each thread
   // counts for a run of rows
   __shared__ int64_t warp_sum[WARPS];
+  __shared__ int last_stage[WARPS];
   __shared__ int64_t found[6];  // first row, first chunk, chunks; W, Pe, u0
   {
     const int per = (p.rows + 32 * WARPS - 1) / (32 * WARPS);
@@ -206,10 +214,14 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       all += warp_sum[w];
     }
     const int64_t W = all * (p.kv_heads / HG);
-    const int64_t want = (W + p.least - 1) / p.least;
+    const int64_t want = q8_div(W + p.least - 1, p.least);
     const int64_t Pe = want < 1 ? 1 : min(want, (int64_t)gridDim.x);
     const int b = blockIdx.x;
-    const int64_t u0 = b < Pe ? b * W / Pe : W, u1 = b + 1 < Pe ? (b + 1) * W / Pe : W;
+    // floor(b W / Pe), Pe <= 160
+    const int64_t each = q8_div(W, Pe);
+    const int over = (int)(W - each * Pe);
+    const int64_t u0 = b < Pe ? each * b + (uint32_t)(over * b) / (uint32_t)Pe : W;
+    const int64_t u1 = b < Pe ? each * (b + 1) + (uint32_t)(over * (b + 1)) / (uint32_t)Pe : W;
     if (threadIdx.x == 0) {
       found[0] = 0;
       found[1] = 0;
@@ -220,7 +232,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
     }
     __syncthreads();
     if (u1 > u0) {
-      const int64_t at = u0 % all;
+      const int64_t lap = q8_div(u0, all), at = u0 - lap * all;
       if (own > 0 && before <= at && at < before + own) {  // one thread's
         int64_t run = before;
         int r = ra;
@@ -229,14 +241,14 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           if (at < run + n) break;
           run += n;
         }
-        found[0] = r + (u0 / all) * p.rows;
+        found[0] = r + lap * p.rows;
         found[1] = at - run;
       }
     }
     __syncthreads();
     if (threadIdx.x == 0) p.cuts[b] = make_int4(-1, 0, 0, 0);  // (unless its last row is cut, below)
   }
-  const int64_t chunks = found[2];
+  const int32_t chunks = (int32_t)found[2];  // (the host bounds them)
   const int64_t v0 = found[0];
 
   // rows without history
@@ -250,99 +262,119 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
 
   unsigned char* ring = q8_smem + (size_t)warp * NS * Geo::STAGE;
   const uint32_t ring_u = smem_u32(ring);
-  // ---- loads: chunk by chunk ahead of the reads.  Lane i < CT looks after token i.
-  Q8Walk<CT> ld;
-  ld.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
-  int64_t lg = wi;         // the next chunk to load, of the block's
-  int32_t block = 0;       // the block of its token `lane`, looked up ahead
-  int32_t inner = 0;       // and the token's place in it
-  bool held = false;       // (a token of the row)
-  auto look_up = [&]() {
-    while (ld.live() && lg >= ld.g1) ld.next(p);
-    held = false;
-    if (!ld.live()) return;
-    const int32_t t = (int32_t)(ld.c0 + (lg - ld.g0)) * CT + (lane % CT);
-    held = t < ld.c;
-    if (held) {
-      const int32_t j = (int32_t)((uint32_t)t / (uint32_t)p.block_size);
-      inner = t - j * p.block_size;
-      block = p.tables[(int64_t)ld.r * p.max_blocks + j];
+  // ---- q of a segment, as it is stored: column n of tile nt is row n + 8 nt of the head's
+  // (query token, head) rows; a lane holds dims 16 (piece) + 4 word .. + 3 of column g
+  Q8Walk<CT> w;
+  w.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
+  using Raw = typename std::conditional<F32, uint4, uint2>::type;  // 4 elements
+  Raw raw[NT][KJ * KW];
+  Q8Row qr;
+  auto load_q = [&]() {
+    qr = q8_row(p, w.r);
+    const int kvh = w.hgi * HG + hl;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = nt * 8 + g;
+      const bool on = row < p.group * qr.n;
+      const int qi = on ? row / p.group : 0, h = on ? row - qi * p.group : 0;
+      const T* src = static_cast<const T*>(p.q) +
+                     ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+          const int d = D >= 128 ? 16 * (2 * t4 + (j & 1) + 8 * (j >> 1)) + 4 * k : t4 * (4 * KW) + 4 * k;
+          Raw x = {};
+          if (on) x = *reinterpret_cast<const Raw*>(src + d);
+          raw[nt][j * KW + k] = x;
+        }
     }
   };
-  auto issue = [&](int slot) {
-    if (ld.live()) {
+  load_q();  // (on its way while the first chunks are looked up)
+
+  // ---- loads: chunk by chunk ahead of the reads.  Lane i < CT looks after token i.  Its
+  // block is looked up two chunks before the copies.
+  Q8Walk<CT> ld = w;
+  int32_t lg = wi;  // the next chunk to look up, of the block's
+  struct Ahead {
+    int32_t block, inner, kvh;  // inner < 0: no token of the row
+  };
+  auto look_up = [&]() -> Ahead {
+    Ahead a{0, -1, -1};
+    while (ld.live() && lg >= ld.g1) ld.next(p);
+    if (!ld.live()) return a;
+    a.kvh = ld.hgi * HG + hl;
+    const int32_t t = (ld.c0 + (lg - ld.g0)) * CT + (lane % CT);
+    if (t < ld.c) {
+      const int32_t j = (int32_t)((uint32_t)t / (uint32_t)p.block_size);
+      a.inner = t - j * p.block_size;
+      a.block = p.tables[(int64_t)ld.r * p.max_blocks + j];
+    }
+    lg += WPH;
+    return a;
+  };
+  auto issue = [&](int slot, Ahead x) {
+    if (x.kvh >= 0) {
       const uint32_t st = ring_u + (uint32_t)slot * Geo::STAGE;
-      if (!held) block = inner = 0;
-      if (block < 0 || block >= p.num_blocks) {
+      const bool held = x.inner >= 0;
+      if (!held) x.inner = 0;
+      if (x.block < 0 || x.block >= p.num_blocks) {
         set_flag(p.err, NP_FLAG_BLOCK_ID);
-        block = 0;
+        x.block = 0;
       }
-      const int kvh = ld.hgi * HG + hl;
-      const int64_t at = ((int64_t)block * p.block_size + inner) * p.kv_heads + kvh;
+      const int64_t at = ((int64_t)x.block * p.block_size + x.inner) * p.kv_heads + x.kvh;
       if (lane < CT) {  // NT 1: 16 lanes; their scales
-        const int64_t sc = (int64_t)block * p.kv_heads + kvh;
+        const int64_t sc = (int64_t)x.block * p.kv_heads + x.kvh;
         copy4(st + 2 * CT * D + 4 * lane, p.k_scale + sc, held);
         copy4(st + 2 * CT * D + 4 * (CT + lane), p.v_scale + sc, held);
       }
       constexpr int LT = D / 16;                    // lanes of a token
       constexpr int TP = 32 / LT < CT ? 32 / LT : CT;  // tokens of a step
       const int sub = lane / LT, ch = lane % LT;
+      const unsigned live = __ballot_sync(FULL, held);
 #pragma unroll
       for (int i = 0; i < CT; i += TP) {
         const int tok = (i + sub) % CT;             // (D 16, NT 1: half the lanes repeat)
         const int64_t off = __shfl_sync(FULL, at, tok) * D + ch * 16;
-        const bool on = __shfl_sync(FULL, (int)held, tok) != 0;
+        const bool on = (live >> tok) & 1u;
         if (TP * LT == 32 || lane < TP * LT) {
           copy16(st + Geo::at(tok, ch), p.k_pool + off, on);
           copy16(st + CT * D + Geo::at(tok, ch), p.v_pool + off, on);
         }
       }
-      lg += WPH;
-      look_up();
     }
     cp_async_commit();
   };
-  look_up();
+  Ahead a0 = look_up(), a1 = look_up();
 #pragma unroll 1
-  for (int s = 0; s < NS - 1; ++s) issue(s);
+  for (int s = 0; s < NS - 1; ++s) {
+    const Ahead a2 = look_up();
+    issue(s, a0);
+    a0 = a1;
+    a1 = a2;
+  }
 
   // ---- reads
-  Q8Walk<CT> w;
-  w.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
-  int64_t cg = wi;  // this warp's next chunk
+  int32_t cg = wi;  // this warp's next chunk
   int slot = 0;     // its stage
   bool first = true;
-  for (; w.live(); w.next(p)) {
+  while (w.live()) {
     const int kvh = w.hgi * HG + hl;
-    const Q8Row qr = q8_row(p, w.r);
     const int rows_used = p.group * qr.n;  // MR at most
-    // q: column n of tile nt is row n + 8 nt of the head's (query token, head) rows; a
-    // lane holds dims 16 (piece) + 4 word .. + 3 of column g
     uint32_t qf[NT][PARTS][KJ * KW][2];
     float qs[NT][2];  // scale of rows 2 t4, + 1
     int32_t lim[NT][2];  // the first position each does not see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = nt * 8 + g;
-      const bool on = row < rows_used;
-      const int qi = on ? row / p.group : 0, h = on ? row - qi * p.group : 0;
-      const T* src = static_cast<const T*>(p.q) +
-                     ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+      const bool on = nt * 8 + g < rows_used;
       float x[KJ * KW][4];
       float big = 0.f;
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
+      for (int i = 0; i < KJ * KW; ++i) {
+        Storage<T>::template load<4>(reinterpret_cast<const T*>(&raw[nt][i]), x[i]);
 #pragma unroll
-        for (int k = 0; k < KW; ++k) {
-          const int d = D >= 128 ? 16 * (2 * t4 + (j & 1) + 8 * (j >> 1)) + 4 * k : t4 * (4 * KW) + 4 * k;
-          float* y = x[j * KW + k];
-          Storage<T>::template load<4>(src + d, y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!on) y[e] = 0.f;
-            big = fmaxf(big, fabsf(y[e]));
-          }
-        }
+        for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[i][e]));
+      }
       big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
       big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
       // the row's largest element to [2^14, 2^15)
@@ -382,11 +414,16 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
     for (; cg < w.g1; cg += WPH) {
       cp_async_wait<NS - 2>();
       __syncwarp();
-      issue(slot == 0 ? NS - 1 : slot - 1);  // into the stage read before
+      {
+        const Ahead a2 = look_up();
+        issue(slot == 0 ? NS - 1 : slot - 1, a0);  // into the stage read before
+        a0 = a1;
+        a1 = a2;
+      }
       const uint32_t st = ring_u + (uint32_t)slot * Geo::STAGE;
       last = slot;
       slot = slot + 1 == NS ? 0 : slot + 1;
-      const int32_t t0 = (int32_t)(w.c0 + (cg - w.g0)) * CT;
+      const int32_t t0 = (w.c0 + (cg - w.g0)) * CT;
 #pragma unroll
       for (int sub = 0; sub < CT; sub += 16) {
         if (sub > 0 && t0 + sub >= w.c) break;  // uniform
@@ -549,70 +586,79 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           }
         }
     }
-    const bool many = WPH > 1;
-    if (many) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
+    if (lane == 0) last_stage[warp] = last;
+    const bool whole = w.c0 == 0 && w.g1 - w.g0 >= (w.c + CT - 1) / CT;
+    const int32_t q0 = qr.q0;
+    if (threadIdx.x == 0 && w.g1 == w.total && w.c0 == 0 && !whole) {
+      // The share ends in this row, which begins here: it is cut, and its last block is the
+      // one with its last chunk.
+      const int64_t end = found[5] + w.g0 + (w.c + CT - 1) / CT;
+      p.cuts[blockIdx.x] = make_int4(w.hgi * p.rows + w.r, blockIdx.x,
+                                     (int)q8_div(end * found[4] - 1, found[3]), first ? 0 : 1);
+    }
+    w.next(p);
+    if (w.live()) load_q();  // the next segment's, on its way meanwhile
+    if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
     else __syncwarp();
     {
-      const bool whole = w.c0 == 0 && (w.g1 - w.g0) * CT >= w.c;
       float* part = p.parts + (((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * HG + hl) * q8_entry_floats(D);
-      // the stage that warp i of the head read last, if it has a chunk here
-      auto entry = [&](int i) -> const float* {
-        if (w.g1 <= i) return nullptr;
-        const int64_t k = (w.g1 - 1 - i) / WPH;  // its chunks before its last one
-        if (i + k * WPH < w.g0) return nullptr;
-        return reinterpret_cast<const float*>(q8_smem +
-                                              ((size_t)(hl + i * HG) * NS + (size_t)(k % NS)) * Geo::STAGE);
-      };
-      for (int row = wi; row < rows_used; row += WPH) {
-        float M = -INFINITY;
-        for (int i = 0; i < WPH; ++i) {
-          const float* e = entry(i);
-          if (e) M = fmaxf(M, e[row]);
-        }
-        const float ref = M == -INFINITY ? 0.f : M;
-        constexpr int DL = D >= 32 ? D / 32 : 1;  // dims of a lane, 32 apart
-        float L = 0.f, acc[DL];
+      // lane i: the stage that warp i of the head read last, -1: it had no chunk here
+      int at = -1;
+      if (lane < WPH) {
+        const int wr = hl + lane * HG, st = last_stage[wr];
+        at = st < 0 ? -1 : (wr * NS + st) * Geo::STAGE;
+      }
+      const unsigned has = __ballot_sync(FULL, at >= 0);
+      // lane r: row r's maximum and sum
+      float M = -INFINITY, L = 0.f;
+      const int mine = lane < MR ? lane : 0;
+      for (unsigned k = has; k != 0; k &= k - 1) {
+        const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
+        const float mx = fmaxf(M, e[mine]), ref = mx == -INFINITY ? 0.f : mx;
+        L = fmaf(ex2(e[mine] - ref), e[MR + mine], L * ex2(M - ref));
+        M = mx;
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      if (!whole && wi == 0 && lane < rows_used) {
+        part[lane] = M;
+        part[kQ8Rows + lane] = L;
+      }
+      // rows in turn over the head's warps, LR lanes a row, 4 (or 2 x 4) dims a lane
+      constexpr int LR = D >= 128 ? 32 : D / 4, RP = 32 / LR, DV = D == 256 ? 2 : 1;
+      for (int r0 = wi * RP; r0 < rows_used; r0 += WPH * RP) {
+        const int row = min(r0 + lane / LR, MR - 1), d = lane % LR * 4;
+        const float Mr = __shfl_sync(FULL, M, row), f0 = whole ? __shfl_sync(FULL, inv, row) : 1.f;
+        const float ref = Mr == -INFINITY ? 0.f : Mr;
+        float acc[DV][4];
 #pragma unroll
-        for (int k = 0; k < DL; ++k) acc[k] = 0.f;
-        for (int i = 0; i < WPH; ++i) {
-          const float* e = entry(i);
-          if (!e) continue;
-          const float f = ex2(e[row] - ref);
-          L = fmaf(f, e[MR + row], L);
+        for (int v = 0; v < DV; ++v) acc[v][0] = acc[v][1] = acc[v][2] = acc[v][3] = 0.f;
+        for (unsigned k = has; k != 0; k &= k - 1) {
+          const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
+          const float f = ex2(e[row] - ref) * f0;
 #pragma unroll
-          for (int k = 0; k < DL; ++k)
-            if (D >= 32 || lane < D) acc[k] = fmaf(f, e[2 * MR + row * LD + lane + 32 * k], acc[k]);
+          for (int v = 0; v < DV; ++v) {
+            const float4 x = *reinterpret_cast<const float4*>(e + 2 * MR + row * LD + d + 128 * v);
+            acc[v][0] = fmaf(f, x.x, acc[v][0]);
+            acc[v][1] = fmaf(f, x.y, acc[v][1]);
+            acc[v][2] = fmaf(f, x.z, acc[v][2]);
+            acc[v][3] = fmaf(f, x.w, acc[v][3]);
+          }
         }
-        if (D < 32 && lane >= D) continue;
+        if (r0 + lane / LR >= rows_used) continue;
         if (whole) {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
           const int qi = row / p.group, h = row - qi * p.group;
           T* out = static_cast<T*>(p.out) +
-                   ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+                   ((int64_t)(q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
 #pragma unroll
-          for (int k = 0; k < DL; ++k) {
-            const float y = acc[k] * inv;
-            Storage<T>::template store<1>(out + lane + 32 * k, &y);
-          }
+          for (int v = 0; v < DV; ++v) Storage<T>::template store<4>(out + d + 128 * v, acc[v]);
         } else {
-          if (lane == 0) {
-            part[row] = M;
-            part[kQ8Rows + row] = L;
-          }
 #pragma unroll
-          for (int k = 0; k < DL; ++k) part[2 * kQ8Rows + row * D + lane + 32 * k] = acc[k];
+          for (int v = 0; v < DV; ++v)
+            Storage<float>::store<4>(part + 2 * kQ8Rows + row * D + d + 128 * v, acc[v]);
         }
       }
     }
-    if (threadIdx.x == 0 && w.g1 == w.total && w.c0 == 0) {
-      // The share ends in this row, which begins here: cut, if chunks of it are left,
-      // and its last block is the one with its last chunk.
-      const int64_t n = (w.c + CT - 1) / CT, end = found[5] + w.g0 + n;
-      if (n > w.g1 - w.g0)
-        p.cuts[blockIdx.x] = make_int4(w.hgi * p.rows + w.r, blockIdx.x,
-                                       (int)((end * found[4] - 1) / found[3]), first ? 0 : 1);
-    }
-    if (many) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
+    if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
     else __syncwarp();
     first = false;
   }
@@ -620,7 +666,8 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
 }
 
 // The join: one warp per (cut row, kv head, (query token, head) row), over the blocks
-// that hold a piece, in block order; eight pieces' loads at a time.
+// that hold a piece, in block order: 32 pieces' m and l in one round, then their rows of O,
+// eight loads in flight.  Bound by the latency of those rounds (the partials are in L2).
 constexpr int kQ8JoinThreads = 256;
 
 template <typename T, int D>
@@ -628,23 +675,29 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
                                                                         DecodeQ8Params p) {
   __shared__ int4 list[kQ8MaxCtas];
   __shared__ int cuts;
+  constexpr unsigned FULL = 0xffffffffu;
   constexpr int WARPS = kQ8JoinThreads / 32, U = 8;
-  constexpr int DL = D >= 32 ? D / 32 : 1;
+  constexpr int LR = D >= 128 ? 32 : D / 4, DV = D == 256 ? 2 : 1;  // lanes of a row, 4 (2 x 4) dims each
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HG = p.head_group, MR = p.group * p.query_len;  // rows at most
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
+    int4 c[kQ8MaxCtas / 32];
+#pragma unroll
+    for (int i = 0; i < kQ8MaxCtas / 32; ++i)
+      c[i] = 32 * i + lane < p.ctas ? __ldcg(p.cuts + 32 * i + lane) : make_int4(-1, 0, 0, 0);
     int n = 0;
-    for (int b0 = 0; b0 < p.ctas; b0 += 32) {
-      const int4 c = b0 + lane < p.ctas ? __ldcg(p.cuts + b0 + lane) : make_int4(-1, 0, 0, 0);
-      const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
-      if (c.x >= 0) list[n + __popc(m & ((1u << lane) - 1u))] = c;
+#pragma unroll
+    for (int i = 0; i < kQ8MaxCtas / 32; ++i) {
+      const unsigned m = __ballot_sync(FULL, c[i].x >= 0);
+      if (c[i].x >= 0) list[n + __popc(m & ((1u << lane) - 1u))] = c[i];
       n += __popc(m);
     }
     if (lane == 0) cuts = n;
   }
   __syncthreads();
   const int tasks = cuts * HG * MR;
+  const int d = lane % LR * 4;
   for (int task = blockIdx.x + warp * gridDim.x; task < tasks; task += WARPS * gridDim.x) {
     const int row = task % MR, hl = task / MR % HG;
     const int4 c = list[task / MR / HG];
@@ -654,47 +707,66 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
     auto entry = [&](int b) {
       return p.parts + (((size_t)b * 2 + (b == c.y ? c.w : 0)) * HG + hl) * q8_entry_floats(D);
     };
-    float M = -INFINITY, L = 0.f, acc[DL];
+    float M = -INFINITY, L = 0.f, acc[DV][4];
 #pragma unroll
-    for (int k = 0; k < DL; ++k) acc[k] = 0.f;
-    for (int b0 = c.y; b0 <= c.z; b0 += U) {
-      float m[U], l[U], o[U][DL];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = b0 + u <= c.z;
-        const float* e = entry(in ? b0 + u : c.y);
-        m[u] = in ? __ldcg(e + row) : -INFINITY;
-        l[u] = __ldcg(e + kQ8Rows + row);
-#pragma unroll
-        for (int k = 0; k < DL; ++k)
-          o[u][k] = D >= 32 || lane < D ? __ldcg(e + 2 * kQ8Rows + row * D + lane + 32 * k) : 0.f;
+    for (int v = 0; v < DV; ++v) acc[v][0] = acc[v][1] = acc[v][2] = acc[v][3] = 0.f;
+    for (int b0 = c.y; b0 <= c.z; b0 += 32) {
+      const int n = min(32, c.z - b0 + 1);
+      float m = -INFINITY, l = 0.f;
+      if (lane < n) {
+        const float* e = entry(b0 + lane);
+        m = __ldcg(e + row);
+        l = __ldcg(e + kQ8Rows + row);
       }
-      float mx = M;
+      float mx = m;
 #pragma unroll
-      for (int u = 0; u < U; ++u) mx = fmaxf(mx, m[u]);
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+      mx = fmaxf(mx, M);
       const float ref = mx == -INFINITY ? 0.f : mx;
-      const float f = ex2(M - ref);
-      L *= f;
-#pragma unroll
-      for (int k = 0; k < DL; ++k) acc[k] *= f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float a = ex2(m[u] - ref);
-        L = fmaf(a, l[u], L);
-#pragma unroll
-        for (int k = 0; k < DL; ++k) acc[k] = fmaf(a, o[u][k], acc[k]);
-      }
+      const float f = ex2(M - ref), a = ex2(m - ref);
       M = mx;
+      float sum = a * l;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+      L = fmaf(L, f, sum);
+#pragma unroll
+      for (int v = 0; v < DV; ++v) {
+        acc[v][0] *= f;
+        acc[v][1] *= f;
+        acc[v][2] *= f;
+        acc[v][3] *= f;
+      }
+      for (int u0 = 0; u0 < n; u0 += U) {
+        float4 x[U][DV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float* e = entry(b0 + min(u0 + u, n - 1)) + 2 * kQ8Rows + row * D + d;
+#pragma unroll
+          for (int v = 0; v < DV; ++v) x[u][v] = __ldcg(reinterpret_cast<const float4*>(e + 128 * v));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float g = u0 + u < n ? __shfl_sync(FULL, a, (u0 + u) & 31) : 0.f;
+#pragma unroll
+          for (int v = 0; v < DV; ++v) {
+            acc[v][0] = fmaf(g, x[u][v].x, acc[v][0]);
+            acc[v][1] = fmaf(g, x[u][v].y, acc[v][1]);
+            acc[v][2] = fmaf(g, x[u][v].z, acc[v][2]);
+            acc[v][3] = fmaf(g, x[u][v].w, acc[v][3]);
+          }
+        }
+      }
     }
+    if (lane >= LR) continue;  // (narrow heads: the other lanes repeat)
     const float inv = L > 0.f ? 1.f / L : 0.f;
     const int qi = row / p.group, h = row - qi * p.group;
-    T* out = static_cast<T*>(p.out) +
-             ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
-    if (D < 32 && lane >= D) continue;
+    T* out = static_cast<T*>(p.out) + ((int64_t)(qr.q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
 #pragma unroll
-    for (int k = 0; k < DL; ++k) {
-      const float y = acc[k] * inv;
-      Storage<T>::template store<1>(out + lane + 32 * k, &y);
+    for (int v = 0; v < DV; ++v) {
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = acc[v][e] * inv;
+      Storage<T>::template store<4>(out + d + 128 * v, y);
     }
   }
 }

@@ -404,7 +404,10 @@ extern "C" np_status np_paged_prefill_q8_packed(const np_read_q8_args* a) {
   // Rows with few tokens go to the decode read's kernel: their (token, head) rows fit
   // one fetch of its tile.  Two launches more, so where rows are short on average.
   const int few = (p.group <= 8 ? 8 : 16) / p.group;
-  if (p.rows > 1 ? p.tokens < 64ll * p.rows : p.tokens <= few) {
+  int64_t work = 0;
+  if ((p.rows > 1 ? p.tokens < 64ll * p.rows : p.tokens <= few) &&
+      mul_ok((int64_t)p.rows * p.kv_heads, (int64_t)p.max_blocks_per_row * p.block_size, &work) &&
+      work <= npk::kQ8MaxWork) {
     p.skip_tokens = few;
     npk::DecodeQ8Params d{};
     d.out = p.out;

@@ -139,6 +139,7 @@ def test_read_refusals(lib, call):
         assert read(ql=9) == 2                          # 18 rows
         assert read(ql=5, dtype=0) == 2
         assert read(rows=65536) == 2
+        assert read(rows=60000, mb=2**26, bs=16) == 2   # more positions than a block can count
 
 
 def test_workspaces(lib):
