@@ -417,7 +417,7 @@ np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
  * Slots past a row's context are never part of a result.  Supported: dtype
  * NP_F32 (g * query_len <= 8) or NP_BF16 (<= 16), g = q_heads / kv_heads; head_dim
  * of the list above; any block_size; any kv_heads; rows up to 65535; tables of up to
- * 2^31 - 1025 tokens, and rows * kv_heads * a table's tokens up to 2^40.  A row without history gets zeros.  rows 0: a no-op.
+ * 2^31 - 1025 tokens, and rows * kv_heads * a table's tokens up to 2^34.  A row without history gets zeros.  rows 0: a no-op.
  */
 size_t np_paged_decode_q8_workspace_bytes(int32_t head_dim);
 /* enough for every head_dim */

@@ -114,12 +114,6 @@ __device__ __forceinline__ int32_t q8_len(const DecodeQ8Params& p, int r) {
   return c < 0 ? 0 : (c > cap ? (int32_t)cap : c);
 }
 
-// a / b for a >= 0, b > 0: a 64-bit division takes several times a 32-bit one
-__device__ __forceinline__ int64_t q8_div(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
 // A block's walk over its share, by each of its warps: segment by segment (a run of
 // one row's chunks), in each the chunks that are this warp's.
 template <int CT>
@@ -178,16 +172,22 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   const int hl = warp % HG, wi = warp / HG;     // kv head of the group, warp of the head
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this block's share: chunks [u0, u1) of all rows' chunks, which each thread
-  // counts for a run of rows
-  __shared__ int64_t warp_sum[WARPS];
+  // ---- this block's share: chunks [u0, u1) of all rows' chunks (W, < 2^31), which each
+  // thread counts for a run of rows.  (What runs once is fetched once, from L2: it is
+  // kept short, 32-bit and rolled.)
+  __shared__ int warp_sum[WARPS];
   __shared__ int last_stage[WARPS];
-  __shared__ int64_t found[6];  // first row, first chunk, chunks; W, Pe, u0
+  __shared__ int found[3];  // the first chunk's kv head group, row, place in the row
+  int W, Pe, each, over;
+  // floor(b W / Pe), Pe <= 160
+  auto start_of = [&](int b) { return b < Pe ? each * b + over * b / Pe : W; };
   {
     const int per = (p.rows + 32 * WARPS - 1) / (32 * WARPS);
     const int ra = min(p.rows, (int)threadIdx.x * per), rb = min(p.rows, ra + per);
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
-    int64_t own = 0;
+    int own = 0;
+    bool empty = false;
+#pragma unroll 1
     for (int r = ra; r < rb; ++r) {
       const int32_t c = p.lens[r];
       if (blockIdx.x == 0) {
@@ -197,67 +197,57 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           if (a < 0 || b < a || b > p.tokens) set_flag(p.err, NP_FLAG_QUERY);
         }
       }
-      own += (q8_len(p, r) + CT - 1) / CT;
+      const int n = (q8_len(p, r) + CT - 1) / CT;
+      own += n;
+      empty |= n == 0;
     }
-    int64_t x = own;
+    int x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(FULL, x, o);
+      const int y = __shfl_up_sync(FULL, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    int64_t before = x - own, all = 0;
+    if (__syncthreads_or(empty)) {  // rows without history: zeros
+#pragma unroll 1
+      for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        if (q8_len(p, r) != 0) continue;
+        const Q8Row qr = q8_row(p, r);
+        T* o = static_cast<T*>(p.out) + (int64_t)qr.q0 * p.q_heads * D;
+        for (int i = threadIdx.x; i < qr.n * p.q_heads * D; i += 32 * WARPS) o[i] = T(0.f);
+      }
+    }
+    int before = x - own, all = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       if (w < warp) before += warp_sum[w];
       all += warp_sum[w];
     }
-    const int64_t W = all * (p.kv_heads / HG);
-    const int64_t want = q8_div(W + p.least - 1, p.least);
-    const int64_t Pe = want < 1 ? 1 : min(want, (int64_t)gridDim.x);
-    const int b = blockIdx.x;
-    // floor(b W / Pe), Pe <= 160
-    const int64_t each = q8_div(W, Pe);
-    const int over = (int)(W - each * Pe);
-    const int64_t u0 = b < Pe ? each * b + (uint32_t)(over * b) / (uint32_t)Pe : W;
-    const int64_t u1 = b < Pe ? each * (b + 1) + (uint32_t)(over * (b + 1)) / (uint32_t)Pe : W;
-    if (threadIdx.x == 0) {
-      found[0] = 0;
-      found[1] = 0;
-      found[2] = u1 - u0;
-      found[3] = W;
-      found[4] = Pe;
-      found[5] = u0;
-    }
-    __syncthreads();
-    if (u1 > u0) {
-      const int64_t lap = q8_div(u0, all), at = u0 - lap * all;
-      if (own > 0 && before <= at && at < before + own) {  // one thread's
-        int64_t run = before;
-        int r = ra;
+    W = all * (p.kv_heads / HG);
+    Pe = max(1, min((W + p.least - 1) / p.least, (int)gridDim.x));
+    each = W / Pe;
+    over = W - each * Pe;
+    const int u0 = start_of(blockIdx.x);
+    if (u0 < W) {
+      const int lap = u0 / all, at = u0 - lap * all;
+      if (before <= at && at < before + own) {  // one thread's
+        int run = before, r = ra;
+#pragma unroll 1
         for (;; ++r) {
-          const int64_t n = (q8_len(p, r) + CT - 1) / CT;
+          const int n = (q8_len(p, r) + CT - 1) / CT;
           if (at < run + n) break;
           run += n;
         }
-        found[0] = r + lap * p.rows;
-        found[1] = at - run;
+        found[0] = lap;
+        found[1] = r;
+        found[2] = at - run;
       }
     }
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);  // (unless its last row is cut, below)
     __syncthreads();
-    if (threadIdx.x == 0) p.cuts[b] = make_int4(-1, 0, 0, 0);  // (unless its last row is cut, below)
   }
-  const int32_t chunks = (int32_t)found[2];  // (the host bounds them)
-  const int64_t v0 = found[0];
-
-  // rows without history
-  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    if (q8_len(p, r) != 0) continue;
-    const Q8Row qr = q8_row(p, r);
-    T* o = static_cast<T*>(p.out) + (int64_t)qr.q0 * p.q_heads * D;
-    for (int64_t i = threadIdx.x; i < (int64_t)qr.n * p.q_heads * D; i += 32 * WARPS) o[i] = T(0.f);
-  }
+  const int u0 = start_of(blockIdx.x);
+  const int32_t chunks = start_of(blockIdx.x + 1) - u0;
   if (wi >= WPH || chunks == 0) return;  // (warps beyond the heads' have nothing to do)
 
   unsigned char* ring = q8_smem + (size_t)warp * NS * Geo::STAGE;
@@ -265,10 +255,11 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   // ---- q of a segment, as it is stored: column n of tile nt is row n + 8 nt of the head's
   // (query token, head) rows; a lane holds dims 16 (piece) + 4 word .. + 3 of column g
   Q8Walk<CT> w;
-  w.start(p, (int)(v0 / p.rows), (int)(v0 % p.rows), (int32_t)found[1], chunks);
+  w.start(p, found[0], found[1], found[2], chunks);
+  // (in the registers of O, which hold nothing then)
   using Raw = typename std::conditional<F32, uint4, uint2>::type;  // 4 elements
-  Raw raw[NT][KJ * KW];
-  Q8Row qr;
+  float o[NT][D / 16][4];
+  Q8Row qr{0, 0};
   auto load_q = [&]() {
     qr = q8_row(p, w.r);
     const int kvh = w.hgi * HG + hl;
@@ -286,11 +277,19 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           const int d = D >= 128 ? 16 * (2 * t4 + (j & 1) + 8 * (j >> 1)) + 4 * k : t4 * (4 * KW) + 4 * k;
           Raw x = {};
           if (on) x = *reinterpret_cast<const Raw*>(src + d);
-          raw[nt][j * KW + k] = x;
+          const int i = j * KW + k;
+          if constexpr (F32) {
+            o[nt][i][0] = __uint_as_float(x.x);
+            o[nt][i][1] = __uint_as_float(x.y);
+            o[nt][i][2] = __uint_as_float(x.z);
+            o[nt][i][3] = __uint_as_float(x.w);
+          } else {
+            o[nt][i / 2][i % 2 * 2] = __uint_as_float(x.x);
+            o[nt][i / 2][i % 2 * 2 + 1] = __uint_as_float(x.y);
+          }
         }
     }
   };
-  load_q();  // (on its way while the first chunks are looked up)
 
   // ---- loads: chunk by chunk ahead of the reads.  Lane i < CT looks after token i.  Its
   // block is looked up two chunks before the copies.
@@ -345,25 +344,20 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
     }
     cp_async_commit();
   };
-  Ahead a0 = look_up(), a1 = look_up();
-#pragma unroll 1
-  for (int s = 0; s < NS - 1; ++s) {
-    const Ahead a2 = look_up();
-    issue(s, a0);
-    a0 = a1;
-    a1 = a2;
-  }
-
-  // ---- reads
-  int32_t cg = wi;  // this warp's next chunk
-  int slot = 0;     // its stage
+  Ahead a0{0, -1, -1}, a1{0, -1, -1};
+  int32_t cg = wi;        // this warp's next chunk
+  int slot = 0;           // its stage
+  uint32_t qf[NT][PARTS][KJ * KW][2];
+  float qs[NT][2];        // scale of rows 2 t4, + 1
+  int32_t lim[NT][2];     // the first position each does not see
+  int32_t all_see = 0;    // positions before it: every row
+  float m[NT][2], l[NT][2];
+  int last = -1;          // the stage read last in this segment; -1: none yet
   bool first = true;
-  while (w.live()) {
-    const int kvh = w.hgi * HG + hl;
+
+  // q to fp16, sums to zero
+  auto begin = [&]() {
     const int rows_used = p.group * qr.n;  // MR at most
-    uint32_t qf[NT][PARTS][KJ * KW][2];
-    float qs[NT][2];  // scale of rows 2 t4, + 1
-    int32_t lim[NT][2];  // the first position each does not see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool on = nt * 8 + g < rows_used;
@@ -371,7 +365,13 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       float big = 0.f;
 #pragma unroll
       for (int i = 0; i < KJ * KW; ++i) {
-        Storage<T>::template load<4>(reinterpret_cast<const T*>(&raw[nt][i]), x[i]);
+        if constexpr (F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = o[nt][i][e];
+        } else {
+          widen_bf16x2(__float_as_uint(o[nt][i / 2][i % 2 * 2]), x[i][0], x[i][1]);
+          widen_bf16x2(__float_as_uint(o[nt][i / 2][i % 2 * 2 + 1]), x[i][2], x[i][3]);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[i][e]));
       }
@@ -397,8 +397,6 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         lim[nt][c] = row2 < rows_used ? w.c - qr.n + row2 / p.group + 1 : w.c;
       }
     }
-    float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -408,9 +406,126 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    int last = -1;  // the stage read last in this segment
-    const int32_t all_see = w.c - qr.n + 1;  // positions before it: every row
+    all_see = w.c - qr.n + 1;
+  };
 
+  // The segment's end: each of the head's warps puts m, l and O into the stage it read
+  // last (which nothing is on its way into), then each joins some of the rows.
+  auto finish = [&]() {
+    const Q8Row now = q8_row(p, w.r);
+    const int32_t q0 = now.q0, kvh = w.hgi * HG + hl, rows_used = p.group * now.n;
+    __syncwarp();
+    if (last >= 0) {
+      float* e = reinterpret_cast<float*>(ring + (size_t)last * Geo::STAGE);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = l[nt][c];
+          x += __shfl_xor_sync(FULL, x, 4);
+          x += __shfl_xor_sync(FULL, x, 8);
+          x += __shfl_xor_sync(FULL, x, 16);
+          const int row = nt * 8 + 2 * t4 + c;
+          if (g == 0) {
+            e[row] = m[nt][c];
+            e[MR + row] = x;
+          }
+          float* orow = e + 2 * MR + row * LD;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int j = i / (VB / 2), d = j * 128 + g * VB + 2 * (i % (VB / 2));
+            *reinterpret_cast<float2*>(orow + d) = make_float2(o[nt][i][c], o[nt][i][2 + c]);
+          }
+        }
+    }
+    if (lane == 0) last_stage[warp] = last;
+    const bool whole = w.c0 == 0 && w.g1 - w.g0 >= (w.c + CT - 1) / CT;
+    if (threadIdx.x == 0 && w.g1 == w.total && w.c0 == 0 && !whole) {
+      // The share ends in this row, which begins here: it is cut, and its last block is the
+      // one with its last chunk.
+      const int end = u0 + w.g0 + (w.c + CT - 1) / CT;
+      int to = min((int)((float)end * (float)Pe / (float)W), Pe - 1);
+      while (to + 1 < Pe && start_of(to + 1) < end) ++to;
+      while (start_of(to) >= end) --to;
+      p.cuts[blockIdx.x] = make_int4(w.hgi * p.rows + w.r, blockIdx.x, to, first ? 0 : 1);
+    }
+    w.next(p);
+    if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
+    else __syncwarp();
+    {
+      float* part = p.parts + (((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * HG + hl) * q8_entry_floats(D);
+      // lane i: the stage that warp i of the head read last, -1: it had no chunk here
+      int at = -1;
+      if (lane < WPH) {
+        const int wr = hl + lane * HG, st = last_stage[wr];
+        at = st < 0 ? -1 : (wr * NS + st) * Geo::STAGE;
+      }
+      const unsigned has = __ballot_sync(FULL, at >= 0);
+      // lane r: row r's maximum and sum
+      float M = -INFINITY, L = 0.f;
+      const int mine = lane < MR ? lane : 0;
+      for (unsigned k = has; k != 0; k &= k - 1) {
+        const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
+        const float mx = fmaxf(M, e[mine]), ref = mx == -INFINITY ? 0.f : mx;
+        L = fmaf(ex2(e[mine] - ref), e[MR + mine], L * ex2(M - ref));
+        M = mx;
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      if (!whole && wi == 0 && lane < rows_used) {
+        part[lane] = M;
+        part[kQ8Rows + lane] = L;
+      }
+      // rows in turn over the head's warps, LR lanes a row, 4 (or 2 x 4) dims a lane
+      constexpr int LR = D >= 128 ? 32 : D / 4, RP = 32 / LR, DV = D == 256 ? 2 : 1;
+      for (int r0 = wi * RP; r0 < rows_used; r0 += WPH * RP) {
+        const int row = min(r0 + lane / LR, MR - 1), d = lane % LR * 4;
+        const float Mr = __shfl_sync(FULL, M, row), f0 = whole ? __shfl_sync(FULL, inv, row) : 1.f;
+        const float ref = Mr == -INFINITY ? 0.f : Mr;
+        float acc[DV][4];
+#pragma unroll
+        for (int v = 0; v < DV; ++v) acc[v][0] = acc[v][1] = acc[v][2] = acc[v][3] = 0.f;
+        for (unsigned k = has; k != 0; k &= k - 1) {
+          const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
+          const float f = ex2(e[row] - ref) * f0;
+#pragma unroll
+          for (int v = 0; v < DV; ++v) {
+            const float4 x = *reinterpret_cast<const float4*>(e + 2 * MR + row * LD + d + 128 * v);
+            acc[v][0] = fmaf(f, x.x, acc[v][0]);
+            acc[v][1] = fmaf(f, x.y, acc[v][1]);
+            acc[v][2] = fmaf(f, x.z, acc[v][2]);
+            acc[v][3] = fmaf(f, x.w, acc[v][3]);
+          }
+        }
+        if (r0 + lane / LR >= rows_used) continue;
+        if (whole) {
+          const int qi = row / p.group, h = row - qi * p.group;
+          T* out = static_cast<T*>(p.out) +
+                   ((int64_t)(q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
+#pragma unroll
+          for (int v = 0; v < DV; ++v) Storage<T>::template store<4>(out + d + 128 * v, acc[v]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < DV; ++v)
+            Storage<float>::store<4>(part + 2 * kQ8Rows + row * D + d + 128 * v, acc[v]);
+        }
+      }
+    }
+    if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
+    else __syncwarp();
+    first = false;
+    last = -1;
+  };
+
+  load_q();  // (on its way while the first chunks are looked up)
+#pragma unroll 1
+  for (int it = -2; it < NS - 1; ++it) {
+    const Ahead a2 = look_up();
+    if (it >= 0) issue(it, a0);
+    a0 = a1;
+    a1 = a2;
+  }
+  while (w.live()) {
+    begin();
     for (; cg < w.g1; cg += WPH) {
       cp_async_wait<NS - 2>();
       __syncwarp();
@@ -559,108 +674,8 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         }
       }
     }
-
-    // ---- the segment's end: each of the head's warps puts m, l and O into the stage it
-    // read last (which nothing is on its way into), then each joins some of the rows
-    __syncwarp();
-    if (last >= 0) {
-      float* e = reinterpret_cast<float*>(ring + (size_t)last * Geo::STAGE);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x = l[nt][c];
-          x += __shfl_xor_sync(FULL, x, 4);
-          x += __shfl_xor_sync(FULL, x, 8);
-          x += __shfl_xor_sync(FULL, x, 16);
-          const int row = nt * 8 + 2 * t4 + c;
-          if (g == 0) {
-            e[row] = m[nt][c];
-            e[MR + row] = x;
-          }
-          float* orow = e + 2 * MR + row * LD;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const int j = i / (VB / 2), d = j * 128 + g * VB + 2 * (i % (VB / 2));
-            *reinterpret_cast<float2*>(orow + d) = make_float2(o[nt][i][c], o[nt][i][2 + c]);
-          }
-        }
-    }
-    if (lane == 0) last_stage[warp] = last;
-    const bool whole = w.c0 == 0 && w.g1 - w.g0 >= (w.c + CT - 1) / CT;
-    const int32_t q0 = qr.q0;
-    if (threadIdx.x == 0 && w.g1 == w.total && w.c0 == 0 && !whole) {
-      // The share ends in this row, which begins here: it is cut, and its last block is the
-      // one with its last chunk.
-      const int64_t end = found[5] + w.g0 + (w.c + CT - 1) / CT;
-      p.cuts[blockIdx.x] = make_int4(w.hgi * p.rows + w.r, blockIdx.x,
-                                     (int)q8_div(end * found[4] - 1, found[3]), first ? 0 : 1);
-    }
-    w.next(p);
-    if (w.live()) load_q();  // the next segment's, on its way meanwhile
-    if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
-    else __syncwarp();
-    {
-      float* part = p.parts + (((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * HG + hl) * q8_entry_floats(D);
-      // lane i: the stage that warp i of the head read last, -1: it had no chunk here
-      int at = -1;
-      if (lane < WPH) {
-        const int wr = hl + lane * HG, st = last_stage[wr];
-        at = st < 0 ? -1 : (wr * NS + st) * Geo::STAGE;
-      }
-      const unsigned has = __ballot_sync(FULL, at >= 0);
-      // lane r: row r's maximum and sum
-      float M = -INFINITY, L = 0.f;
-      const int mine = lane < MR ? lane : 0;
-      for (unsigned k = has; k != 0; k &= k - 1) {
-        const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
-        const float mx = fmaxf(M, e[mine]), ref = mx == -INFINITY ? 0.f : mx;
-        L = fmaf(ex2(e[mine] - ref), e[MR + mine], L * ex2(M - ref));
-        M = mx;
-      }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      if (!whole && wi == 0 && lane < rows_used) {
-        part[lane] = M;
-        part[kQ8Rows + lane] = L;
-      }
-      // rows in turn over the head's warps, LR lanes a row, 4 (or 2 x 4) dims a lane
-      constexpr int LR = D >= 128 ? 32 : D / 4, RP = 32 / LR, DV = D == 256 ? 2 : 1;
-      for (int r0 = wi * RP; r0 < rows_used; r0 += WPH * RP) {
-        const int row = min(r0 + lane / LR, MR - 1), d = lane % LR * 4;
-        const float Mr = __shfl_sync(FULL, M, row), f0 = whole ? __shfl_sync(FULL, inv, row) : 1.f;
-        const float ref = Mr == -INFINITY ? 0.f : Mr;
-        float acc[DV][4];
-#pragma unroll
-        for (int v = 0; v < DV; ++v) acc[v][0] = acc[v][1] = acc[v][2] = acc[v][3] = 0.f;
-        for (unsigned k = has; k != 0; k &= k - 1) {
-          const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
-          const float f = ex2(e[row] - ref) * f0;
-#pragma unroll
-          for (int v = 0; v < DV; ++v) {
-            const float4 x = *reinterpret_cast<const float4*>(e + 2 * MR + row * LD + d + 128 * v);
-            acc[v][0] = fmaf(f, x.x, acc[v][0]);
-            acc[v][1] = fmaf(f, x.y, acc[v][1]);
-            acc[v][2] = fmaf(f, x.z, acc[v][2]);
-            acc[v][3] = fmaf(f, x.w, acc[v][3]);
-          }
-        }
-        if (r0 + lane / LR >= rows_used) continue;
-        if (whole) {
-          const int qi = row / p.group, h = row - qi * p.group;
-          T* out = static_cast<T*>(p.out) +
-                   ((int64_t)(q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
-#pragma unroll
-          for (int v = 0; v < DV; ++v) Storage<T>::template store<4>(out + d + 128 * v, acc[v]);
-        } else {
-#pragma unroll
-          for (int v = 0; v < DV; ++v)
-            Storage<float>::store<4>(part + 2 * kQ8Rows + row * D + d + 128 * v, acc[v]);
-        }
-      }
-    }
-    if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
-    else __syncwarp();
-    first = false;
+    finish();
+    if (w.live()) load_q();
   }
   cp_async_wait<0>();
 }

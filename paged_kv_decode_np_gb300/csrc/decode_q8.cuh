@@ -50,8 +50,8 @@ NPK_Q8_DECLARE(256)
 
 // The launches for a head_dim and form, after everything that they need but head_group,
 // least and ctas is in p (decode_q8_api.cu).
-// rows x table tokens x kv heads: a block's chunks of 16 tokens then fit an int32
-constexpr int64_t kQ8MaxWork = 1ll << 40;
+// rows x table tokens x kv heads: all rows' chunks of 16 tokens then are below 2^31
+constexpr int64_t kQ8MaxWork = 1ll << 34;
 np_status launch_decode_q8(DecodeQ8Params& p, int32_t head_dim, np_dtype dtype, np_form8 form, int sms,
                            cudaStream_t s);
 

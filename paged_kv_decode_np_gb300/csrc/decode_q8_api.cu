@@ -44,7 +44,7 @@ np_status check_decode_q8(const np_read_q8_args& a, bool* run) {
       !mul_fits((int64_t)a.rows * a.query_len, a.q_heads * d * es, &qn))
     return NP_ERR_OUT_OF_RANGE;
   if (a.rows > 65535 || cap > INT32_MAX - 1024) return NP_ERR_UNSUPPORTED;
-  // a row of the stream (row, group of kv heads) is an int32, and so are a block's chunks
+  // a row of the stream (row, group of kv heads) is an int32, and so are all their chunks
   int64_t work = 0;
   if ((int64_t)a.rows * a.kv_heads > INT32_MAX || !mul_fits((int64_t)a.rows * a.kv_heads, cap, &work) ||
       work > kQ8MaxWork)
