@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       p.cuts[blockIdx.x] = make_int4(w.hgi * p.rows + w.r, blockIdx.x, to, first ? 0 : 1);
     }
     w.next(p);
+    if (w.live()) load_q();  // the next segment's, on its way meanwhile
     if (WPH > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + hl), "r"(32 * WPH) : "memory");
     else __syncwarp();
     {
@@ -475,38 +476,56 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         part[lane] = M;
         part[kQ8Rows + lane] = L;
       }
-      // rows in turn over the head's warps, LR lanes a row, 4 (or 2 x 4) dims a lane
+      // rows in turn over the head's warps, LR lanes a row, 4 (or 2 x 4) dims a lane, RU rows
+      // of a lane side by side
       constexpr int LR = D >= 128 ? 32 : D / 4, RP = 32 / LR, DV = D == 256 ? 2 : 1;
-      for (int r0 = wi * RP; r0 < rows_used; r0 += WPH * RP) {
-        const int row = min(r0 + lane / LR, MR - 1), d = lane % LR * 4;
-        const float Mr = __shfl_sync(FULL, M, row), f0 = whole ? __shfl_sync(FULL, inv, row) : 1.f;
-        const float ref = Mr == -INFINITY ? 0.f : Mr;
-        float acc[DV][4];
+      constexpr int RU = D == 256 ? 2 : 4;
+      const int d = lane % LR * 4;
+#pragma unroll 1
+      for (int r0 = wi * RP + lane / LR; r0 - lane / LR < rows_used; r0 += RU * WPH * RP) {
+        float ref[RU], f0[RU], acc[RU][DV][4];
 #pragma unroll
-        for (int v = 0; v < DV; ++v) acc[v][0] = acc[v][1] = acc[v][2] = acc[v][3] = 0.f;
+        for (int u = 0; u < RU; ++u) {
+          const int row = min(r0 + u * WPH * RP, MR - 1);
+          const float Mr = __shfl_sync(FULL, M, row), iv = __shfl_sync(FULL, inv, row);
+          ref[u] = Mr == -INFINITY ? 0.f : Mr;
+          f0[u] = whole ? iv : 1.f;
+#pragma unroll
+          for (int v = 0; v < DV; ++v) acc[u][v][0] = acc[u][v][1] = acc[u][v][2] = acc[u][v][3] = 0.f;
+        }
+#pragma unroll 1
         for (unsigned k = has; k != 0; k &= k - 1) {
           const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
-          const float f = ex2(e[row] - ref) * f0;
 #pragma unroll
-          for (int v = 0; v < DV; ++v) {
-            const float4 x = *reinterpret_cast<const float4*>(e + 2 * MR + row * LD + d + 128 * v);
-            acc[v][0] = fmaf(f, x.x, acc[v][0]);
-            acc[v][1] = fmaf(f, x.y, acc[v][1]);
-            acc[v][2] = fmaf(f, x.z, acc[v][2]);
-            acc[v][3] = fmaf(f, x.w, acc[v][3]);
+          for (int u = 0; u < RU; ++u) {
+            const int row = min(r0 + u * WPH * RP, MR - 1);
+            const float f = ex2(e[row] - ref[u]) * f0[u];
+#pragma unroll
+            for (int v = 0; v < DV; ++v) {
+              const float4 x = *reinterpret_cast<const float4*>(e + 2 * MR + row * LD + d + 128 * v);
+              acc[u][v][0] = fmaf(f, x.x, acc[u][v][0]);
+              acc[u][v][1] = fmaf(f, x.y, acc[u][v][1]);
+              acc[u][v][2] = fmaf(f, x.z, acc[u][v][2]);
+              acc[u][v][3] = fmaf(f, x.w, acc[u][v][3]);
+            }
           }
         }
-        if (r0 + lane / LR >= rows_used) continue;
-        if (whole) {
-          const int qi = row / p.group, h = row - qi * p.group;
-          T* out = static_cast<T*>(p.out) +
-                   ((int64_t)(q0 + qi) * p.q_heads + (int64_t)kvh * p.group + h) * D;
 #pragma unroll
-          for (int v = 0; v < DV; ++v) Storage<T>::template store<4>(out + d + 128 * v, acc[v]);
-        } else {
+        for (int u = 0; u < RU; ++u) {
+          const int row = r0 + u * WPH * RP;
+          if (row >= rows_used) continue;
+          if (whole) {
+            // rows are the query tokens' heads of this kv head: a token's lie side by side
+            const int qi = row / p.group;
+            T* out = static_cast<T*>(p.out) +
+                     ((int64_t)(q0 + qi) * p.q_heads + (int64_t)(kvh - qi) * p.group + row) * D;
 #pragma unroll
-          for (int v = 0; v < DV; ++v)
-            Storage<float>::store<4>(part + 2 * kQ8Rows + row * D + d + 128 * v, acc[v]);
+            for (int v = 0; v < DV; ++v) Storage<T>::template store<4>(out + d + 128 * v, acc[u][v]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < DV; ++v)
+              Storage<float>::store<4>(part + 2 * kQ8Rows + row * D + d + 128 * v, acc[u][v]);
+          }
         }
       }
     }
@@ -541,7 +560,6 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       const int32_t t0 = (w.c0 + (cg - w.g0)) * CT;
 #pragma unroll
       for (int sub = 0; sub < CT; sub += 16) {
-        if (sub > 0 && t0 + sub >= w.c) break;  // uniform
         // ---- S
         float s[NT][4];
 #pragma unroll
@@ -675,7 +693,6 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       }
     }
     finish();
-    if (w.live()) load_q();
   }
   cp_async_wait<0>();
 }
@@ -684,6 +701,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
 // that hold a piece, in block order: 32 pieces' m and l in one round, then their rows of O,
 // eight loads in flight.  Bound by the latency of those rounds (the partials are in L2).
 constexpr int kQ8JoinThreads = 256;
+constexpr int kQ8JoinGrid = 4;  // blocks an SM
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __grid_constant__
@@ -733,6 +751,16 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
         m = __ldcg(e + row);
         l = __ldcg(e + kQ8Rows + row);
       }
+      float4 x[U][DV];
+      auto fetch = [&](int u0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float* e = entry(b0 + min(u0 + u, n - 1)) + 2 * kQ8Rows + row * D + d;
+#pragma unroll
+          for (int v = 0; v < DV; ++v) x[u][v] = __ldcg(reinterpret_cast<const float4*>(e + 128 * v));
+        }
+      };
+      fetch(0);  // (with m and l on their way)
       float mx = m;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
@@ -751,14 +779,9 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
         acc[v][2] *= f;
         acc[v][3] *= f;
       }
+#pragma unroll 1
       for (int u0 = 0; u0 < n; u0 += U) {
-        float4 x[U][DV];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float* e = entry(b0 + min(u0 + u, n - 1)) + 2 * kQ8Rows + row * D + d;
-#pragma unroll
-          for (int v = 0; v < DV; ++v) x[u][v] = __ldcg(reinterpret_cast<const float4*>(e + 128 * v));
-        }
+        if (u0 > 0) fetch(u0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float g = u0 + u < n ? __shfl_sync(FULL, a, (u0 + u) & 31) : 0.f;
@@ -794,7 +817,7 @@ static np_status launch(const DecodeQ8Params& p, cudaStream_t s) {
   if (rc != NP_OK) return rc;
   decode_q8_kernel<T, D, FORM, NT><<<p.ctas, 32 * Geo::WARPS, Geo::SMEM, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NP_ERR_CUDA;
-  return launch_dependent(decode_q8_join_kernel<T, D>, p.ctas, 1, kQ8JoinThreads, 0, s, p);
+  return launch_dependent(decode_q8_join_kernel<T, D>, kQ8JoinGrid * p.ctas, 1, kQ8JoinThreads, 0, s, p);
 }
 
 #define NPK_CAT2(a, b) a##b
