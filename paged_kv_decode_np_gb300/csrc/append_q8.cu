@@ -8,7 +8,7 @@
 //   older codes of the block: rne(code 2^(e_old - e')) where e' > e_old
 //   new codes: rne(x 2^-e')
 // One warp does that: it reads the run's values (a 16-byte vector a lane and
-// step), keeps them in registers where they fit (16 tokens of 128 bf16 dims),
+// step), keeps them in registers where they fit (32 tokens of 128 bf16 dims),
 // takes the maximum, and writes the codes.  No two warps touch the same block
 // and head, so there is nothing to wait for and nothing atomic.
 //
@@ -39,75 +39,111 @@ __device__ __forceinline__ int64_t block_of(const Append8Params& p, int64_t slot
                                      : slot / p.block_size;
 }
 
-template <typename T, int D, int FORM>
-__device__ __forceinline__ void append8_run(const Append8Params& p, int t0, int64_t blk, int h, int kv,
-                                            int lane) {
+// The largest |x| of a vector joins `top`, as bits (bf16: two at a time); what is not
+// finite is past any number.
+template <typename T>
+__device__ __forceinline__ uint32_t largest(uint32_t top, const uint4& r) {
+  for (uint32_t w : {r.x, r.y, r.z, r.w}) {
+    if constexpr (sizeof(T) == 2) top = __vmaxu2(top, w & 0x7fff7fffu);
+    else top = max(top, w & 0x7fffffffu);
+  }
+  return top;
+}
+
+template <typename T, int D, int FORM, int STEPS>
+__device__ __forceinline__ void append8_run(const Append8Params& p, int t0, int h, int kv, int lane) {
   constexpr unsigned FULL = 0xffffffffu;
   using F = Form8<FORM>;
   constexpr int V = 16 / (int)sizeof(T);         // values of a vector
-  constexpr int LT = D / V;                      // lanes of a token (1 to 64)
+  constexpr int LT = D / V;                      // lanes of a token (2 to 64)
   constexpr int PT = LT <= 32 ? 1 : LT / 32;     // vectors of a lane and token
   constexpr int TP = LT <= 32 ? 32 / LT : 1;     // tokens of a step
-  constexpr int U = 8 / PT;                      // steps whose values stay in registers
+  constexpr int U = STEPS / PT;                  // steps whose values stay in registers
   const int sub = LT <= 32 ? lane / LT : 0;
   const int col = (LT <= 32 ? lane % LT : lane) * V;
-
-  // the run's length, and whether it holds the block's first slot
-  int n = 0;
-  bool anew = false;
-  const int64_t first = blk * p.block_size;
-  for (int i0 = 0;; i0 += 32) {
-    const int64_t s = t0 + i0 + lane < p.tokens ? p.slots[t0 + i0 + lane] : -1;
-    const bool in = s >= first && s < first + p.block_size && s < p.num_slots;
-    const unsigned m = __ballot_sync(FULL, in);
-    const int run = m == FULL ? 32 : __ffs(~m) - 1;
-    anew |= __any_sync(FULL, in && lane < run && s == first);
-    n += run;
-    if (run < 32) break;
-  }
 
   const T* src = static_cast<const T*>(p.src[kv]) + (int64_t)h * D + col;
   const int64_t stride = p.stride[kv];
   uint4 held[U][PT];
-  uint32_t top = 0;  // the largest |x| that is finite, as bits
-  bool odd = false;
-  auto load = [&](int i, uint4* r) {  // token i + sub of the run
+  auto load = [&](int i, int n, uint4* r) {  // token i + sub, of n
 #pragma unroll
     for (int k = 0; k < PT; ++k)
       r[k] = i + sub < n
                  ? *reinterpret_cast<const uint4*>(src + (t0 + i + sub) * stride + k * 32 * V)
                  : make_uint4(0u, 0u, 0u, 0u);
   };
+  load(0, p.tokens - t0, held[0]);  // (before it is known whose they are)
+
+  // the run's length, and whether it holds the block's first slot
+  const int64_t blk = block_of(p, p.slots[t0]), start = blk * p.block_size;
+  float* sp = p.scale[kv] + blk * p.kv_heads + h;
+  const int e_old = scale_exp(__float_as_uint(*sp));
+  int n = 0;
+  bool anew = false;
+#pragma unroll 1
+  for (int i0 = 0;; i0 += 32) {
+    const int64_t s = t0 + i0 + lane < p.tokens ? p.slots[t0 + i0 + lane] : -1;
+    const bool in = s >= start && s < start + p.block_size && s < p.num_slots;
+    const unsigned m = __ballot_sync(FULL, in);
+    const int run = m == FULL ? 32 : __ffs(~m) - 1;
+    anew |= __any_sync(FULL, in && lane < run && s == start);
+    n += run;
+    if (run < 32) break;
+  }
+#pragma unroll
+  for (int u = 1; u < U; ++u)
+    if (u * TP < n) load(u * TP, n, held[u]);
+  if (sub >= n) {
+#pragma unroll
+    for (int k = 0; k < PT; ++k) held[0][k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u * TP < n) {
+#pragma unroll
+      for (int k = 0; k < PT; ++k) top = largest<T>(top, held[u][k]);
+    }
+  // (runs that do not fit are read in batches, and again for their codes: from L2)
+  auto batches = [&](auto use) {
+#pragma unroll 1
+    for (int i = U * TP; i < n; i += 4 * TP) {
+      uint4 r[4][PT];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load(i + u * TP, n, r[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) use(i + u * TP, r[u]);
+    }
+  };
+  batches([&](int, const uint4* r) {
+#pragma unroll
+    for (int k = 0; k < PT; ++k) top = largest<T>(top, r[k]);
+  });
+  if constexpr (sizeof(T) == 2) top = max(top << 16, top & 0xffff0000u);
+  top = __reduce_max_sync(FULL, top);
   auto widen = [&](const uint4& r, float* x) {
     Storage<T>::template load<V>(reinterpret_cast<const T*>(&r), x);
   };
-  auto look = [&](const uint4& r) {
-    float x[V];
-    widen(r, x);
+  if (top >= 0x7f800000u) {  // something is not finite: the largest of what is
+    if (lane == 0) set_flag(p.err, NP_FLAG_VALUE);
+    top = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; i += TP) {
+      uint4 r[PT];
+      load(i, n, r);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
-      if (a >= 0x7f800000u) odd = true;
-      else top = max(top, a);
+      for (int k = 0; k < PT; ++k) {
+        float x[V];
+        widen(r[k], x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
+          if (a < 0x7f800000u) top = max(top, a);
+        }
+      }
     }
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u) load(u * TP, held[u]);
-  // the scale found, on its way meanwhile
-  float* sp = p.scale[kv] + blk * p.kv_heads + h;
-  const int e_old = scale_exp(__float_as_uint(*sp));
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int k = 0; k < PT; ++k) look(held[u][k]);
-  for (int i = U * TP; i < n; i += TP) {
-    uint4 r[PT];
-    load(i, r);
-#pragma unroll
-    for (int k = 0; k < PT; ++k) look(r[k]);
+    top = __reduce_max_sync(FULL, top);
   }
-  top = __reduce_max_sync(FULL, top);
-  if (odd) set_flag(p.err, NP_FLAG_VALUE);
   int e = top < 0x00800000u ? kScaleMin : min(max(F::need(top), kScaleMin), kScaleMax);
   if (!anew) e = max(e, e_old);
 
@@ -116,12 +152,12 @@ __device__ __forceinline__ void append8_run(const Append8Params& p, int t0, int6
   if (!anew && e > e_old) {
     // the codes of the block's other slots, to the new scale
     const float f = pow2f(max(e_old - e, -126));
+#pragma unroll 1
     for (int o = 0; o < p.block_size; ++o) {
-      if (first + o >= p.num_slots) break;
       bool mine = false;  // written by this run
-      for (int i = lane; i < n; i += 32) mine |= p.slots[t0 + i] == first + o;
+      for (int i = lane; i < n; i += 32) mine |= p.slots[t0 + i] == start + o;
       if (__any_sync(FULL, mine)) continue;
-      uint8_t* at = pool + (first + o) * row;
+      uint8_t* at = pool + (start + o) * row;
       for (int d = 4 * lane; d < D; d += 128) {
         float x[4];
         widen8x4<FORM>(*reinterpret_cast<const uint32_t*>(at + d), x);
@@ -149,50 +185,37 @@ __device__ __forceinline__ void append8_run(const Append8Params& p, int t0, int6
     }
   };
 #pragma unroll
-  for (int u = 0; u < U; ++u) store(u * TP, held[u]);
-  for (int i = U * TP; i < n; i += TP) {
-    uint4 r[PT];
-    load(i, r);
-    store(i, r);
-  }
+  for (int u = 0; u < U; ++u)
+    if (u * TP < n) store(u * TP, held[u]);
+  batches(store);
 }
 
-template <typename T, int D, int FORM>
-__global__ void __launch_bounds__(32 * kAppend8Warps) append8_kernel(const __grid_constant__
+template <typename T, int D, int FORM, int STEPS>
+__global__ void __launch_bounds__(32 * kAppend8Warps, STEPS == 16 ? 2 : STEPS == 8 ? 3 : 4) append8_kernel(const __grid_constant__
                                                                      Append8Params p) {
-  __shared__ int64_t run_block[32];
-  __shared__ int run_token[32];
-  __shared__ int runs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w0 = blockIdx.x * p.window;  // this block's tokens
-  if (warp == 0) {
-    const int t = w0 + lane;
-    const bool live = lane < p.window && t < p.tokens;
-    const int64_t s = live ? p.slots[t] : -1;
-    const int64_t before = live && t > 0 ? p.slots[t - 1] : -1;
-    if (s >= p.num_slots && blockIdx.y == 0) set_flag(p.err, NP_FLAG_SLOT);
-    const bool in = s >= 0 && s < p.num_slots;
-    const int64_t b = in ? block_of(p, s) : -1;
-    const bool joined = before >= 0 && before < p.num_slots && block_of(p, before) == b;
-    const bool lead = in && !joined;
-    const unsigned m = __ballot_sync(0xffffffffu, lead);
-    if (lead) {
-      const int k = __popc(m & ((1u << lane) - 1u));
-      run_block[k] = b;
-      run_token[k] = t;
-    }
-    if (lane == 0) runs = __popc(m);
-  }
-  __syncthreads();
-  const int tasks = runs * 2 * p.kv_heads;
-  for (int i = blockIdx.y * kAppend8Warps + warp; i < tasks; i += gridDim.y * kAppend8Warps) {
+  // which of this block's tokens begin a run: every warp looks for itself
+  const int t = blockIdx.x * p.window + lane;
+  const bool live = lane < p.window && t < p.tokens;
+  const int64_t s = live ? p.slots[t] : -1;
+  const int64_t before = live && t > 0 ? p.slots[t - 1] : -1;
+  if (s >= p.num_slots && blockIdx.y == 0 && warp == 0) set_flag(p.err, NP_FLAG_SLOT);
+  const bool in = s >= 0 && s < p.num_slots;
+  const bool joined = before >= 0 && before < p.num_slots && in && block_of(p, before) == block_of(p, s);
+  unsigned leads = __ballot_sync(0xffffffffu, in && !joined);
+  const int per = 2 * p.kv_heads, step = gridDim.y * kAppend8Warps;
+  const int tasks = __popc(leads) * per;
+  int at = 0;  // the run of the lowest bit of `leads`
+  for (int i = blockIdx.y * kAppend8Warps + warp; i < tasks; i += step) {
+    const int x = i / per, rest = i - x * per;
+    for (; at < x; ++at) leads &= leads - 1;
     // neighbouring warps: neighbouring heads of the same tokens
-    const int h = i % p.kv_heads, x = i / p.kv_heads;
-    append8_run<T, D, FORM>(p, run_token[x >> 1], run_block[x >> 1], h, x & 1, lane);
+    const int kv = rest >= p.kv_heads ? 1 : 0;
+    append8_run<T, D, FORM, STEPS>(p, blockIdx.x * p.window + __ffs(leads) - 1, rest - kv * p.kv_heads, kv, lane);
   }
 }
 
-template <typename T, int D, int FORM>
+template <typename T, int D, int FORM, int STEPS>
 static np_status launch_append8(Append8Params& p, cudaStream_t s) {
   // few tokens: few of them a block, so that all warps find work
   p.window = p.tokens >= 4096 ? 32 : p.tokens >= 512 ? 8 : 1;
@@ -200,18 +223,27 @@ static np_status launch_append8(Append8Params& p, cudaStream_t s) {
   const int tasks = 2 * p.kv_heads;  // of one run
   unsigned y = (unsigned)((tasks + kAppend8Warps - 1) / kAppend8Warps);
   if (y > 64) y = 64;
-  append8_kernel<T, D, FORM><<<dim3(x, y), 32 * kAppend8Warps, 0, s>>>(p);
+  append8_kernel<T, D, FORM, STEPS><<<dim3(x, y), 32 * kAppend8Warps, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? NP_OK : NP_ERR_CUDA;
+}
+
+// How many steps of a run's values stay in registers: those of a whole block, 8 or 16;
+// few tokens (decode batches) are mostly runs of one.
+template <typename T, int D, int FORM>
+static np_status launch_append8_steps(Append8Params& p, cudaStream_t s) {
+  if (p.tokens < 512) return launch_append8<T, D, FORM, 2>(p, s);
+  return (int64_t)p.block_size * D * (int)sizeof(T) > 8 * 512 ? launch_append8<T, D, FORM, 16>(p, s)
+                                                              : launch_append8<T, D, FORM, 8>(p, s);
 }
 
 template <typename T, int FORM>
 static np_status launch_append8_dim(Append8Params& p, int32_t d, cudaStream_t s) {
   switch (d) {
-    case 16: return launch_append8<T, 16, FORM>(p, s);
-    case 32: return launch_append8<T, 32, FORM>(p, s);
-    case 64: return launch_append8<T, 64, FORM>(p, s);
-    case 128: return launch_append8<T, 128, FORM>(p, s);
-    case 256: return launch_append8<T, 256, FORM>(p, s);
+    case 16: return launch_append8_steps<T, 16, FORM>(p, s);
+    case 32: return launch_append8_steps<T, 32, FORM>(p, s);
+    case 64: return launch_append8_steps<T, 64, FORM>(p, s);
+    case 128: return launch_append8_steps<T, 128, FORM>(p, s);
+    case 256: return launch_append8_steps<T, 256, FORM>(p, s);
   }
   return NP_ERR_UNSUPPORTED;
 }
