@@ -556,7 +556,18 @@ def q8_pools(num_blocks, block_size, kv_heads, head_dim, form=torch.float8_e4m3f
     return (*pools, *scales)
 
 
+_INT32, _INT64, _FLOAT = torch.int32, torch.int64, torch.float32
+
+
 def _q8_shape(name, k_pool, v_pool, k_scale, v_scale):
+    """(form, blocks, block size, kv heads, head_dim) of a cache, after the checks."""
+    dt, shape = k_pool.dtype, k_pool.shape
+    form = _FORMS.get(dt)
+    if len(shape) == 4 and form is not None and v_pool.dtype is dt and v_pool.shape == shape and \
+            k_scale.dtype is _FLOAT and v_scale.dtype is _FLOAT:
+        nb, bs, hk, d = shape
+        if k_scale.shape == (nb, hk) and v_scale.shape == (nb, hk):
+            return form, nb, bs, hk, d
     if k_pool.dim() != 4 or v_pool.shape != k_pool.shape:
         raise ValueError(f"{name}: pools must be [blocks, block_size, kv_heads, head_dim]")
     form = _FORMS.get(k_pool.dtype)
@@ -567,15 +578,6 @@ def _q8_shape(name, k_pool, v_pool, k_scale, v_scale):
             k_scale.shape != (nb, hk) or v_scale.shape != (nb, hk):
         raise ValueError(f"{name}: scales must be float32 [blocks, kv_heads]")
     return form, nb, bs, hk, d
-
-
-def _on(cur: int, *tensors) -> bool:
-    """Whether all of them (None aside) are contiguous on device ``cur``."""
-    return all(t is None or (t.get_device() == cur and t.is_contiguous()) for t in tensors)
-
-
-def _ptr(t) -> int:
-    return 0 if t is None else t.data_ptr()
 
 
 def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, query_starts,
@@ -590,38 +592,70 @@ def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, 
     free_blocks int32 [num_blocks]; free_count int32 [1]; query_starts int32 [rows + 1];
     slot_mapping int64 [tokens]; positions int32 [tokens]."""
     name = "np_block_map"
-    if block_tables.dtype is not torch.int32 or block_tables.dim() != 2:
-        raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
-    rows, mb = block_tables.shape
-    for t, what in ((context_lens, "context_lens"), (new_lens, "new_lens"), (kept_lens, "kept_lens")):
-        if t is not None and (t.dtype is not torch.int32 or t.shape != (rows,)):
-            raise ValueError(f"{name}: {what} must be int32 [rows]")
-    if free_blocks.dtype is not torch.int32 or free_blocks.dim() != 1:
-        raise ValueError(f"{name}: free_blocks must be int32 [num_blocks]")
-    if free_count.dtype is not torch.int32 or free_count.numel() != 1:
-        raise ValueError(f"{name}: free_count must be one int32")
-    if query_starts.dtype is not torch.int32 or query_starts.shape != (rows + 1,):
-        raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
-    if slot_mapping is not None and (slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1):
-        raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
-    if positions is not None and (slot_mapping is None or positions.dtype is not torch.int32 or
-                                  positions.shape != slot_mapping.shape):
-        raise ValueError(f"{name}: positions must be int32 [tokens], beside a slot_mapping")
+    shape = block_tables.shape
+    lens = context_lens.shape
+    n = 0 if slot_mapping is None else slot_mapping.numel()
     cur = _device_now()
-    if not _on(cur, block_tables, context_lens, new_lens, kept_lens, free_blocks, free_count,
-               query_starts, slot_mapping, positions, err_word):
-        _refuse(cur, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
-                kept_lens=kept_lens, free_blocks=free_blocks, free_count=free_count,
-                query_starts=query_starts, slot_mapping=slot_mapping, positions=positions,
-                err_word=err_word)
-    n = 0 if slot_mapping is None else slot_mapping.shape[0]
+    # (one condition: what it refuses is looked at again to say why)
+    if not (block_tables.dtype is _INT32 and len(shape) == 2 and
+            context_lens.dtype is _INT32 and len(lens) == 1 and lens[0] == shape[0] and
+            new_lens.dtype is _INT32 and new_lens.shape == lens and
+            free_blocks.dtype is _INT32 and free_blocks.dim() == 1 and
+            free_count.dtype is _INT32 and free_count.numel() == 1 and
+            query_starts.dtype is _INT32 and query_starts.dim() == 1 and
+            query_starts.numel() == shape[0] + 1 and
+            block_tables.get_device() == context_lens.get_device() == new_lens.get_device() ==
+            free_blocks.get_device() == free_count.get_device() == query_starts.get_device() == cur and
+            block_tables.is_contiguous() and context_lens.is_contiguous() and
+            new_lens.is_contiguous() and free_blocks.is_contiguous() and
+            query_starts.is_contiguous() and
+            (kept_lens is None or (kept_lens.dtype is _INT32 and kept_lens.shape == lens and
+                                   kept_lens.get_device() == cur and kept_lens.is_contiguous())) and
+            (slot_mapping is None or (slot_mapping.dtype is _INT64 and slot_mapping.dim() == 1 and
+                                      slot_mapping.get_device() == cur and
+                                      slot_mapping.is_contiguous())) and
+            (positions is None or (n > 0 and positions.dtype is _INT32 and positions.dim() == 1 and
+                                   positions.numel() == n and positions.get_device() == cur and
+                                   positions.is_contiguous())) and
+            (err_word is None or (err_word.get_device() == cur and err_word.is_contiguous()))):
+        _refuse_map(name, cur, block_tables, context_lens, new_lens, free_blocks, free_count,
+                    query_starts, slot_mapping, positions, kept_lens, err_word)
+    rows, mb = shape
     st = load().np_block_map_packed(_pack(
         _MAP_ARGS, name, block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(),
-        _ptr(kept_lens), free_blocks.data_ptr(), free_count.data_ptr(), query_starts.data_ptr(),
-        _ptr(slot_mapping) if n else 0, _ptr(positions) if n else 0, _ptr(err_word),
-        _stream_now(stream, cur), free_blocks.shape[0], mb, rows, block_size, n))
+        0 if kept_lens is None else kept_lens.data_ptr(), free_blocks.data_ptr(),
+        free_count.data_ptr(), query_starts.data_ptr(), slot_mapping.data_ptr() if n else 0,
+        positions.data_ptr() if n and positions is not None else 0,
+        0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur),
+        free_blocks.numel(), mb, rows, block_size, n))
     if st != NP_OK:
         raise NPError(st, name)
+
+
+def _refuse_map(name, cur, block_tables, context_lens, new_lens, free_blocks, free_count,
+                query_starts, slot_mapping, positions, kept_lens, err_word) -> None:
+    """np_block_map's refusal of its arguments (those of a mapping without tokens pass)."""
+    if block_tables.dtype is not _INT32 or block_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
+    rows = block_tables.shape[0]
+    for t, what in ((context_lens, "context_lens"), (new_lens, "new_lens"), (kept_lens, "kept_lens")):
+        if t is not None and (t.dtype is not _INT32 or t.shape != (rows,)):
+            raise ValueError(f"{name}: {what} must be int32 [rows]")
+    if free_blocks.dtype is not _INT32 or free_blocks.dim() != 1:
+        raise ValueError(f"{name}: free_blocks must be int32 [num_blocks]")
+    if free_count.dtype is not _INT32 or free_count.numel() != 1:
+        raise ValueError(f"{name}: free_count must be one int32")
+    if query_starts.dtype is not _INT32 or query_starts.shape != (rows + 1,):
+        raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
+    if slot_mapping is not None and (slot_mapping.dtype is not _INT64 or slot_mapping.dim() != 1):
+        raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
+    if positions is not None and (slot_mapping is None or positions.dtype is not _INT32 or
+                                  positions.shape != slot_mapping.shape):
+        raise ValueError(f"{name}: positions must be int32 [tokens], beside a slot_mapping")
+    _refuse(cur, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
+            kept_lens=kept_lens, free_blocks=free_blocks, free_count=free_count,
+            query_starts=query_starts, slot_mapping=slot_mapping, positions=positions,
+            err_word=err_word)
 
 
 def np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, err_word=None,
@@ -631,23 +665,29 @@ def np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping
     np_paged.h).  The tokens of a block stand side by side in ``slot_mapping``."""
     name = "np_kv_append_q8"
     form, nb, bs, hk, d = _q8_shape(name, k_pool, v_pool, k_scale, v_scale)
-    if k_new.dim() != 3 or v_new.shape != k_new.shape or k_new.shape[1] != hk or k_new.shape[2] != d:
+    shape, dt = k_new.shape, k_new.dtype
+    if len(shape) != 3 or shape[1] != hk or shape[2] != d or v_new.shape != shape:
         raise ValueError(f"{name}: k_new/v_new must be [tokens, kv_heads, head_dim] of the pools")
-    if v_new.dtype is not k_new.dtype:
+    if v_new.dtype is not dt:
         raise ValueError(f"{name}: k_new and v_new must share a dtype")
-    n = k_new.shape[0]
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,):
+    n = shape[0]
+    if slot_mapping.dtype is not _INT64 or slot_mapping.dim() != 1 or slot_mapping.numel() != n:
         raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
     cur = _device_now()
     kp, ks = _token_rows(k_new, "k_new", cur, n, hk, d)
     vp, vs = _token_rows(v_new, "v_new", cur, n, hk, d)
-    if not _on(cur, k_pool, v_pool, k_scale, v_scale, slot_mapping, err_word):
+    if not (k_pool.get_device() == v_pool.get_device() == k_scale.get_device() ==
+            v_scale.get_device() == slot_mapping.get_device() == cur and
+            k_pool.is_contiguous() and v_pool.is_contiguous() and k_scale.is_contiguous() and
+            v_scale.is_contiguous() and slot_mapping.is_contiguous() and
+            (err_word is None or (err_word.get_device() == cur and err_word.is_contiguous()))):
         _refuse(cur, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
                 slot_mapping=slot_mapping, err_word=err_word)
     st = load().np_kv_append_q8_packed(_pack(
         _APPEND_Q8_ARGS, name, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), kp, vp, slot_mapping.data_ptr(), _ptr(err_word),
-        _stream_now(stream, cur), nb, ks, vs, form, _CODES[k_new.dtype], bs, hk, d, n))
+        v_scale.data_ptr(), kp, vp, slot_mapping.data_ptr(),
+        0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur), nb, ks, vs, form,
+        _CODES[dt], bs, hk, d, n))
     if st != NP_OK:
         raise NPError(st, name)
 
@@ -669,15 +709,25 @@ def _read_q8_args(name, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, 
                                      query_starts.shape != (rows + 1,)):
         raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
     cur = _device_now()
-    if not _on(cur, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
-               query_starts, workspace, err_word):
+    if not (out.get_device() == q.get_device() == k_pool.get_device() == v_pool.get_device() ==
+            k_scale.get_device() == v_scale.get_device() == block_tables.get_device() ==
+            context_lens.get_device() == cur and
+            (query_starts is None or (query_starts.get_device() == cur and
+                                      query_starts.is_contiguous())) and
+            (workspace is None or (workspace.get_device() == cur and workspace.is_contiguous())) and
+            (err_word is None or (err_word.get_device() == cur and err_word.is_contiguous())) and
+            out.is_contiguous() and q.is_contiguous() and k_pool.is_contiguous() and
+            v_pool.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous() and
+            block_tables.is_contiguous() and context_lens.is_contiguous()):
         _refuse(cur, out=out, q=q, k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale,
                 block_tables=block_tables, context_lens=context_lens, query_starts=query_starts,
                 workspace=workspace, err_word=err_word)
     return _pack(
         _READ_Q8_ARGS, name, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-        _ptr(query_starts), _ptr(workspace), _ptr(err_word), _stream_now(stream, cur), nb,
+        0 if query_starts is None else query_starts.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(),
+        0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur), nb,
         0 if workspace is None else workspace.nbytes, form, _CODES[q.dtype], bs, hk, d, mb, rows,
         query_len, tokens, q.shape[-2], scale)
 

@@ -35,6 +35,7 @@ struct MapParams {
   int64_t num_blocks;
   int32_t rows, block_size, max_blocks, tokens;
   int32_t token_cap;  // num_tokens, or what int32 holds without a slot mapping
+  int32_t apart;      // the tokens are a launch of their own
 };
 
 // the last i with a[i] <= x, of n + 1 ascending entries with a[0] = 0 <= x < a[n]
@@ -52,18 +53,36 @@ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
   return (int32_t)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b);  // a < 2^31, b < 2^31
 }
 
-// the slot and position of token i of a row with kept positions `base`, its first
-// token `first`
-__device__ __forceinline__ void map_token(const MapParams& p, int i, int row, int32_t base,
-                                          int32_t first) {
-  const int32_t pos = base + (i - first);
-  const int32_t j = pos / p.block_size;
-  const int32_t b = __ldcg(p.tables + (int64_t)row * p.max_blocks + j);
-  int64_t slot = -1;
-  if (b >= 0 && b < p.num_blocks) slot = (int64_t)b * p.block_size + (pos - j * p.block_size);
-  else set_flag(p.err, NP_FLAG_BLOCK_ID);
-  p.slots[i] = slot;
-  if (p.positions) p.positions[i] = pos;
+// Slots and positions of tokens i0, i0 + stride, .. below `end`, of `tokens` in all: four
+// at a time, their table entries on the way together.
+__device__ __forceinline__ void map_tokens(const MapParams& p, const int32_t* tok, const int32_t* base,
+                                           int32_t tokens, int i0, int stride, int end) {
+#pragma unroll 1
+  for (; i0 < end; i0 += 4 * stride) {
+    int32_t pos[4], in[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * stride;
+      b[u] = -1;
+      pos[u] = in[u] = 0;
+      if (i < tokens && i < end) {
+        const int r = map_row(tok, p.rows, i);
+        pos[u] = base[r] + (i - tok[r]);
+        const int32_t j = (int32_t)((uint32_t)pos[u] / (uint32_t)p.block_size);
+        in[u] = pos[u] - j * p.block_size;
+        b[u] = p.tables[(int64_t)r * p.max_blocks + j];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * stride;
+      if (i >= end) break;
+      const bool good = b[u] >= 0 && b[u] < p.num_blocks;
+      if (i < tokens && !good) set_flag(p.err, NP_FLAG_BLOCK_ID);
+      p.slots[i] = good ? (int64_t)b[u] * p.block_size + in[u] : -1;
+      if (p.positions) p.positions[i] = pos[u];
+    }
+  }
 }
 
 struct MapSum {
@@ -221,24 +240,42 @@ __global__ void __launch_bounds__(kMapThreads) block_map_kernel(const __grid_con
   }
   if (flags) set_flag(p.err, flags);
   __syncthreads();
-  for (int i = tid; i < p.tokens; i += kMapThreads) {
-    if (i < tokens) {
-      const int r = map_row(tok, p.rows, i);
-      map_token(p, i, r, base[r], tok[r]);
-    } else {
-      p.slots[i] = -1;
-      if (p.positions) p.positions[i] = 0;
-    }
-  }
+  if (!p.apart) map_tokens(p, tok, base, tokens, tid, kMapThreads, p.tokens);
 }
 
-np_status launch_block_map(const MapParams& p, cudaStream_t s) {
+// The tokens of long steps: kMapFill a block, from what the first launch left.
+constexpr int kMapFill = 2048, kMapFillThreads = 512;
+
+__global__ void __launch_bounds__(kMapFillThreads) block_map_fill_kernel(const __grid_constant__
+                                                                         MapParams p) {
+  extern __shared__ __align__(16) int32_t map_smem[];
+  int32_t* tok = map_smem;                 // [rows + 1]
+  int32_t* base = tok + kMapMaxRows + 1;   // [rows]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int r = threadIdx.x; r <= p.rows; r += kMapFillThreads) {
+    tok[r] = p.starts[r];
+    if (r < p.rows) base[r] = p.lens[r] - (p.starts[r + 1] - p.starts[r]);
+  }
+  __syncthreads();
+  const int first = blockIdx.x * kMapFill;
+  map_tokens(p, tok, base, tok[p.rows], first + (int)threadIdx.x, kMapFillThreads,
+             min(p.tokens, first + kMapFill));
+}
+
+np_status launch_block_map(MapParams& p, cudaStream_t s) {
   constexpr size_t smem = (size_t)(4 * (kMapMaxRows + 1)) * 4;
   static unsigned long long allowed = 0;
   const np_status rc = allow_smem(block_map_kernel, smem, &allowed);
   if (rc != NP_OK) return rc;
+  // Long steps' tokens over many blocks: us of a step and its undoing, 64 rows, one
+  // launch / two: 2000 tokens 9.5 / 10.9, 4000 10.9 / 10.7, 8000 13.6 / 10.7, 18000 17.6 / 10.7.
+  p.apart = p.tokens > 2 * kMapFill;
   block_map_kernel<<<1, kMapThreads, smem, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? NP_OK : NP_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return NP_ERR_CUDA;
+  if (!p.apart) return NP_OK;
+  constexpr size_t fill = (size_t)(2 * (kMapMaxRows + 1)) * 4;
+  return launch_dependent(block_map_fill_kernel, (unsigned)((p.tokens + kMapFill - 1) / kMapFill), 1,
+                          kMapFillThreads, fill, s, p);
 }
 
 }  // namespace npk
