@@ -6,9 +6,11 @@
 //     x_j = c (q . k_j) 2^a_j + b_j                (log2 units; c = scale log2 e)
 //     O  = sum_j 2^(x_j - M) v_j,   l = sum_j 2^(x_j - M - b_j),   out = O / l
 // so V's scale is an addition to the exponent, and its product stays a product
-// of codes.  M is set 6 below the largest x seen, and again only where an x passes it by
-// more than 14: weights stay within fp16's 2^15, and what is too small for its
-// subnormals is below 2^-30 of the largest.
+// of codes.  M is a whole number, the largest x rounded up, and replaced only where an x
+// passes it by more than 8; x - M then has one rounding, and M's changes are exact powers
+// of two.  Weights are taken 2^6 larger (both sums are; bf16: in the exponent, fp32: as a
+// factor, so that x - M keeps its small steps): they stay within fp16's 2^15, and what is
+// too small for its subnormals is below 2^-30 of the largest.
 //
 // The products are m16n8k16 mma (fp16 in, fp32 out) with the cache as the A
 // operand -- 16 tokens x 16 dims of K, 16 dims x 16 tokens of V -- and the rows
@@ -40,6 +42,8 @@
 #endif
 
 namespace npk {
+
+constexpr float kAbove = 8.f, kWeight = 64.f;
 
 // Geometry of a stage.  Rows of D bytes; 128-byte lines; 16-byte pieces of a line are
 // swizzled so that both products' reads are free of bank conflicts.
@@ -75,6 +79,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the same without a sum before it
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -151,7 +165,11 @@ struct Q8Walk {
   }
 };
 
-template <typename T, int D, int FORM, int NT>
+// MANY (fp32): a warp may sum many chunks.  An mma's sum truncates, and hundreds in a row
+// add that up, so each chunk's O is summed by itself and then added with rounding.  64 rows
+// of 15000 positions (470 chunks a warp): 4.9e-6 of the result off without and 5.0e-7 with,
+// 322 and 469 us; 94 chunks: 1.3e-6 and 3.7e-7, 119 and 150 us.
+template <typename T, int D, int FORM, int NT, bool MANY>
 __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
     decode_q8_kernel(const __grid_constant__ DecodeQ8Params p) {
   using Geo = Q8Geo<D, NT>;
@@ -564,6 +582,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        float rest[4] = {0.f, 0.f, 0.f, 0.f};  // fp32: of q's second part
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
           uint32_t a[KW], b[KW];
@@ -581,11 +600,16 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
             const uint32_t a0 = F::half_lo(a[k]), a2 = F::half_hi(a[k]);
             const uint32_t a1 = F::half_lo(b[k]), a3 = F::half_hi(b[k]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int pt = 0; pt < PARTS; ++pt)
-                mma_f16(s[nt], a0, a1, a2, a3, qf[nt][pt][j * KW + k][0], qf[nt][pt][j * KW + k][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(s[nt], a0, a1, a2, a3, qf[nt][0][j * KW + k][0], qf[nt][0][j * KW + k][1]);
+              if constexpr (F32)
+                mma_f16(rest, a0, a1, a2, a3, qf[nt][1][j * KW + k][0], qf[nt][1][j * KW + k][1]);
+            }
           }
+        }
+        if constexpr (F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[0][e] += rest[e];
         }
         // ---- softmax: rows of S are tokens g and g + 8
         uint32_t sc[4];
@@ -597,18 +621,22 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         const int ea = scale_exp(sc[2]), eb = scale_exp(sc[3]);
         const float va = (float)ea, vb = (float)eb, ia = pow2f(-ea), ib = pow2f(-eb);
         const bool edge = t0 + sub + 16 > all_see;  // uniform
+        // x - M (+ UP), with one rounding; M is a whole number
+        constexpr float UP = F32 ? 0.f : 6.f;
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], va);
-            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], vb);
+            const bool none = m[nt][c] == -INFINITY;
+            const float ref = none ? -UP : m[nt][c] - UP;
+            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], va - ref);
+            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], vb - ref);
             if (edge) {
               if (t0 + sub + g >= lim[nt][c]) s[nt][c] = -INFINITY;
               if (t0 + sub + g + 8 >= lim[nt][c]) s[nt][2 + c] = -INFINITY;
             }
-            grow |= fmaxf(s[nt][c], s[nt][2 + c]) > m[nt][c] + 14.f;
+            grow |= fmaxf(s[nt][c], s[nt][2 + c]) > (none ? -INFINITY : kAbove + UP);
           }
         }
         if (__any_sync(FULL, grow)) {
@@ -620,9 +648,13 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
-              if (x > m[nt][c] + 14.f) {
-                const float f = ex2(m[nt][c] - (x - 6.f));
-                m[nt][c] = x - 6.f;
+              const bool none = m[nt][c] == -INFINITY;
+              if (x > (none ? -INFINITY : kAbove + UP)) {
+                x = ceilf(x - UP);
+                const float f = none ? 0.f : ex2(-x);
+                m[nt][c] = none ? x : m[nt][c] + x;
+                s[nt][c] -= x;
+                s[nt][2 + c] -= x;
                 l[nt][c] *= f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -638,9 +670,8 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float ref = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
-            s[nt][c] = ex2(s[nt][c] - ref);
-            s[nt][2 + c] = ex2(s[nt][2 + c] - ref);
+            s[nt][c] = ex2(s[nt][c]) * (F32 ? kWeight : 1.f);
+            s[nt][2 + c] = ex2(s[nt][2 + c]) * (F32 ? kWeight : 1.f);
             l[nt][c] = fmaf(s[nt][c], ia, fmaf(s[nt][2 + c], ib, l[nt][c]));
           }
 #pragma unroll
@@ -651,6 +682,23 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           }
         }
         // ---- O += V^T P: a lane's dims are VB bytes of tokens 2 t4, + 1, + 8, + 9
+        auto add = [&](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                       const uint32_t (&w)[PARTS][2]) {
+          if constexpr (F32) {
+            if constexpr (MANY) {
+              float x[4];
+              mma_f16_first(x, a0, a1, a2, a3, w[1][0], w[1][1]);
+              mma_f16(x, a0, a1, a2, a3, w[0][0], w[0][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) c[e] += x[e];
+            } else {
+              mma_f16(c, a0, a1, a2, a3, w[1][0], w[1][1]);
+              mma_f16(c, a0, a1, a2, a3, w[0][0], w[0][1]);
+            }
+          } else {
+            mma_f16(c, a0, a1, a2, a3, w[0][0], w[0][1]);
+          }
+        };
 #pragma unroll
         for (int j = 0; j < VJ; ++j) {
           uint32_t x[4][(VB + 3) / 4];
@@ -673,20 +721,14 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
             const uint32_t a0 = F::half_lo(p01), a1 = F::half_hi(p01);
             const uint32_t a2 = F::half_lo(p23), a3 = F::half_hi(p23);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int pt = 0; pt < PARTS; ++pt)
-                mma_f16(o[nt][j * (VB / 2) + 2 * k], a0, a1, a2, a3, pf[nt][pt][0], pf[nt][pt][1]);
+            for (int nt = 0; nt < NT; ++nt) add(o[nt][j * (VB / 2) + 2 * k], a0, a1, a2, a3, pf[nt]);
             if constexpr (VB >= 4) {
               const uint32_t q01 = __byte_perm(x[0][k], x[1][k], 0x7362),
                              q23 = __byte_perm(x[2][k], x[3][k], 0x7362);
               const uint32_t b0 = F::half_lo(q01), b1 = F::half_hi(q01);
               const uint32_t b2 = F::half_lo(q23), b3 = F::half_hi(q23);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int pt = 0; pt < PARTS; ++pt)
-                  mma_f16(o[nt][j * (VB / 2) + 2 * k + 1], b0, b1, b2, b3, pf[nt][pt][0], pf[nt][pt][1]);
+              for (int nt = 0; nt < NT; ++nt) add(o[nt][j * (VB / 2) + 2 * k + 1], b0, b1, b2, b3, pf[nt]);
             }
           }
         }
@@ -809,13 +851,13 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
   }
 }
 
-template <typename T, int D, int FORM, int NT>
+template <typename T, int D, int FORM, int NT, bool MANY>
 static np_status launch(const DecodeQ8Params& p, cudaStream_t s) {
   using Geo = Q8Geo<D, NT>;
   static unsigned long long allowed = 0;
-  np_status rc = allow_smem(decode_q8_kernel<T, D, FORM, NT>, Geo::SMEM, &allowed);
+  np_status rc = allow_smem(decode_q8_kernel<T, D, FORM, NT, MANY>, Geo::SMEM, &allowed);
   if (rc != NP_OK) return rc;
-  decode_q8_kernel<T, D, FORM, NT><<<p.ctas, 32 * Geo::WARPS, Geo::SMEM, s>>>(p);
+  decode_q8_kernel<T, D, FORM, NT, MANY><<<p.ctas, 32 * Geo::WARPS, Geo::SMEM, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NP_ERR_CUDA;
   return launch_dependent(decode_q8_join_kernel<T, D>, kQ8JoinGrid * p.ctas, 1, kQ8JoinThreads, 0, s, p);
 }
@@ -830,9 +872,15 @@ static np_status launch(const DecodeQ8Params& p, cudaStream_t s) {
 #endif
 
 np_status NPK_NAME(const DecodeQ8Params& p, np_dtype dtype, cudaStream_t s) {
-  if (dtype == NP_F32) return launch<float, NPK_D, NPK_FORM, 1>(p, s);
-  return p.group * p.query_len <= 8 ? launch<__nv_bfloat16, NPK_D, NPK_FORM, 1>(p, s)
-                                    : launch<__nv_bfloat16, NPK_D, NPK_FORM, 2>(p, s);
+  if (dtype == NP_F32) {
+    // chunks that a warp may have to sum, from the tables' size
+    const int64_t most = (int64_t)p.rows * p.max_blocks * p.block_size / 16 * (p.kv_heads / p.head_group) /
+                         ((int64_t)p.ctas * (q8_warps(NPK_D, 1) / p.head_group));
+    return most > 128 ? launch<float, NPK_D, NPK_FORM, 1, true>(p, s)
+                      : launch<float, NPK_D, NPK_FORM, 1, false>(p, s);
+  }
+  return p.group * p.query_len <= 8 ? launch<__nv_bfloat16, NPK_D, NPK_FORM, 1, false>(p, s)
+                                    : launch<__nv_bfloat16, NPK_D, NPK_FORM, 2, false>(p, s);
 }
 
 }  // namespace npk
