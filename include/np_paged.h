@@ -414,7 +414,8 @@ np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
  * row's largest element); a weight is rounded to fp16 for its product with V,
  * bf16 out; for fp32, q and the weights are two fp16 parts each (22 bits).  The
  * softmax and its sums are fp32.
- * Slots past a row's context are never part of a result.  Supported: dtype
+ * Slots past a row's context are never part of a result; no element of its context may
+ * be NaN (where a query token does not see the position either).  Supported: dtype
  * NP_F32 (g * query_len <= 8) or NP_BF16 (<= 16), g = q_heads / kv_heads; head_dim
  * of the list above; any block_size; any kv_heads; rows up to 65535; tables of up to
  * 2^31 - 1025 tokens, and rows * kv_heads * a table's tokens up to 2^34.  A row without history gets zeros.  rows 0: a no-op.
@@ -439,7 +440,16 @@ np_status np_paged_decode_q8(void* out, const void* q, np_dtype dtype,
  * np_paged_prefill_q8 -- np_paged_prefill over an 8-bit cache: ragged chunks of
  * new tokens, already appended (np_kv_append_q8), attend causally over their
  * rows' histories.  out and q of `dtype`; pools, scales and form as above; the
- * other arguments, limits and errors as np_paged_prefill's.
+ * other arguments, limits and errors as np_paged_prefill's (no element of a row's c
+ * positions may be NaN).
+ * Arithmetic, fp32 sums and softmax throughout.  bf16, head_dim 64 and up, block_size
+ * a multiple of 8: fp16 products; q times a power of two, codes exact but where
+ * their block's scale is over 2^15 (e4m3; int8 2^24) below the largest of the 128 (head_dim 256:
+ * 64) positions around, there to 2^-33 of those positions' largest value; weights
+ * rounded to fp16.  Other bf16 calls: codes times scales exact in bf16, weights rounded to bf16.  fp32:
+ * fp32 products.  Where num_tokens < 64 rows, rows with at most 8 / g tokens (g > 8:
+ * one) are read as np_paged_decode_q8 reads them.
+ * Two to five launches on `stream`; the same call gives the same bits.
  */
 np_status np_paged_prefill_q8(void* out, const void* q, np_dtype dtype,
                               const void* k_pool, const void* v_pool,

@@ -73,6 +73,46 @@ def test_kv_heads(nplib, hk, d, g):
     _compare(nplib, BF16, torch.float8_e4m3fn, d, hk, g, 16, [300, 1, 0, 77, 1200], seed=hk)
 
 
+@pytest.mark.parametrize("hk", [1, 3, 4, 5, 8, 10])
+def test_kv_heads_wide(nplib, hk):
+    """Four warps a block at head_dim 256 with more than eight rows a head: fewer heads a block."""
+    _compare(nplib, BF16, torch.int8, 256, hk, 16, 16, [300, 1, 0, 77], seed=hk)
+    _compare(nplib, F32, torch.float8_e4m3fn, 256, hk, 4, 16, [300, 1, 0, 77], 2, seed=hk)
+
+
+def test_fp32_with_long_tables(nplib):
+    """Tables that may hold long rows take the kernel that adds each chunk's sum with rounding."""
+    rows = [(1, c) for c in (3000, 17, 0, 20000)]
+    for d, form in ((128, torch.float8_e4m3fn), (32, torch.int8)):
+        inp = h.read_inputs(F32, form, d, 2, 4, 16, rows, cap=200000)
+        out, err = _read(nplib, inp, rows, 0.05, 1)
+        ref, bound = chunk_reference(h.as_values(inp), rows, 0.05)
+        vtop = float(inp["v_scale"].nan_to_num(0, 0).max()) * h.QMAX[form]
+        tol = h.decode_tolerance(ref, bound, F32, d, 20000, vtop)
+        assert err == 0 and ((out.double() - ref).abs() <= tol).all()
+        # far below the bound, which adds up every rounding at its worst: as near as fp32 sums are
+        assert float((out.double() - ref).norm() / bound[0].norm()) < 2.0 ** -20
+
+
+def test_captured_and_replayed(nplib):
+    """A process' later calls in a graph: lengths and tables change between replays."""
+    rows = [(1, c) for c in (900, 3, 64, 0, 2222)]
+    inp = h.read_inputs(BF16, torch.int8, 128, 4, 4, 16, rows)
+    ws, out = nplib.decode_q8_workspace(128), torch.zeros_like(inp["q"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nplib.np_paged_decode_q8(out, inp["q"], inp["k_pool"], inp["v_pool"], inp["k_scale"], inp["v_scale"],
+                                 inp["block_tables"], inp["context_lens"], 0.1, ws)
+    for lens in ([c for _, c in rows], [16, 1, 0, 5, 2000], [0, 0, 0, 0, 0]):
+        lens = [min(a, c) for a, (_, c) in zip(lens, rows)]
+        inp["context_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        want, _ = _read(nplib, inp, rows, 0.1, 1)
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("hk", [1, 8])
 def test_one_long_row(nplib, dtype, hk):
