@@ -64,6 +64,8 @@ def _units(extra: list[str], build_dir: str, csrc: str) -> list[tuple[str, str, 
         if d <= 128:
             units.append((os.path.join(csrc, "prefill_tc32.cu"),
                           os.path.join(objdir, f"prefill_tc32_d{d}.o"), [f"-DNPK_D={d}"]))
+            units.append((os.path.join(csrc, "prefill_tc32.cu"),
+                          os.path.join(objdir, f"prefill_tc32q8_d{d}.o"), [f"-DNPK_D={d}", "-DNPK_Q8"]))
     return [(s, o, ["-I", csrc] + f + extra) for s, o, f in units]
 
 

@@ -342,6 +342,12 @@ np_status prefill_tc32_d32(const PrefillParams& p, cudaStream_t s);
 np_status prefill_tc32_d64(const PrefillParams& p, cudaStream_t s);
 np_status prefill_tc32_d128(const PrefillParams& p, cudaStream_t s);
 
+// the same for an 8-bit cache
+np_status prefill_tc32q8_d16(const PrefillParams& p, np_form8 form, cudaStream_t s);
+np_status prefill_tc32q8_d32(const PrefillParams& p, np_form8 form, cudaStream_t s);
+np_status prefill_tc32q8_d64(const PrefillParams& p, np_form8 form, cudaStream_t s);
+np_status prefill_tc32q8_d128(const PrefillParams& p, np_form8 form, cudaStream_t s);
+
 // The opt-in shared-memory limit of a kernel, a per-device attribute: set at
 // its first launch on a device.  `done`: one word per kernel, bit d for device d.
 template <typename K>

@@ -151,18 +151,21 @@ np_status launch_f32(PrefillParams& p, cudaStream_t s) {
   return NP_ERR_UNSUPPORTED;
 }
 
-// An 8-bit cache: bf16 on the tensor cores, fp32 on the FMA pipes.
+// An 8-bit cache: on the tensor cores, but for fp32 at head_dim 256.
 np_status launch_q8(PrefillParams& p, np_dtype dtype, np_form8 form, cudaStream_t s) {
   if (dtype == NP_F32) {
-    p.tiles = 1;
-    p.tile_rows = 64;
-    p.bn = 64;
-    p.tile_tokens = p.tile_rows / p.group;
-    p.full_cost = p.single_cost = 1;
-    p.unit_cost = 3;
-    p.min_share = 2;
+    npk::prefill_tiling(p, NP_F32);
+    if (p.head_dim <= 128) p.qscale = fmaxf(p.qscale, 1e-30f);
     const np_status rc = npk::launch_prefill_plan(p, s);
-    return rc == NP_OK ? npk::launch_prefill_q8_simt(p, form, s) : rc;
+    if (rc != NP_OK) return rc;
+    switch (p.head_dim) {
+      case 16: return npk::prefill_tc32q8_d16(p, form, s);
+      case 32: return npk::prefill_tc32q8_d32(p, form, s);
+      case 64: return npk::prefill_tc32q8_d64(p, form, s);
+      case 128: return npk::prefill_tc32q8_d128(p, form, s);
+      case 256: return npk::launch_prefill_q8_simt(p, form, s);
+    }
+    return NP_ERR_UNSUPPORTED;
   }
   p.qscale = fmaxf(p.qscale, 1e-30f);  // (as above)
   npk::prefill_tiling(p, NP_BF16);

@@ -4,7 +4,7 @@
 namespace npk {
 
 np_status launch_prefill_simt(const PrefillParams& p, cudaStream_t s) {
-  return launch_simt<float, 256, -1>(p, s);
+  return launch_simt<-1>(p, s);
 }
 
 }  // namespace npk

@@ -1,5 +1,5 @@
-// prefill_simt.cuh -- np_paged_prefill on the FMA pipes: fp32 pools of head_dim
-// 256.  (Narrower heads: prefill_tc32.cu, whose tiles of 128 rows and 64 tokens do
+// prefill_simt.cuh -- np_paged_prefill and np_paged_prefill_q8 on the FMA pipes: fp32
+// at head_dim 256.  (Narrower heads: prefill_tc32.cu, whose tiles of 128 rows and 64 tokens do
 // not fit in shared memory in three bf16 parts at this width.  Smaller ones
 // would: 64 rows and 32 tokens, 192 KB; not built.)
 //
@@ -21,23 +21,26 @@ constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 64;
 constexpr int kSimtBn = 64;
 
-template <int D>
+constexpr int kSimtD = 256;
+
 struct SimtSmem {
+  static constexpr int D = kSimtD;
   static constexpr int LD = D + 4;        // rows start on different banks
   static constexpr int LP = kSimtBn + 4;
   static constexpr size_t floats = (size_t)(kSimtRows + 2 * kSimtBn) * LD + (size_t)kSimtRows * LP;
   static constexpr size_t bytes = floats * 4 + kSimtBn * 8;
 };
 
-// T: q's and out's type.  FORM: the pools' 8-bit form, or -1 for fp32.
-template <typename T, int D, int FORM>
+// FORM: the pools' 8-bit form, or -1 for fp32.
+template <int FORM>
 __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __grid_constant__
                                                                        PrefillParams p) {
-  using S = Storage<T>;
-  using M = SimtSmem<D>;
+  using S = Storage<float>;
+  using M = SimtSmem;
+  constexpr int D = kSimtD;
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int V = 4;        // values of an access
-  constexpr int NG = (D + 63) / 64;  // groups of 4 dims a thread owns: 4 tx + 64 j (below D)
+  constexpr int NG = D / 64;  // groups of 4 dims a thread owns: 4 tx + 64 j
   extern __shared__ __align__(16) unsigned char smem[];
   float* qs = reinterpret_cast<float*>(smem);
   float* ks = qs + kSimtRows * M::LD;
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 #pragma unroll
       for (int k = 0; k < V; ++k) x[k] = 0.f;
       if (tt < p.tile_tokens && tok0 + tt < w.g.n)
-        S::template load<V>(static_cast<const T*>(p.q) +
+        S::template load<V>(static_cast<const float*>(p.q) +
                             ((int64_t)(w.g.q0 + tok0 + tt) * p.q_heads + w.kvh * G + h) * D + d,
                             x);
 #pragma unroll
@@ -196,7 +199,6 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int d = 4 * tx + 64 * j;
-          if (D % 64 != 0 && d >= D) continue;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const float4 v = *reinterpret_cast<const float4*>(&vs[(k + kk) * M::LD + d]);
@@ -221,12 +223,11 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
       if (w.whole()) {
         if (tt >= p.tile_tokens || tok0 + tt >= w.g.n) continue;
         const float inv = l_run[i] > 0.f ? 1.f / l_run[i] : 0.f;
-        T* out = static_cast<T*>(p.out) +
-                 ((int64_t)(w.g.q0 + tok0 + tt) * p.q_heads + w.kvh * G + h) * D;
+        float* out = static_cast<float*>(p.out) +
+                     ((int64_t)(w.g.q0 + tok0 + tt) * p.q_heads + w.kvh * G + h) * D;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int d = 4 * tx + 64 * j;
-          if (D % 64 != 0 && d >= D) continue;
           float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = o[i][j][e] * inv;
@@ -242,7 +243,6 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int g = tx + 16 * j;  // dims 4 g .. 4 g + 3
-          if (D % 64 != 0 && 4 * g >= D) continue;
           *reinterpret_cast<float4*>(part + 2 * kSimtRows + ((size_t)g * kSimtRows + row) * 4) =
               make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
         }
@@ -252,14 +252,14 @@ __global__ void __launch_bounds__(kSimtThreads, 1) prefill_simt_kernel(const __g
   }
 }
 
-template <typename T, int D, int FORM>
+template <int FORM>
 np_status launch_simt(const PrefillParams& p, cudaStream_t s) {
-  constexpr size_t bytes = SimtSmem<D>::bytes;
+  constexpr size_t bytes = SimtSmem::bytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
   static unsigned long long allowed = 0;
-  const np_status rc = allow_smem(prefill_simt_kernel<T, D, FORM>, bytes, &allowed);
+  const np_status rc = allow_smem(prefill_simt_kernel<FORM>, bytes, &allowed);
   if (rc != NP_OK) return rc;
-  return launch_dependent(prefill_simt_kernel<T, D, FORM>, p.ctas, 1, kSimtThreads, bytes, s, p);
+  return launch_dependent(prefill_simt_kernel<FORM>, p.ctas, 1, kSimtThreads, bytes, s, p);
 }
 
 }  // namespace npk

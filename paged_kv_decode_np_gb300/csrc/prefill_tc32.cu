@@ -36,8 +36,15 @@
 // positions, 32 / 8 heads of 128: 167 us, 143 TFLOP/s of fp32 products (950 us on
 // the FMA pipes); without the wait 162; with all products 64 columns wide, no
 // wait and half the adding up, 173.  Error against exact values 3e-7 of their norm.
+//
+// An 8-bit cache (FORM, compiled apart): a code times its scale, a power of two, is
+// one bf16 number, so K and V are their first part alone: q's three parts times K into
+// one S of 64 columns, P's three parts times V, exact products all of them.
 #include <limits.h>
 
+#include <type_traits>
+
+#include "cache8.cuh"
 #include "prefill.cuh"
 #include "tcgen05.cuh"
 
@@ -101,13 +108,15 @@ __device__ __forceinline__ void split8(const float4& a, const float4& b, uint4 (
   }
 }
 
-template <int D>
+// FORM: the pools' 8-bit form, or -1 for fp32
+template <int D, int FORM>
 __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
     prefill_tc32_kernel(const __grid_constant__ PrefillParams p) {
   using C = Tc32Cfg<D>;
   using B = Tc32Bars;
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int BN = C::BN, SL = C::SL, NS = C::NS;
+  constexpr bool Q8 = FORM >= 0;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -234,15 +243,17 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
         tmem_ld32(lanes + 32, r + 32);
         tmem_wait_ld();
         tmem_pin<BN>(r);
+        if constexpr (!Q8) {
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) {
-          uint32_t y[32];
-          tmem_ld32(lanes + BN + c, y);
-          tmem_wait_ld();
-          tmem_pin<32>(y);
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(lanes + BN + c, y);
+            tmem_wait_ld();
+            tmem_pin<32>(y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            r[c + e] = __float_as_uint(__uint_as_float(r[c + e]) + __uint_as_float(y[e]));
+            for (int e = 0; e < 32; ++e)
+              r[c + e] = __float_as_uint(__uint_as_float(r[c + e]) + __uint_as_float(y[e]));
+          }
         }
         tmem_fence_before();
         __syncwarp();
@@ -338,16 +349,23 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
     constexpr int NP = PT / 2;               // times: 16 tokens of the 64 are a warp's
     constexpr int HP = NP > 1 ? NP / 2 : 1;  // as many times at once: half a tile
     const int piece = lane % PT, sub = lane / PT;
-    const float* pool = static_cast<const float*>(isv ? p.v_pool : p.k_pool);
+    using E = typename std::conditional<Q8, uint8_t, float>::type;
+    const E* pool = static_cast<const E*>(isv ? p.v_pool : p.k_pool);
+    const float* scales = isv ? p.v_scale : p.k_scale;
     const int64_t token = (int64_t)p.kv_heads * D;
     const int full = isv ? B::v_full : B::k_full, empty = isv ? B::v_empty : B::k_empty;
     uint32_t it = 0;
-    float4 x[HP][2];
+    float4 x[HP][2];   // fp32: the pieces; 8 bits: codes and exponent of each
+    uint2 codes[HP];
+    int exps[HP];
+    struct Token {     // lane i: element offset of the warp's token i, -1 past the context; its scale
+      int64_t at;
+      uint32_t scale;
+    };
     // token i of the warp's 16 (i = pass * TW + sub) is row pass * 4 TW + wl TW + sub
     auto row_of = [&](int pass, int s) { return (pass * 4 + wl) * TW + s; };
-    // lane i: element offset of the warp's token i of kv tile kt, -1 past the context
-    auto look_up = [&](int kt) {
-      int64_t at = -1;
+    auto look_up = [&](int kt) {  // of kv tile kt
+      Token k{-1, 0u};
       if (lane < 16) {
         const int64_t t = (int64_t)kt * BN + row_of(lane / TW, lane % TW);
         if (t < w.g.c) {
@@ -357,15 +375,21 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
             set_flag(p.err, NP_FLAG_BLOCK_ID);
             b = 0;
           }
-          at = (b * p.block_size + ((unsigned)t - j * p.block_size)) * token + (int64_t)w.kvh * D;
+          k.at = (b * p.block_size + ((unsigned)t - j * p.block_size)) * token + (int64_t)w.kvh * D;
+          if constexpr (Q8) k.scale = __float_as_uint(scales[b * p.kv_heads + w.kvh]);
         }
       }
-      return at;
+      return k;
     };
-    auto fetch = [&](int64_t at, int first) {  // passes first .. first + HP - 1; zeros past the context
+    auto fetch = [&](const Token& k, int first) {  // passes first .. first + HP - 1; zeros past the context
 #pragma unroll
       for (int i = 0; i < HP; ++i) {
-        const int64_t a = __shfl_sync(FULL, at, (first + i) * TW + sub);
+        const int64_t a = __shfl_sync(FULL, k.at, (first + i) * TW + sub);
+        if constexpr (Q8) {
+          exps[i] = scale_exp(__shfl_sync(FULL, k.scale, (first + i) * TW + sub));
+          codes[i] = a >= 0 ? *reinterpret_cast<const uint2*>(pool + a + piece * 8) : make_uint2(0u, 0u);
+          continue;
+        }
         x[i][0] = x[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (a >= 0) {
           const float4* src = reinterpret_cast<const float4*>(pool + a + piece * 8);
@@ -376,36 +400,49 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
     };
     // brings this warp's tokens of a tile into L2: the registers hold half a tile
     // ahead, too little for HBM's latency.  Lines of 128 bytes, two a lane.
-    auto prefetch = [&](int64_t at) {
-      constexpr int LINES = D / 32 > 0 ? D / 32 : 1;  // of a token
+    auto prefetch = [&](const Token& k) {
+      constexpr int LE = 128 / (int)sizeof(E);              // elements of a line
+      constexpr int LINES = D / LE > 0 ? D / LE : 1;        // of a token
 #pragma unroll
       for (int i = 0; i < (16 * LINES + 31) / 32; ++i) {
         const int x = i * 32 + lane;
-        const int64_t a = __shfl_sync(FULL, at, (x / LINES) & 15);
+        const int64_t a = __shfl_sync(FULL, k.at, (x / LINES) & 15);
         if (x < 16 * LINES && a >= 0)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(pool + a + (x % LINES) * 32));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(pool + a + (x % LINES) * LE));
       }
     };
     while (ok && w.next(p)) {
       const int n = w.kv1 - w.kv0;
-      int64_t at = look_up(w.kv0);
-      int64_t ahead = n > 1 ? look_up(w.kv0 + 1) : -1;
+      Token at = look_up(w.kv0);
+      Token ahead = n > 1 ? look_up(w.kv0 + 1) : Token{-1, 0u};
       fetch(at, 0);
       if (n > 1) prefetch(ahead);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t slot = it % NS, use = it / NS;
-        const int64_t ahead2 = j + 2 < n ? look_up(w.kv0 + j + 2) : -1;
+        const Token ahead2 = j + 2 < n ? look_up(w.kv0 + j + 2) : Token{-1, 0u};
         if (use > 0 && !wait(empty + slot, (use - 1) & 1u)) break;
         unsigned char* dst = smem + (isv ? C::V0 : C::K0) + slot * (3 * C::PART);
 #pragma unroll 1
         for (int first = 0; first < NP; first += HP) {
 #pragma unroll
           for (int i = 0; i < HP; ++i) {
-            uint4 o[3];
-            split8(x[i][0], x[i][1], o);
             unsigned char* d = dst + tc_kv_at<SL>(row_of(first + i, sub), piece);
+            if constexpr (Q8) {
+              const Scaled8<FORM> sc(exps[i]);
+              uint4 o;
+              sc.widen(codes[i].x, o.x, o.y);
+              sc.widen(codes[i].y, o.z, o.w);
+              if (sc.large()) {
+                sc.widen_large(o.x, o.y);
+                sc.widen_large(o.z, o.w);
+              }
+              *reinterpret_cast<uint4*>(d) = o;
+            } else {
+              uint4 o[3];
+              split8(x[i][0], x[i][1], o);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(d + k * C::PART) = o[k];
+              for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(d + k * C::PART) = o[k];
+            }
           }
           if (first + HP < NP) fetch(at, first + HP);
         }
@@ -447,20 +484,22 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
               return k + (uint32_t)(part * C::PART + (ks >> 2) * 1024 + (ks & 3) * 32) / 16;
             };
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)  // q2 [K0; K1]
-              umma_ss(tmem, q2 + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, QHI, kd(0, ks), KVHI, QK2,
-                      ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks)  // q2 [K0; K1]  (8 bits: K0)
+              umma_ss(tmem, q2 + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, QHI, kd(0, ks), KVHI,
+                      Q8 ? QK1 : QK2, ks > 0);
 #pragma unroll
             for (int i = 1; i >= 0; --i)  // q1 [K0; K1], q0 [K0; K1]
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
-                umma_ts(tmem, tmem + C::Q0 + i * (D / 2) + ks * 8, kd(0, ks), KVHI, QK2, 1);
-            umma_commit(bar(B::s_part));  // another shape follows on their columns
-            if (!wait(B::s_part, t & 1u)) break;
-            tmem_fence_after();
+                umma_ts(tmem, tmem + C::Q0 + i * (D / 2) + ks * 8, kd(0, ks), KVHI, Q8 ? QK1 : QK2, 1);
+            if constexpr (!Q8) {
+              umma_commit(bar(B::s_part));  // another shape follows on their columns
+              if (!wait(B::s_part, t & 1u)) break;
+              tmem_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)  // q0 K2
-              umma_ts(tmem + BN, tmem + C::Q0 + ks * 8, kd(2, ks), KVHI, QK1, 1);
+              for (int ks = 0; ks < D / 16; ++ks)  // q0 K2
+                umma_ts(tmem + BN, tmem + C::Q0 + ks * 8, kd(2, ks), KVHI, QK1, 1);
+            }
             umma_commit(bar(B::s_full));
             umma_commit(bar(B::k_empty + slot));
           }
@@ -470,11 +509,11 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
             tmem_fence_after();
             const uint32_t v = umma_desc_lo(base + C::V0 + slot * (3 * C::PART), 1024);
 #pragma unroll
-            for (int x = 0; x < 6; ++x)
+            for (int x = 0; x < (Q8 ? 3 : 6); ++x)
 #pragma unroll
               for (int ks = 0; ks < BN / 16; ++ks)
-                umma_ts(tmem + C::O0, tmem + C::P0 + kPartA[x] * 32 + ks * 8,
-                        v + (kPartB[x] * C::PART + ks * (2 * SL * 1024)) / 16, KVHI, PV,
+                umma_ts(tmem + C::O0, tmem + C::P0 + (Q8 ? 2 - x : kPartA[x]) * 32 + ks * 8,
+                        v + ((Q8 ? 0 : kPartB[x]) * C::PART + ks * (2 * SL * 1024)) / 16, KVHI, PV,
                         x > 0 || ks > 0);
             umma_commit(bar(B::pv_done));
             umma_commit(bar(B::v_empty + slot));
@@ -502,12 +541,22 @@ __global__ void __launch_bounds__(Tc32Cfg<D>::THREADS, 1)
 #define NPK_CAT2(a, b) a##b
 #define NPK_CAT(a, b) NPK_CAT2(a, b)
 
-np_status NPK_CAT(prefill_tc32_d, NPK_D)(const PrefillParams& p, cudaStream_t s) {
+template <int FORM>
+static np_status launch(const PrefillParams& p, cudaStream_t s) {
   constexpr int bytes = Tc32Cfg<NPK_D>::SMEM;
   static unsigned long long allowed = 0;
-  const np_status rc = allow_smem(prefill_tc32_kernel<NPK_D>, bytes, &allowed);
+  const np_status rc = allow_smem(prefill_tc32_kernel<NPK_D, FORM>, bytes, &allowed);
   if (rc != NP_OK) return rc;
-  return launch_dependent(prefill_tc32_kernel<NPK_D>, p.ctas, 1, Tc32Cfg<NPK_D>::THREADS, bytes, s, p);
+  return launch_dependent(prefill_tc32_kernel<NPK_D, FORM>, p.ctas, 1, Tc32Cfg<NPK_D>::THREADS, bytes, s,
+                          p);
 }
+
+#ifdef NPK_Q8
+np_status NPK_CAT(prefill_tc32q8_d, NPK_D)(const PrefillParams& p, np_form8 form, cudaStream_t s) {
+  return form == NP_E4M3 ? launch<NP_E4M3>(p, s) : launch<NP_INT8>(p, s);
+}
+#else
+np_status NPK_CAT(prefill_tc32_d, NPK_D)(const PrefillParams& p, cudaStream_t s) { return launch<-1>(p, s); }
+#endif
 
 }  // namespace npk
