@@ -37,6 +37,10 @@ A prompt, or a chunk of one, of several rows (rotated, appended, attended)::
 
 The new tokens of a decode step are rotated and appended by np_rope_append,
 then read by np_paged_decode.
+
+A cache in 8 bits (q8_pools) is filled by np_kv_append_q8 and read by
+np_paged_decode_q8 and np_paged_prefill_q8 (decode_step_q8, prefill_step_q8);
+np_block_map keeps a batch's block tables, lengths and slots on the GPU.
 """
 from __future__ import annotations
 

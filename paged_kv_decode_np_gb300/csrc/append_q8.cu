@@ -12,9 +12,13 @@
 // takes the maximum, and writes the codes.  No two warps touch the same block
 // and head, so there is nothing to wait for and nothing atomic.
 //
-// Bound: HBM for prompts, latency for decode batches.  A block of the grid takes
-// `window` tokens: its warps find which of them begin runs and deal out
-// (run, head, K or V).
+// Bound: the chain of a run's loads, maximum, scale and stores; enough runs side by side
+// reach two thirds of the copy rate (16384 tokens, 8 heads of 128, bf16, blocks of 32:
+// 22.4 us, 4.5 TB/s), decode batches are latency (64 tokens 3.1 us, 256 3.9).  A block of the
+// grid takes `window` tokens: every warp finds by itself which of them begin runs, and
+// they deal out (run, head, K or V).  The first token's values are on their way before the
+// run's length is known.  (A shared list of the runs, 16 tokens in registers and the rest one by
+// one: 32, 3.5 and 7.4 us.)
 #include "cache8.cuh"
 #include "decode_launch.h"
 #include "host_checks.h"
@@ -217,7 +221,8 @@ __global__ void __launch_bounds__(32 * kAppend8Warps, STEPS == 16 ? 2 : STEPS ==
 
 template <typename T, int D, int FORM, int STEPS>
 static np_status launch_append8(Append8Params& p, cudaStream_t s) {
-  // few tokens: few of them a block, so that all warps find work
+  // few tokens: few of them a block, so that all warps find work.  us of 16384 tokens with
+  // 4, 8, 16, 32 a block: 39, 29, 25, 22; of 2000 tokens with 4, 8, 16: 8.3, 6.2, 7.2.
   p.window = p.tokens >= 4096 ? 32 : p.tokens >= 512 ? 8 : 1;
   const unsigned x = (unsigned)((p.tokens + p.window - 1) / p.window);
   const int tasks = 2 * p.kv_heads;  // of one run
@@ -228,7 +233,8 @@ static np_status launch_append8(Append8Params& p, cudaStream_t s) {
 }
 
 // How many steps of a run's values stay in registers: those of a whole block, 8 or 16;
-// few tokens (decode batches) are mostly runs of one.
+// few tokens (decode batches) are mostly runs of one.  us, 8 / 16 steps: 16000 tokens in
+// blocks of 16 22.0 / 29.4, of 64 over 30 / 24.6; 256 rows 2 / 16 steps 3.9 / 7.4.
 template <typename T, int D, int FORM>
 static np_status launch_append8_steps(Append8Params& p, cudaStream_t s) {
   if (p.tokens < 512) return launch_append8<T, D, FORM, 2>(p, s);

@@ -31,6 +31,19 @@
 // equal share per block, one block an SM, from the context lengths on the device.
 // A row inside one block is stored directly; one that is cut leaves partials
 // that a second launch joins in block order.
+//
+// Bound: HBM on long rows (16 rows of 32768-131072 positions, 64 / 8 heads: 458 us, 6.8
+// TB/s).  Shorter ones pay what runs once: about 5 us until the first chunk is there, 3 at
+// each row's end, 6 for the join (64 rows of 1024-8192: 99 us, 82 at the copy rate; 8 fp32
+// rows of 512-2048: 20, latency throughout).  More than eight rows a head take two column
+// tiles, whose sums leave registers for eight warps only: 4 query tokens of 4 heads, int8,
+// 125-130 us against 86; the issue slots are half used and each warp waits for its own
+// products.  Why warps that read for themselves: the loop's copies, widening and products
+// overlap across 16 warps without a barrier, and a stage is 4 KB, so that three of them a
+// warp keep 130 KB an SM on the way.  Measured against: table look-ups in line with the copies
+// and each row of a segment's end by itself 110 us (64 rows); copies of chunks inside one
+// block in a branch of their own 159 us for 146 (4 tokens: the branch keeps the copies from
+// being scheduled among the products); join with one block an SM 137 us for 125.
 #include <type_traits>
 
 #include "cache8.cuh"
@@ -743,7 +756,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
 // that hold a piece, in block order: 32 pieces' m and l in one round, then their rows of O,
 // eight loads in flight.  Bound by the latency of those rounds (the partials are in L2).
 constexpr int kQ8JoinThreads = 256;
-constexpr int kQ8JoinGrid = 4;  // blocks an SM
+constexpr int kQ8JoinGrid = 4;  // blocks an SM: 64 rows 102, 100, 99, 101 us with 1, 2, 4, 6
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __grid_constant__

@@ -80,6 +80,8 @@ np_status launch_decode_q8(DecodeQ8Params& p, int32_t head_dim, np_dtype t, np_f
   p.head_group = 1;
   for (int h = 2; h <= 8 && h <= warps; ++h)
     if (p.kv_heads % h == 0) p.head_group = h;
+  // Two chunks a warp at least, us with 1, 2, 3, 4: 8 fp32 rows of 512-2048 21.6, 20.3, 21.2,
+  // 22.2; one row of 4000 23.0, 17.1, 17.2, 17.0; 16 of 300-600 16.0, 16.9, 17.7, 19.1.
   p.least = 2 * (warps / p.head_group);
   const bool e4m3 = form == NP_E4M3;
   switch (head_dim) {

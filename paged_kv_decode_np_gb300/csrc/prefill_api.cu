@@ -405,7 +405,8 @@ extern "C" np_status np_paged_prefill_q8_packed(const np_read_q8_args* a) {
   const np_dtype dtype = static_cast<np_dtype>(a->dtype);
   const np_form8 form = static_cast<np_form8>(a->form);
   // Rows with few tokens go to the decode read's kernel: their (token, head) rows fit
-  // one fetch of its tile.  Two launches more, so where rows are short on average.
+  // one fetch of its tile.  Two launches more (about 5 us), so where rows are short on
+  // average: 62 rows of one token and two of 512 305 us without, 229 with.
   const int few = (p.group <= 8 ? 8 : 16) / p.group;
   int64_t work = 0;
   if ((p.rows > 1 ? p.tokens < 64ll * p.rows : p.tokens <= few) &&

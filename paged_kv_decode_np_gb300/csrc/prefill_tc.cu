@@ -52,6 +52,10 @@
 // int8 2^-24) and beyond that to 2^-33 of the tile's largest value.  q is fp16 as well,
 // each row times a power of two that brings its largest element to 2^14 .. 2^15; the same
 // four warps turn it in place.
+// 1024 tokens of 65536, 64 / 8 heads: 1.77 ms, 1230 TFLOP/s (the bf16 pools' kernel takes
+// about 1.65); the four warps take ~1000 cycles a tile and the softmax 10 % longer beside
+// them.  (Widened to bf16 by six instructions a pair, all pieces unrolled 3.63 ms: their
+// fetching stalled everybody; rolled 2.93.)
 // Token by token, six warps widen to bf16 with the scales multiplied in, exactly: they
 // take the 8-token groups of the tiles in turn, each group through a ring of the warp's
 // own, filled by asynchronous copies of which every lane reads back its own alone.

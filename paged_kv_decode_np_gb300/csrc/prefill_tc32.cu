@@ -39,7 +39,8 @@
 //
 // An 8-bit cache (FORM, compiled apart): a code times its scale, a power of two, is
 // one bf16 number, so K and V are their first part alone: q's three parts times K into
-// one S of 64 columns, P's three parts times V, exact products all of them.
+// one S of 64 columns, P's three parts times V, exact products all of them.  Eight chunks of
+// 64-192 tokens over 512-2048 positions: 118 us (954 on the FMA pipes), 2.5e-7 off.
 #include <limits.h>
 
 #include <type_traits>
