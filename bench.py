@@ -95,11 +95,12 @@ def measured_peak() -> tuple[float, str]:
 
 
 def kernel_sources_hash() -> str:
-    """Of the decode step's sources: the prompt side's files are none of it."""
+    """Of the decode step's sources: the prompt side's files and the 8-bit cache's are none of it."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "paged_kv_decode_np_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.startswith(("prefill", "rope_append", "tcgen05")):
+        if f.startswith(("prefill", "rope_append", "tcgen05", "append_q8", "block_map", "cache8",
+                         "decode_q8", "host_checks")):
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())
