@@ -382,8 +382,8 @@ np_status np_block_map(int32_t* block_tables, int32_t max_blocks_per_row,
  * Values past QMAX 2^60 become the largest code; so do infinities, which do
  * not count in A; NaN becomes NaN in e4m3 and 0 in int8 (all three but the
  * first: NP_FLAG_VALUE).
- * dtype NP_F32 or NP_BF16; head_dim as in the list above; any block_size and
- * kv_heads.  Pointers 16-byte aligned, strides a multiple of 16 bytes, at least
+ * dtype NP_F32 or NP_BF16; head_dim as in the list above; any block_size;
+ * kv_heads up to 4096.  Pointers 16-byte aligned (scales, in every call: 4), strides a multiple of 16 bytes, at least
  * a token's heads.  The pools and scales must not overlap one another, nor what is
  * read.  num_tokens == 0 is a no-op.
  */
@@ -523,6 +523,7 @@ typedef struct np_read_q8_args {
 np_status np_paged_decode_q8_packed(const np_read_q8_args* args);
 np_status np_paged_prefill_q8_packed(const np_read_q8_args* args);
 /* as np_paged_prefill_check */
+np_status np_paged_decode_q8_check(const np_read_q8_args* args);
 np_status np_paged_prefill_q8_check(const np_read_q8_args* args);
 
 /*

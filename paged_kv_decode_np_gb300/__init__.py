@@ -181,7 +181,7 @@ def _declare_prompt(lib: ctypes.CDLL) -> None:
 
 def _declare_q8(lib: ctypes.CDLL) -> None:
     for name in ("np_block_map_packed", "np_kv_append_q8_packed", "np_paged_decode_q8_packed",
-                 "np_paged_prefill_q8_packed", "np_paged_prefill_q8_check"):
+                 "np_paged_decode_q8_check", "np_paged_prefill_q8_packed", "np_paged_prefill_q8_check"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.c_char_p]
@@ -752,15 +752,24 @@ def np_paged_decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, c
                        workspace, err_word=None, stream=None):
     """The decode read of an 8-bit cache (see np_paged.h): q/out [rows, q_heads, head_dim], or
     [rows, query_len, q_heads, head_dim] (the rows' last query_len positions), bf16 or fp32."""
+    _launch_decode_q8(_decode_q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                                      context_lens, scale, workspace, err_word, stream))
+
+
+def _decode_q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                    workspace, err_word, stream) -> bytes:
     name = "np_paged_decode_q8"
     rows, qn, _, _ = _q_shape(q)
     if block_tables.dim() == 2 and block_tables.shape[0] != rows:
         raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
-    st = load().np_paged_decode_q8_packed(_read_q8_args(
-        name, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, None, scale,
-        workspace, err_word, stream, qn, rows * qn))
+    return _read_q8_args(name, out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                         context_lens, None, scale, workspace, err_word, stream, qn, rows * qn)
+
+
+def _launch_decode_q8(packed: bytes) -> None:
+    st = load().np_paged_decode_q8_packed(packed)
     if st != NP_OK:
-        raise NPError(st, name)
+        raise NPError(st, "np_paged_decode_q8")
 
 
 def np_paged_prefill_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
@@ -794,14 +803,18 @@ def decode_step_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, conte
                    stream=None):
     """One decode step of an 8-bit cache: the rows' new K/V ([rows, kv_heads, head_dim], or
     [rows, query_len, kv_heads, head_dim] with slots [rows, query_len]) appended, if given, then
-    the read."""
+    the read.  What the read refuses is refused before the append."""
+    read = _decode_q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens,
+                           scale, workspace, err_word, stream)
     if k_new is not None:
+        st = load().np_paged_decode_q8_check(read)
+        if st != NP_OK:
+            raise NPError(st, "np_paged_decode_q8")
         if k_new.dim() == 4:
             k_new, v_new = k_new.flatten(0, 1), v_new.flatten(0, 1)
         np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping.flatten(),
                         err_word, stream)
-    np_paged_decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
-                       workspace, err_word, stream)
+    _launch_decode_q8(read)
 
 
 def prefill_step_q8(out, q, k_new, v_new, slot_mapping, k_pool, v_pool, k_scale, v_scale,

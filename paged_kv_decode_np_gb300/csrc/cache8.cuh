@@ -33,7 +33,6 @@ struct Form8<NP_E4M3> {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
   }
-  // (A NaN is all ones in both; cvt keeps its sign out.)
   // the two low codes of w as fp16, exact
   __device__ __forceinline__ static uint32_t half_lo(uint32_t w) {
     uint32_t r;

@@ -52,10 +52,9 @@ np_status check_decode_q8(const np_read_q8_args& a, bool* run) {
   if (a.rows == 0) return NP_OK;
   if (!a.out || !a.q || !a.k_pool || !a.v_pool || !a.k_scale || !a.v_scale || !a.block_tables || !a.context_lens)
     return NP_ERR_INVALID_ARG;
-  for (const void* x : {static_cast<const void*>(a.out), a.q, a.k_pool, a.v_pool,
-                        static_cast<const void*>(a.k_scale), static_cast<const void*>(a.v_scale)})
+  for (const void* x : {static_cast<const void*>(a.out), a.q, a.k_pool, a.v_pool})
     if (!aligned_to(x, 16)) return NP_ERR_INVALID_ARG;
-  if (!aligned_to(a.block_tables, 4) || !aligned_to(a.context_lens, 4) || !aligned_to(a.err_word, 4))
+  if (!aligned_to(a.k_scale, 4) || !aligned_to(a.v_scale, 4) || !aligned_to(a.block_tables, 4) || !aligned_to(a.context_lens, 4) || !aligned_to(a.err_word, 4))
     return NP_ERR_INVALID_ARG;
   const Span spans[] = {{a.out, qn}, {a.q, qn}, {a.k_pool, pool}, {a.v_pool, pool}, {a.k_scale, scales},
                         {a.v_scale, scales}, {a.block_tables, tab}, {a.context_lens, 4ll * a.rows}};
@@ -98,6 +97,11 @@ np_status launch_decode_q8(DecodeQ8Params& p, int32_t head_dim, np_dtype t, np_f
 
 extern "C" size_t np_paged_decode_q8_workspace_bytes(int32_t head_dim) {
   return head_dim_ok(head_dim) ? npk::q8_workspace_bytes(head_dim) : 0;
+}
+
+extern "C" np_status np_paged_decode_q8_check(const np_read_q8_args* a) {
+  bool run;
+  return a ? check_decode_q8(*a, &run) : NP_ERR_INVALID_ARG;
 }
 
 extern "C" np_status np_paged_decode_q8_packed(const np_read_q8_args* a) {

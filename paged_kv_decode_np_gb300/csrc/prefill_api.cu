@@ -377,7 +377,7 @@ np_status check_prefill_q8(const np_read_q8_args& a, bool* run) {
   *run = false;
   int64_t scales = 0;
   if (!mul_ok(a.num_blocks, 4ll * a.kv_heads, &scales)) return NP_ERR_OUT_OF_RANGE;
-  if (!a.k_scale || !a.v_scale || !aligned(a.k_scale, 16) || !aligned(a.v_scale, 16)) return NP_ERR_INVALID_ARG;
+  if (!a.k_scale || !a.v_scale || !aligned(a.k_scale, 4) || !aligned(a.v_scale, 4)) return NP_ERR_INVALID_ARG;
   const int64_t out = (int64_t)a.num_tokens * a.q_heads * a.head_dim * (a.dtype == NP_BF16 ? 2 : 4);
   if (overlap(a.out, out, a.k_scale, scales) || overlap(a.out, out, a.v_scale, scales)) return NP_ERR_INVALID_ARG;
   *run = true;

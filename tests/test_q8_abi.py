@@ -67,7 +67,9 @@ def test_append_refusals(lib):
     assert _append(lib, n=0) == 0
     for name in ("kp", "vp", "ks", "vs", "k", "v", "sm"):
         assert _append(lib, **{name: None}) == 1, name
-        assert _append(lib, **{name: FAKE + 8 * MB + 4}) == 1, name
+        assert _append(lib, **{name: FAKE + 8 * MB + 2}) == 1, name
+    assert _append(lib, kp=FAKE + 8 * MB + 4) == 1
+    assert _append(lib, hk=4097) == 2
     assert _append(lib, n=-1) == 1
     assert _append(lib, form=2) == 2
     assert _append(lib, dtype=2) == 2
@@ -100,8 +102,8 @@ def _read(lib, call="np_paged_decode_q8_packed", **kw):
         a["scale"]))
 
 
-@pytest.mark.parametrize("call", ["np_paged_decode_q8_packed", "np_paged_prefill_q8_packed",
-                                  "np_paged_prefill_q8_check"])
+@pytest.mark.parametrize("call", ["np_paged_decode_q8_packed", "np_paged_decode_q8_check",
+                                  "np_paged_prefill_q8_packed", "np_paged_prefill_q8_check"])
 def test_read_refusals(lib, call):
     def read(**kw):
         return _read(lib, call, **kw)

@@ -187,3 +187,37 @@ def test_tensors_off_the_current_device_are_refused(nplib):
     with pytest.raises(ValueError, match="contiguous"):
         nplib.np_paged_decode_q8(out, inp["q"], inp["k_pool"], inp["v_pool"], inp["k_scale"].T.contiguous().T,
                                  inp["v_scale"], inp["block_tables"], inp["context_lens"], 0.1, ws)
+
+
+def test_a_refused_step_has_written_nothing(nplib):
+    """What the read or the attention refuses (too small a workspace, too many heads a kv head) is
+    refused before the append; scales may begin on any four bytes."""
+    npg = nplib
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kp, vp, _, _ = npg.q8_pools(3, 16, 1, 64)
+    layers = torch.zeros(2, 3, 1, device="cuda")  # a layer's scales: 12 bytes apart
+    cache = (kp, vp, layers[1], torch.zeros(3, 1, device="cuda"))
+    before = [t.view(torch.uint8).clone() if t.dtype is not torch.float32 else t.clone() for t in cache]
+    k = torch.randn(2, 1, 64, device="cuda", dtype=torch.bfloat16)
+    slots = torch.tensor([0, 16], device="cuda")
+    tables, lens = torch.tensor([[0], [1]], **i32), torch.ones(2, **i32)
+    starts = torch.tensor([0, 1, 2], **i32)
+    small = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    for heads, ws in ((4, small), (17, npg.decode_q8_workspace(64))):
+        q = torch.randn(2, heads, 64, device="cuda", dtype=torch.bfloat16)
+        with pytest.raises(npg.NPError):
+            npg.decode_step_q8(torch.empty_like(q), q, *cache, tables, lens, 0.1, ws, k_new=k, v_new=k,
+                               slot_mapping=slots)
+        with pytest.raises(npg.NPError):
+            npg.prefill_step_q8(torch.empty_like(q), q, k, k, slots, *cache, tables, lens, starts, 0.1,
+                                small if ws is small else npg.prefill_workspace(64))
+    torch.cuda.synchronize()
+    for t, x in zip(cache, before):
+        assert torch.equal(t.view(torch.uint8) if t.dtype is not torch.float32 else t, x)
+    q = torch.randn(2, 4, 64, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty_like(q)
+    npg.decode_step_q8(out, q, *cache, tables, lens, 0.1, npg.decode_q8_workspace(64), k_new=k, v_new=k,
+                       slot_mapping=slots)
+    # one position a row: its own value, by e4m3's half step, then bf16's
+    assert ((out.double() - k.double()).abs() <= k.double().abs() * (2.0 ** -4 + 2.0 ** -8) * 1.01 + 2.0 ** -16).all()
+    assert (layers[0] == 0).all() and (layers[1, :2] > 0).all() and (layers[1, 2] == 0).all()
