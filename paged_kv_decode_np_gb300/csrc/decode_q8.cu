@@ -37,7 +37,7 @@
 // each row's end, 6 for the join (64 rows of 1024-8192: 99 us, 82 at the copy rate; 8 fp32
 // rows of 512-2048: 20, latency throughout).  More than eight rows a head take two column
 // tiles, whose sums leave registers for eight warps only: 4 query tokens of 4 heads, int8,
-// 125-130 us against 86; the issue slots are half used and each warp waits for its own
+// 127 us against 86; the issue slots are half used and each warp waits for its own
 // products.  Why warps that read for themselves: the loop's copies, widening and products
 // overlap across 16 warps without a barrier, and a stage is 4 KB, so that three of them a
 // warp keep 130 KB an SM on the way.  Measured against: table look-ups in line with the copies
@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   float qs[NT][2];        // scale of rows 2 t4, + 1
   int32_t lim[NT][2];     // the first position each does not see
   int32_t all_see = 0;    // positions before it: every row
-  float m[NT][2], l[NT][2];
+  // of rows 2 t4, + 1: UP - M, what x - M may not pass (-inf: no M yet), the sum
+  constexpr float UP = F32 ? 0.f : 6.f;
+  float off[NT][2], top[NT][2], l[NT][2];
   int last = -1;          // the stage read last in this segment; -1: none yet
   bool first = true;
 
@@ -434,7 +436,8 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      off[nt][0] = off[nt][1] = UP;
+      top[nt][0] = top[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
     all_see = w.c - qr.n + 1;
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           x += __shfl_xor_sync(FULL, x, 16);
           const int row = nt * 8 + 2 * t4 + c;
           if (g == 0) {
-            e[row] = m[nt][c];
+            e[row] = top[nt][c] == -INFINITY ? -INFINITY : UP - off[nt][c];
             e[MR + row] = x;
           }
           float* orow = e + 2 * MR + row * LD;
@@ -635,21 +638,18 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         const float va = (float)ea, vb = (float)eb, ia = pow2f(-ea), ib = pow2f(-eb);
         const bool edge = t0 + sub + 16 > all_see;  // uniform
         // x - M (+ UP), with one rounding; M is a whole number
-        constexpr float UP = F32 ? 0.f : 6.f;
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const bool none = m[nt][c] == -INFINITY;
-            const float ref = none ? -UP : m[nt][c] - UP;
-            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], va - ref);
-            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], vb - ref);
+            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], va + off[nt][c]);
+            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], vb + off[nt][c]);
             if (edge) {
               if (t0 + sub + g >= lim[nt][c]) s[nt][c] = -INFINITY;
               if (t0 + sub + g + 8 >= lim[nt][c]) s[nt][2 + c] = -INFINITY;
             }
-            grow |= fmaxf(s[nt][c], s[nt][2 + c]) > (none ? -INFINITY : kAbove + UP);
+            grow |= fmaxf(s[nt][c], s[nt][2 + c]) > top[nt][c];
           }
         }
         if (__any_sync(FULL, grow)) {
@@ -661,11 +661,11 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
-              const bool none = m[nt][c] == -INFINITY;
-              if (x > (none ? -INFINITY : kAbove + UP)) {
+              if (x > top[nt][c]) {
                 x = ceilf(x - UP);
-                const float f = none ? 0.f : ex2(-x);
-                m[nt][c] = none ? x : m[nt][c] + x;
+                const float f = top[nt][c] == -INFINITY ? 0.f : ex2(-x);
+                off[nt][c] -= x;
+                top[nt][c] = kAbove + UP;
                 s[nt][c] -= x;
                 s[nt][2 + c] -= x;
                 l[nt][c] *= f;
