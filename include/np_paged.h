@@ -413,7 +413,9 @@ np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
  * scaled by a power of two first (bf16 is then exact but below 2^-28 of the
  * row's largest element); a weight is rounded to fp16 for its product with V,
  * bf16 out; for fp32, q and the weights are two fp16 parts each (22 bits).  The
- * softmax and its sums are fp32.
+ * softmax and its sums are fp32.  A weight is the softmax's times V's scale: one
+ * below 2^-30 of the row's largest adds nothing to the sum over V, and its full
+ * share to the softmax's, however far the scales lie apart.
  * Slots past a row's context are never part of a result; no element of its context may
  * be NaN (where a query token does not see the position either).  Supported: dtype
  * NP_F32 (g * query_len <= 8) or NP_BF16 (<= 16), g = q_heads / kv_heads; head_dim

@@ -3,14 +3,16 @@
 //
 // Per row, kv head and its MR = G Q (query token, head) rows, with codes k, v and
 // exponents a, b of their scales:
-//     x_j = c (q . k_j) 2^a_j + b_j                (log2 units; c = scale log2 e)
-//     O  = sum_j 2^(x_j - M) v_j,   l = sum_j 2^(x_j - M - b_j),   out = O / l
-// so V's scale is an addition to the exponent, and its product stays a product
-// of codes.  M is a whole number, the largest x rounded up, and replaced only where an x
-// passes it by more than 8; x - M then has one rounding, and M's changes are exact powers
-// of two.  Weights are taken 2^6 larger (both sums are; bf16: in the exponent, fp32: as a
-// factor, so that x - M keeps its small steps): they stay within fp16's 2^15, and what is
-// too small for its subnormals is below 2^-30 of the largest.
+//     y_j = c (q . k_j) 2^a_j - M                  (log2 units; c = scale log2 e)
+//     O  = sum_j 2^(y_j + b_j) v_j,   l = sum_j 2^y_j,   out = O / l
+// so V's scale is a power of two at the weight, and its product stays a product
+// of codes.  M is a whole number, the largest y + M + b rounded up, and replaced only where
+// one passes it by more than 8; y then has one rounding, and M's changes are exact powers
+// of two.  Weights are taken 2^6 larger: they stay within fp16's 2^15, and what is too small
+// for its subnormals is below 2^-30 of the largest.  The exponential is l's term and the
+// weight its product with 2^(b + 6), not the other way round: M is at most 60 above the
+// largest score and 2^y leaves fp32's range only below 2^-66 of the largest term of l, while
+// 2^(y + b) may be 2^-120 of O's largest where V's scales lie that far apart.
 //
 // The products are m16n8k16 mma (fp16 in, fp32 out) with the cache as the A
 // operand -- 16 tokens x 16 dims of K, 16 dims x 16 tokens of V -- and the rows
@@ -56,7 +58,14 @@
 
 namespace npk {
 
-constexpr float kAbove = 8.f, kWeight = 64.f;
+constexpr float kAbove = 8.f;
+constexpr int kWeightExp = 6;
+
+// x 2^d, d <= 0: in two steps, for 2^d alone may be no number where x 2^d is one (l and its
+// partials reach 2^68 per position).
+__device__ __forceinline__ float scaled_down(float x, float d) {
+  return x * ex2(fmaxf(d, -100.f)) * ex2(fminf(d + 100.f, 0.f));
+}
 
 // Geometry of a stage.  Rows of D bytes; 128-byte lines; 16-byte pieces of a line are
 // swizzled so that both products' reads are free of bank conflicts.
@@ -382,8 +391,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
   float qs[NT][2];        // scale of rows 2 t4, + 1
   int32_t lim[NT][2];     // the first position each does not see
   int32_t all_see = 0;    // positions before it: every row
-  // of rows 2 t4, + 1: UP - M, what x - M may not pass (-inf: no M yet), the sum
-  constexpr float UP = F32 ? 0.f : 6.f;
+  // of rows 2 t4, + 1: -M, what y + b may not pass (-inf: no M yet), the sum
   float off[NT][2], top[NT][2], l[NT][2];
   int last = -1;          // the stage read last in this segment; -1: none yet
   bool first = true;
@@ -436,7 +444,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-      off[nt][0] = off[nt][1] = UP;
+      off[nt][0] = off[nt][1] = 0.f;
       top[nt][0] = top[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
@@ -461,8 +469,8 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           x += __shfl_xor_sync(FULL, x, 16);
           const int row = nt * 8 + 2 * t4 + c;
           if (g == 0) {
-            e[row] = top[nt][c] == -INFINITY ? -INFINITY : UP - off[nt][c];
-            e[MR + row] = x;
+            e[row] = top[nt][c] == -INFINITY ? -INFINITY : -off[nt][c];
+            e[MR + row] = x * pow2f(kWeightExp);  // (as O is)
           }
           float* orow = e + 2 * MR + row * LD;
 #pragma unroll
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
       for (unsigned k = has; k != 0; k &= k - 1) {
         const float* e = reinterpret_cast<const float*>(q8_smem + __shfl_sync(FULL, at, __ffs(k) - 1));
         const float mx = fmaxf(M, e[mine]), ref = mx == -INFINITY ? 0.f : mx;
-        L = fmaf(ex2(e[mine] - ref), e[MR + mine], L * ex2(M - ref));
+        L = scaled_down(e[MR + mine], e[mine] - ref) + scaled_down(L, M - ref);
         M = mx;
       }
       const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -635,21 +643,21 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         lds<1>(st + 2 * CT * D + 4 * (CT + sub + g + 8), &sc[3]);
         const float ka = pow2f(scale_exp(sc[0])), kb = pow2f(scale_exp(sc[1]));
         const int ea = scale_exp(sc[2]), eb = scale_exp(sc[3]);
-        const float va = (float)ea, vb = (float)eb, ia = pow2f(-ea), ib = pow2f(-eb);
+        const float va = (float)ea, vb = (float)eb, wa = pow2f(ea + kWeightExp), wb = pow2f(eb + kWeightExp);
         const bool edge = t0 + sub + 16 > all_see;  // uniform
-        // x - M (+ UP), with one rounding; M is a whole number
+        // y, with one rounding; M is a whole number
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], va + off[nt][c]);
-            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], vb + off[nt][c]);
+            s[nt][c] = fmaf(s[nt][c], ka * qs[nt][c], off[nt][c]);
+            s[nt][2 + c] = fmaf(s[nt][2 + c], kb * qs[nt][c], off[nt][c]);
             if (edge) {
               if (t0 + sub + g >= lim[nt][c]) s[nt][c] = -INFINITY;
               if (t0 + sub + g + 8 >= lim[nt][c]) s[nt][2 + c] = -INFINITY;
             }
-            grow |= fmaxf(s[nt][c], s[nt][2 + c]) > top[nt][c];
+            grow |= fmaxf(s[nt][c] + va, s[nt][2 + c] + vb) > top[nt][c];
           }
         }
         if (__any_sync(FULL, grow)) {
@@ -657,18 +665,18 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float x = fmaxf(s[nt][c], s[nt][2 + c]);
+              float x = fmaxf(s[nt][c] + va, s[nt][2 + c] + vb);
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
               x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
               if (x > top[nt][c]) {
-                x = ceilf(x - UP);
+                x = ceilf(x);
                 const float f = top[nt][c] == -INFINITY ? 0.f : ex2(-x);
+                l[nt][c] = top[nt][c] == -INFINITY ? 0.f : scaled_down(l[nt][c], -x);
                 off[nt][c] -= x;
-                top[nt][c] = kAbove + UP;
+                top[nt][c] = kAbove;
                 s[nt][c] -= x;
                 s[nt][2 + c] -= x;
-                l[nt][c] *= f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                   o[nt][i][c] *= f;
@@ -683,9 +691,11 @@ __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            s[nt][c] = ex2(s[nt][c]) * (F32 ? kWeight : 1.f);
-            s[nt][2 + c] = ex2(s[nt][2 + c]) * (F32 ? kWeight : 1.f);
-            l[nt][c] = fmaf(s[nt][c], ia, fmaf(s[nt][2 + c], ib, l[nt][c]));
+            s[nt][c] = ex2(s[nt][c]);
+            s[nt][2 + c] = ex2(s[nt][2 + c]);
+            l[nt][c] += s[nt][c] + s[nt][2 + c];
+            s[nt][c] *= wa;
+            s[nt][2 + c] *= wb;
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -822,11 +832,11 @@ __global__ void __launch_bounds__(kQ8JoinThreads) decode_q8_join_kernel(const __
       mx = fmaxf(mx, M);
       const float ref = mx == -INFINITY ? 0.f : mx;
       const float f = ex2(M - ref), a = ex2(m - ref);
-      M = mx;
-      float sum = a * l;
+      float sum = scaled_down(l, m - ref);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-      L = fmaf(L, f, sum);
+      L = scaled_down(L, M - ref) + sum;
+      M = mx;
 #pragma unroll
       for (int v = 0; v < DV; ++v) {
         acc[v][0] *= f;
