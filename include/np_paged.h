@@ -445,12 +445,12 @@ np_status np_paged_decode_q8(void* out, const void* q, np_dtype dtype,
  * other arguments, limits and errors as np_paged_prefill's (no element of a row's c
  * positions may be NaN).
  * Arithmetic, fp32 sums and softmax throughout.  bf16, head_dim 64 and up, block_size
- * a multiple of 8: fp16 products; q times a power of two, codes exact but where
- * their block's scale is over 2^15 (e4m3; int8 2^24) below the largest of the 128 (head_dim 256:
- * 64) positions around, there to 2^-33 of those positions' largest value; weights
- * rounded to fp16.  Other bf16 calls: codes times scales exact in bf16, weights rounded to bf16.  fp32:
- * fp32 products (to head_dim 128 as exact products of bf16 parts).  Where num_tokens < 64 rows, rows with at most 8 / g tokens (g > 8:
- * one) are read as np_paged_decode_q8 reads them.
+ * a multiple of 8: fp16 products; q times a power of two, codes exact; weights (the
+ * softmax's times V's scale) rounded to fp16, those below 2^-26 of the row's largest add
+ * nothing to the sum over V.  Other bf16 calls: codes times scales exact in bf16,
+ * weights rounded to bf16.  fp32: fp32 products (to head_dim 128 as exact products of
+ * bf16 parts).  Where num_tokens < 64 rows, rows with at most 8 / g tokens (g > 8: one)
+ * are read as np_paged_decode_q8 reads them.
  * Two to five launches on `stream`; the same call gives the same bits.
  */
 np_status np_paged_prefill_q8(void* out, const void* q, np_dtype dtype,

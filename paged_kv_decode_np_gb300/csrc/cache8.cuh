@@ -127,12 +127,12 @@ struct Scaled8<NP_INT8> {
   __device__ __forceinline__ void widen_large(uint32_t&, uint32_t&) const {}
 };
 
-// Four codes as fp16, times 2^-d (d >= 0): exact where the result is no finer than fp16's
-// 2^-24.
+// Four codes as fp16, times 2^-d: exact to d = 15 (an e4m3 code is no finer than 2^-9, fp16
+// than 2^-24); the caller has smaller d only.
 template <int FORM>
 struct Below8;
 
-// 2^-d in both halves, d <= 126; 0 past 24
+// 2^-d in both halves
 __device__ __forceinline__ __half2 half_twice_below(uint32_t d) {
   return __float2half2_rn(__uint_as_float((127u - d) << 23));
 }

@@ -48,12 +48,14 @@
 // exponents (of its blocks' scales; one for K, one for V) stay apart from its values: K's
 // is a factor of the tile's scores, V's is added to the exponents of its weights and
 // taken back in l, as 2^(x + b) v and 2^x are a weight's two shares.  Blocks of smaller
-// scales are multiplied by what they are below the largest: exact down to 2^-15 (e4m3;
-// int8 2^-24) and beyond that to 2^-33 of the tile's largest value.  q is fp16 as well,
-// each row times a power of two that brings its largest element to 2^14 .. 2^15; the same
-// four warps turn it in place.
-// 1024 tokens of 65536, 64 / 8 heads: 1.77 ms, 1230 TFLOP/s (the bf16 pools' kernel takes
-// about 1.65); the four warps take ~1000 cycles a tile and the softmax 10 % longer beside
+// scales are multiplied by what they are below the largest, 2^-kWide at most, which is
+// exact.  In a tile whose scales lie further apart (it is wide) the codes stay as they are,
+// and the softmax takes the exponents group by group: a largest one that belongs to
+// positions without weight, or not yet seen, would push the others' values out of fp16's
+// range, and their weights too (tc_wide_tile).  q is fp16 as well, each row times a power of two
+// that brings its largest element to 2^14 .. 2^15; the same four warps turn it in place.
+// 1024 tokens of 65536, 64 / 8 heads: 1.83 ms, 1190 TFLOP/s, 60 us of it for telling wide
+// tiles from others; the four warps take ~1000 cycles a tile and the softmax 10 % longer beside
 // them.  (Widened to bf16 by six instructions a pair, all pieces unrolled 3.63 ms: their
 // fetching stalled everybody; rolled 2.93.)
 // Token by token, six warps widen to bf16 with the scales multiplied in, exactly: they
@@ -82,6 +84,10 @@ namespace npk {
 
 // How K and V come: bf16 token by token, bf16 by tiled copies; 8 bits (+ form) the same two ways
 enum : int { kTokens = 0, kTiled = 1, kQ8 = 2, kQ8Tiled = 4 };
+// How far the exponents of a tile's scales lie apart at most that are one factor's.  (Weights
+// lose as many bits at fp16's small end; a cache of tokens of one model is within two.  All
+// tiles wide: chunk 1024 of 65536 4.74 ms for 1.83.)
+constexpr int kWide = 4;
 // 0: bf16, 1: 8 bits token by token, 2: 8 bits by tiled copies
 __host__ __device__ constexpr int tc_kind(int kv) { return kv >= kQ8Tiled ? 2 : kv >= kQ8 ? 1 : 0; }
 
@@ -109,8 +115,11 @@ struct TcCfg {
   static constexpr int BARS = RAW_T + (KIND == 2 ? STG : 0);  // offset of the barriers
   static constexpr int RAW = BARS + 512;            // offset of the widening warps' rings
   // Q8T: raw rings (1024-byte aligned: swizzled copies), then barriers, a ring of the
-  // tiles' exponents (TE bytes a tile), the exponents of q's rows by segment parity
-  static constexpr int TE = 48, TILES = 16;
+  // tiles' exponents (TE bytes a tile: how far the groups' are below the tile's, K's and
+  // V's, 0 where it is wide; the tile's K and V exponent and whether it is wide; a wide
+  // one's groups, K's and V's), the exponents of q's rows by segment parity
+  static constexpr int TEK = 2 * (BN / 8), TEW = TEK + 4;
+  static constexpr int TE = (TEW + 2 * (BN / 8) + 3) / 4 * 4, TILES = RS + NS + 3 <= 8 ? 8 : 16;
   static constexpr int EXPS = BARS + 512, QEXP = EXPS + TILES * TE;
   static constexpr int SMEM = 1024 + (KIND == 2 ? QEXP + 2 * 128 * MT : RAW + STG);  // + up to 1024 of alignment
   static constexpr int THREADS = 128 * (MT + (Q8 ? 2 : 1));  // whole warpgroups: setmaxnreg is theirs
@@ -201,6 +210,74 @@ __device__ __forceinline__ bool tc_wait_beside(uint32_t bar, uint32_t parity, vo
       }
     }
   }
+}
+
+// A wide tile of the softmax, 16 columns at a time: x = c S 2^-k + b - v with the groups'
+// k and v in its place, its maximum, then weights 2^(x - m) and l's terms 2^(x - b + v - m).
+// Returns m and l.  (A function of its own: in line, its code made tiles that never run it a
+// fifth slower, chunk 1024 of 65536 2.21 ms.)
+template <int D>
+__device__ __noinline__ float2 tc_wide_tile(uint32_t s_at, uint32_t p_at, uint32_t o_at,
+                                            const volatile unsigned char* te, float row_scale, uint32_t tx,
+                                            int rel, bool any_o, float m, float l) {
+  constexpr int BN = TcCfg<D, 2>::BN;
+  const float c = row_scale * pow2f((signed char)(tx & 0xffu)), b = (float)(signed char)(tx >> 8);
+  float most = -INFINITY;
+#pragma unroll 1
+  for (int d = 0; d < BN; d += 16) {
+    uint32_t y[16];
+    tmem_ld16(s_at + d, y);
+    tmem_wait_ld();
+    tmem_pin<16>(y);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float cg = c * pow2f(-(int)te[d / 8 + g]), vg = b - (float)te[BN / 8 + d / 8 + g];
+#pragma unroll
+      for (int e = 8 * g; e < 8 * g + 8; ++e) {
+        const float x = d + e <= rel ? fmaf(__uint_as_float(y[e]), cg, vg) : -INFINITY;
+        most = fmaxf(most, x);
+        y[e] = __float_as_uint(x);
+      }
+    }
+    tmem_st16(s_at + d, y);
+  }
+  tmem_wait_st();
+  const bool grow = most > m + 14.f;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float f = grow ? ex2(m - (most - 6.f)) : 1.f;
+    if (grow) m = most - 6.f;
+    l *= f;
+#pragma unroll 1
+    for (int d = 0; any_o && d < D; d += 16) {
+      uint32_t o[16];
+      tmem_ld16(o_at + d, o);
+      tmem_wait_ld();
+      tmem_pin<16>(o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+      tmem_st16(o_at + d, o);
+    }
+    tmem_wait_st();
+  }
+  const float ref = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+  for (int d = 0; d < BN; d += 16) {
+    uint32_t y[16], pk[8];
+    tmem_ld16(s_at + d, y);
+    tmem_wait_ld();
+    tmem_pin<16>(y);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float lg = (float)te[BN / 8 + (d + e) / 8] - b + ref;
+      const float u = __uint_as_float(y[e]), v = __uint_as_float(y[e + 1]);
+      l += ex2(u + lg) + ex2(v + lg);
+      const __half2 hh = __floats2half2_rn(ex2(u + ref), ex2(v + ref));
+      pk[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+    }
+    tmem_st8(p_at + (d >> 1), pk);
+  }
+  tmem_wait_st();
+  return make_float2(m, l);
 }
 
 struct RingPos {
@@ -314,24 +391,44 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
         const uint32_t p_at = lanes + C::P0 + pb * (BN / 2);
         const int rel = lim - (w.kv0 + j) * BN;  // last visible column
         const bool masked = __any_sync(FULL, rel < BN - 1);
+        const volatile unsigned char* te = smem + C::EXPS + (tile0 + (uint32_t)j) % C::TILES * C::TE;
+        uint32_t tx = 0;
+        if constexpr (Q8T) {
+          // (before S is given back: the next segment's exponents may come after that)
+          if (j == 0)
+            row_scale *= pow2f(-(int)*reinterpret_cast<volatile signed char*>(
+                smem + C::QEXP + (segs & 1u) * (128 * MT) + t * 128 + row));
+          tx = *reinterpret_cast<const volatile uint32_t*>(te + C::TEK);
+          if (__builtin_expect(tx >> 16 != 0u, 0)) {  // uniform
+            if (single && j > 0) {  // as below
+              ok = __all_sync(FULL, mbar_wait(bar(B::pv_done), (pv + (uint32_t)j - 1u) & 1u, abort));
+              if (!ok) break;
+              tmem_fence_after();
+            }
+            const float2 ml = tc_wide_tile<D>(lanes, p_at, o_at, te + C::TEW, row_scale, tx, rel, j > 0, m, l);
+            m = ml.x;
+            l = ml.y;
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(B::s_read + t));
+              mbar_arrive(bar(B::p_full + pb));
+            }
+            continue;
+          }
+        }
         uint32_t r[BN];  // the row of S
 #pragma unroll
         for (int c = 0; c < BN; c += 32) tmem_ld32(lanes + c, r + c);
         tmem_wait_ld();
         tmem_pin<BN>(r);
         tmem_fence_before();
-        // (before S is given back: the next segment's exponents may come after that)
-        if (Q8T && j == 0)
-          row_scale *= pow2f(-(int)*reinterpret_cast<volatile signed char*>(
-              smem + C::QEXP + (segs & 1u) * (128 * MT) + t * 128 + row));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::s_read + t));
-        float c = row_scale, b = 0.f, back = 1.f;
+        float c = p.qscale, b = 0.f, back = 1.f;
         if constexpr (Q8T) {
-          const short te = *reinterpret_cast<volatile short*>(
-              smem + C::EXPS + (tile0 + (uint32_t)j) % C::TILES * C::TE + 2 * (BN / 8));
-          const int ke = (signed char)(te & 0xff), ve = te >> 8;
-          c = fmaxf(c * pow2f(ke), 1.2e-38f);  // (a masked score is -inf before it is scaled)
+          const int ke = (signed char)(tx & 0xffu), ve = (signed char)(tx >> 8);
+          c = fmaxf(row_scale * pow2f(ke), 1.2e-38f);  // (a masked score is -inf before it is scaled)
           b = (float)ve;
           back = pow2f(-ve);
         }
@@ -551,7 +648,7 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
               lds<4>(from + at, q[k]);
             }
           };
-          uint32_t below;  // how far the groups' scales are below the tile's, a byte each
+          uint32_t below;  // how far the groups' scales are below the tile's, a byte each (0: wide)
           {
             const uint32_t at = base + C::EXPS + te * C::TE + (isv ? BN / 8 : 0) + wc * GW;
             if constexpr (GW == 4) lds<1>(at, &below);
@@ -692,10 +789,9 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
     // ============================================================ raw tiles
     // One warp copies K's tiles, the other V's; lane i looks after 8-token group i, whose
     // block is looked up two tiles ahead.  K's warp also brings the tile's exponents, of
-    // K and V, a tile ahead: ring entry {how far each group's is below the tile's, K and
-    // V; the tile's}.  An entry is written TILES tiles after the one it replaces, whose
-    // readers are done: K's tile is at most RS + NS tiles before one whose scores have been
-    // read, and the softmax of the tile two before that is over.
+    // K and V, a tile ahead (TcCfg::TE).  An entry is written TILES tiles after the one it
+    // replaces, whose readers are done: K's tile is at most RS + NS tiles before one whose
+    // scores have been read, and the softmax of the tile two before that is over.
     if constexpr (Q8T) {
       constexpr int RS = C::RS;
       static_assert(RS + NS + 3 <= C::TILES, "ring of exponents");
@@ -761,12 +857,19 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
             const bool on = mine && lane * 8 < valid;
             const int ke = on ? scale_exp(ks0) : kScaleMin, ve = on ? scale_exp(vs0) : kScaleMin;
             const int kt = __reduce_max_sync(FULL, ke), vt = __reduce_max_sync(FULL, ve);
+            const int kd = on ? kt - ke : 0, vd = on ? vt - ve : 0;  // (past the context: masked)
+            const bool wide = __any_sync(FULL, kd > kWide || vd > kWide);
             unsigned char* te = smem + C::EXPS + tile % C::TILES * C::TE;
             if (mine) {
-              te[lane] = (unsigned char)(kt - ke);
-              te[BN / 8 + lane] = (unsigned char)(vt - ve);
+              te[lane] = (unsigned char)(wide ? 0 : kd);
+              te[BN / 8 + lane] = (unsigned char)(wide ? 0 : vd);
+              if (wide) {
+                te[C::TEW + lane] = (unsigned char)kd;
+                te[C::TEW + BN / 8 + lane] = (unsigned char)vd;
+              }
             }
-            if (lane == 0) *reinterpret_cast<short*>(te + 2 * (BN / 8)) = (short)((kt & 0xff) | (vt * 256));
+            if (lane == 0)
+              *reinterpret_cast<uint32_t*>(te + C::TEK) = (kt & 0xff) | (vt & 0xff) << 8 | (wide ? 0x10000 : 0);
             __syncwarp();
           }
           const int nbox = valid <= 0 ? 0 : (valid + p.box_tokens - 1) / p.box_tokens;
