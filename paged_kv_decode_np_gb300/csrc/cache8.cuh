@@ -17,6 +17,13 @@ __device__ __forceinline__ int scale_exp(uint32_t bits) {
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// x 2^d, d <= 0: in two steps, for 2^d alone may be no number where x 2^d is one (softmax
+// sums and their partials reach 2^74 per position: V's exponents are not in them, but in
+// their reference).
+__device__ __forceinline__ float scaled_down(float x, float d) {
+  return x * ex2(fminf(d + 100.f, 0.f)) * ex2(fmaxf(d, -100.f));
+}
+
 template <int FORM>
 struct Form8;
 

@@ -61,11 +61,6 @@ namespace npk {
 constexpr float kAbove = 8.f;
 constexpr int kWeightExp = 6;
 
-// x 2^d, d <= 0: in two steps, for 2^d alone may be no number where x 2^d is one (l and its
-// partials reach 2^68 per position).
-__device__ __forceinline__ float scaled_down(float x, float d) {
-  return x * ex2(fmaxf(d, -100.f)) * ex2(fminf(d + 100.f, 0.f));
-}
 
 // Geometry of a stage.  Rows of D bytes; 128-byte lines; 16-byte pieces of a line are
 // swizzled so that both products' reads are free of bank conflicts.

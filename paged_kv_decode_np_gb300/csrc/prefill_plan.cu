@@ -1,5 +1,6 @@
 // prefill_plan.cu -- the shares of np_paged_prefill's thread blocks, and the
 // join of the units that a share's end cuts.
+#include "cache8.cuh"
 #include "prefill.cuh"
 
 namespace npk {
@@ -129,7 +130,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
   for (int i = 0; i < np; ++i) M = fmaxf(M, ms[i][lane]);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int i = 0; i < np; ++i) L = fmaf(ex2(ms[i][lane] - ref), ls[i][lane], L);
+  for (int i = 0; i < np; ++i) {  // (in two steps: scaled_down's reason)
+    const float d = ms[i][lane] - ref;
+    L = fmaf(ex2(fmaxf(d, -100.f)), ls[i][lane] * ex2(fminf(d + 100.f, 0.f)), L);
+  }
   const float inv = L > 0.f ? 1.f / L : 0.f;
   constexpr int GW = D / 4 < WARPS ? 1 : D / 4 / WARPS;  // groups of 4 dims a warp
   const bool some = warp * GW < D / 4;

@@ -88,6 +88,11 @@ enum : int { kTokens = 0, kTiled = 1, kQ8 = 2, kQ8Tiled = 4 };
 // lose as many bits at fp16's small end; a cache of tokens of one model is within two.  All
 // tiles wide: chunk 1024 of 65536 4.74 ms for 1.83.)
 constexpr int kWide = 4;
+// How far V's may be from 0 in such a tile.  2^(x - m) is also l's term, times 2^-b: no number below
+// 2^-126, which m 60 above the largest score (another tile's b) and b = -20 reach for terms
+// below 2^-40 of the largest only, as does the factor of l where m grows.  Wide tiles form l's
+// terms without b.
+constexpr int kFar = 20;
 // 0: bf16, 1: 8 bits token by token, 2: 8 bits by tiled copies
 __host__ __device__ constexpr int tc_kind(int kv) { return kv >= kQ8Tiled ? 2 : kv >= kQ8 ? 1 : 0; }
 
@@ -244,9 +249,9 @@ __device__ __noinline__ float2 tc_wide_tile(uint32_t s_at, uint32_t p_at, uint32
   tmem_wait_st();
   const bool grow = most > m + 14.f;
   if (__any_sync(0xffffffffu, grow)) {
-    const float f = grow ? ex2(m - (most - 6.f)) : 1.f;
+    const float fe = grow ? m - (most - 6.f) : 0.f, f = ex2(fe);
     if (grow) m = most - 6.f;
-    l *= f;
+    l = scaled_down(l, fe);
 #pragma unroll 1
     for (int d = 0; any_o && d < D; d += 16) {
       uint32_t o[16];
@@ -858,7 +863,8 @@ __global__ void __launch_bounds__(TcCfg<D, tc_kind(KV)>::THREADS, 1)
             const int ke = on ? scale_exp(ks0) : kScaleMin, ve = on ? scale_exp(vs0) : kScaleMin;
             const int kt = __reduce_max_sync(FULL, ke), vt = __reduce_max_sync(FULL, ve);
             const int kd = on ? kt - ke : 0, vd = on ? vt - ve : 0;  // (past the context: masked)
-            const bool wide = __any_sync(FULL, kd > kWide || vd > kWide);
+            const bool far = on && (unsigned)(ve + kFar) > 2u * kFar;
+            const bool wide = __any_sync(FULL, kd > kWide || vd > kWide || far);
             unsigned char* te = smem + C::EXPS + tile % C::TILES * C::TE;
             if (mine) {
               te[lane] = (unsigned char)(wide ? 0 : kd);

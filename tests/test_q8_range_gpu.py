@@ -148,3 +148,16 @@ def test_large_values_without_weight_change_nothing(nplib, dtype, d, form, n, e)
     # the same row without the blocks: the same formula but for weights of e^-655
     _within(few, [(n, 1000 - 32)], 0.02, out, dtype)
     assert (ref - out).isfinite().all() and bound[0].isfinite().all()
+
+
+@FORMS
+@TYPES
+@pytest.mark.parametrize("n", [1, 20, 300])
+@pytest.mark.parametrize("top,low,c,where,gap", SPREADS)
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 16), (256, 16), (128, 5)])
+def test_chunks_count_positions_whose_v_is_far_smaller(nplib, dtype, form, d, bs, n, top, low, c, where, gap):
+    if c < n:
+        n = c
+    inp, scale = _zero_v_beside_large_v(dtype, form, d, bs, n, c, top, low, where, gap)
+    out = _prefill(nplib, inp, scale)
+    _within(inp, [(n, c)], scale, out, dtype)
