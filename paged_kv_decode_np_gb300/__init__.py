@@ -798,6 +798,21 @@ def _launch_prefill_q8(packed: bytes) -> None:
         raise NPError(st, "np_paged_prefill_q8")
 
 
+def _flat_tokens(t: torch.Tensor, stream) -> torch.Tensor:
+    """``t`` with its first two dims as one.  Where that is no view (a slice of padded rows), a copy
+    that is made on ``stream``, and belongs to it: the call reads it there."""
+    try:
+        return t.view(-1, *t.shape[2:]) if t.numel() else t.flatten(0, 1)
+    except RuntimeError:
+        pass
+    if stream is None:
+        return t.flatten(0, 1)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return t.flatten(0, 1)
+
+
 def decode_step_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
                    workspace, *, k_new=None, v_new=None, slot_mapping=None, err_word=None,
                    stream=None):
@@ -811,9 +826,11 @@ def decode_step_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, conte
         if st != NP_OK:
             raise NPError(st, "np_paged_decode_q8")
         if k_new.dim() == 4:
-            k_new, v_new = k_new.flatten(0, 1), v_new.flatten(0, 1)
-        np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping.flatten(),
-                        err_word, stream)
+            k_new, v_new = _flat_tokens(k_new, stream), _flat_tokens(v_new, stream)
+        if slot_mapping.dim() == 2:
+            slot_mapping = _flat_tokens(slot_mapping, stream)
+        np_kv_append_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slot_mapping, err_word,
+                        stream)
     _launch_decode_q8(read)
 
 
