@@ -347,7 +347,9 @@ np_status np_paged_prefill_check(const np_paged_prefill_args* args);
  * free list or num_tokens has no room for and the rows after it
  * (NP_FLAG_BLOCKS, NP_FLAG_QUERY); such a row still keeps min(c, kept).  A list
  * entry outside [0, num_blocks) becomes -1 in the table and its slots -1
- * (NP_FLAG_BLOCK_ID).  Up to 4096 rows; tables of up to 2^31 - 1025 tokens.  The
+ * (NP_FLAG_BLOCK_ID).  A table entry outside it that a row gives back is dropped
+ * (NP_FLAG_BLOCK_ID); where the step counted on it, the last entries taken are -1.
+ * Up to 4096 rows; tables of up to 2^31 - 1025 tokens.  The
  * arrays must not overlap but for kept_lens.  rows 0 with tokens: all of them
  * are past the last.
  */

@@ -209,24 +209,45 @@ __global__ void __launch_bounds__(kMapThreads) block_map_kernel(const __grid_con
   // the list after what is put there; what has no room (a count that was wrong) is dropped
   const int64_t full = (int64_t)held + given;
   if (full > p.num_blocks) flags |= NP_FLAG_BLOCKS;
-  const int32_t top = (int32_t)min(full, p.num_blocks);
+  int32_t top = (int32_t)min(full, p.num_blocks);
   if (tid == 0) {
     tok[p.rows] = tokens;
     take[p.rows] = taken;
     back[p.rows] = given;
     p.starts[p.rows] = tokens;
-    p.count[0] = max(top - taken, 0);
   }
   __syncthreads();
   auto need_of = [&](int r) { return ceil_div(base[r] + (tok[r + 1] - tok[r]), p.block_size); };
+  bool lost = false;
   for (int32_t e = tid; e < given; e += kMapThreads) {
     const int r = map_row(back, p.rows, e);
     int32_t* t = p.tables + (int64_t)r * p.max_blocks + need_of(r) + (e - back[r]);
     const int64_t to = (int64_t)held + given - 1 - e;
-    if (to < p.num_blocks) p.list[to] = *t;
+    const int32_t b = *t;
+    lost |= b < 0 || b >= p.num_blocks;
+    if (to < p.num_blocks) p.list[to] = b;
     *t = -1;
   }
-  __syncthreads();
+  if (__syncthreads_or(lost)) {
+    // What is no block does not stay in the list: one warp moves the others up.
+    if (lost) flags |= NP_FLAG_BLOCK_ID;
+    __shared__ int32_t left;
+    if (warp == 0) {
+      int32_t to = held;
+      for (int32_t i0 = held; i0 < top; i0 += 32) {  // (at most num_blocks of them)
+        const int32_t i = i0 + lane, b = i < top ? p.list[i] : -1;
+        const bool good = b >= 0 && b < p.num_blocks;
+        const unsigned m = __ballot_sync(0xffffffffu, good);  // every lane has read its entry
+        if (good) p.list[to + __popc(m & ((1u << lane) - 1u))] = b;
+        to += __popc(m);
+        __syncwarp();
+      }
+      if (lane == 0) left = to;
+    }
+    __syncthreads();
+    top = left;
+  }
+  if (tid == 0) p.count[0] = max(top - taken, 0);
   for (int32_t e = tid; e < taken; e += kMapThreads) {
     const int r = map_row(take, p.rows, e);
     const int32_t n = take[r + 1] - take[r];
