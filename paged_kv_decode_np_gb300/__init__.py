@@ -594,7 +594,7 @@ def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, 
 
     block_tables int32 [rows, max_blocks]; context_lens, new_lens, kept_lens int32 [rows];
     free_blocks int32 [num_blocks]; free_count int32 [1]; query_starts int32 [rows + 1];
-    slot_mapping int64 [tokens]; positions int32 [tokens]."""
+    slot_mapping int64 [tokens], one at least; positions int32 [tokens]."""
     name = "np_block_map"
     shape = block_tables.shape
     lens = context_lens.shape
@@ -615,8 +615,8 @@ def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, 
             query_starts.is_contiguous() and
             (kept_lens is None or (kept_lens.dtype is _INT32 and kept_lens.shape == lens and
                                    kept_lens.get_device() == cur and kept_lens.is_contiguous())) and
-            (slot_mapping is None or (slot_mapping.dtype is _INT64 and slot_mapping.dim() == 1 and
-                                      slot_mapping.get_device() == cur and
+            (slot_mapping is None or (n > 0 and slot_mapping.dtype is _INT64 and
+                                      slot_mapping.dim() == 1 and slot_mapping.get_device() == cur and
                                       slot_mapping.is_contiguous())) and
             (positions is None or (n > 0 and positions.dtype is _INT32 and positions.dim() == 1 and
                                    positions.numel() == n and positions.get_device() == cur and
@@ -628,8 +628,9 @@ def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, 
     st = load().np_block_map_packed(_pack(
         _MAP_ARGS, name, block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(),
         0 if kept_lens is None else kept_lens.data_ptr(), free_blocks.data_ptr(),
-        free_count.data_ptr(), query_starts.data_ptr(), slot_mapping.data_ptr() if n else 0,
-        positions.data_ptr() if n and positions is not None else 0,
+        free_count.data_ptr(), query_starts.data_ptr(),
+        0 if slot_mapping is None else slot_mapping.data_ptr(),
+        0 if positions is None else positions.data_ptr(),
         0 if err_word is None else err_word.data_ptr(), _stream_now(stream, cur),
         free_blocks.numel(), mb, rows, block_size, n))
     if st != NP_OK:
@@ -638,7 +639,7 @@ def np_block_map(block_tables, context_lens, new_lens, free_blocks, free_count, 
 
 def _refuse_map(name, cur, block_tables, context_lens, new_lens, free_blocks, free_count,
                 query_starts, slot_mapping, positions, kept_lens, err_word) -> None:
-    """np_block_map's refusal of its arguments (those of a mapping without tokens pass)."""
+    """np_block_map's refusal of its arguments."""
     if block_tables.dtype is not _INT32 or block_tables.dim() != 2:
         raise ValueError(f"{name}: block_tables must be int32 [rows, max_blocks]")
     rows = block_tables.shape[0]
@@ -653,6 +654,8 @@ def _refuse_map(name, cur, block_tables, context_lens, new_lens, free_blocks, fr
         raise ValueError(f"{name}: query_starts must be int32 [rows + 1]")
     if slot_mapping is not None and (slot_mapping.dtype is not _INT64 or slot_mapping.dim() != 1):
         raise ValueError(f"{name}: slot_mapping must be int64 [tokens]")
+    if slot_mapping is not None and slot_mapping.numel() == 0:
+        raise ValueError(f"{name}: slot_mapping has room for no tokens; None asks for the tables only")
     if positions is not None and (slot_mapping is None or positions.dtype is not _INT32 or
                                   positions.shape != slot_mapping.shape):
         raise ValueError(f"{name}: positions must be int32 [tokens], beside a slot_mapping")
