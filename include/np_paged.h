@@ -351,7 +351,7 @@ np_status np_paged_prefill_check(const np_paged_prefill_args* args);
  * (NP_FLAG_BLOCK_ID); where the step counted on it, the last entries taken are -1.
  * Up to 4096 rows; tables of up to 2^31 - 1025 tokens.  The
  * arrays must not overlap but for kept_lens.  rows 0 with tokens: all of them
- * are past the last.
+ * are past the last.  rows 0 without: a no-op (query_starts is not written).
  */
 np_status np_block_map(int32_t* block_tables, int32_t max_blocks_per_row,
                        int32_t* context_lens, const int32_t* new_lens,
