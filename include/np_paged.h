@@ -349,8 +349,8 @@ np_status np_paged_prefill_check(const np_paged_prefill_args* args);
  * entry outside [0, num_blocks) becomes -1 in the table and its slots -1
  * (NP_FLAG_BLOCK_ID).  A table entry outside it that a row gives back is dropped
  * (NP_FLAG_BLOCK_ID); where the step counted on it, the last entries taken are -1.
- * Up to 4096 rows; tables of up to 2^31 - 1025 tokens.  The
- * arrays must not overlap but for kept_lens.  rows 0 with tokens: all of them
+ * Up to 4096 rows; tables of up to 2^31 - 1025 tokens; num_tokens, num_blocks and all
+ * rows' tables up to 2^31 - 4097 entries.  The arrays must not overlap but for kept_lens.  rows 0 with tokens: all of them
  * are past the last.  rows 0 without: a no-op (query_starts is not written).
  */
 np_status np_block_map(int32_t* block_tables, int32_t max_blocks_per_row,
@@ -385,8 +385,8 @@ np_status np_block_map(int32_t* block_tables, int32_t max_blocks_per_row,
  * not count in A; NaN becomes NaN in e4m3 and 0 in int8 (all three but the
  * first: NP_FLAG_VALUE).
  * dtype NP_F32 or NP_BF16; head_dim as in the list above; any block_size;
- * kv_heads up to 4096.  Pointers 16-byte aligned (scales, in every call: 4), strides a multiple of 16 bytes, at least
- * a token's heads.  The pools and scales must not overlap one another, nor what is
+ * kv_heads up to 4096; num_tokens up to 2^31 - 4097.  Pointers 16-byte aligned (scales,
+ * in every call: 4), strides a multiple of 16 bytes, at least a token's heads.  The pools and scales must not overlap one another, nor what is
  * read.  num_tokens == 0 is a no-op.
  */
 np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
@@ -422,7 +422,8 @@ np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
  * be NaN (where a query token does not see the position either).  Supported: dtype
  * NP_F32 (g * query_len <= 8) or NP_BF16 (<= 16), g = q_heads / kv_heads; head_dim
  * of the list above; any block_size; any kv_heads; rows up to 65535; tables of up to
- * 2^31 - 1025 tokens, and rows * kv_heads * a table's tokens up to 2^34.  A row without history gets zeros.  rows 0: a no-op.
+ * 2^31 - 1025 tokens, and rows * kv_heads * a table's tokens (rounded up to 16) up to
+ * 2^34.  A row without history gets zeros.  rows 0: a no-op.
  */
 size_t np_paged_decode_q8_workspace_bytes(int32_t head_dim);
 /* enough for every head_dim */

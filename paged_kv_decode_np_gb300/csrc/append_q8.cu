@@ -266,6 +266,7 @@ extern "C" np_status np_kv_append_q8_packed(const np_kv_append_q8_args* a) {
     return NP_ERR_INVALID_ARG;
   if (d != 16 && d != 32 && d != 64 && d != 128 && d != 256) return NP_ERR_UNSUPPORTED;
   if (a->kv_heads > 4096) return NP_ERR_UNSUPPORTED;  // far above any model's
+  if (a->num_tokens > INT32_MAX - 4096) return NP_ERR_UNSUPPORTED;  // loops step past the last
   const int64_t row = (int64_t)a->kv_heads * d;
   int64_t slots = 0, pool = 0, scales = 0, kn = 0, vn = 0;
   if (!mul_fits(a->num_blocks, a->block_size, &slots) || !mul_fits(slots, row, &pool) ||
@@ -286,7 +287,9 @@ extern "C" np_status np_kv_append_q8_packed(const np_kv_append_q8_args* a) {
   for (const void* x : {static_cast<const void*>(a->k_pool), static_cast<const void*>(a->v_pool), a->k_new,
                         a->v_new})
     if (!aligned_to(x, 16)) return NP_ERR_INVALID_ARG;
-  if (!aligned_to(a->k_scale, 4) || !aligned_to(a->v_scale, 4) || !aligned_to(a->slot_mapping, 8) || !aligned_to(a->err_word, 4)) return NP_ERR_INVALID_ARG;
+  if (!aligned_to(a->k_scale, 4) || !aligned_to(a->v_scale, 4) || !aligned_to(a->slot_mapping, 8) ||
+      !aligned_to(a->err_word, 4))
+    return NP_ERR_INVALID_ARG;
   const Span spans[] = {{a->k_pool, pool}, {a->v_pool, pool}, {a->k_scale, scales}, {a->v_scale, scales},
                         {a->k_new, kn},    {a->v_new, vn},    {a->slot_mapping, 8ll * a->num_tokens}};
   if (any_overlap(spans, 4)) return NP_ERR_INVALID_ARG;

@@ -312,9 +312,12 @@ extern "C" np_status np_block_map_packed(const np_block_map_args* a) {
       !mul_fits(a->num_blocks, a->block_size, &slots) ||
       !mul_fits(a->rows, (int64_t)a->max_blocks_per_row * 4, &tab))
     return NP_ERR_OUT_OF_RANGE;
-  if (a->rows > kMapMaxRows || cap > INT32_MAX - 1024 || a->num_blocks > INT32_MAX) return NP_ERR_UNSUPPORTED;
-  // every block of every row's table has its number among 32-bit prefix sums
-  if ((int64_t)a->rows * a->max_blocks_per_row > INT32_MAX) return NP_ERR_UNSUPPORTED;
+  if (a->rows > kMapMaxRows || cap > INT32_MAX - 1024) return NP_ERR_UNSUPPORTED;
+  // every block of every row's table has its number among 32-bit prefix sums, and every
+  // block and token in loops that step past the last by less than 4096
+  if ((int64_t)a->rows * a->max_blocks_per_row > INT32_MAX - 4096 || a->num_blocks > INT32_MAX - 4096 ||
+      a->num_tokens > INT32_MAX - 4096)
+    return NP_ERR_UNSUPPORTED;
   if (a->rows == 0 && a->num_tokens == 0) return NP_OK;
   if (!a->query_starts || !a->free_blocks || !a->free_count || (a->num_tokens > 0 && !a->slot_mapping) ||
       (a->num_tokens == 0 && a->slot_mapping) || (a->positions && !a->slot_mapping) ||

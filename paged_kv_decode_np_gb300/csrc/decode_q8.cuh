@@ -50,8 +50,12 @@ NPK_Q8_DECLARE(256)
 
 // The launches for a head_dim and form, after everything that they need but head_group,
 // least and ctas is in p (decode_q8_api.cu).
-// rows x table tokens x kv heads: all rows' chunks of 16 tokens then are below 2^31
-constexpr int64_t kQ8MaxWork = 1ll << 34;
+// Whether all rows' chunks (of 16 tokens, per kv head) can be counted in an int32: 2^30 at
+// most, with tables of `cap` tokens.  rows < 2^16, cap < 2^31.
+constexpr bool q8_work_fits(int64_t rows, int64_t kv_heads, int64_t cap) {
+  const int64_t chunks = rows * ((cap + 15) / 16);  // < 2^43
+  return chunks == 0 || kv_heads <= (1ll << 30) / chunks;
+}
 np_status launch_decode_q8(DecodeQ8Params& p, int32_t head_dim, np_dtype dtype, np_form8 form, int sms,
                            cudaStream_t s);
 

@@ -44,17 +44,14 @@ np_status check_decode_q8(const np_read_q8_args& a, bool* run) {
       !mul_fits((int64_t)a.rows * a.query_len, a.q_heads * d * es, &qn))
     return NP_ERR_OUT_OF_RANGE;
   if (a.rows > 65535 || cap > INT32_MAX - 1024) return NP_ERR_UNSUPPORTED;
-  // a row of the stream (row, group of kv heads) is an int32, and so are all their chunks
-  int64_t work = 0;
-  if ((int64_t)a.rows * a.kv_heads > INT32_MAX || !mul_fits((int64_t)a.rows * a.kv_heads, cap, &work) ||
-      work > kQ8MaxWork)
-    return NP_ERR_UNSUPPORTED;
+  if (!q8_work_fits(a.rows, a.kv_heads, cap)) return NP_ERR_UNSUPPORTED;
   if (a.rows == 0) return NP_OK;
   if (!a.out || !a.q || !a.k_pool || !a.v_pool || !a.k_scale || !a.v_scale || !a.block_tables || !a.context_lens)
     return NP_ERR_INVALID_ARG;
   for (const void* x : {static_cast<const void*>(a.out), a.q, a.k_pool, a.v_pool})
     if (!aligned_to(x, 16)) return NP_ERR_INVALID_ARG;
-  if (!aligned_to(a.k_scale, 4) || !aligned_to(a.v_scale, 4) || !aligned_to(a.block_tables, 4) || !aligned_to(a.context_lens, 4) || !aligned_to(a.err_word, 4))
+  if (!aligned_to(a.k_scale, 4) || !aligned_to(a.v_scale, 4) || !aligned_to(a.block_tables, 4) ||
+      !aligned_to(a.context_lens, 4) || !aligned_to(a.err_word, 4))
     return NP_ERR_INVALID_ARG;
   const Span spans[] = {{a.out, qn}, {a.q, qn}, {a.k_pool, pool}, {a.v_pool, pool}, {a.k_scale, scales},
                         {a.v_scale, scales}, {a.block_tables, tab}, {a.context_lens, 4ll * a.rows}};

@@ -408,10 +408,8 @@ extern "C" np_status np_paged_prefill_q8_packed(const np_read_q8_args* a) {
   // one fetch of its tile.  Two launches more (about 5 us), so where rows are short on
   // average: 62 rows of one token and two of 512 305 us without, 229 with.
   const int few = (p.group <= 8 ? 8 : 16) / p.group;
-  int64_t work = 0;
   if ((p.rows > 1 ? p.tokens < 64ll * p.rows : p.tokens <= few) &&
-      mul_ok((int64_t)p.rows * p.kv_heads, (int64_t)p.max_blocks_per_row * p.block_size, &work) &&
-      work <= npk::kQ8MaxWork) {
+      npk::q8_work_fits(p.rows, p.kv_heads, (int64_t)p.max_blocks_per_row * p.block_size)) {
     p.skip_tokens = few;
     npk::DecodeQ8Params d{};
     d.out = p.out;
