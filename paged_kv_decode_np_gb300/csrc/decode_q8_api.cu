@@ -1,27 +1,12 @@
 // decode_q8_api.cu -- np_paged_decode_q8: argument validation and the launches.
 #include <limits.h>
 
-#include <atomic>
-
 #include "decode_q8.cuh"
 #include "host_checks.h"
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-std::atomic<int> g_sms[64];
-
-int sm_count() {
-  int dev = 0, s = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev < 64) s = g_sms[dev].load();
-  if (s == 0) {
-    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev < 64) g_sms[dev].store(s);
-  }
-  return s;
-}
 
 bool head_dim_ok(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
 
@@ -106,7 +91,7 @@ extern "C" np_status np_paged_decode_q8_packed(const np_read_q8_args* a) {
   bool run;
   const np_status st = check_decode_q8(*a, &run);
   if (st != NP_OK || !run) return st;
-  const int sms = sm_count();
+  const int sms = npk::sm_count();
   if (sms <= 0) return NP_ERR_CUDA;
   npk::DecodeQ8Params p{};
   p.out = a->out;

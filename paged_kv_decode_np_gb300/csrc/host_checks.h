@@ -1,8 +1,12 @@
-// host_checks.h -- what the entry points of the 8-bit cache check their
-// arguments with.
+// host_checks.h -- what the entry points of the prompt side and of the 8-bit
+// cache check their arguments with, and the device's size.
 #pragma once
 
 #include <stdint.h>
+
+#include <atomic>
+
+#include <cuda_runtime.h>
 
 namespace npk {
 
@@ -29,6 +33,19 @@ inline bool any_overlap(const Span (&s)[N], int written) {
     for (int j = i + 1; j < N; ++j)
       if (overlaps(s[i], s[j])) return true;
   return false;
+}
+
+// The current device's SMs; 0: no device.
+inline int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, s = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64) s = known[dev].load();
+  if (s == 0) {
+    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(s);
+  }
+  return s;
 }
 
 }  // namespace npk

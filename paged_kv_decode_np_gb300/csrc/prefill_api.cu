@@ -2,28 +2,23 @@
 // layout and the launches.
 #include <limits.h>
 
-#include <atomic>
 #include <mutex>
 
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled_v12000
 
 #include "decode_q8.cuh"
+#include "host_checks.h"
 #include "prefill.cuh"
 
 namespace {
 
+using npk::aligned_to;
+using npk::mul_fits;
+using npk::overlaps;
 using npk::PrefillParams;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
+using npk::sm_count;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && n > 0 && m > 0 && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
-}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -36,19 +31,6 @@ static_assert(npk::kQ8MaxCtas <= npk::kPrefillMaxCtas && 8 * npk::kQ8Rows <= 128
 
 // rows of the largest unit any kernel of this head_dim takes
 int unit_rows(int32_t head_dim) { return head_dim == 256 ? 128 : 256; }
-
-std::atomic<int> g_sms[64];
-
-int sm_count() {
-  int dev = 0, s = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev < 64) s = g_sms[dev].load();
-  if (s == 0) {
-    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev < 64) g_sms[dev].store(s);
-  }
-  return s;
-}
 
 // The driver's tensor map encoder, through the runtime (no libcuda link).
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
@@ -226,10 +208,10 @@ np_status check_prefill(const np_paged_prefill_args& a, bool* run, int pool_es =
   if (d != 16 && d != 32 && d != 64 && d != 128 && d != 256) return NP_ERR_UNSUPPORTED;
   if (a.q_heads / a.kv_heads > (a.dtype == NP_BF16 ? 16 : 8)) return NP_ERR_UNSUPPORTED;
   int64_t slots = 0, pool = 0, cap = 0, qn = 0, tab = 0;
-  if (!mul_ok(a.num_blocks, a.block_size, &slots) ||
-      !mul_ok(slots, (int64_t)a.kv_heads * d * (pool_es ? pool_es : es), &pool) ||
-      !mul_ok(a.num_tokens, (int64_t)a.q_heads * d * es, &qn) ||
-      !mul_ok(a.max_blocks_per_row, a.block_size, &cap) || !mul_ok(a.rows, a.max_blocks_per_row, &tab))
+  if (!mul_fits(a.num_blocks, a.block_size, &slots) ||
+      !mul_fits(slots, (int64_t)a.kv_heads * d * (pool_es ? pool_es : es), &pool) ||
+      !mul_fits(a.num_tokens, (int64_t)a.q_heads * d * es, &qn) ||
+      !mul_fits(a.max_blocks_per_row, a.block_size, &cap) || !mul_fits(a.rows, a.max_blocks_per_row, &tab))
     return NP_ERR_OUT_OF_RANGE;
   // positions are int32 with some kv tiles to spare
   if (cap > INT32_MAX - 1024 || a.num_tokens > INT32_MAX - 512) return NP_ERR_UNSUPPORTED;
@@ -237,15 +219,16 @@ np_status check_prefill(const np_paged_prefill_args& a, bool* run, int pool_es =
   if (a.rows == 0 || a.num_tokens == 0) return NP_OK;
   if (!a.out || !a.q || !a.k_pool || !a.v_pool || !a.block_tables || !a.context_lens || !a.query_starts)
     return NP_ERR_INVALID_ARG;
-  if (!aligned(a.out, 16) || !aligned(a.q, 16) || !aligned(a.k_pool, 16) || !aligned(a.v_pool, 16) ||
-      !aligned(a.block_tables, 4) || !aligned(a.context_lens, 4) || !aligned(a.query_starts, 4) ||
-      (a.err_word && !aligned(a.err_word, 4)))
+  if (!aligned_to(a.out, 16) || !aligned_to(a.q, 16) || !aligned_to(a.k_pool, 16) ||
+      !aligned_to(a.v_pool, 16) || !aligned_to(a.block_tables, 4) || !aligned_to(a.context_lens, 4) ||
+      !aligned_to(a.query_starts, 4) ||
+      (a.err_word && !aligned_to(a.err_word, 4)))
     return NP_ERR_INVALID_ARG;
-  if (overlap(a.out, qn, a.q, qn) || overlap(a.out, qn, a.k_pool, pool) ||
-      overlap(a.out, qn, a.v_pool, pool))
+  if (overlaps({a.out, qn}, {a.q, qn}) || overlaps({a.out, qn}, {a.k_pool, pool}) ||
+      overlaps({a.out, qn}, {a.v_pool, pool}))
     return NP_ERR_INVALID_ARG;
   if (!a.workspace || a.workspace_bytes < 0 ||
-      (size_t)a.workspace_bytes < np_paged_prefill_workspace_bytes(d) || !aligned(a.workspace, 256))
+      (size_t)a.workspace_bytes < np_paged_prefill_workspace_bytes(d) || !aligned_to(a.workspace, 256))
     return NP_ERR_WORKSPACE;
   *run = true;
   return NP_OK;
@@ -376,10 +359,12 @@ np_status check_prefill_q8(const np_read_q8_args& a, bool* run) {
   if (st != NP_OK || !*run) return st;
   *run = false;
   int64_t scales = 0;
-  if (!mul_ok(a.num_blocks, 4ll * a.kv_heads, &scales)) return NP_ERR_OUT_OF_RANGE;
-  if (!a.k_scale || !a.v_scale || !aligned(a.k_scale, 4) || !aligned(a.v_scale, 4)) return NP_ERR_INVALID_ARG;
+  if (!mul_fits(a.num_blocks, 4ll * a.kv_heads, &scales)) return NP_ERR_OUT_OF_RANGE;
+  if (!a.k_scale || !a.v_scale || !aligned_to(a.k_scale, 4) || !aligned_to(a.v_scale, 4))
+    return NP_ERR_INVALID_ARG;
   const int64_t out = (int64_t)a.num_tokens * a.q_heads * a.head_dim * (a.dtype == NP_BF16 ? 2 : 4);
-  if (overlap(a.out, out, a.k_scale, scales) || overlap(a.out, out, a.v_scale, scales)) return NP_ERR_INVALID_ARG;
+  if (overlaps({a.out, out}, {a.k_scale, scales}) || overlaps({a.out, out}, {a.v_scale, scales}))
+    return NP_ERR_INVALID_ARG;
   *run = true;
   return NP_OK;
 }
