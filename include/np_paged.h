@@ -410,7 +410,10 @@ np_status np_kv_append_q8(void* k_pool, void* v_pool, float* k_scale,
  *                  aligned, not shared by calls that may overlap; needs no
  *                  initialisation
  * One schedule: the balanced one (equal shares of all rows' history, cut rows
- * joined by a second launch; the same call gives the same bits).  q, K, V and the
+ * joined by a second launch; the same call gives the same bits).  fp32: where rows *
+ * kv_heads * a table's tokens pass 32768 (head_dim 256: 16384) an SM, sums take more
+ * roundings, against truncation in long ones, and a third longer: tables that wide
+ * cost that, and change last bits, whatever they hold.  q, K, V and the
  * weights are multiplied in fp16 with fp32 sums: codes are exact in fp16, q is
  * scaled by a power of two first (bf16 is then exact but below 2^-28 of the
  * row's largest element); a weight is rounded to fp16 for its product with V,

@@ -13,9 +13,12 @@
 // and head, so there is nothing to wait for and nothing atomic.
 //
 // Bound: the chain of a run's loads, maximum, scale and stores; enough runs side by side
-// reach two thirds of the copy rate (16384 tokens, 8 heads of 128, bf16, blocks of 32:
-// 22.4 us, 4.5 TB/s), decode batches are latency (64 tokens 3.1 us, 256 3.9).  A block of the
-// grid takes `window` tokens: every warp finds by itself which of them begin runs, and
+// reach half of the copy rate (16384 tokens, 8 heads of 128, bf16, blocks of 32: 28 us as
+// calls, 3.6 TB/s; 22.4 replayed, when L2 still holds part of it), decode batches are latency
+// (64 tokens 2.7 us where no scale grows, 256 3.9).  Where one grows, the block's other slots
+// are read, rounded and written one by one: with 6 % of a decode batch's (block, head) pairs,
+// about what its steps have, 64 tokens take 8.6 us in blocks of 16 and 26 in blocks of 64.  A
+// block of the grid takes `window` tokens: every warp finds by itself which of them begin runs, and
 // they deal out (run, head, K or V).  The first token's values are on their way before the
 // run's length is known.  (A shared list of the runs, 16 tokens in registers and the rest one by
 // one: 32, 3.5 and 7.4 us.)

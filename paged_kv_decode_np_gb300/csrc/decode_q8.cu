@@ -36,10 +36,10 @@
 //
 // Bound: HBM on long rows (16 rows of 32768-131072 positions, 64 / 8 heads: 458 us, 6.8
 // TB/s).  Shorter ones pay what runs once: about 5 us until the first chunk is there, 3 at
-// each row's end, 6 for the join (64 rows of 1024-8192: 99 us, 82 at the copy rate; 8 fp32
+// each row's end, 6 for the join (64 rows of 1024-8192: 100 us, 82 at the copy rate; 8 fp32
 // rows of 512-2048: 20, latency throughout).  More than eight rows a head take two column
 // tiles, whose sums leave registers for eight warps only: 4 query tokens of 4 heads, int8,
-// 127 us against 86; the issue slots are half used and each warp waits for its own
+// 125 us against 86; the issue slots are half used and each warp waits for its own
 // products.  Why warps that read for themselves: the loop's copies, widening and products
 // overlap across 16 warps without a barrier, and a stage is 4 KB, so that three of them a
 // warp keep 130 KB an SM on the way.  Measured against: table look-ups in line with the copies
@@ -185,7 +185,9 @@ struct Q8Walk {
 // MANY (fp32): a warp may sum many chunks.  An mma's sum truncates, and hundreds in a row
 // add that up, so each chunk's O is summed by itself and then added with rounding.  64 rows
 // of 15000 positions (470 chunks a warp): 4.9e-6 of the result off without and 5.0e-7 with,
-// 322 and 469 us; 94 chunks: 1.3e-6 and 3.7e-7, 119 and 150 us.
+// 322 and 469 us; 94 chunks: 1.3e-6 and 3.7e-7, 109 and 151 us.  The launch goes by what the
+// tables may hold, not by what they do (lengths are the device's): 64 rows of 1024-8192 take
+// the 151 us under tables of 131072 tokens, 8 rows of 512-2048 21.8 for 20.3.
 template <typename T, int D, int FORM, int NT, bool MANY>
 __global__ void __launch_bounds__(32 * Q8Geo<D, NT>::WARPS, 1)
     decode_q8_kernel(const __grid_constant__ DecodeQ8Params p) {

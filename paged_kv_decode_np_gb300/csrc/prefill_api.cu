@@ -390,8 +390,14 @@ extern "C" np_status np_paged_prefill_q8_packed(const np_read_q8_args* a) {
   const np_dtype dtype = static_cast<np_dtype>(a->dtype);
   const np_form8 form = static_cast<np_form8>(a->form);
   // Rows with few tokens go to the decode read's kernel: their (token, head) rows fit
-  // one fetch of its tile.  Two launches more (about 5 us), so where rows are short on
-  // average: 62 rows of one token and two of 512 305 us without, 229 with.
+  // one fetch of its tile.  Two launches more (5 to 15 us), so where rows are short on
+  // average.  us, replayed, bf16 / fp32, all rows here -> the short ones there (heads 32 / 8,
+  // histories of 1024-8192): 62 rows of one token and two of 512 (17 a row) 288 / 772 -> 193 /
+  // 315; 30 and two of 900 (57) 242 / 650 -> 206 / 413; 64 of two 219 / 552 -> 107 / 120; 64
+  // of 4, 8, 16 and 48, none short: 218-304 -> 224-313.  Past the border: 30 and two of 1024
+  // (65) 285 / 680, 208 / 446 if they went there; 14 and two of 1024 (129) 237 / 658, 224 /
+  // 523; 12 and four of 400 (101) 224 / 648, 227 / 516; 3 and one of 300 (76) 51 / 99, 66 / 109:
+  // few rows lose by it, many gain, and the average does not tell them apart.
   const int few = (p.group <= 8 ? 8 : 16) / p.group;
   if ((p.rows > 1 ? p.tokens < 64ll * p.rows : p.tokens <= few) &&
       npk::q8_work_fits(p.rows, p.kv_heads, (int64_t)p.max_blocks_per_row * p.block_size)) {

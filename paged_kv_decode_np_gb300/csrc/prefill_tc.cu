@@ -55,7 +55,7 @@
 // range, and their weights too (tc_wide_tile).  q is fp16 as well, each row times a power of two
 // that brings its largest element to 2^14 .. 2^15; the same four warps turn it in place.
 // 1024 tokens of 65536, 64 / 8 heads: 1.83 ms, 1190 TFLOP/s, 60 us of it for telling wide
-// tiles from others; the four warps take ~1000 cycles a tile and the softmax 10 % longer beside
+// tiles from others (the bf16 pools' kernel: 1.50); the four warps take ~1000 cycles a tile and the softmax 10 % longer beside
 // them.  (Widened to bf16 by six instructions a pair, all pieces unrolled 3.63 ms: their
 // fetching stalled everybody; rolled 2.93.)
 // Token by token, six warps widen to bf16 with the scales multiplied in, exactly: they
