@@ -161,3 +161,17 @@ def test_chunks_count_positions_whose_v_is_far_smaller(nplib, dtype, form, d, bs
     inp, scale = _zero_v_beside_large_v(dtype, form, d, bs, n, c, top, low, where, gap)
     out = _prefill(nplib, inp, scale)
     _within(inp, [(n, c)], scale, out, dtype)
+
+
+@pytest.mark.parametrize("dtype,d,g", [(BF, 64, 1), (BF, 64, 16), (BF, 128, 3), (BF, 128, 8), (BF, 256, 5), (F32, 128, 4)])
+@pytest.mark.parametrize("bs,scale", [(8, -0.06), (24, 0.06), (64, -0.06), (256, 0.06)])
+def test_far_scales_in_every_shape(nplib, dtype, d, g, bs, scale):
+    """Blocks of K up to 2^6 and of V up to 2^46 apart, in ragged chunks, short rows among them."""
+    rows = [(5, 5), (1, 300), (130, 700), (64, 64), (33, 1000), (2, 2), (257, 257), (90, 2100)]
+    form = E4M3 if bs in (8, 64) else INT8
+    inp = h.read_inputs(dtype, form, d, 2, g, bs, rows, seed=bs + g, spread=3)
+    gen = torch.Generator().manual_seed(bs)
+    inp["v_scale"] *= torch.ldexp(torch.ones(inp["v_scale"].shape),
+                                  torch.randint(-20, 21, inp["v_scale"].shape, generator=gen)).cuda()
+    out = _prefill(nplib, inp, scale)
+    _within(inp, rows, scale, out, dtype)
